@@ -233,13 +233,7 @@ def _plain_product(state):
     w = state["w"].float()
     if case["nk"]:
         w = w.t()
-    # 1024 products of at most 2^14 each are summed exactly in 32-bit floats;
-    # the pieces are added as integers.
-    total = None
-    for k0 in range(0, case["k"], 1024):
-        part = (a[:, k0:k0 + 1024] @ w[k0:k0 + 1024]).to(torch.int32)
-        total = part if total is None else total + part
-    y = total.float() * sa * state["sb"]
+    y = (a @ w) * sa * state["sb"]
     if state["bias"] is not None:
         y = y + state["bias"].float()
     return y.to(DTYPES[case["out"]])
