@@ -303,6 +303,131 @@ mm_status mm_int_plan_create(const int64_t *a_shape, int a_rank, const int64_t *
 mm_status mm_int_execute(mm_plan_t plan, const void *A, const void *B, const void *a_zero_point,
                          const void *b_zero_point, void *Y, void *stream);
 
+/* INT8 product with one scale for each row of A (token) and each column of B
+ * (output channel), beside MatMulInteger: MatMul's shapes, broadcasting and
+ * rank-one rules, and
+ *
+ *   Y[i, m, n] = a_scale[iA(i), m] * b_scale[iB(i), n]
+ *                * sum_k A[iA(i), m, k] * B[iB(i), k, n]  (+ bias[n])
+ *
+ * A is INT8 with scales the caller has (a_type MM_INT8), or a FLOAT, FLOAT16
+ * or BFLOAT16 tensor that every execution quantizes row by row first
+ * (mm_quantize_rows' rule) into plan-owned memory.  B is INT8, stored [.., K,
+ * N] or, with trans_b, [.., N, K] (the order of linear-layer weights; b_shape
+ * then is the stored shape, and B may not be rank one).  Scales are FP32:
+ * a_scale has one value for each row of A (the product of A's dimensions but
+ * the last), b_scale one for each column of every B matrix (B's batch
+ * dimensions times N).  bias, if has_bias, holds N values of the output type
+ * (out_type: FLOAT, FLOAT16 or BFLOAT16), shared by every batch.
+ *
+ * The integer sum is exact: K is at most 131071 (MM_ERR_TOO_LARGE above), so
+ * INT32 holds any sum of INT8 products.  It is rounded to FP32 once,
+ * multiplied by the row's, then the column's scale, the bias is added in
+ * FP32, and the result is narrowed once.  Results do not depend on the
+ * algorithm or on a split of K.  A scale that is NaN or infinite makes its
+ * row or column what IEEE arithmetic makes of it; K == 0 gives the bias (or
+ * zeros).
+ *
+ * Options: force_algo SKINNY_M (a folded product of at most 32 rows with
+ * trans_b), GENERAL or SPLIT_K; tile k >= 1 is entry k of 256 x 256, 128 x
+ * 128, 64 x 128, 32 x 128; split_k as for MatMul.  A plan with an A to
+ * quantize or a split K owns a workspace: its executions must not overlap,
+ * and it is allocated and bound to a device as described above.  Other errors
+ * are those of mm_plan_create. */
+typedef struct mm_scaled_int_desc {
+    int32_t a_type;   /* MM_INT8, or the type of an A to be quantized */
+    int32_t out_type; /* MM_FLOAT, MM_FLOAT16 or MM_BFLOAT16 */
+    int32_t trans_b;  /* 0 or 1 */
+    int32_t has_bias; /* 0 or 1 */
+    int32_t reserved; /* must be 0 */
+} mm_scaled_int_desc;
+
+mm_status mm_scaled_int_plan_create(const int64_t *a_shape, int a_rank, const int64_t *b_shape, int b_rank,
+                                    const mm_scaled_int_desc *desc, const mm_plan_options *opt, mm_plan_t *out);
+
+/* Enqueue the scaled product on `stream`.  a_scale is required for an INT8 A
+ * and must be NULL for an A that the call quantizes (MM_ERR_BAD_OPTION);
+ * b_scale is required; bias is non-NULL exactly when the plan has one
+ * (MM_ERR_NULL_ARG / MM_ERR_BAD_OPTION).  Other rules as for mm_execute. */
+mm_status mm_scaled_int_execute(mm_plan_t plan, const void *A, const void *B, const float *a_scale,
+                                const float *b_scale, const void *bias, void *Y, void *stream);
+
+/* Quantize each row of a dense row-major [rows, cols] device tensor X (FLOAT,
+ * FLOAT16 or BFLOAT16) to INT8, on `stream`:
+ *
+ *   amax = max(max_k |x_k|, 2^-100)     scale = amax / 127
+ *   q_k = rint(x_k * r), ties to even   r = 127 / amax
+ *
+ * all in FP32, each operation rounded once.  Q is dense [rows, cols] INT8
+ * with values -127 .. 127, scale holds `rows` FP32 values.  A row with an
+ * infinity or a NaN gets the scale NaN and zeros.  cols == 0 writes the
+ * scales only.  MM_ERR_NEG_DIM, MM_ERR_DTYPE, MM_ERR_TOO_LARGE (a size of
+ * 2^31 or more), MM_ERR_NULL_ARG, MM_ERR_HIP. */
+mm_status mm_quantize_rows(const void *X, int dtype, int64_t rows, int64_t cols, void *Q, float *scale, void *stream);
+
+/* Gated feed-forward block, beside Gemm: with X [rows, in_features],
+ *
+ *   G = X Wg,  U = X Wu,  H = f(G) * U     (H, G, U: [rows, hidden])
+ *
+ * in one kernel, and its backward pass from dH:
+ *
+ *   dG = dH * U * f'(G)   dX  = dG Wg^T + dU Wu^T
+ *   dU = dH * f(G)        dWg = X^T dG,  dWu = X^T dU
+ *
+ * Wg and Wu are stored [in_features, hidden] or, with trans_w, [hidden,
+ * in_features], with rows w_pitch elements apart (0: dense; the gate and up
+ * halves of one merged matrix are two pointers with its pitch).  dWg and dWu
+ * have the weights' layout and pitch.  Everything has the plan's type (FLOAT,
+ * FLOAT16 or BFLOAT16); X, H, G, U, dH and dX are dense.
+ *
+ * Products accumulate in FP32, f and the element-wise products are computed
+ * in FP32, H, G and U are each rounded once.  The backward pass starts from
+ * the rounded G and U and rounds dG and dU to the plan's type for the matrix
+ * cores.  relu's derivative at 0 is 0.  Infinities and NaN follow the
+ * formulas.
+ *
+ * Options: force_algo SKINNY_M (at most 32 rows, trans_w) or GENERAL; tile
+ * k >= 1 is entry k of 256 x 256 (16-bit types), 128 x 128, 64 x 128, 32 x
+ * 128 for the forward pass (columns count gate and up); the backward pass
+ * takes the first two, and the second for the others. */
+typedef enum mm_activation {
+    MM_ACT_SILU = 1,      /* g / (1 + exp(-g)) */
+    MM_ACT_GELU = 2,      /* g Phi(g), by erf */
+    MM_ACT_GELU_TANH = 3, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+    MM_ACT_RELU = 4,      /* max(g, 0) */
+    MM_ACT_SIGMOID = 5    /* 1 / (1 + exp(-g)) */
+} mm_activation;
+
+typedef struct mm_glu_desc {
+    int64_t rows, in_features, hidden;
+    int64_t w_pitch;    /* 0, or at least the length of a stored weight row */
+    int32_t trans_w;    /* 0 or 1 */
+    int32_t activation; /* an mm_activation value */
+    int32_t training;   /* 1: the plan owns the backward pass's workspace (dG, dU) */
+    int32_t reserved;   /* must be 0 */
+} mm_glu_desc;
+
+/* Create a gated-block plan.  MM_ERR_NEG_DIM, MM_ERR_DTYPE, MM_ERR_BAD_OPTION
+ * (an invalid field or option), MM_ERR_TOO_LARGE, MM_ERR_ALLOC.  Forward
+ * executions use no workspace and may overlap; backward executions of one
+ * plan must not overlap.  The plan answers the introspection calls (output
+ * shape [rows, hidden]). */
+mm_status mm_glu_plan_create(const mm_glu_desc *desc, int dtype, const mm_plan_options *opt, mm_plan_t *out);
+
+/* Enqueue H = f(X Wg) * (X Wu) on `stream`; G and U, both or neither (NULL),
+ * receive X Wg and X Wu for the backward pass.  H, G and U may not overlap
+ * each other or an input.  in_features == 0 gives zeros without reading. */
+mm_status mm_glu_execute(mm_plan_t plan, const void *X, const void *Wg, const void *Wu, void *H, void *G, void *U,
+                         void *stream);
+
+/* Enqueue the backward pass of a plan with `training` (else MM_ERR_BAD_OPTION)
+ * on `stream`, from the G and U of the forward pass on the same X and
+ * weights.  dX may be NULL (inputs without a gradient), and dWg and dWu may
+ * both be NULL (frozen weights); what is computed is written, not added.
+ * rows == 0 writes zero weight gradients, hidden == 0 a zero dX. */
+mm_status mm_glu_backward(mm_plan_t plan, const void *X, const void *Wg, const void *Wu, const void *G, const void *U,
+                          const void *dH, void *dX, void *dWg, void *dWu, void *stream);
+
 /* Output shape: writes up to MM_MAX_RANK entries to `shape` and the rank to
  * *rank (0 when both inputs are rank one). */
 mm_status mm_plan_output_shape(mm_plan_t plan, int64_t *shape, int *rank);

@@ -18,6 +18,9 @@ LIB_PATH = os.path.join(PKG, "libmm.so")
 FLOAT, FLOAT16, DOUBLE, BFLOAT16 = 1, 10, 11, 16
 UINT8, INT8, INT32 = 2, 3, 6
 ZP_NONE, ZP_SCALAR, ZP_VECTOR = 0, 1, 2
+ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SIGMOID = 1, 2, 3, 4, 5
+ACTIVATIONS = {"silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU,
+               "sigmoid": ACT_SIGMOID}
 MAX_BATCH_DIMS = 8
 MAX_RANK = MAX_BATCH_DIMS + 2
 
@@ -68,6 +71,17 @@ class GemmDesc(ctypes.Structure):
         ("c_shape", ctypes.c_int64 * 2),
         ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
     ]
+
+
+class ScaledIntDesc(ctypes.Structure):
+    _fields_ = [("a_type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("trans_b", ctypes.c_int32),
+                ("has_bias", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GluDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_features", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("w_pitch", ctypes.c_int64), ("trans_w", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("training", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -128,6 +142,20 @@ def lib() -> ctypes.CDLL:
         L.mm_int_plan_create.restype = ctypes.c_int
         L.mm_int_execute.argtypes = [vp, vp, vp, vp, vp, vp, vp]
         L.mm_int_execute.restype = ctypes.c_int
+        L.mm_scaled_int_plan_create.argtypes = [i64p, ctypes.c_int, i64p, ctypes.c_int, ctypes.POINTER(ScaledIntDesc),
+                                                 ctypes.POINTER(PlanOptions), ctypes.POINTER(vp)]
+        L.mm_scaled_int_plan_create.restype = ctypes.c_int
+        L.mm_scaled_int_execute.argtypes = [vp] * 8
+        L.mm_scaled_int_execute.restype = ctypes.c_int
+        L.mm_quantize_rows.argtypes = [vp, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, vp, vp, vp]
+        L.mm_quantize_rows.restype = ctypes.c_int
+        L.mm_glu_plan_create.argtypes = [ctypes.POINTER(GluDesc), ctypes.c_int, ctypes.POINTER(PlanOptions),
+                                         ctypes.POINTER(vp)]
+        L.mm_glu_plan_create.restype = ctypes.c_int
+        L.mm_glu_execute.argtypes = [vp] * 8
+        L.mm_glu_execute.restype = ctypes.c_int
+        L.mm_glu_backward.argtypes = [vp] * 11
+        L.mm_glu_backward.restype = ctypes.c_int
         L.mm_status_string.argtypes = [ctypes.c_int]
         L.mm_status_string.restype = ctypes.c_char_p
         L.mm_last_error.argtypes = []
@@ -429,6 +457,187 @@ class IntPlan(Plan):
         with self._lock:
             self.execute_ptr(A.data_ptr(), B.data_ptr(), Y.data_ptr(), stream.cuda_stream,
                              a_zp.data_ptr() if a_zp is not None else 0, b_zp.data_ptr() if b_zp is not None else 0)
+
+
+def _require(tensors, device) -> None:
+    """Each (name, tensor, dtype, shape) dense, on `device`."""
+    for name, t, want, shape in tensors:
+        if t.dtype != want or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {want} tensor of shape {tuple(shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the output on {device}")
+
+
+def _launch(device, stream, call) -> None:
+    """call(raw stream) with `device` current; stream defaults to its current stream."""
+    import torch
+
+    if device.type != "cuda":
+        raise ValueError("the tensors must be device tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if torch.cuda.current_device() == device.index:
+        _check(call(stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(call(stream.cuda_stream))
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def quantize_rows(X, q=None, scale=None, stream=None):
+    """mm_quantize_rows: (q, scale) of X's rows (its last dimension), q INT8 of
+    X's shape, scale FP32 of X's shape without the last dimension."""
+    import torch
+
+    code = torch_dtype_code(X.dtype)
+    if X.dim() < 1:
+        raise ValueError("X needs at least one dimension")
+    if q is None:
+        q = torch.empty(X.shape, dtype=torch.int8, device=X.device)
+    if scale is None:
+        scale = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+    _require((("X", X, X.dtype, X.shape), ("q", q, torch.int8, X.shape),
+              ("scale", scale, torch.float32, X.shape[:-1])), X.device)
+    cols = X.shape[-1]
+    rows = 1
+    for d in X.shape[:-1]:
+        rows *= d
+    _launch(X.device, stream, lambda s: lib().mm_quantize_rows(X.data_ptr(), code, rows, cols, q.data_ptr(),
+                                                               scale.data_ptr(), s))
+    return q, scale
+
+
+class ScaledIntPlan(Plan):
+    """mm_scaled_int_plan_create / mm_scaled_int_execute: INT8 product with a
+    scale for each row of A and each column of B.  a_type is INT8, or the
+    float type of an A that every execution quantizes by rows first."""
+
+    def __init__(self, a_shape, b_shape, out_type: int, a_type: int = INT8, trans_b: bool = False, bias: bool = False,
+                 force_algo: int = 0, tile: int = 0, split_k: int = 0):
+        import torch
+
+        L = lib()
+        self._handle = ctypes.c_void_p()
+        self.a_shape = torch.Size(int(d) for d in a_shape)
+        self.b_shape = torch.Size(int(d) for d in b_shape)
+        self.a_type, self.dtype = int(a_type), int(out_type)
+        self.trans_b, self.bias = bool(trans_b), bool(bias)
+        desc = ScaledIntDesc(self.a_type, self.dtype, int(self.trans_b), int(self.bias), 0)
+        opt = PlanOptions(force_algo, tile, split_k, 0)
+        _check(L.mm_scaled_int_plan_create(_shape(self.a_shape), len(self.a_shape), _shape(self.b_shape),
+                                           len(self.b_shape), ctypes.byref(desc), ctypes.byref(opt),
+                                           ctypes.byref(self._handle)))
+        self._lock = threading.Lock()
+        self._a_dt, self._out_dt = torch_dtype(self.a_type), torch_dtype(self.dtype)
+        self._y_shape = torch.Size(self.output_shape)
+        n = 1 if len(self.b_shape) == 1 else self.b_shape[-2 if self.trans_b else -1]
+        self._bias_shape = torch.Size((n,))
+        self.a_scale_shape = self.a_shape[:-1]
+        self.b_scale_shape = torch.Size(()) if len(self.b_shape) == 1 else self.b_shape[:-2] + self._bias_shape
+
+    def execute_ptr(self, A: int, B: int, Y: int, stream: int = 0, a_scale: int = 0, b_scale: int = 0,
+                    bias: int = 0) -> None:
+        _check(lib().mm_scaled_int_execute(self._handle, A, B, a_scale, b_scale, bias, Y, stream))
+
+    def execute(self, A, B, Y, a_scale=None, b_scale=None, bias=None, stream=None) -> None:
+        """a_scale: FP32, A's shape without K (None where the plan quantizes
+        A); b_scale: FP32, B's batch dimensions and N; bias: N values of Y's type."""
+        import torch
+
+        f32 = torch.float32
+        if (a_scale is None) != (self.a_type != INT8):
+            raise ValueError("a_scale: " + ("the plan quantizes A itself" if a_scale is not None
+                                            else "an INT8 A needs its scales"))
+        if b_scale is None:
+            raise ValueError("b_scale is missing")
+        if (bias is None) == self.bias:
+            raise ValueError("bias: the plan has " + ("one" if self.bias else "none"))
+        checks = [("A", A, self._a_dt, self.a_shape), ("B", B, torch.int8, self.b_shape),
+                  ("Y", Y, self._out_dt, self._y_shape), ("b_scale", b_scale, f32, self.b_scale_shape)]
+        if a_scale is not None:
+            checks.append(("a_scale", a_scale, f32, self.a_scale_shape))
+        if bias is not None:
+            checks.append(("bias", bias, self._out_dt, self._bias_shape))
+        _require(checks, Y.device)
+        with self._lock:
+            _launch(Y.device, stream, lambda s: lib().mm_scaled_int_execute(
+                self._handle, A.data_ptr(), B.data_ptr(), _ptr(a_scale), b_scale.data_ptr(), _ptr(bias), Y.data_ptr(), s))
+
+
+class GluPlan(Plan):
+    """mm_glu_plan_create / mm_glu_execute / mm_glu_backward: the gated
+    feed-forward block H = f(X Wg) * (X Wu) and its gradients.  The weights are
+    [in_features, hidden], or [hidden, in_features] with trans_w; they may be
+    views of a merged matrix (rows w_pitch elements apart)."""
+
+    def __init__(self, rows: int, in_features: int, hidden: int, dtype: int, activation: int = ACT_SILU,
+                 trans_w: bool = False, training: bool = False, w_pitch: int = 0, force_algo: int = 0, tile: int = 0):
+        import torch
+
+        L = lib()
+        self._handle = ctypes.c_void_p()
+        self.dtype = int(dtype)
+        self.rows, self.in_features, self.hidden = int(rows), int(in_features), int(hidden)
+        self.trans_w, self.training = bool(trans_w), bool(training)
+        desc = GluDesc(self.rows, self.in_features, self.hidden, int(w_pitch), int(self.trans_w), int(activation),
+                       int(self.training), 0)
+        opt = PlanOptions(force_algo, tile, 0, 0)
+        _check(L.mm_glu_plan_create(ctypes.byref(desc), self.dtype, ctypes.byref(opt), ctypes.byref(self._handle)))
+        self._lock = threading.Lock()
+        self._dt = torch_dtype(self.dtype)
+        self._x = torch.Size((self.rows, self.in_features))
+        self._h = torch.Size((self.rows, self.hidden))
+        self._w = torch.Size((self.hidden, self.in_features) if self.trans_w else (self.in_features, self.hidden))
+        self._pitch = int(w_pitch) or self._w[1]
+
+    def _require_weights(self, tensors, device) -> None:
+        for name, t in tensors:
+            ok = t.dtype == self._dt and t.shape == self._w
+            if ok and t.numel():
+                ok = (t.stride(1) == 1 or t.shape[1] == 1) and (t.stride(0) == self._pitch or t.shape[0] == 1)
+            if not ok:
+                raise ValueError(f"{name} must be a {self._dt} tensor of shape {tuple(self._w)} with rows "
+                                 f"{self._pitch} elements apart")
+            if t.device != device:
+                raise ValueError(f"{name} is on {t.device}, the others on {device}")
+
+    def execute_ptr(self, X: int, Wg: int, Wu: int, H: int, G: int = 0, U: int = 0, stream: int = 0) -> None:
+        _check(lib().mm_glu_execute(self._handle, X, Wg, Wu, H, G, U, stream))
+
+    def execute(self, X, Wg, Wu, H, G=None, U=None, stream=None) -> None:
+        """The forward pass; G and U (both or neither) keep X Wg and X Wu."""
+        if (G is None) != (U is None):
+            raise ValueError("G and U are given together or not at all")
+        dt = self._dt
+        checks = [("X", X, dt, self._x), ("H", H, dt, self._h)]
+        if G is not None:
+            checks += [("G", G, dt, self._h), ("U", U, dt, self._h)]
+        _require(checks, H.device)
+        self._require_weights((("Wg", Wg), ("Wu", Wu)), H.device)
+        with self._lock:
+            _launch(H.device, stream, lambda s: lib().mm_glu_execute(
+                self._handle, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), H.data_ptr(), _ptr(G), _ptr(U), s))
+
+    def backward(self, X, Wg, Wu, G, U, dH, dX=None, dWg=None, dWu=None, stream=None) -> None:
+        """The backward pass into dX and / or dWg and dWu (overwritten)."""
+        if (dWg is None) != (dWu is None):
+            raise ValueError("dWg and dWu are given together or not at all")
+        dt = self._dt
+        checks = [("X", X, dt, self._x), ("G", G, dt, self._h), ("U", U, dt, self._h), ("dH", dH, dt, self._h)]
+        weights = [("Wg", Wg), ("Wu", Wu)]
+        if dX is not None:
+            checks.append(("dX", dX, dt, self._x))
+        if dWg is not None:
+            weights += [("dWg", dWg), ("dWu", dWu)]
+        _require(checks, dH.device)
+        self._require_weights(weights, dH.device)
+        with self._lock:
+            _launch(dH.device, stream, lambda s: lib().mm_glu_backward(
+                self._handle, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), G.data_ptr(), U.data_ptr(), dH.data_ptr(),
+                _ptr(dX), _ptr(dWg), _ptr(dWu), s))
 
 
 _plan_cache = {}

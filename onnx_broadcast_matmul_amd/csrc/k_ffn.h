@@ -1,0 +1,560 @@
+// k_ffn.h -- tiled products of the feed-forward operators on the gfx950
+// matrix cores: the gated block (two weight matrices, one fused epilogue), the
+// two-term input gradient, the pair of weight gradients, and the INT8 product
+// with row and column scales.
+//
+// One workgroup owns a BM x BN tile (for the gated block BN counts the gate
+// and the up columns: BN / 2 hidden features).  K moves through STAGES LDS
+// buffers of BKB bytes per staged row, and the pipeline looks one stage
+// further ahead than the one computed: at stage kt's barrier every wave's
+// loads of stage kt + 1 have landed, so the first fragments of kt + 1 are
+// read while the last MFMAs of kt run and the matrix cores do not wait for
+// LDS at the stage's start.  The loads of kt + STAGES - 1 are issued right
+// after that barrier, into the buffer whose last reads ended before it.
+//
+// Operands are staged as they lie in memory: K-contiguous rows (chunk c of
+// row r at c ^ aswz(r)) or M/N-contiguous rows of one k each (chunk c at
+// c ^ kn_swizzle(k)), read back as 16-byte MFMA operands directly or through
+// the transposing LDS reads.
+//
+// DMA = true needs 16-byte aligned rows and bases and moves global memory
+// straight into LDS.  DMA = false takes any alignment: every thread loads its
+// chunks into registers one stage ahead (whole 16-byte chunks where they lie
+// inside the row, single elements at its end) and writes them to the same LDS
+// layout, so odd sizes run on the same matrix-core loop.
+#pragma once
+
+#include <type_traits>
+
+#include "activation.h"
+#include "device.h"
+#include "ffn.h"
+
+namespace mm {
+
+// 16-byte chunk swizzle of M/N-contiguous rows (one k each) of cpr chunks:
+// 16-bit transposing reads cover 4 rows x 4 chunks per half-wave, 8-bit ones
+// 8 rows x 2 neighbouring chunks, FP32 column reads rows k and k + 4.
+template <int ES>
+__device__ __forceinline__ int row_swizzle(int k, int cpr) {
+    if constexpr (ES == 4) return cpr >= 16 ? 8 * ((k >> 2) & 1) : 0;
+    else if constexpr (ES == 1) return cpr >= 16 ? 2 * (k & 7) : 2 * ((k >> 1) & 3);
+    else return cpr >= 16 ? 4 * (k & 3) : 4 * ((k >> 1) & 1);
+}
+
+// Which products a kernel computes.
+//   kGlu:    H = act(A B0) * (A B1), optionally also A B0 and A B1
+//   kSum2:   Y0 = A0 B0 + A1 B1 (the K loop runs over both terms)
+//   kPair:   Y0 = A B0 and Y1 = A B1, or Y0 = A0 B and Y1 = A1 B (grid half each)
+//   kScaled: Y = sa[m] sb[n] (A B) + bias[n], INT8 operands
+//   kScaledSplit: INT32 partial sums of one K partition
+enum FfnMode { kGlu = 0, kSum2 = 1, kPair = 2, kScaled = 3, kScaledSplit = 4 };
+
+template <int DT, int OD, int MODE, bool TA, bool TB, int BM, int BN, int WGM, int WGN, int BKB, int STAGES, int PW, bool DMA>
+__global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using E = Elem<DT>;
+    using S = typename E::S;
+    constexpr bool INT = DT == MM_INT8;
+    constexpr int NW = WGM * WGN;
+    constexpr int NT = 64 * NW;
+    constexpr int ES = (int)sizeof(S);
+    constexpr int VE = 16 / ES;
+    constexpr int BK = BKB / ES;
+    constexpr int CA = BKB / 16;           // chunks of a K-contiguous row
+    constexpr int KS = BKB / 32;           // MFMA steps per stage
+    constexpr int NPAN = MODE == kGlu ? 2 : 1;  // B panels (gate, up)
+    constexpr int PN = BN / NPAN;          // columns of one panel = output columns of the tile
+    constexpr int WM = BM / WGM, WNP = PN / WGN;
+    constexpr int FM = WM / 32, FNP = WNP / 32, FN = FNP * NPAN;
+    constexpr int RBA = BM * ES, CPRA = RBA / 16;  // M-contiguous A rows
+    constexpr int RBB = PN * ES, CPRB = RBB / 16;  // N-contiguous B rows
+    constexpr int A_BYTES = BM * BKB;
+    constexpr int P_BYTES = PN * BKB;      // one B panel
+    constexpr int STAGE_BYTES = A_BYTES + NPAN * P_BYTES;
+    static_assert(CA == 4 || CA == 8, "K-contiguous rows are 64 or 128 bytes");
+    static_assert(FM >= 1 && FNP >= 1 && BM % (32 * WGM) == 0 && PN % (32 * WGN) == 0, "wave tile");
+    static_assert(STAGES >= 3 && STAGES * STAGE_BYTES <= 160 * 1024, "LDS");
+    static_assert(!TA || (CPRA >= 8 && CPRA <= 64), "transposed A rows");
+    static_assert(TB || (CPRB >= 8 && CPRB <= 64), "B rows");
+    auto aswz = [](int row) { return CA == 8 ? ((row >> 1) & 7) : ((row >> 2) & 3); };
+
+    __shared__ __attribute__((aligned(1024))) char lds[STAGES * STAGE_BYTES];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave / WGN, wc = wave % WGN;
+
+    const int64_t M = a.M, N = a.N, K = a.K;
+    const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + PN - 1) / PN;
+    const int64_t per = tiles_m * tiles_n;
+    constexpr bool SPLIT = MODE == kScaledSplit;
+    const int64_t nsplit = SPLIT ? a.split : 1;
+    int64_t id = xcd_remap(blockIdx.x, (int64_t)gridDim.x);
+    const int64_t sidx = SPLIT ? id % nsplit : 0;
+    if constexpr (SPLIT) id /= nsplit;
+    const int64_t b = id / per;  // batch (kScaled) or which of the pair
+    const int64_t t = id % per;
+    // 8 tile rows sweep the tile columns together, so that they share B.
+    constexpr int64_t GM = 8;
+    const int64_t group = t / (GM * tiles_n);
+    const int64_t first_m = group * GM;
+    const int64_t gsize = (tiles_m - first_m) < GM ? (tiles_m - first_m) : GM;
+    const int64_t tm = first_m + (t % (GM * tiles_n)) % gsize;
+    const int64_t tn = (t % (GM * tiles_n)) / gsize;
+    const int64_t m0 = tm * BM, n0 = tn * PN;
+
+    int64_t oa = 0, ob = 0;
+    if constexpr (INT) batch_offsets(a.bd, b, oa, ob);
+    // Tile origins of the two A and B operands (the modes that have one use [0]).
+    const int64_t ta_off = oa + (TA ? m0 : m0 * a.lda), tb_off = ob + (TB ? n0 * a.ldb : n0);
+    const int pick = MODE == kPair ? (int)b : 0;
+    const char *At0 = (const char *)((const S *)a.A[pick] + ta_off);
+    const char *Bt0 = (const char *)((const S *)a.B[pick] + tb_off);
+    const char *At1 = MODE == kSum2 ? (const char *)((const S *)a.A[1] + ta_off) : At0;
+    const char *Bt1 = MODE == kSum2 || MODE == kGlu ? (const char *)((const S *)a.B[1] + tb_off) : Bt0;
+
+    const int64_t kbeg = SPLIT ? sidx * a.kchunk : 0;
+    const int64_t kend = SPLIT ? ((kbeg + a.kchunk) < K ? (kbeg + a.kchunk) : K) : K;
+    const int nk1 = (int)((kend - kbeg + BK - 1) / BK);
+    const int nk = MODE == kSum2 ? 2 * nk1 : nk1;
+
+    using AccT = typename std::conditional<INT, i32x16, f32x16>::type;
+    AccT acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+    // ---- fragments
+    uint4 fa[2][FM], fb[2][FN];
+    auto read_k = [&](const char *Xs, int row, int c) -> uint4 {
+        return *(const uint4 *)(Xs + row * BKB + ((c ^ aswz(row)) * 16));
+    };
+    // 16 bytes of consecutive k of index base + lane % 32, from rows of one k
+    // each.  Transposing reads: in each 16-lane group the lanes address the
+    // pieces of a (16 / ES / 2) x 16 block and lane i receives column i.
+    auto read_mn = [&](const char *Xs, int rbytes, int cpr, int base, int ks) -> uint4 {
+        const int G = lane >> 4, jl = lane & 15;
+        if constexpr (ES == 1) {
+            typedef int i32x2v __attribute__((ext_vector_type(2)));
+            const int n = base + (G & 1) * 16 + (jl & 1) * 8;
+            uint2 h2[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = ks * 32 + (G >> 1) * 16 + h * 8 + (jl >> 1);
+                const char *addr = Xs + k * rbytes + ((n >> 4) ^ row_swizzle<ES>(k, cpr)) * 16 + ((n >> 3) & 1) * 8;
+                h2[h] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                                                      (__attribute__((address_space(3))) i32x2v *)(addr)));
+            }
+            return make_uint4(h2[0].x, h2[0].y, h2[1].x, h2[1].y);
+        } else if constexpr (ES == 2) {
+            const int n = base + (G & 1) * 16 + (jl & 3) * 4;
+            uint2 h2[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = ks * 16 + (G >> 1) * 8 + h * 4 + (jl >> 2);
+                const char *addr = Xs + k * rbytes + ((n >> 3) ^ row_swizzle<ES>(k, cpr)) * 16 + ((n >> 2) & 1) * 8;
+                h2[h] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                                                      (__attribute__((address_space(3))) bf16x4 *)(addr)));
+            }
+            return make_uint4(h2[0].x, h2[0].y, h2[1].x, h2[1].y);
+        } else {
+            const int n = base + (lane & 31), c = 2 * ks + (lane >> 5);
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = c * 4 + e;
+                v[e] = *(const uint32_t *)(Xs + k * rbytes + ((n >> 2) ^ row_swizzle<ES>(k, cpr)) * 16 + (n & 3) * 4);
+            }
+            return make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    };
+    auto read_frags = [&](int buf, int ks, int slot) {
+        const char *As = lds + buf * STAGE_BYTES;
+        const char *Bs = As + A_BYTES;
+        const int c = 2 * ks + (lane >> 5);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            if constexpr (TA) fa[slot][i] = read_mn(As, RBA, CPRA, wr * WM + i * 32, ks);
+            else fa[slot][i] = read_k(As, wr * WM + i * 32 + (lane & 31), c);
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const char *Ps = Bs + (j / FNP) * P_BYTES;
+            const int col = wc * WNP + (j % FNP) * 32;
+            if constexpr (TB) fb[slot][j] = read_k(Ps, col + (lane & 31), c);
+            else fb[slot][j] = read_mn(Ps, RBB, CPRB, col, ks);
+        }
+    };
+    // B is the first MFMA operand: accumulator element r of a lane is output
+    // row lane % 32 and column 8 (r / 4) + 4 (lane / 32) + r % 4 of the block.
+    auto mfmas = [&](int slot) {
+        if constexpr (DT == MM_FLOAT) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) {
+                        const uint4 &x = fa[slot][i];
+                        const uint4 &y = fb[slot][j];
+                        const float av = __uint_as_float(e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w);
+                        const float bv = __uint_as_float(e == 0 ? y.x : e == 1 ? y.y : e == 2 ? y.z : y.w);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(bv, av, acc[i][j], 0, 0, 0);
+                    }
+        } else {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    if constexpr (INT) {
+                        typedef int i32x4v __attribute__((ext_vector_type(4)));
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4v, fb[slot][j]),
+                                                                         __builtin_bit_cast(i32x4v, fa[slot][i]),
+                                                                         acc[i][j], 0, 0, 0);
+                    } else if constexpr (DT == MM_BFLOAT16) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fb[slot][j]),
+                                                                           __builtin_bit_cast(bf16x8, fa[slot][i]),
+                                                                           acc[i][j], 0, 0, 0);
+                    } else {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, fb[slot][j]),
+                                                                          __builtin_bit_cast(f16x8, fa[slot][i]),
+                                                                          acc[i][j], 0, 0, 0);
+                    }
+                }
+        }
+    };
+    // One stage's MFMA steps; the last step reads the next stage's first
+    // fragments (after the last stage: stale bytes that nothing uses).
+    auto compute = [&](int buf, int next) {
+        constexpr bool SCHED = DT != MM_FLOAT;
+        constexpr int RPS = FM * (TA ? 2 : 1) + FN * (TB ? 1 : 2);  // LDS reads per step
+        constexpr int MPS = FM * FN;                              // MFMAs per step
+        constexpr int R2 = (RPS + 1) / 2;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks + 1 < KS) read_frags(buf, ks + 1, (ks + 1) & 1);
+            else read_frags(next, 0, (ks + 1) & 1);
+            mfmas(ks & 1);
+            if constexpr (SCHED) {
+                {
+#pragma unroll
+                    for (int q = 0; q < (R2 < MPS ? R2 : MPS); ++q) {
+                        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    }
+                    if constexpr (MPS > R2) __builtin_amdgcn_sched_group_barrier(0x008, MPS - R2, 0);
+                }
+            }
+        }
+    };
+    static_assert(KS % 2 == 0, "the next stage's first fragments go to slot 0");
+
+    // A stage's first k and operands: kSum2 runs over the first term's stages,
+    // then the second's.
+    auto stage_k0 = [&](int st) { return kbeg + (int64_t)(MODE == kSum2 && st >= nk1 ? st - nk1 : st) * BK; };
+    auto stage_second = [&](int st) { return MODE == kSum2 && st >= nk1; };
+
+    if constexpr (DMA) {
+        constexpr int A_INSTR = A_BYTES / 1024 / PW;  // 1 KB loads per producer and stage
+        constexpr int B_INSTR = NPAN * P_BYTES / 1024 / PW;
+        constexpr int LPW = A_INSTR + B_INSTR;
+        constexpr int A_RPB = TA ? 1024 / RBA : 1024 / BKB;
+        constexpr int B_RPB = TB ? 1024 / BKB : 1024 / RBB;
+        static_assert(PW >= 1 && PW <= NW && A_INSTR * PW * 1024 == A_BYTES && A_INSTR >= 1, "A loads");
+        static_assert(B_INSTR * PW * 1024 == NPAN * P_BYTES && B_INSTR >= NPAN && B_INSTR % NPAN == 0, "B loads");
+        static_assert((STAGES - 2) * LPW < 64, "vmcnt range");
+        const uint32_t lds_base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char *)lds);
+        const bool producer = wave < PW;
+        // 1 KB block of load q of this producer: q * PW + wave, so that a B
+        // load's panel depends on q only.
+        uint32_t a_off[A_INSTR], b_off[B_INSTR];
+        int a_k[A_INSTR], b_k[B_INSTR];
+#pragma unroll
+        for (int q = 0; q < A_INSTR; ++q) {
+            const int blk = q * PW + wave;
+            if constexpr (!TA) {
+                const int row = blk * A_RPB + lane / CA;
+                const int c = (lane % CA) ^ aswz(row);
+                a_off[q] = m0 + row < M ? (uint32_t)((int64_t)row * a.lda * ES + c * 16) : kOutOfRange;
+                a_k[q] = c * VE;
+            } else {
+                const int row = blk * A_RPB + lane / CPRA;
+                const int c = (lane % CPRA) ^ row_swizzle<ES>(row, CPRA);
+                a_off[q] = m0 + c * VE < M ? (uint32_t)((int64_t)row * a.lda * ES + c * 16) : kOutOfRange;
+                a_k[q] = row;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < B_INSTR; ++q) {
+            const int blk = (q * PW + wave) % (P_BYTES / 1024);
+            if constexpr (!TB) {
+                const int row = blk * B_RPB + lane / CPRB;
+                const int c = (lane % CPRB) ^ row_swizzle<ES>(row, CPRB);
+                b_off[q] = n0 + c * VE < N ? (uint32_t)((int64_t)row * a.ldb * ES + c * 16) : kOutOfRange;
+                b_k[q] = row;
+            } else {
+                const int row = blk * B_RPB + lane / CA;
+                const int c = (lane % CA) ^ aswz(row);
+                b_off[q] = n0 + row < N ? (uint32_t)((int64_t)row * a.ldb * ES + c * 16) : kOutOfRange;
+                b_k[q] = c * VE;
+            }
+        }
+        auto issue = [&](int st) {
+            if (!producer) return;
+            const uint32_t sbase = lds_base + (st % STAGES) * STAGE_BYTES;
+            const int64_t k0 = stage_k0(st);
+            const bool second = stage_second(st);
+            const int64_t ka = (TA ? k0 * a.lda : k0) * ES, kb = (TB ? k0 : k0 * a.ldb) * ES;
+            const i32x4 ra = buffer_rsrc((second ? At1 : At0) + ka);
+            const i32x4 rb0 = buffer_rsrc((second ? Bt1 : Bt0) + kb);
+            const i32x4 rb1 = MODE == kGlu ? buffer_rsrc(Bt1 + kb) : rb0;
+            if (k0 + BK <= kend) {
+#pragma unroll
+                for (int q = 0; q < A_INSTR; ++q) load_to_lds16(ra, sbase + (q * PW + wave) * 1024, a_off[q]);
+#pragma unroll
+                for (int q = 0; q < B_INSTR; ++q)
+                    load_to_lds16(q * NPAN >= B_INSTR ? rb1 : rb0, sbase + A_BYTES + (q * PW + wave) * 1024, b_off[q]);
+            } else {
+                const int rem = (int)(kend - k0);
+#pragma unroll
+                for (int q = 0; q < A_INSTR; ++q)
+                    load_to_lds16(ra, sbase + (q * PW + wave) * 1024, a_k[q] < rem ? a_off[q] : kOutOfRange);
+#pragma unroll
+                for (int q = 0; q < B_INSTR; ++q)
+                    load_to_lds16(q * NPAN >= B_INSTR ? rb1 : rb0, sbase + A_BYTES + (q * PW + wave) * 1024,
+                                  b_k[q] < rem ? b_off[q] : kOutOfRange);
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (s < nk) issue(s);
+        // Stage 0 has landed in every wave's share before its first fragments are read.
+        if (nk >= STAGES - 1) wait_vmcnt<(STAGES - 2) * LPW>();
+        else wait_vmcnt<0>();
+        asm volatile("s_barrier" ::: "memory");
+        if (nk > 0) read_frags(0, 0, 0);
+        for (int kt = 0; kt < nk; ++kt) {
+            // Loads of stage kt + 1 are complete once at most those of the
+            // STAGES - 3 stages issued after it are outstanding.
+            if (nk - 2 - kt >= STAGES - 3) wait_vmcnt<(STAGES - 3) * LPW>();
+            else wait_vmcnt<0>();
+            // Every wave's reads of stage kt - 1 have ended: lgkmcnt(0).
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (kt + STAGES - 1 < nk) issue(kt + STAGES - 1);
+            compute(kt % STAGES, (kt + 1) % STAGES);
+        }
+    } else {
+        constexpr int A_CH = A_BYTES / 16, CHUNKS = STAGE_BYTES / 16;
+        constexpr int CPT = (CHUNKS + NT - 1) / NT;
+        uint4 rg[CPT];
+        // Chunk x of a stage: LDS position, and its elements in memory.
+        auto load = [&](int st) {
+            const int64_t k0 = stage_k0(st);
+            const bool second = stage_second(st);
+            const int64_t krem = kend - k0;
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                const int x = tid + NT * i;
+                rg[i] = make_uint4(0, 0, 0, 0);
+                if (CHUNKS % NT != 0 && x >= CHUNKS) continue;
+                const bool isA = x < A_CH;
+                const int y = isA ? x : (x - A_CH) % (P_BYTES / 16);
+                const bool up = !isA && MODE == kGlu && x - A_CH >= P_BYTES / 16;
+                const bool kc = isA ? !TA : TB;  // K-contiguous rows
+                const int cpr = kc ? CA : isA ? CPRA : CPRB;
+                const int row = y / cpr, p = y % cpr;
+                const int c = p ^ (kc ? aswz(row) : row_swizzle<ES>(row, cpr));
+                const int64_t ld = isA ? a.lda : a.ldb;
+                const int64_t lim_mn = isA ? M - m0 : N - n0;
+                const char *base = isA ? (second ? At1 : At0) : (second || up ? Bt1 : Bt0);
+                int64_t left;  // elements of this chunk inside the matrix
+                const S *src;
+                if (kc) {
+                    left = row < lim_mn ? krem - c * VE : 0;
+                    src = (const S *)base + (int64_t)row * ld + k0 + c * VE;
+                } else {
+                    left = row < krem ? lim_mn - c * VE : 0;
+                    src = (const S *)base + (k0 + row) * ld + c * VE;
+                }
+                if (left >= VE) {
+                    __builtin_memcpy(&rg[i], src, 16);
+                } else if (left > 0) {
+                    S tmp[VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) tmp[e] = e < left ? src[e] : (S)0;
+                    __builtin_memcpy(&rg[i], tmp, 16);
+                }
+            }
+        };
+        auto store = [&](int st) {
+            char *sb = lds + (st % STAGES) * STAGE_BYTES;
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                const int x = tid + NT * i;
+                if (CHUNKS % NT == 0 || x < CHUNKS) *(uint4 *)(sb + x * 16) = rg[i];
+            }
+        };
+        if (nk > 0) {
+            load(0);
+            store(0);
+        }
+        if (nk > 1) {
+            load(1);
+            store(1);
+        }
+        if (nk > 2) load(2);
+        __syncthreads();
+        if (nk > 0) read_frags(0, 0, 0);
+        for (int kt = 0; kt < nk; ++kt) {
+            // Stage kt + 2 goes to a buffer last read before the previous
+            // barrier and is visible after the next one.
+            __syncthreads();
+            if (kt + 2 < nk) store(kt + 2);
+            if (kt + 3 < nk) load(kt + 3);
+            compute(kt % STAGES, (kt + 1) % STAGES);
+        }
+    }
+
+    // ---- epilogue
+    // A wave's blocks go through LDS (chunk c of tile row r at c ^ r % OCPR)
+    // so that the workgroup writes whole 16-byte chunks of output rows; tiles
+    // larger than the stage buffers go in row passes.
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    using OE = Elem<OD>;
+    auto emit = [&](auto zero, int jbase, auto value, void *outp, int64_t ldo, bool vec) {
+        using O = decltype(zero);
+        constexpr int OS = (int)sizeof(O), OV = 16 / OS;
+        constexpr int OCPR = PN * OS / 16;
+        constexpr int NP = (BM * PN * OS + STAGES * STAGE_BYTES - 1) / (STAGES * STAGE_BYTES);
+        constexpr int PR = BM / NP;
+        static_assert(BM % NP == 0 && (OCPR & (OCPR - 1)) == 0, "epilogue passes");
+        O *out = (O *)outp;
+#pragma unroll
+        for (int pass = 0; pass < NP; ++pass) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int rl = wr * WM + i * 32 + (lane & 31) - pass * PR;
+                if (NP == 1 || (rl >= 0 && rl < PR)) {
+                    char *trow = lds + rl * (PN * OS);
+#pragma unroll
+                    for (int j = 0; j < FNP; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int cl = wc * WNP + j * 32 + 8 * q + 4 * (lane >> 5);
+                            char *dst = trow + ((cl / OV) ^ (rl & (OCPR - 1))) * 16 + (cl % OV) * OS;
+                            const AccT &v = acc[i][jbase + j];
+                            if constexpr (std::is_same<O, int32_t>::value) {
+                                *(uint4 *)dst = make_uint4((uint32_t)v[4 * q], (uint32_t)v[4 * q + 1],
+                                                           (uint32_t)v[4 * q + 2], (uint32_t)v[4 * q + 3]);
+                            } else {
+                                float w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) w[e] = value(i, cl + e, v[4 * q + e]);
+                                using PK = Elem<OS == 4 ? MM_BFLOAT16 : OD>;
+                                if constexpr (OS == 4) *(float4 *)dst = make_float4(w[0], w[1], w[2], w[3]);
+                                else *(uint2 *)dst = make_uint2(PK::pack2(w[0], w[1]), PK::pack2(w[2], w[3]));
+                            }
+                        }
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            for (int idx = tid; idx < PR * OCPR; idx += NT) {
+                const int rl = idx / OCPR, c = idx % OCPR;
+                const int64_t row = m0 + pass * PR + rl, col = n0 + (int64_t)c * OV;
+                if (row < M && col < N) {
+                    const uint4 v = *(const uint4 *)(lds + rl * (PN * OS) + (c ^ (rl & (OCPR - 1))) * 16);
+                    O *dst = out + row * ldo + col;
+                    if (vec) {
+                        const u32x4 w = {v.x, v.y, v.z, v.w};
+                        __builtin_nontemporal_store(w, (u32x4 *)dst);
+                    } else if (col + OV <= N) {
+                        __builtin_memcpy(dst, &v, 16);  // any alignment
+                    } else {
+                        O e[OV];
+                        __builtin_memcpy(e, &v, 16);
+#pragma unroll
+                        for (int q = 0; q < OV; ++q)
+                            if (col + q < N) dst[q] = e[q];
+                    }
+                }
+            }
+        }
+    };
+    auto plain = [](int, int, auto v) { return (float)v; };
+    if constexpr (MODE == kGlu) {
+        if (a.G) {
+            emit((typename OE::S)0, 0, plain, a.G, a.ldy, a.y_vec != 0);
+            emit((typename OE::S)0, FNP, plain, a.U, a.ldy, a.y_vec != 0);
+        }
+        auto apply = [&](auto kind) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FNP; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        acc[i][j][r] = act_value<decltype(kind)::value, DT == MM_FLOAT>(acc[i][j][r]) * acc[i][FNP + j][r];
+        };
+        switch (a.act) {
+        case MM_ACT_SILU: apply(std::integral_constant<int, MM_ACT_SILU>()); break;
+        case MM_ACT_GELU: apply(std::integral_constant<int, MM_ACT_GELU>()); break;
+        case MM_ACT_GELU_TANH: apply(std::integral_constant<int, MM_ACT_GELU_TANH>()); break;
+        case MM_ACT_RELU: apply(std::integral_constant<int, MM_ACT_RELU>()); break;
+        default: apply(std::integral_constant<int, MM_ACT_SIGMOID>()); break;
+        }
+        emit((typename OE::S)0, 0, plain, a.Y[0], a.ldy, a.y_vec != 0);
+    } else if constexpr (MODE == kScaledSplit) {
+        emit((int32_t)0, 0, plain, a.W + (sidx * a.batch + b) * M * N, N, N % 4 == 0);
+    } else if constexpr (MODE == kScaled) {
+        // Scales of this lane's rows, and of the tile's columns in LDS after
+        // the main loop's last reads.
+        __shared__ __attribute__((aligned(16))) float cs[PN], cb[PN];
+        const int64_t kd = K > 0 ? K : 1;      // K == 0: one empty matrix, offsets 0
+        const int64_t sb0 = ob / kd + n0;  // scale of column n of B matrix i: i N + n
+        for (int x = tid; x < PN; x += NT) {
+            const bool in = n0 + x < N;
+            cs[x] = in ? a.sb[sb0 + x] : 0.0f;
+            cb[x] = in && a.bias ? OE::to_f32(((const typename OE::S *)a.bias)[n0 + x]) : 0.0f;
+        }
+        float rs[FM];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int64_t row = m0 + wr * WM + i * 32 + (lane & 31);
+            rs[i] = row < M ? a.sa[oa / a.lda + row] : 0.0f;
+        }
+        __syncthreads();
+        emit((typename OE::S)0, 0, [&](int i, int cl, int v) { return scaled_value(v, rs[i], cs[cl], cb[cl]); },
+             (typename OE::S *)a.Y[0] + b * M * a.ldy, a.ldy, a.y_vec != 0);
+    } else {
+        emit((typename OE::S)0, 0, plain, MODE == kPair ? a.Y[pick] : a.Y[0], a.ldy, a.y_vec != 0);
+    }
+#endif
+}
+
+// Launch one entry; DMA where the operands allow it (`vec`).
+template <int DT, int OD, int MODE, bool TA, bool TB, int BM, int BN, int WGM, int WGN, int BKB, int STAGES, int PW>
+static hipError_t launch_ffn(bool vec, const FfnArgs &a, hipStream_t s) {
+    constexpr int PN = MODE == kGlu ? BN / 2 : BN;
+    constexpr int ES = (int)sizeof(typename Elem<DT>::S);
+    const int64_t tiles = a.batch * ((a.M + BM - 1) / BM) * ((a.N + PN - 1) / PN) * (MODE == kScaledSplit ? a.split : 1);
+    if (tiles <= 0) return hipSuccess;
+    if (tiles > 0x7fffffff) return hipErrorInvalidValue;
+    // Buffer offsets are 32-bit: the rows that one stage of a tile spans.
+    const int64_t a_span = (TA ? (int64_t)(BKB / ES) : (int64_t)BM) * a.lda;
+    const int64_t b_span = (TB ? (int64_t)PN : (int64_t)(BKB / ES)) * a.ldb;
+    const bool fits = a_span * ES < 0x7fff0000LL && b_span * ES < 0x7fff0000LL;
+    const dim3 g((unsigned)tiles), blk(64 * WGM * WGN);
+    if (vec && fits)
+        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, TA, TB, BM, BN, WGM, WGN, BKB, STAGES, PW, true>), g, blk, 0, s, a);
+    else
+        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, TA, TB, BM, BN, WGM, WGN, BKB, STAGES, PW, false>), g, blk, 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace mm

@@ -1,0 +1,110 @@
+// k_glu.hip -- gated feed-forward block: dispatch of the tiled products by
+// element type, and the element-wise part of the backward pass.
+#include "activation.h"
+#include "device.h"
+#include "ffn.h"
+
+namespace mm {
+
+#define MM_GLU_DECLARE(NAME)                                                                       \
+    hipError_t glu_fwd_##NAME(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);        \
+    hipError_t glu_dx_##NAME(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);         \
+    hipError_t glu_dw_##NAME(int tile, bool vec, const FfnArgs &a, hipStream_t s);
+MM_GLU_DECLARE(f32)
+MM_GLU_DECLARE(f16)
+MM_GLU_DECLARE(bf16)
+
+hipError_t launch_glu_fwd(int dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s) {
+    return dtype == MM_FLOAT ? glu_fwd_f32(tb, tile, vec, a, s)
+           : dtype == MM_FLOAT16 ? glu_fwd_f16(tb, tile, vec, a, s) : glu_fwd_bf16(tb, tile, vec, a, s);
+}
+
+hipError_t launch_glu_dx(int dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s) {
+    return dtype == MM_FLOAT ? glu_dx_f32(tb, tile, vec, a, s)
+           : dtype == MM_FLOAT16 ? glu_dx_f16(tb, tile, vec, a, s) : glu_dx_bf16(tb, tile, vec, a, s);
+}
+
+hipError_t launch_glu_dw(int dtype, int tile, bool vec, const FfnArgs &a, hipStream_t s) {
+    return dtype == MM_FLOAT ? glu_dw_f32(tile, vec, a, s)
+           : dtype == MM_FLOAT16 ? glu_dw_f16(tile, vec, a, s) : glu_dw_bf16(tile, vec, a, s);
+}
+
+// dG = dH U f'(G) and dU = dH f(G), a thread per 16 bytes of each tensor's
+// row.  Three tensors are read and two written once.  G and U come in the
+// element type (the forward pass rounded them once) and dG, dU are rounded to
+// it because the matrix cores take them in it: the roundings, half a step
+// each, that an unfused block in this type makes too.  dG and dU have rows of
+// ldw elements, whole 16-byte chunks; the columns past N hold zeros, so the
+// products may read them.
+template <int DT, int ACT>
+__global__ __launch_bounds__(256) void k_glu_dact(const void *G, const void *U, const void *dH, void *dG, void *dU,
+                                                  int64_t M, int64_t N, int64_t ldw) {
+    using E = Elem<DT>;
+    using S = typename E::S;
+    constexpr int VE = E::kVE;
+    const int64_t cpr = ldw / VE;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (x >= M * cpr) return;
+    // cpr < 2^31: one 32-bit division where the index allows it.
+    const int64_t row = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
+    const int64_t col = (x - row * cpr) * VE, i0 = row * N + col;
+    S g[VE], u[VE], h[VE], og[VE], ou[VE];
+    if (col + VE <= N) {
+        __builtin_memcpy(g, (const S *)G + i0, 16);
+        __builtin_memcpy(u, (const S *)U + i0, 16);
+        __builtin_memcpy(h, (const S *)dH + i0, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            const bool in = col + e < N;
+            g[e] = in ? ((const S *)G)[i0 + e] : (S)0;
+            u[e] = in ? ((const S *)U)[i0 + e] : (S)0;
+            h[e] = in ? ((const S *)dH)[i0 + e] : (S)0;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+        float f, d;
+        act_grad<ACT, DT == MM_FLOAT>(E::to_f32(g[e]), f, d);
+        const float dh = E::to_f32(h[e]);
+        og[e] = E::from_f32(dh * E::to_f32(u[e]) * d);
+        ou[e] = E::from_f32(dh * f);
+    }
+    uint4 vg, vu;
+    __builtin_memcpy(&vg, og, 16);
+    __builtin_memcpy(&vu, ou, 16);
+    *(uint4 *)((S *)dG + row * ldw + col) = vg;
+    *(uint4 *)((S *)dU + row * ldw + col) = vu;
+}
+
+template <int DT, int ACT>
+static hipError_t dact(const void *G, const void *U, const void *dH, void *dG, void *dU, int64_t M, int64_t N,
+                       int64_t ldw, hipStream_t s) {
+    const int64_t g = (M * (ldw / Elem<DT>::kVE) + 255) / 256;
+    if (g <= 0) return hipSuccess;
+    if (g > 0x7fffffff) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_glu_dact<DT, ACT>), dim3((unsigned)g), dim3(256), 0, s, G, U, dH, dG, dU, M, N, ldw);
+    return hipGetLastError();
+}
+
+template <int DT>
+static hipError_t dact(int act, const void *G, const void *U, const void *dH, void *dG, void *dU, int64_t M, int64_t N,
+                       int64_t ldw, hipStream_t s) {
+    switch (act) {
+    case MM_ACT_SILU: return dact<DT, MM_ACT_SILU>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_GELU: return dact<DT, MM_ACT_GELU>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_GELU_TANH: return dact<DT, MM_ACT_GELU_TANH>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_RELU: return dact<DT, MM_ACT_RELU>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_SIGMOID: return dact<DT, MM_ACT_SIGMOID>(G, U, dH, dG, dU, M, N, ldw, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_glu_dact(int dtype, int act, const void *G, const void *U, const void *dH, void *dG, void *dU,
+                           int64_t M, int64_t N, int64_t ldw, hipStream_t s) {
+    return dtype == MM_FLOAT ? dact<MM_FLOAT>(act, G, U, dH, dG, dU, M, N, ldw, s)
+           : dtype == MM_FLOAT16 ? dact<MM_FLOAT16>(act, G, U, dH, dG, dU, M, N, ldw, s)
+                                 : dact<MM_BFLOAT16>(act, G, U, dH, dG, dU, M, N, ldw, s);
+}
+
+}  // namespace mm

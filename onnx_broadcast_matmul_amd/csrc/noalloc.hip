@@ -60,8 +60,8 @@ using namespace mm;
 extern "C" mm_status mm_execute_noalloc(mm_plan_t p, const void *A, const void *B, void *Y, void *stream) {
     clear_error();
     if (!p) return fail(MM_ERR_NULL_ARG, "plan is NULL");
-    if (p->is_gemm) return fail(MM_ERR_BAD_OPTION, "a Gemm plan runs through mm_gemm_execute");
-    if (p->is_int) return fail(MM_ERR_BAD_OPTION, "a MatMulInteger plan runs through mm_int_execute");
+    mm_status kind = require_matmul(p);
+    if (kind != MM_OK) return kind;
     if (p->workspace_bytes > (int64_t)kScratchBytes)
         return fail(MM_ERR_TOO_LARGE,
                     "the plan needs %lld workspace bytes; mm_execute_noalloc has %zu (use mm_execute, or a plan "

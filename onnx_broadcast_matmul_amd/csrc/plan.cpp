@@ -545,8 +545,7 @@ static int choose_split_tile(int dtype, int64_t batch, int64_t M, int64_t N, int
 }
 
 // Resolve shapes, strides, collapse and fold into `p`.
-static mm_status resolve(const int64_t *a_shape, int a_rank, const int64_t *b_shape, int b_rank,
-                         mm_plan_s *p) {
+mm_status resolve(const int64_t *a_shape, int a_rank, const int64_t *b_shape, int b_rank, mm_plan_s *p) {
     if (a_rank < 1 || b_rank < 1)
         return fail(MM_ERR_RANK, "input rank must be >= 1 (got A rank %d, B rank %d)", a_rank, b_rank);
     if (a_rank > MM_MAX_RANK || b_rank > MM_MAX_RANK)
@@ -723,7 +722,7 @@ static void plan_skinny_split(mm_plan_s *p, int requested) {
     p->workspace_bytes = p->split > 1 ? (int64_t)p->split * p->batch * M * N * 4 : 0;
 }
 
-static mm_status check_limits(const mm_plan_s *p) {
+mm_status check_limits(const mm_plan_s *p) {
     const int64_t lim = INT32_MAX;
     if (p->kernel_m > lim || p->N > lim || p->K > lim || p->batch > lim)
         return fail(MM_ERR_TOO_LARGE, "M, N, K and batch must each be below 2^31");
@@ -1101,11 +1100,20 @@ mm_status mm_plan_get_info(mm_plan_t p, mm_plan_info *info) {
         info->constant_b_packed = p->cb_set && p->cbp_ok ? 1 : 0;
     }
     info->flops = 2.0 * (double)p->total_batch * (double)p->M * (double)p->N * (double)p->K;
+    if (p->is_glu) {  // forward pass: two products, X, two weights and H once
+        info->flops *= 2.0;
+        info->min_bytes = (double)elem_size(p->dtype) *
+                          ((double)p->M * (double)p->K + 2.0 * (double)p->K * (double)p->N + (double)p->M * (double)p->N);
+        return MM_OK;
+    }
     int64_t na = 1, nb = 1;
     for (int i = 0; i < p->a_rank; ++i) na *= p->a_shape[i];
     for (int i = 0; i < p->b_rank; ++i) nb *= p->b_shape[i];
     if (p->is_int)  // one-byte inputs, INT32 output
         info->min_bytes = (double)na + (double)nb + 4.0 * (double)p->out_numel;
+    else if (p->is_scaled)  // one-byte B, A as given, output type
+        info->min_bytes = (double)elem_size(p->a_type) * (double)na + (double)nb +
+                          (double)elem_size(p->dtype) * (double)p->out_numel;
     else
         info->min_bytes = (double)elem_size(p->dtype) * ((double)na + (double)nb + (double)p->out_numel);
     return MM_OK;

@@ -54,6 +54,23 @@ struct mm_plan_s {
     int zpa_kind = 0, zpb_kind = 0;
     bool need_ra = false, need_cb = false;
 
+    // Scaled INT8 product (mm_scaled_int_plan_create): dtype is the output
+    // type, a_type the type of A as given; tb says how B is stored.  An A to
+    // be quantized goes to the workspace: its rows (q_pitch bytes each, at
+    // q_off), then its scales (at qs_off); split partials lie before it.
+    bool is_scaled = false;
+    bool has_bias = false;
+    int64_t a_rows = 0;  // rows of the whole A tensor
+    int64_t q_pitch = 0, q_off = 0, qs_off = 0;
+
+    // Gated feed-forward block (mm_glu_plan_create): tb is trans_w, M, N, K
+    // are rows, hidden, in_features.  The training workspace holds dG and dU
+    // with rows of d_pitch elements, d_bytes each.
+    bool is_glu = false;
+    int act = 0;
+    bool training = false;
+    int64_t w_pitch = 0, d_pitch = 0, d_bytes = 0;
+
     // Plan-owned constant B (mm_plan_set_constant_b).
     std::mutex cb_mutex;
     bool cb_set = false;
@@ -80,6 +97,13 @@ mm_status alloc_workspace(mm_plan_s *p, bool at_create);
 // 16-bit kernel runs; B must then be the plan's row-major constant B.
 mm_status execute_plan(mm_plan_s *p, const void *A, const void *B, const void *C, void *Y, void *stream, void *ws,
                        bool packed_b = false);
+// Resolve MatMul shapes, strides, collapse and fold into `p`, and check the
+// sizes the kernels index (plan.cpp).
+mm_status resolve(const int64_t *a_shape, int a_rank, const int64_t *b_shape, int b_rank, mm_plan_s *p);
+mm_status check_limits(const mm_plan_s *p);
+// MM_OK for a plan of MatMul; MM_ERR_BAD_OPTION naming the call that runs it
+// for any other (execute.cpp).
+mm_status require_matmul(const mm_plan_s *p);
 mm_status fail(mm_status st, const char *fmt, ...);
 void clear_error();
 int elem_size(int dtype);

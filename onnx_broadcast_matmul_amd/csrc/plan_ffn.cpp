@@ -1,0 +1,404 @@
+// plan_ffn.cpp -- plans and executions of the feed-forward operators: the
+// scaled INT8 product, row quantization and the gated block.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <new>
+
+#include "ffn.h"
+#include "plan.h"
+
+namespace mm {
+
+static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+static bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+static mm_status launched(hipError_t e) {
+    return e == hipSuccess ? MM_OK : fail(MM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+}
+
+static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
+
+// Relative rate of a tile entry once its workgroups fill the GPU.
+static const double kQuality[kNumFfnTiles] = {1.0, 0.8, 0.55, 0.3};
+
+// Entry with the largest useful share of the machine: the last round's idle
+// CUs, the padding at the edges, and the entry's rate.  cols counts the
+// kernel's columns (gate and up for the gated block).
+static int pick_tile(int64_t batch, int64_t M, int64_t cols, int first, int last) {
+    int best = last;
+    double top = -1.0;
+    for (int i = first; i <= last; ++i) {
+        const double tiles = (double)batch * (double)cdiv(M, kFfnTiles[i].bm) * (double)cdiv(cols, kFfnTiles[i].bn);
+        const double rounds = ceil(tiles / kNumCUs);
+        const double pad = ((double)batch * (double)M * (double)cols) / (tiles * kFfnTiles[i].bm * kFfnTiles[i].bn);
+        const double score = tiles / (rounds * kNumCUs) * pad * kQuality[i];
+        if (score > top) {
+            top = score;
+            best = i;
+        }
+    }
+    return best;
+}
+
+static mm_status tile_option(const mm_plan_options *opt, int first, int *tile) {
+    const int req = opt ? opt->tile : 0;
+    if (req == 0) return MM_OK;
+    if (req - 1 < first || req > kNumFfnTiles)
+        return fail(MM_ERR_BAD_OPTION, "tile %d out of range %d..%d", req, first + 1, kNumFfnTiles);
+    *tile = req - 1;
+    return MM_OK;
+}
+
+// Algorithm, tile and split of a scaled product whose output is not empty.
+static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
+    const int64_t M = p->kernel_m, N = p->N, K = p->K;
+    const int force = opt ? opt->force_algo : MM_ALGO_AUTO;
+    const int sreq = opt ? opt->split_k : 0;
+    if (sreq < 0) return fail(MM_ERR_BAD_OPTION, "split_k %d is negative", sreq);
+    const bool rows_ok = p->tb && p->batch == 1 && M <= kFfnRows;
+    p->tile = pick_tile(p->batch, M, N, 0, kNumFfnTiles - 1);
+    mm_status st = tile_option(opt, 0, &p->tile);
+    if (st != MM_OK) return st;
+    const bool tile_forced = opt && opt->tile > 0;
+    int algo = force;
+    if (force == MM_ALGO_SKINNY_M && !rows_ok)
+        return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes one product of at most %d rows with trans_b", kFfnRows);
+    if (force != MM_ALGO_AUTO && force != MM_ALGO_SKINNY_M && force != MM_ALGO_GENERAL && force != MM_ALGO_SPLIT_K)
+        return fail(MM_ERR_BAD_OPTION, "the scaled INT8 product runs on the skinny-M, general and split-K kernels only");
+    int64_t split = 1;
+    if (force == MM_ALGO_AUTO) algo = rows_ok && !tile_forced && sreq == 0 ? MM_ALGO_SKINNY_M : MM_ALGO_GENERAL;
+    if ((force == MM_ALGO_AUTO && algo == MM_ALGO_GENERAL && sreq == 0) || (force == MM_ALGO_SPLIT_K && sreq == 0)) {
+        const int64_t tiles = p->batch * cdiv(M, kFfnTiles[p->tile].bm) * cdiv(N, kFfnTiles[p->tile].bn);
+        split = std::min<int64_t>(kNumCUs / std::max<int64_t>(tiles, 1), K / 512);
+    } else if (sreq > 0 && force != MM_ALGO_GENERAL) {
+        split = sreq;
+    }
+    split = std::max<int64_t>(1, std::min<int64_t>(split, cdiv(K, 128)));
+    if (algo == MM_ALGO_GENERAL && force == MM_ALGO_AUTO && split > 1) algo = MM_ALGO_SPLIT_K;
+    if (K == 0) algo = MM_ALGO_GENERAL;  // the epilogue of an empty sum
+    p->algo = algo;
+    if (algo == MM_ALGO_SKINNY_M) p->tile = -1;
+    if (algo == MM_ALGO_SPLIT_K) {
+        p->kchunk = round_up(cdiv(K, split), 128);
+        p->split = (int32_t)cdiv(K, p->kchunk);
+        p->workspace_bytes = round_up((int64_t)p->split * p->batch * M * N * 4, 256);
+    }
+    if (algo != MM_ALGO_SKINNY_M) {
+        const int64_t tiles = p->batch * cdiv(M, kFfnTiles[p->tile].bm) * cdiv(N, kFfnTiles[p->tile].bn);
+        if (tiles * p->split > INT32_MAX) return fail(MM_ERR_TOO_LARGE, "too many workgroups (%lld)", (long long)tiles);
+    }
+    return MM_OK;
+}
+
+}  // namespace mm
+
+using namespace mm;
+
+extern "C" {
+
+mm_status mm_scaled_int_plan_create(const int64_t *a_shape, int a_rank, const int64_t *b_shape, int b_rank,
+                                    const mm_scaled_int_desc *d, const mm_plan_options *opt, mm_plan_t *out) {
+    clear_error();
+    if (!out) return fail(MM_ERR_NULL_ARG, "out is NULL");
+    *out = nullptr;
+    if (!d) return fail(MM_ERR_NULL_ARG, "descriptor is NULL");
+    if ((!a_shape && a_rank > 0) || (!b_shape && b_rank > 0)) return fail(MM_ERR_NULL_ARG, "shape pointer is NULL");
+    if (d->a_type != MM_INT8 && !float_type(d->a_type))
+        return fail(MM_ERR_DTYPE, "A is INT8, or FLOAT, FLOAT16 or BFLOAT16 to be quantized (got %d)", d->a_type);
+    if (!float_type(d->out_type))
+        return fail(MM_ERR_DTYPE, "the output is FLOAT, FLOAT16 or BFLOAT16 (got %d)", d->out_type);
+    if (d->reserved != 0 || (opt && opt->reserved != 0)) return fail(MM_ERR_BAD_OPTION, "reserved field must be 0");
+    if ((d->trans_b != 0 && d->trans_b != 1) || (d->has_bias != 0 && d->has_bias != 1))
+        return fail(MM_ERR_BAD_OPTION, "trans_b and has_bias must be 0 or 1");
+    if (d->trans_b && b_rank == 1) return fail(MM_ERR_BAD_OPTION, "trans_b needs a B of rank two or more");
+    int64_t bs[MM_MAX_RANK] = {};
+    if (b_rank >= 1 && b_rank <= MM_MAX_RANK) {
+        for (int i = 0; i < b_rank; ++i) bs[i] = b_shape[i];
+        if (d->trans_b) std::swap(bs[b_rank - 1], bs[b_rank - 2]);
+    }
+    mm_plan_s *p = new (std::nothrow) mm_plan_s();
+    if (!p) return fail(MM_ERR_ALLOC, "host allocation failed");
+    p->dtype = d->out_type;
+    p->is_scaled = true;
+    p->a_type = d->a_type;
+    p->b_type = MM_INT8;
+    p->tb = d->trans_b;
+    p->has_bias = d->has_bias != 0;
+    mm_status st = resolve(a_shape, a_rank, bs, b_rank, p);
+    if (st == MM_OK) st = check_limits(p);
+    if (st == MM_OK && p->K > 131071)
+        st = fail(MM_ERR_TOO_LARGE, "K = %lld: INT32 sums hold at most 131071 INT8 products", (long long)p->K);
+    if (st == MM_OK && p->out_numel == 0) {
+        p->algo = MM_ALGO_EMPTY;
+    } else if (st == MM_OK) {
+        st = select_scaled(p, opt);
+        if (st == MM_OK && p->a_type != MM_INT8) {
+            p->a_rows = 1;
+            for (int i = 0; i + 1 < a_rank; ++i) p->a_rows *= a_shape[i];
+            p->q_pitch = round_up(p->K, 16);
+            p->q_off = p->workspace_bytes;
+            p->qs_off = p->q_off + round_up(p->a_rows * p->q_pitch, 256);
+            p->workspace_bytes = p->qs_off + round_up(p->a_rows * 4, 256);
+            // The batch strides of A count elements of its dense rows.
+            if (p->K > 0)
+                for (int i = 0; i < p->bd.nb; ++i) p->bd.sa[i] = p->bd.sa[i] / p->K * p->q_pitch;
+        }
+    }
+    if (st == MM_OK) st = alloc_workspace(p, true);
+    if (st != MM_OK) {
+        delete p;
+        return st;
+    }
+    *out = p;
+    return MM_OK;
+}
+
+mm_status mm_quantize_rows(const void *X, int dtype, int64_t rows, int64_t cols, void *Q, float *scale, void *stream) {
+    clear_error();
+    if (rows < 0 || cols < 0) return fail(MM_ERR_NEG_DIM, "rows and cols must not be negative");
+    if (!float_type(dtype)) return fail(MM_ERR_DTYPE, "quantize_rows takes FLOAT, FLOAT16 or BFLOAT16 (got %d)", dtype);
+    if (rows > INT32_MAX || cols > INT32_MAX) return fail(MM_ERR_TOO_LARGE, "rows and cols must each be below 2^31");
+    if (rows == 0) return MM_OK;
+    if (!scale || (cols > 0 && (!X || !Q))) return fail(MM_ERR_NULL_ARG, "X, Q or scale is NULL");
+    return launched(launch_quantize_rows(dtype, X, rows, cols, Q, cols, scale, (hipStream_t)stream));
+}
+
+mm_status mm_scaled_int_execute(mm_plan_t p, const void *A, const void *B, const float *a_scale, const float *b_scale,
+                                const void *bias, void *Y, void *stream) {
+    clear_error();
+    if (!p) return fail(MM_ERR_NULL_ARG, "plan is NULL");
+    if (!p->is_scaled) return fail(MM_ERR_BAD_OPTION, "not a scaled INT8 plan");
+    if (p->algo == MM_ALGO_EMPTY) return MM_OK;
+    const bool quant = p->a_type != MM_INT8;
+    if (!Y) return fail(MM_ERR_NULL_ARG, "Y is NULL for a non-empty output");
+    if (p->K > 0 && (!A || !B)) return fail(MM_ERR_NULL_ARG, "A or B is NULL");
+    if (!b_scale || (!quant && !a_scale)) return fail(MM_ERR_NULL_ARG, "a scale is NULL");
+    if (quant && a_scale) return fail(MM_ERR_BAD_OPTION, "the plan quantizes A itself: a_scale must be NULL");
+    if (p->has_bias && !bias) return fail(MM_ERR_NULL_ARG, "the plan has a bias but bias is NULL");
+    if (!p->has_bias && bias) return fail(MM_ERR_BAD_OPTION, "the plan has no bias");
+    hipStream_t s = (hipStream_t)stream;
+    if (p->workspace_bytes > 0) {
+        mm_status st = alloc_workspace(p, false);
+        if (st != MM_OK) return st;
+    }
+    char *ws = (char *)p->ws;
+    FfnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.A[0] = quant ? ws + p->q_off : A;
+    a.B[0] = B;
+    a.Y[0] = Y;
+    a.M = p->kernel_m;
+    a.N = p->N;
+    a.K = p->K;
+    a.lda = std::max<int64_t>(quant ? p->q_pitch : p->K, 1);
+    a.ldb = p->tb ? p->K : p->N;
+    a.ldy = p->N;
+    a.batch = p->batch;
+    a.y_vec = aligned16(Y) && (p->N * elem_size(p->dtype)) % 16 == 0;
+    a.sa = quant ? (const float *)(ws + p->qs_off) : a_scale;
+    a.sb = b_scale;
+    a.bias = bias;
+    a.kchunk = p->kchunk;
+    a.split = p->split;
+    a.bd = p->bd;
+    if (quant) {
+        mm_status st = launched(launch_quantize_rows(p->a_type, A, p->a_rows, p->K, ws + p->q_off, p->q_pitch,
+                                                     (float *)(ws + p->qs_off), s));
+        if (st != MM_OK) return st;
+    }
+    if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_scaled_rows(p->dtype, a, s));
+    const bool vec = aligned16(a.A[0]) && a.lda % 16 == 0 && aligned16(B) && a.ldb % 16 == 0;
+    if (p->algo == MM_ALGO_SPLIT_K) {
+        a.W = (int32_t *)ws;
+        hipError_t e = launch_scaled_split(p->tb != 0, p->tile, vec, a, s);
+        if (e == hipSuccess) e = launch_scaled_reduce(p->dtype, a, s);
+        return launched(e);
+    }
+    return launched(launch_scaled(p->dtype, p->tb != 0, p->tile, vec, a, s));
+}
+
+mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_options *opt, mm_plan_t *out) {
+    clear_error();
+    if (!out) return fail(MM_ERR_NULL_ARG, "out is NULL");
+    *out = nullptr;
+    if (!d) return fail(MM_ERR_NULL_ARG, "descriptor is NULL");
+    if (!float_type(dtype))
+        return fail(MM_ERR_DTYPE, "the gated block takes FLOAT, FLOAT16 and BFLOAT16 (got %d)", dtype);
+    if (d->reserved != 0 || (opt && opt->reserved != 0)) return fail(MM_ERR_BAD_OPTION, "reserved field must be 0");
+    if ((d->trans_w != 0 && d->trans_w != 1) || (d->training != 0 && d->training != 1))
+        return fail(MM_ERR_BAD_OPTION, "trans_w and training must be 0 or 1");
+    if (d->activation < MM_ACT_SILU || d->activation > MM_ACT_SIGMOID)
+        return fail(MM_ERR_BAD_OPTION, "unknown activation %d", d->activation);
+    if (d->rows < 0 || d->in_features < 0 || d->hidden < 0)
+        return fail(MM_ERR_NEG_DIM, "rows, in_features and hidden must not be negative");
+    const int64_t M = d->rows, K = d->in_features, N = d->hidden;
+    const int64_t row = d->trans_w ? K : N;
+    if (d->w_pitch != 0 && d->w_pitch < row)
+        return fail(MM_ERR_BAD_OPTION, "w_pitch %lld is below the weights' row length %lld", (long long)d->w_pitch,
+                    (long long)row);
+    if (M > INT32_MAX || K > INT32_MAX || N > INT32_MAX || d->w_pitch > INT32_MAX)
+        return fail(MM_ERR_TOO_LARGE, "rows, in_features, hidden and w_pitch must each be below 2^31");
+    const int force = opt ? opt->force_algo : MM_ALGO_AUTO;
+    const bool rows_ok = d->trans_w && M <= kFfnRows;
+    if (force != MM_ALGO_AUTO && force != MM_ALGO_GENERAL && force != MM_ALGO_SKINNY_M)
+        return fail(MM_ERR_BAD_OPTION, "the gated block runs on the skinny-M and general kernels only");
+    if (force == MM_ALGO_SKINNY_M && !rows_ok)
+        return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes at most %d rows with trans_w", kFfnRows);
+    if (opt && opt->split_k != 0) return fail(MM_ERR_BAD_OPTION, "the gated block does not split K");
+    mm_plan_s *p = new (std::nothrow) mm_plan_s();
+    if (!p) return fail(MM_ERR_ALLOC, "host allocation failed");
+    p->dtype = dtype;
+    p->is_glu = true;
+    p->tb = d->trans_w;
+    p->act = d->activation;
+    p->training = d->training != 0;
+    p->w_pitch = d->w_pitch ? d->w_pitch : row;
+    p->out_rank = 2;
+    p->out_shape[0] = M;
+    p->out_shape[1] = N;
+    p->M = p->kernel_m = M;
+    p->N = N;
+    p->K = K;
+    p->out_numel = M * N;
+    p->total_batch = p->batch = 1;
+    mm_status st = MM_OK;
+    if (p->out_numel == 0) {
+        p->algo = MM_ALGO_EMPTY;
+    } else {
+        const int first = dtype == MM_FLOAT ? 1 : 0;  // no 256 x 256 FLOAT tile
+        p->tile = pick_tile(1, M, 2 * N, first, kNumFfnTiles - 1);
+        st = tile_option(opt, first, &p->tile);
+        p->algo = force != MM_ALGO_AUTO ? force
+                  : rows_ok && !(opt && opt->tile > 0) ? MM_ALGO_SKINNY_M : MM_ALGO_GENERAL;
+        if (p->algo == MM_ALGO_SKINNY_M) p->tile = -1;
+    }
+    if (st == MM_OK && p->training && p->out_numel > 0) {
+        p->d_pitch = round_up(N, 16 / elem_size(dtype));
+        p->d_bytes = round_up(M * p->d_pitch * elem_size(dtype), 256);
+        p->workspace_bytes = 2 * p->d_bytes;
+        st = alloc_workspace(p, true);
+    }
+    if (st != MM_OK) {
+        delete p;
+        return st;
+    }
+    *out = p;
+    return MM_OK;
+}
+
+mm_status mm_glu_execute(mm_plan_t p, const void *X, const void *Wg, const void *Wu, void *H, void *G, void *U,
+                         void *stream) {
+    clear_error();
+    if (!p) return fail(MM_ERR_NULL_ARG, "plan is NULL");
+    if (!p->is_glu) return fail(MM_ERR_BAD_OPTION, "not a gated-block plan");
+    if (p->algo == MM_ALGO_EMPTY) return MM_OK;
+    if (!H) return fail(MM_ERR_NULL_ARG, "H is NULL for a non-empty output");
+    if (!G != !U) return fail(MM_ERR_NULL_ARG, "G and U are given together or not at all");
+    if (p->K > 0 && (!X || !Wg || !Wu)) return fail(MM_ERR_NULL_ARG, "X, Wg or Wu is NULL");
+    hipStream_t s = (hipStream_t)stream;
+    const int64_t es = elem_size(p->dtype);
+    FfnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.A[0] = X;
+    a.B[0] = Wg;
+    a.B[1] = Wu;
+    a.Y[0] = H;
+    a.G = G;
+    a.U = U;
+    a.M = p->M;
+    a.N = p->N;
+    a.K = p->K;
+    a.lda = p->K;
+    a.ldb = p->w_pitch;
+    a.ldy = p->N;
+    a.batch = 1;
+    a.split = 1;
+    a.act = p->act;
+    a.y_vec = aligned16(H) && aligned16(G) && aligned16(U) && (p->N * es) % 16 == 0;
+    if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_glu_rows(p->dtype, a, s));
+    const bool vec = aligned16(X) && aligned16(Wg) && aligned16(Wu) && (p->K * es) % 16 == 0 &&
+                     (p->w_pitch * es) % 16 == 0 && (p->tb || (p->N * es) % 16 == 0);
+    return launched(launch_glu_fwd(p->dtype, p->tb != 0, p->tile, vec, a, s));
+}
+
+mm_status mm_glu_backward(mm_plan_t p, const void *X, const void *Wg, const void *Wu, const void *G, const void *U,
+                          const void *dH, void *dX, void *dWg, void *dWu, void *stream) {
+    clear_error();
+    if (!p) return fail(MM_ERR_NULL_ARG, "plan is NULL");
+    if (!p->is_glu) return fail(MM_ERR_BAD_OPTION, "not a gated-block plan");
+    if (!p->training) return fail(MM_ERR_BAD_OPTION, "the plan was created without training");
+    if (!dWg != !dWu) return fail(MM_ERR_NULL_ARG, "dWg and dWu are given together or not at all");
+    const int64_t M = p->M, N = p->N, K = p->K, es = elem_size(p->dtype);
+    const bool want_x = dX && M > 0 && K > 0, want_w = dWg && N > 0 && K > 0;
+    if (!want_x && !want_w) return MM_OK;
+    hipStream_t s = (hipStream_t)stream;
+    if (p->out_numel > 0) {
+        if (!G || !U || !dH) return fail(MM_ERR_NULL_ARG, "G, U or dH is NULL");
+        if (want_x && (!Wg || !Wu)) return fail(MM_ERR_NULL_ARG, "Wg or Wu is NULL");
+        if (want_w && !X) return fail(MM_ERR_NULL_ARG, "X is NULL");
+        mm_status st = alloc_workspace(p, false);
+        if (st != MM_OK) return st;
+    }
+    void *dG = p->ws, *dU = (char *)p->ws + p->d_bytes;
+    if (p->out_numel > 0) {
+        mm_status st = launched(launch_glu_dact(p->dtype, p->act, G, U, dH, dG, dU, M, N, p->d_pitch, s));
+        if (st != MM_OK) return st;
+    }
+    auto bwd_tile = [&](int64_t batch, int64_t rows, int64_t cols) {
+        return pick_tile(batch, rows, cols, p->dtype == MM_FLOAT ? 1 : 0, 1);
+    };
+    const bool w_vec = (p->w_pitch * es) % 16 == 0;
+    if (want_x) {
+        // dX [M, K] = dG Wg' + dU Wu', the reduction over the hidden features:
+        // weights stored [K, N] are K-contiguous rows, [N, K] rows of one n.
+        FfnArgs a;
+        memset(&a, 0, sizeof(a));
+        a.A[0] = dG;
+        a.A[1] = dU;
+        a.B[0] = Wg;
+        a.B[1] = Wu;
+        a.Y[0] = dX;
+        a.M = M;
+        a.N = K;
+        a.K = N;
+        a.lda = std::max<int64_t>(p->d_pitch, 1);
+        a.ldb = p->w_pitch;
+        a.ldy = K;
+        a.batch = 1;
+        a.split = 1;
+        a.y_vec = aligned16(dX) && (K * es) % 16 == 0;
+        const bool vec = w_vec && aligned16(Wg) && aligned16(Wu) && ((p->tb ? K : N) * es) % 16 == 0;
+        mm_status st = launched(launch_glu_dx(p->dtype, !p->tb, bwd_tile(1, M, K), vec, a, s));
+        if (st != MM_OK) return st;
+    }
+    if (want_w) {
+        // Weights [N, K]: dW = dG^T X; [K, N]: dW = X^T dG.  The reduction
+        // over the rows reads both operands as rows of one k.
+        FfnArgs a;
+        memset(&a, 0, sizeof(a));
+        a.A[0] = p->tb ? dG : X;
+        a.A[1] = p->tb ? dU : X;
+        a.B[0] = p->tb ? X : dG;
+        a.B[1] = p->tb ? X : dU;
+        a.Y[0] = dWg;
+        a.Y[1] = dWu;
+        a.M = p->tb ? N : K;
+        a.N = p->tb ? K : N;
+        a.K = M;
+        a.lda = std::max<int64_t>(p->tb ? p->d_pitch : K, 1);
+        a.ldb = std::max<int64_t>(p->tb ? K : p->d_pitch, 1);
+        a.ldy = p->w_pitch;
+        a.batch = 2;
+        a.split = 1;
+        a.y_vec = aligned16(dWg) && aligned16(dWu) && w_vec && (a.N * es) % 16 == 0;
+        const bool vec = aligned16(X) && (K * es) % 16 == 0;
+        mm_status st = launched(launch_glu_dw(p->dtype, bwd_tile(2, a.M, a.N), vec, a, s));
+        if (st != MM_OK) return st;
+    }
+    return MM_OK;
+}
+
+}  // extern "C"
