@@ -22,19 +22,19 @@ struct FfnArgs {
     // scaled INT8 product
     const float *sa, *sb;
     const void *bias;      // of the output type, or NULL
-    int32_t *W;            // INT32 partials [split][batch][M][N]
-    int64_t kchunk;
+    void *W;               // partial sums [split][batch][M][N], INT32 (INT8 operands) or FP32
     int32_t split;
-    int32_t pad_;
+    int32_t kstages;       // K stages of a partition
     BatchDesc bd;
 };
 
 // Tile table of the tiled products: block rows and columns (the gated
-// block's columns count gate and up), see k_ffn.h.
+// block's columns count gate and up) and the bytes of K in a stage, see
+// k_ffn.h.
 struct FfnTile {
-    int bm, bn;
+    int bm, bn, bkb;
 };
-constexpr FfnTile kFfnTiles[] = {{256, 256}, {128, 128}, {64, 128}, {32, 128}};
+constexpr FfnTile kFfnTiles[] = {{256, 256, 64}, {128, 128, 64}, {64, 128, 128}, {32, 128, 256}};
 constexpr int kNumFfnTiles = sizeof(kFfnTiles) / sizeof(kFfnTiles[0]);
 
 // Element-wise part of the gated block's backward pass: dG = dH * U * f'(G),
@@ -42,10 +42,12 @@ constexpr int kNumFfnTiles = sizeof(kFfnTiles) / sizeof(kFfnTiles[0]);
 // (whole 16-byte chunks, 16-byte aligned), zero past N.
 hipError_t launch_glu_dact(int dtype, int act, const void *G, const void *U, const void *dH, void *dG, void *dU,
                            int64_t M, int64_t N, int64_t ldw, hipStream_t s);
-// Tiled products (vec: every operand row and base is 16-byte aligned).
+// Tiled products (vec: every operand row and base is 16-byte aligned; split:
+// partial sums to W, to be joined by launch_sum_reduce / launch_scaled_reduce).
 hipError_t launch_glu_fwd(int dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);
-hipError_t launch_glu_dx(int dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);
-hipError_t launch_glu_dw(int dtype, int tile, bool vec, const FfnArgs &a, hipStream_t s);
+hipError_t launch_glu_dx(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
+hipError_t launch_glu_dw(int dtype, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
+hipError_t launch_sum_reduce(int dtype, const FfnArgs &a, hipStream_t s);
 hipError_t launch_scaled(int out_dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);
 hipError_t launch_scaled_split(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);
 hipError_t launch_scaled_reduce(int out_dtype, const FfnArgs &a, hipStream_t s);

@@ -45,18 +45,23 @@ __device__ __forceinline__ int row_swizzle(int k, int cpr) {
 // Which products a kernel computes.
 //   kGlu:    H = act(A B0) * (A B1), optionally also A B0 and A B1
 //   kSum2:   Y0 = A0 B0 + A1 B1 (the K loop runs over both terms)
-//   kPair:   Y0 = A B0 and Y1 = A B1, or Y0 = A0 B and Y1 = A1 B (grid half each)
+//   kPair:   Y0 = A0 B0 and Y1 = A1 B1 (half of the grid each)
 //   kScaled: Y = sa[m] sb[n] (A B) + bias[n], INT8 operands
-//   kScaledSplit: INT32 partial sums of one K partition
-enum FfnMode { kGlu = 0, kSum2 = 1, kPair = 2, kScaled = 3, kScaledSplit = 4 };
+// SPLIT: a workgroup takes a range of K stages and writes FP32 (INT8
+// operands: INT32) partial sums to the workspace.
+// KG groups of WGM x WGN waves share the tile; group g takes every KG-th MFMA
+// step of a stage, and their sums are added in group order at the end.
+enum FfnMode { kGlu = 0, kSum2 = 1, kPair = 2, kScaled = 3 };
 
-template <int DT, int OD, int MODE, bool TA, bool TB, int BM, int BN, int WGM, int WGN, int BKB, int STAGES, int PW, bool DMA>
-__global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
+template <int DT, int OD, int MODE, bool SPLIT, bool TA, bool TB, int BM, int BN, int WGM, int WGN, int KG, int BKB,
+          int STAGES, int PW, bool DMA>
+__global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using E = Elem<DT>;
     using S = typename E::S;
     constexpr bool INT = DT == MM_INT8;
-    constexpr int NW = WGM * WGN;
+    constexpr int NWG = WGM * WGN;         // waves of one K group
+    constexpr int NW = NWG * KG;
     constexpr int NT = 64 * NW;
     constexpr int ES = (int)sizeof(S);
     constexpr int VE = 16 / ES;
@@ -72,24 +77,25 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
     constexpr int A_BYTES = BM * BKB;
     constexpr int P_BYTES = PN * BKB;      // one B panel
     constexpr int STAGE_BYTES = A_BYTES + NPAN * P_BYTES;
-    static_assert(CA == 4 || CA == 8, "K-contiguous rows are 64 or 128 bytes");
+    static_assert(CA == 4 || CA == 8 || CA == 16, "K-contiguous rows are 64, 128 or 256 bytes");
+    static_assert(KS % (2 * KG) == 0, "an even number of steps per group and stage");
     static_assert(FM >= 1 && FNP >= 1 && BM % (32 * WGM) == 0 && PN % (32 * WGN) == 0, "wave tile");
     static_assert(STAGES >= 3 && STAGES * STAGE_BYTES <= 160 * 1024, "LDS");
     static_assert(!TA || (CPRA >= 8 && CPRA <= 64), "transposed A rows");
     static_assert(TB || (CPRB >= 8 && CPRB <= 64), "B rows");
-    auto aswz = [](int row) { return CA == 8 ? ((row >> 1) & 7) : ((row >> 2) & 3); };
+    auto aswz = [](int row) { return CA == 16 ? (row & 15) : CA == 8 ? ((row >> 1) & 7) : ((row >> 2) & 3); };
 
     __shared__ __attribute__((aligned(1024))) char lds[STAGES * STAGE_BYTES];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wr = wave / WGN, wc = wave % WGN;
+    const int kg = wave / NWG;
+    const int wr = (wave % NWG) / WGN, wc = wave % WGN;
 
     const int64_t M = a.M, N = a.N, K = a.K;
     const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + PN - 1) / PN;
     const int64_t per = tiles_m * tiles_n;
-    constexpr bool SPLIT = MODE == kScaledSplit;
     const int64_t nsplit = SPLIT ? a.split : 1;
     int64_t id = xcd_remap(blockIdx.x, (int64_t)gridDim.x);
     const int64_t sidx = SPLIT ? id % nsplit : 0;
@@ -115,10 +121,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
     const char *At1 = MODE == kSum2 ? (const char *)((const S *)a.A[1] + ta_off) : At0;
     const char *Bt1 = MODE == kSum2 || MODE == kGlu ? (const char *)((const S *)a.B[1] + tb_off) : Bt0;
 
-    const int64_t kbeg = SPLIT ? sidx * a.kchunk : 0;
-    const int64_t kend = SPLIT ? ((kbeg + a.kchunk) < K ? (kbeg + a.kchunk) : K) : K;
-    const int nk1 = (int)((kend - kbeg + BK - 1) / BK);
-    const int nk = MODE == kSum2 ? 2 * nk1 : nk1;
+    // Stages of this workgroup: all of them (kSum2: both terms' in turn), or
+    // its partition's.
+    const int64_t kend = K;
+    const int nk1 = (int)((K + BK - 1) / BK);
+    const int nkall = MODE == kSum2 ? 2 * nk1 : nk1;
+    const int st0 = SPLIT ? (int)sidx * a.kstages : 0;
+    const int nk = SPLIT ? (nkall - st0 < a.kstages ? nkall - st0 : a.kstages) : nkall;
 
     using AccT = typename std::conditional<INT, i32x16, f32x16>::type;
     AccT acc[FM][FN];
@@ -236,10 +245,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
         constexpr int MPS = FM * FN;                              // MFMAs per step
         constexpr int R2 = (RPS + 1) / 2;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            if (ks + 1 < KS) read_frags(buf, ks + 1, (ks + 1) & 1);
-            else read_frags(next, 0, (ks + 1) & 1);
-            mfmas(ks & 1);
+        for (int j = 0; j < KS / KG; ++j) {
+            if (j + 1 < KS / KG) read_frags(buf, kg + (j + 1) * KG, (j + 1) & 1);
+            else read_frags(next, kg, (j + 1) & 1);
+            mfmas(j & 1);
             if constexpr (SCHED) {
                 {
 #pragma unroll
@@ -252,12 +261,11 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
             }
         }
     };
-    static_assert(KS % 2 == 0, "the next stage's first fragments go to slot 0");
 
     // A stage's first k and operands: kSum2 runs over the first term's stages,
     // then the second's.
-    auto stage_k0 = [&](int st) { return kbeg + (int64_t)(MODE == kSum2 && st >= nk1 ? st - nk1 : st) * BK; };
-    auto stage_second = [&](int st) { return MODE == kSum2 && st >= nk1; };
+    auto stage_second = [&](int st) { return MODE == kSum2 && st0 + st >= nk1; };
+    auto stage_k0 = [&](int st) { return (int64_t)(st0 + st - (stage_second(st) ? nk1 : 0)) * BK; };
 
     if constexpr (DMA) {
         constexpr int A_INSTR = A_BYTES / 1024 / PW;  // 1 KB loads per producer and stage
@@ -337,7 +345,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
         if (nk >= STAGES - 1) wait_vmcnt<(STAGES - 2) * LPW>();
         else wait_vmcnt<0>();
         asm volatile("s_barrier" ::: "memory");
-        if (nk > 0) read_frags(0, 0, 0);
+        if (nk > 0) read_frags(0, kg, 0);
         for (int kt = 0; kt < nk; ++kt) {
             // Loads of stage kt + 1 are complete once at most those of the
             // STAGES - 3 stages issued after it are outstanding.
@@ -349,55 +357,78 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
             compute(kt % STAGES, (kt + 1) % STAGES);
         }
     } else {
-        constexpr int A_CH = A_BYTES / 16, CHUNKS = STAGE_BYTES / 16;
-        constexpr int CPT = (CHUNKS + NT - 1) / NT;
-        uint4 rg[CPT];
-        // Chunk x of a stage: LDS position, and its elements in memory.
+        // Chunks of A and of each B panel per thread and stage.
+        constexpr int AC = A_BYTES / 16 / NT, BC = P_BYTES / 16 / NT;
+        static_assert(AC * NT * 16 == A_BYTES && BC * NT * 16 == P_BYTES, "whole chunks per thread");
+        uint4 rga[AC], rgb[NPAN][BC];
+        // One operand's chunks of a stage starting at k0.  kc: K-contiguous
+        // rows.  A whole stage loads whole chunks without a test: rows past
+        // the matrix read its last row, and chunks that cross a row's end
+        // read on into the next rows (where the matrix goes on for that long);
+        // both reach only outputs that are not stored.  The last stage may
+        // neither read past the matrix nor bring in values past K.
+        auto gather = [&](auto kc_t, auto cpr_t, auto count_t, const char *base, int64_t ld, int64_t left_mn, int64_t k0, uint4 *out) {
+            constexpr bool KC = decltype(kc_t)::value;
+            constexpr int CPR = decltype(cpr_t)::value, COUNT = decltype(count_t)::value;
+            typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
+            typedef const __attribute__((address_space(1))) S *gptr;
+            const gptr g = (gptr)base;
+            const int64_t krem = kend - k0;
+            const bool whole = krem >= BK && (KC || left_mn >= (int64_t)CPR * VE || (krem - BK) * ld >= VE);
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < COUNT; ++i) {
+                    const int y = tid + NT * i;
+                    int row = y / CPR;
+                    const int c = (y % CPR) ^ (KC ? aswz(row) : row_swizzle<ES>(row, CPR));
+                    int64_t at;
+                    if constexpr (KC) {
+                        if (row >= left_mn) row = (int)left_mn - 1;
+                        at = (int64_t)row * ld + k0 + c * VE;
+                    } else {
+                        // Columns wholly past the matrix: its first ones.
+                        at = (k0 + row) * ld + (c * VE < left_mn ? c * VE : 0);
+                    }
+                    out[i] = __builtin_bit_cast(uint4, *(const __attribute__((address_space(1))) u32x4u *)(g + at));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < COUNT; ++i) {
+                    const int y = tid + NT * i;
+                    const int row = y / CPR;
+                    const int c = (y % CPR) ^ (KC ? aswz(row) : row_swizzle<ES>(row, CPR));
+                    const int64_t left = KC ? (row < left_mn ? krem - c * VE : 0) : (row < krem ? left_mn - c * VE : 0);
+                    const int64_t at = KC ? (int64_t)row * ld + k0 + c * VE : (k0 + row) * ld + c * VE;
+                    S tmp[VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) tmp[e] = e < left ? g[at + e] : (S)0;
+                    uint4 v;
+                    __builtin_memcpy(&v, tmp, 16);
+                    // Bytes are packed here: otherwise the whole stages' words
+                    // are taken apart and packed again where the paths meet.
+                    if constexpr (ES == 1) asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+                    out[i] = v;
+                }
+            }
+        };
         auto load = [&](int st) {
             const int64_t k0 = stage_k0(st);
             const bool second = stage_second(st);
-            const int64_t krem = kend - k0;
+            gather(std::integral_constant<bool, !TA>(), std::integral_constant<int, TA ? CPRA : CA>(),
+                   std::integral_constant<int, AC>(), second ? At1 : At0, a.lda, M - m0, k0, rga);
 #pragma unroll
-            for (int i = 0; i < CPT; ++i) {
-                const int x = tid + NT * i;
-                rg[i] = make_uint4(0, 0, 0, 0);
-                if (CHUNKS % NT != 0 && x >= CHUNKS) continue;
-                const bool isA = x < A_CH;
-                const int y = isA ? x : (x - A_CH) % (P_BYTES / 16);
-                const bool up = !isA && MODE == kGlu && x - A_CH >= P_BYTES / 16;
-                const bool kc = isA ? !TA : TB;  // K-contiguous rows
-                const int cpr = kc ? CA : isA ? CPRA : CPRB;
-                const int row = y / cpr, p = y % cpr;
-                const int c = p ^ (kc ? aswz(row) : row_swizzle<ES>(row, cpr));
-                const int64_t ld = isA ? a.lda : a.ldb;
-                const int64_t lim_mn = isA ? M - m0 : N - n0;
-                const char *base = isA ? (second ? At1 : At0) : (second || up ? Bt1 : Bt0);
-                int64_t left;  // elements of this chunk inside the matrix
-                const S *src;
-                if (kc) {
-                    left = row < lim_mn ? krem - c * VE : 0;
-                    src = (const S *)base + (int64_t)row * ld + k0 + c * VE;
-                } else {
-                    left = row < krem ? lim_mn - c * VE : 0;
-                    src = (const S *)base + (k0 + row) * ld + c * VE;
-                }
-                if (left >= VE) {
-                    __builtin_memcpy(&rg[i], src, 16);
-                } else if (left > 0) {
-                    S tmp[VE];
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) tmp[e] = e < left ? src[e] : (S)0;
-                    __builtin_memcpy(&rg[i], tmp, 16);
-                }
-            }
+            for (int p = 0; p < NPAN; ++p)
+                gather(std::integral_constant<bool, TB>(), std::integral_constant<int, TB ? CA : CPRB>(),
+                       std::integral_constant<int, BC>(), second || p == 1 ? Bt1 : Bt0, a.ldb, N - n0, k0, rgb[p]);
         };
         auto store = [&](int st) {
             char *sb = lds + (st % STAGES) * STAGE_BYTES;
 #pragma unroll
-            for (int i = 0; i < CPT; ++i) {
-                const int x = tid + NT * i;
-                if (CHUNKS % NT == 0 || x < CHUNKS) *(uint4 *)(sb + x * 16) = rg[i];
-            }
+            for (int i = 0; i < AC; ++i) *(uint4 *)(sb + (tid + NT * i) * 16) = rga[i];
+#pragma unroll
+            for (int p = 0; p < NPAN; ++p)
+#pragma unroll
+                for (int i = 0; i < BC; ++i) *(uint4 *)(sb + A_BYTES + p * P_BYTES + (tid + NT * i) * 16) = rgb[p][i];
         };
         if (nk > 0) {
             load(0);
@@ -409,7 +440,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
         }
         if (nk > 2) load(2);
         __syncthreads();
-        if (nk > 0) read_frags(0, 0, 0);
+        if (nk > 0) read_frags(0, kg, 0);
         for (int kt = 0; kt < nk; ++kt) {
             // Stage kt + 2 goes to a buffer last read before the previous
             // barrier and is visible after the next one.
@@ -426,6 +457,35 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
     // larger than the stage buffers go in row passes.
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     using OE = Elem<OD>;
+    if constexpr (KG > 1) {
+        // Groups 1 .. KG - 1 hand their sums to group 0 through LDS.
+        static_assert((KG - 1) * BM * BN * 4 <= STAGES * STAGE_BYTES, "K group exchange");
+        using T = typename std::conditional<INT, int, float>::type;
+        T *xch = (T *)lds;
+        auto at = [&](int g, int i, int j, int r) {
+            return ((((g - 1) * NWG + wave % NWG) * FM + i) * FN * 16 + j * 16 + r) * 64 + lane;
+        };
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) xch[at(kg, i, j, r)] = acc[i][j][r];
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (kg == 0) {
+#pragma unroll
+            for (int g = 1; g < KG; ++g)
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[i][j][r] += xch[at(g, i, j, r)];
+        }
+    }
     auto emit = [&](auto zero, int jbase, auto value, void *outp, int64_t ldo, bool vec) {
         using O = decltype(zero);
         constexpr int OS = (int)sizeof(O), OV = 16 / OS;
@@ -440,7 +500,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const int rl = wr * WM + i * 32 + (lane & 31) - pass * PR;
-                if (NP == 1 || (rl >= 0 && rl < PR)) {
+                if (kg == 0 && (NP == 1 || (rl >= 0 && rl < PR))) {
                     char *trow = lds + rl * (PN * OS);
 #pragma unroll
                     for (int j = 0; j < FNP; ++j)
@@ -487,7 +547,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
         }
     };
     auto plain = [](int, int, auto v) { return (float)v; };
-    if constexpr (MODE == kGlu) {
+    if constexpr (SPLIT) {
+        using T = typename std::conditional<INT, int32_t, float>::type;
+        emit((T)0, 0, plain, (T *)a.W + (sidx * a.batch + b) * M * N, N, N % 4 == 0);
+    } else if constexpr (MODE == kGlu) {
         if (a.G) {
             emit((typename OE::S)0, 0, plain, a.G, a.ldy, a.y_vec != 0);
             emit((typename OE::S)0, FNP, plain, a.U, a.ldy, a.y_vec != 0);
@@ -509,8 +572,6 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
         default: apply(std::integral_constant<int, MM_ACT_SIGMOID>()); break;
         }
         emit((typename OE::S)0, 0, plain, a.Y[0], a.ldy, a.y_vec != 0);
-    } else if constexpr (MODE == kScaledSplit) {
-        emit((int32_t)0, 0, plain, a.W + (sidx * a.batch + b) * M * N, N, N % 4 == 0);
     } else if constexpr (MODE == kScaled) {
         // Scales of this lane's rows, and of the tile's columns in LDS after
         // the main loop's last reads.
@@ -538,23 +599,48 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(FfnArgs a) {
 }
 
 // Launch one entry; DMA where the operands allow it (`vec`).
-template <int DT, int OD, int MODE, bool TA, bool TB, int BM, int BN, int WGM, int WGN, int BKB, int STAGES, int PW>
+template <int DT, int OD, int MODE, bool SPLIT, bool TA, bool TB, int BM, int BN, int WGM, int WGN, int KG, int BKB,
+          int STAGES, int PW>
 static hipError_t launch_ffn(bool vec, const FfnArgs &a, hipStream_t s) {
     constexpr int PN = MODE == kGlu ? BN / 2 : BN;
     constexpr int ES = (int)sizeof(typename Elem<DT>::S);
-    const int64_t tiles = a.batch * ((a.M + BM - 1) / BM) * ((a.N + PN - 1) / PN) * (MODE == kScaledSplit ? a.split : 1);
+    const int64_t tiles = a.batch * ((a.M + BM - 1) / BM) * ((a.N + PN - 1) / PN) * (SPLIT ? a.split : 1);
     if (tiles <= 0) return hipSuccess;
     if (tiles > 0x7fffffff) return hipErrorInvalidValue;
     // Buffer offsets are 32-bit: the rows that one stage of a tile spans.
     const int64_t a_span = (TA ? (int64_t)(BKB / ES) : (int64_t)BM) * a.lda;
     const int64_t b_span = (TB ? (int64_t)PN : (int64_t)(BKB / ES)) * a.ldb;
     const bool fits = a_span * ES < 0x7fff0000LL && b_span * ES < 0x7fff0000LL;
-    const dim3 g((unsigned)tiles), blk(64 * WGM * WGN);
+    const dim3 g((unsigned)tiles), blk(64 * WGM * WGN * KG);
     if (vec && fits)
-        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, TA, TB, BM, BN, WGM, WGN, BKB, STAGES, PW, true>), g, blk, 0, s, a);
-    else
-        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, TA, TB, BM, BN, WGM, WGN, BKB, STAGES, PW, false>), g, blk, 0, s, a);
+        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, SPLIT, TA, TB, BM, BN, WGM, WGN, KG, BKB, STAGES, PW, true>), g, blk, 0, s, a);
+    else if constexpr (BM * BN < 256 * 256)
+        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, SPLIT, TA, TB, BM, BN, WGM, WGN, KG, BKB, STAGES, PW, false>), g, blk, 0, s, a);
+    else  // the register-staged form would not fit the registers of this tile
+        return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 128, 128, 2, 2, 1, 64, 4, 4>(false, a, s);
     return hipGetLastError();
+}
+
+// The entries of kFfnTiles for one kind of product.
+template <int DT, int OD, int MODE, bool SPLIT, bool TA, bool TB>
+static hipError_t launch_entry(int tile, bool vec, const FfnArgs &a, hipStream_t s) {
+    switch (tile) {
+    case 0:
+        // FLOAT fills the matrix cores with smaller tiles, and partial sums
+        // of 256 x 256 tiles are never wanted.
+        if constexpr (DT != MM_FLOAT && !SPLIT) {
+            constexpr int WGM = MODE == kGlu ? 4 : 2;
+            return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 256, 256, WGM, 8 / WGM, 1, 64, 4, 4>(vec, a, s);
+        }
+        break;
+    case 1: return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 128, 128, 2, 2, 1, 64, 4, 4>(vec, a, s);
+    case 2: return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 64, 128, 2, 2, 2, 128, 3, 4>(vec, a, s);
+    case 3:
+        // A 32-row tile of a transposed 16-bit A has rows too short to stage.
+        if constexpr (!TA || DT == MM_FLOAT) return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 32, 128, 1, 2, 4, 256, 3, 8>(vec, a, s);
+        break;
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace mm

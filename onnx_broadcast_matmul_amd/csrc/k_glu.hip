@@ -6,10 +6,10 @@
 
 namespace mm {
 
-#define MM_GLU_DECLARE(NAME)                                                                       \
-    hipError_t glu_fwd_##NAME(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);        \
-    hipError_t glu_dx_##NAME(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);         \
-    hipError_t glu_dw_##NAME(int tile, bool vec, const FfnArgs &a, hipStream_t s);
+#define MM_GLU_DECLARE(NAME)                                                                               \
+    hipError_t glu_fwd_##NAME(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);                \
+    hipError_t glu_dx_##NAME(bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);     \
+    hipError_t glu_dw_##NAME(int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
 MM_GLU_DECLARE(f32)
 MM_GLU_DECLARE(f16)
 MM_GLU_DECLARE(bf16)
@@ -19,14 +19,63 @@ hipError_t launch_glu_fwd(int dtype, bool tb, int tile, bool vec, const FfnArgs 
            : dtype == MM_FLOAT16 ? glu_fwd_f16(tb, tile, vec, a, s) : glu_fwd_bf16(tb, tile, vec, a, s);
 }
 
-hipError_t launch_glu_dx(int dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s) {
-    return dtype == MM_FLOAT ? glu_dx_f32(tb, tile, vec, a, s)
-           : dtype == MM_FLOAT16 ? glu_dx_f16(tb, tile, vec, a, s) : glu_dx_bf16(tb, tile, vec, a, s);
+hipError_t launch_glu_dx(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {
+    return dtype == MM_FLOAT ? glu_dx_f32(tb, tile, split, vec, a, s)
+           : dtype == MM_FLOAT16 ? glu_dx_f16(tb, tile, split, vec, a, s) : glu_dx_bf16(tb, tile, split, vec, a, s);
 }
 
-hipError_t launch_glu_dw(int dtype, int tile, bool vec, const FfnArgs &a, hipStream_t s) {
-    return dtype == MM_FLOAT ? glu_dw_f32(tile, vec, a, s)
-           : dtype == MM_FLOAT16 ? glu_dw_f16(tile, vec, a, s) : glu_dw_bf16(tile, vec, a, s);
+hipError_t launch_glu_dw(int dtype, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {
+    return dtype == MM_FLOAT ? glu_dw_f32(tile, split, vec, a, s)
+           : dtype == MM_FLOAT16 ? glu_dw_f16(tile, split, vec, a, s) : glu_dw_bf16(tile, split, vec, a, s);
+}
+
+// Sum of the K partitions' FP32 partials in partition order, narrowed once;
+// product b (blockIdx.y) of a.batch goes to Y[b], rows ldy elements apart.  A
+// thread owns four consecutive columns of one row.
+template <int DT>
+__global__ __launch_bounds__(256) void k_sum_reduce(FfnArgs a) {
+    using E = Elem<DT>;
+    using S = typename E::S;
+    const uint32_t N = (uint32_t)a.N, cpr = (N + 3) / 4;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (x >= a.M * cpr) return;
+    const int64_t row = x < 0x7fffffff ? (int64_t)((uint32_t)x / cpr) : x / cpr;
+    const uint32_t col = (uint32_t)(x - row * cpr) * 4;
+    const int64_t stride = a.batch * a.M * N;
+    const float *w = (const float *)a.W + (int64_t)blockIdx.y * a.M * N + row * N + col;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    S *y = (S *)a.Y[blockIdx.y] + row * a.ldy + col;
+    if (N % 4 == 0) {
+#pragma unroll 4
+        for (int p = 0; p < a.split; ++p) {
+            const float4 v = *(const float4 *)(w + p * stride);
+            acc[0] += v.x; acc[1] += v.y; acc[2] += v.z; acc[3] += v.w;
+        }
+    } else {
+        for (int p = 0; p < a.split; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < N) acc[e] += w[p * stride + e];
+    }
+    S out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = E::from_f32(acc[e]);
+    if (col + 4 <= N) __builtin_memcpy(y, out, sizeof(out));
+    else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < N) y[e] = out[e];
+}
+
+hipError_t launch_sum_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
+    const int64_t g = (a.M * ((a.N + 3) / 4) + 255) / 256;
+    if (g <= 0 || a.batch <= 0) return hipSuccess;
+    if (g > 0x7fffffff) return hipErrorInvalidValue;
+    const dim3 gr((unsigned)g, (unsigned)a.batch), bl(256);
+    if (dtype == MM_FLOAT) hipLaunchKernelGGL(k_sum_reduce<MM_FLOAT>, gr, bl, 0, s, a);
+    else if (dtype == MM_FLOAT16) hipLaunchKernelGGL(k_sum_reduce<MM_FLOAT16>, gr, bl, 0, s, a);
+    else hipLaunchKernelGGL(k_sum_reduce<MM_BFLOAT16>, gr, bl, 0, s, a);
+    return hipGetLastError();
 }
 
 // dG = dH U f'(G) and dU = dH f(G), a thread per 16 bytes of each tensor's

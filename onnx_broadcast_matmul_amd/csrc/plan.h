@@ -8,6 +8,15 @@
 
 #include "internal.h"
 
+namespace mm {
+// Tile entry and split of one tiled product of the feed-forward operators.
+struct FfnChoice {
+    int tile = 0;
+    int32_t split = 1;
+    int32_t kstages = 0;  // K stages of a partition
+};
+}  // namespace mm
+
 struct mm_plan_s {
     int dtype = 0;
     int a_rank = 0, b_rank = 0;
@@ -70,6 +79,8 @@ struct mm_plan_s {
     int act = 0;
     bool training = false;
     int64_t w_pitch = 0, d_pitch = 0, d_bytes = 0;
+    mm::FfnChoice dx, dw;  // the backward products; split partials follow dG and dU
+    int32_t kstages = 0;   // scaled INT8 product: K stages of a partition
 
     // Plan-owned constant B (mm_plan_set_constant_b).
     std::mutex cb_mutex;

@@ -21,26 +21,73 @@ static mm_status launched(hipError_t e) {
 
 static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
 
-// Relative rate of a tile entry once its workgroups fill the GPU.
-static const double kQuality[kNumFfnTiles] = {1.0, 0.8, 0.55, 0.3};
+// Time model of the tiled products: a CU runs up to kOcc workgroups of an
+// entry together, and a round of o workgroups per CU takes kFixed + kStep[o - 1]
+// for each 32 bytes of K.  Measured with forced entries on grids of 256 and
+// 512 workgroups, 1 and 8 KiB of K, over the forward, dX, dW and INT8 kinds,
+// which lie within 10 % of each other; rows that are not 16-byte aligned run
+// the register-staged form (entry 0 has none and runs entry 1's).
+enum { kClass16 = 0, kClass8 = 1, kClass32 = 2 };
+static const int kOcc[kNumFfnTiles] = {1, 2, 2, 1};
+static const double kLaunch = 2.5;                                 // us
+static const double kFixed[kNumFfnTiles] = {7.0, 3.2, 2.5, 2.0};  // us
+static const double kStep[2][3][kNumFfnTiles][2] = {               // us: aligned, not aligned
+    {{{0.44, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}},
+     {{0.42, 0}, {0.17, 0.285}, {0.145, 0.160}, {0.095, 0}},
+     {{1e9, 0}, {0.54, 0.970}, {0.260, 0.490}, {0.148, 0}}},
+    {{{1e9, 0}, {0.29, 0.340}, {0.150, 0.195}, {0.110, 0}},
+     {{1e9, 0}, {0.30, 0.355}, {0.175, 0.195}, {0.090, 0}},
+     {{1e9, 0}, {0.78, 1.160}, {0.400, 0.610}, {0.200, 0}}}};
 
-// Entry with the largest useful share of the machine: the last round's idle
-// CUs, the padding at the edges, and the entry's rate.  cols counts the
-// kernel's columns (gate and up for the gated block).
-static int pick_tile(int64_t batch, int64_t M, int64_t cols, int first, int last) {
-    int best = last;
-    double top = -1.0;
-    for (int i = first; i <= last; ++i) {
-        const double tiles = (double)batch * (double)cdiv(M, kFfnTiles[i].bm) * (double)cdiv(cols, kFfnTiles[i].bn);
-        const double rounds = ceil(tiles / kNumCUs);
-        const double pad = ((double)batch * (double)M * (double)cols) / (tiles * kFfnTiles[i].bm * kFfnTiles[i].bn);
-        const double score = tiles / (rounds * kNumCUs) * pad * kQuality[i];
-        if (score > top) {
-            top = score;
-            best = i;
+static int type_class(int dtype) { return dtype == MM_FLOAT ? kClass32 : dtype == MM_INT8 ? kClass8 : kClass16; }
+
+static double est_us(int cls, bool aligned, int tile, double wgs, double steps) {
+    const double *step = kStep[aligned ? 0 : 1][cls][tile];
+    const int occ = kOcc[tile];
+    const double per_cu = ceil(wgs / kNumCUs);
+    const double full = floor(per_cu / occ), rest = per_cu - full * occ;
+    double us = kLaunch + full * (kFixed[tile] + step[occ - 1] * steps);
+    if (rest > 0) us += kFixed[tile] + step[(int)rest - 1] * steps;
+    return us;
+}
+
+// Entry and split with the least estimated time for `batch` products of
+// [M, cols] over `kbytes` bytes of K (terms: that many times in one K loop;
+// cols counts gate and up columns).  Partials cost their write, read and a
+// launch.
+static FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t cols, int64_t kbytes, int terms,
+                        unsigned tiles, bool may_split) {
+    FfnChoice best;
+    double top = 1e30;
+    for (int i = 0; i < kNumFfnTiles; ++i) {
+        if (!(tiles >> i & 1)) continue;
+        const FfnTile &t = kFfnTiles[i];
+        const int64_t wgs = batch * cdiv(M, t.bm) * cdiv(cols, t.bn), stages = terms * cdiv(kbytes, t.bkb);
+        int64_t most = 1;
+        if (may_split && i > 0)
+            most = std::max<int64_t>(1, std::min(stages * t.bkb / 512, 2 * kNumCUs / std::max<int64_t>(wgs, 1)));
+        for (int64_t sp = 1; sp <= most; ++sp) {
+            const int64_t per = std::max<int64_t>(1, cdiv(stages, sp)), parts = std::max<int64_t>(1, cdiv(stages, per));
+            if (parts != sp) continue;
+            double us = est_us(cls, aligned, i, (double)(wgs * parts), (double)(per * t.bkb / 32));
+            if (parts > 1) us += 3.0 + (double)parts * (double)batch * (double)M * (double)cols * 8.0 / 3.5e6;
+            if (us < top) {
+                top = us;
+                best.tile = i;
+                best.split = (int32_t)parts;
+                best.kstages = (int32_t)per;
+            }
         }
     }
     return best;
+}
+
+// A requested number of partitions for an entry, as whole stages.
+static void set_split(FfnChoice *c, int64_t kbytes, int terms, int64_t split) {
+    const int64_t stages = std::max<int64_t>(1, terms * cdiv(kbytes, kFfnTiles[c->tile].bkb));
+    const int64_t per = cdiv(stages, std::max<int64_t>(1, std::min<int64_t>(split, stages)));
+    c->kstages = (int32_t)per;
+    c->split = (int32_t)cdiv(stages, per);
 }
 
 static mm_status tile_option(const mm_plan_options *opt, int first, int *tile) {
@@ -56,40 +103,39 @@ static mm_status tile_option(const mm_plan_options *opt, int first, int *tile) {
 static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     const int64_t M = p->kernel_m, N = p->N, K = p->K;
     const int force = opt ? opt->force_algo : MM_ALGO_AUTO;
-    const int sreq = opt ? opt->split_k : 0;
+    const int sreq = opt ? opt->split_k : 0, treq = opt ? opt->tile : 0;
     if (sreq < 0) return fail(MM_ERR_BAD_OPTION, "split_k %d is negative", sreq);
-    const bool rows_ok = p->tb && p->batch == 1 && M <= kFfnRows;
-    p->tile = pick_tile(p->batch, M, N, 0, kNumFfnTiles - 1);
-    mm_status st = tile_option(opt, 0, &p->tile);
-    if (st != MM_OK) return st;
-    const bool tile_forced = opt && opt->tile > 0;
-    int algo = force;
-    if (force == MM_ALGO_SKINNY_M && !rows_ok)
-        return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes one product of at most %d rows with trans_b", kFfnRows);
     if (force != MM_ALGO_AUTO && force != MM_ALGO_SKINNY_M && force != MM_ALGO_GENERAL && force != MM_ALGO_SPLIT_K)
         return fail(MM_ERR_BAD_OPTION, "the scaled INT8 product runs on the skinny-M, general and split-K kernels only");
-    int64_t split = 1;
-    if (force == MM_ALGO_AUTO) algo = rows_ok && !tile_forced && sreq == 0 ? MM_ALGO_SKINNY_M : MM_ALGO_GENERAL;
-    if ((force == MM_ALGO_AUTO && algo == MM_ALGO_GENERAL && sreq == 0) || (force == MM_ALGO_SPLIT_K && sreq == 0)) {
-        const int64_t tiles = p->batch * cdiv(M, kFfnTiles[p->tile].bm) * cdiv(N, kFfnTiles[p->tile].bn);
-        split = std::min<int64_t>(kNumCUs / std::max<int64_t>(tiles, 1), K / 512);
-    } else if (sreq > 0 && force != MM_ALGO_GENERAL) {
-        split = sreq;
+    const bool rows_ok = p->tb && p->batch == 1 && M <= kFfnRows;
+    if (force == MM_ALGO_SKINNY_M && !rows_ok)
+        return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes one product of at most %d rows with trans_b", kFfnRows);
+    int only = -1;
+    mm_status st = tile_option(opt, 0, &only);
+    if (st != MM_OK) return st;
+    if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && treq == 0 && sreq == 0 && K > 0)) {
+        p->algo = MM_ALGO_SKINNY_M;
+        return MM_OK;
     }
-    split = std::max<int64_t>(1, std::min<int64_t>(split, cdiv(K, 128)));
-    if (algo == MM_ALGO_GENERAL && force == MM_ALGO_AUTO && split > 1) algo = MM_ALGO_SPLIT_K;
-    if (K == 0) algo = MM_ALGO_GENERAL;  // the epilogue of an empty sum
-    p->algo = algo;
-    if (algo == MM_ALGO_SKINNY_M) p->tile = -1;
-    if (algo == MM_ALGO_SPLIT_K) {
-        p->kchunk = round_up(cdiv(K, split), 128);
-        p->split = (int32_t)cdiv(K, p->kchunk);
+    // Partials are added by a grid of at most 65535 products.
+    const bool may_split = force != MM_ALGO_GENERAL && K > 0 && p->batch <= 65535;
+    const unsigned all = (1u << kNumFfnTiles) - 1;
+    unsigned tiles = only >= 0 ? 1u << only : all;
+    if (force == MM_ALGO_SPLIT_K || sreq > 1) tiles &= ~1u;  // no 256 x 256 partials
+    if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile 1 does not split K");
+    const bool aligned = (p->tb ? K : N) % 16 == 0 && (p->a_type != MM_INT8 || K % 16 == 0);
+    FfnChoice c = choose(kClass8, aligned, p->batch, M, N, K, 1, tiles, may_split && sreq == 0);
+    if (may_split && sreq > 0) set_split(&c, K, 1, sreq);
+    p->tile = c.tile;
+    p->algo = c.split > 1 || (force == MM_ALGO_SPLIT_K && may_split) ? MM_ALGO_SPLIT_K : MM_ALGO_GENERAL;
+    if (p->algo == MM_ALGO_SPLIT_K) {
+        p->split = c.split;
+        p->kstages = c.kstages;
+        p->kchunk = (int64_t)c.kstages * kFfnTiles[c.tile].bkb;
         p->workspace_bytes = round_up((int64_t)p->split * p->batch * M * N * 4, 256);
     }
-    if (algo != MM_ALGO_SKINNY_M) {
-        const int64_t tiles = p->batch * cdiv(M, kFfnTiles[p->tile].bm) * cdiv(N, kFfnTiles[p->tile].bn);
-        if (tiles * p->split > INT32_MAX) return fail(MM_ERR_TOO_LARGE, "too many workgroups (%lld)", (long long)tiles);
-    }
+    const int64_t wgs = p->batch * cdiv(M, kFfnTiles[p->tile].bm) * cdiv(N, kFfnTiles[p->tile].bn);
+    if (wgs * p->split > INT32_MAX) return fail(MM_ERR_TOO_LARGE, "too many workgroups (%lld)", (long long)wgs);
     return MM_OK;
 }
 
@@ -201,7 +247,7 @@ mm_status mm_scaled_int_execute(mm_plan_t p, const void *A, const void *B, const
     a.sa = quant ? (const float *)(ws + p->qs_off) : a_scale;
     a.sb = b_scale;
     a.bias = bias;
-    a.kchunk = p->kchunk;
+    a.kstages = p->kstages;
     a.split = p->split;
     a.bd = p->bd;
     if (quant) {
@@ -212,7 +258,7 @@ mm_status mm_scaled_int_execute(mm_plan_t p, const void *A, const void *B, const
     if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_scaled_rows(p->dtype, a, s));
     const bool vec = aligned16(a.A[0]) && a.lda % 16 == 0 && aligned16(B) && a.ldb % 16 == 0;
     if (p->algo == MM_ALGO_SPLIT_K) {
-        a.W = (int32_t *)ws;
+        a.W = ws;
         hipError_t e = launch_scaled_split(p->tb != 0, p->tile, vec, a, s);
         if (e == hipSuccess) e = launch_scaled_reduce(p->dtype, a, s);
         return launched(e);
@@ -269,16 +315,30 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         p->algo = MM_ALGO_EMPTY;
     } else {
         const int first = dtype == MM_FLOAT ? 1 : 0;  // no 256 x 256 FLOAT tile
-        p->tile = pick_tile(1, M, 2 * N, first, kNumFfnTiles - 1);
+        const unsigned tiles = (1u << kNumFfnTiles) - (1u << first);
+        const int64_t es = elem_size(dtype);
+        const bool aligned = (K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 && (p->tb || (N * es) % 16 == 0);
+        p->tile = choose(type_class(dtype), aligned, 1, M, 2 * N, K * es, 1, tiles, false).tile;
         st = tile_option(opt, first, &p->tile);
         p->algo = force != MM_ALGO_AUTO ? force
                   : rows_ok && !(opt && opt->tile > 0) ? MM_ALGO_SKINNY_M : MM_ALGO_GENERAL;
         if (p->algo == MM_ALGO_SKINNY_M) p->tile = -1;
     }
-    if (st == MM_OK && p->training && p->out_numel > 0) {
+    if (st == MM_OK && p->training) {
         p->d_pitch = round_up(N, 16 / elem_size(dtype));
         p->d_bytes = round_up(M * p->d_pitch * elem_size(dtype), 256);
-        p->workspace_bytes = 2 * p->d_bytes;
+        const int cls = type_class(dtype);
+        const int64_t es = elem_size(dtype);
+        // dW's reduction runs over the rows of X; a 16-bit 32-row tile of its
+        // transposed operand has rows too short to stage.
+        const unsigned dx_tiles = dtype == MM_FLOAT ? 0xe : 0xf, dw_tiles = dtype == MM_FLOAT ? 0xe : 0x7;
+        const bool dx_al = (p->w_pitch * es) % 16 == 0 && ((p->tb ? K : N) * es) % 16 == 0, dw_al = (K * es) % 16 == 0;
+        p->dx = choose(cls, dx_al, 1, M, K, N * es, 2, dx_tiles, true);
+        p->dw = choose(cls, dw_al, 2, p->tb ? N : K, p->tb ? K : N, M * es, 1, dw_tiles, true);
+        int64_t part = 0;
+        if (p->dx.split > 1) part = (int64_t)p->dx.split * M * K * 4;
+        if (p->dw.split > 1) part = std::max(part, (int64_t)p->dw.split * 2 * K * N * 4);
+        p->workspace_bytes = 2 * p->d_bytes + part;
         st = alloc_workspace(p, true);
     }
     if (st != MM_OK) {
@@ -347,9 +407,7 @@ mm_status mm_glu_backward(mm_plan_t p, const void *X, const void *Wg, const void
         mm_status st = launched(launch_glu_dact(p->dtype, p->act, G, U, dH, dG, dU, M, N, p->d_pitch, s));
         if (st != MM_OK) return st;
     }
-    auto bwd_tile = [&](int64_t batch, int64_t rows, int64_t cols) {
-        return pick_tile(batch, rows, cols, p->dtype == MM_FLOAT ? 1 : 0, 1);
-    };
+    void *part = p->ws ? (char *)p->ws + 2 * p->d_bytes : nullptr;
     const bool w_vec = (p->w_pitch * es) % 16 == 0;
     if (want_x) {
         // dX [M, K] = dG Wg' + dU Wu', the reduction over the hidden features:
@@ -368,10 +426,14 @@ mm_status mm_glu_backward(mm_plan_t p, const void *X, const void *Wg, const void
         a.ldb = p->w_pitch;
         a.ldy = K;
         a.batch = 1;
-        a.split = 1;
         a.y_vec = aligned16(dX) && (K * es) % 16 == 0;
         const bool vec = w_vec && aligned16(Wg) && aligned16(Wu) && ((p->tb ? K : N) * es) % 16 == 0;
-        mm_status st = launched(launch_glu_dx(p->dtype, !p->tb, bwd_tile(1, M, K), vec, a, s));
+        a.W = part;
+        a.split = p->dx.split;
+        a.kstages = p->dx.kstages;
+        hipError_t e = launch_glu_dx(p->dtype, !p->tb, p->dx.tile, a.split > 1, vec, a, s);
+        if (e == hipSuccess && a.split > 1) e = launch_sum_reduce(p->dtype, a, s);
+        mm_status st = launched(e);
         if (st != MM_OK) return st;
     }
     if (want_w) {
@@ -392,10 +454,14 @@ mm_status mm_glu_backward(mm_plan_t p, const void *X, const void *Wg, const void
         a.ldb = std::max<int64_t>(p->tb ? K : p->d_pitch, 1);
         a.ldy = p->w_pitch;
         a.batch = 2;
-        a.split = 1;
         a.y_vec = aligned16(dWg) && aligned16(dWu) && w_vec && (a.N * es) % 16 == 0;
         const bool vec = aligned16(X) && (K * es) % 16 == 0;
-        mm_status st = launched(launch_glu_dw(p->dtype, bwd_tile(2, a.M, a.N), vec, a, s));
+        a.W = part;
+        a.split = p->dw.split;
+        a.kstages = p->dw.kstages;
+        hipError_t e = launch_glu_dw(p->dtype, p->dw.tile, a.split > 1, vec, a, s);
+        if (e == hipSuccess && a.split > 1) e = launch_sum_reduce(p->dtype, a, s);
+        mm_status st = launched(e);
         if (st != MM_OK) return st;
     }
     return MM_OK;
