@@ -328,11 +328,12 @@ mm_status mm_int_execute(mm_plan_t plan, const void *A, const void *B, const voi
  * row or column what IEEE arithmetic makes of it; K == 0 gives the bias (or
  * zeros).
  *
- * Options: force_algo SKINNY_M (a folded product of at most 32 rows with
- * trans_b), GENERAL or SPLIT_K; tile k >= 1 is entry k of 256 x 256, 128 x
+ * Options: force_algo SKINNY_M (one product, after folding, of at most 32
+ * rows), GENERAL or SPLIT_K; tile k >= 1 is entry k of 256 x 256, 128 x
  * 128, 64 x 128, 32 x 128; split_k as for MatMul.  A plan with an A to
- * quantize or a split K owns a workspace: its executions must not overlap,
- * and it is allocated and bound to a device as described above.  Other errors
+ * quantize or a split K may own a workspace (mm_plan_workspace_bytes > 0):
+ * its executions must then not overlap, and it is allocated and bound to a
+ * device as described above.  Other errors
  * are those of mm_plan_create. */
 typedef struct mm_scaled_int_desc {
     int32_t a_type;   /* MM_INT8, or the type of an A to be quantized */
@@ -386,7 +387,7 @@ mm_status mm_quantize_rows(const void *X, int dtype, int64_t rows, int64_t cols,
  * cores.  relu's derivative at 0 is 0.  Infinities and NaN follow the
  * formulas.
  *
- * Options: force_algo SKINNY_M (at most 32 rows, trans_w) or GENERAL; tile
+ * Options: force_algo SKINNY_M (at most 32 rows) or GENERAL; tile
  * k >= 1 is entry k of 256 x 256 (16-bit types), 128 x 128, 64 x 128, 32 x
  * 128 for the forward pass (columns count gate and up); the backward pass
  * takes the first two, and the second for the others. */

@@ -459,32 +459,44 @@ class IntPlan(Plan):
                              a_zp.data_ptr() if a_zp is not None else 0, b_zp.data_ptr() if b_zp is not None else 0)
 
 
-def _require(tensors, device) -> None:
-    """Each (name, tensor, dtype, shape) dense, on `device`."""
-    for name, t, want, shape in tensors:
-        if t.dtype != want or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {want} tensor of shape {tuple(shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the output on {device}")
+def _wrong(name, t, dt, shape, dev) -> None:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the output on GPU {dev}")
+    raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)}")
 
 
-def _launch(device, stream, call) -> None:
-    """call(raw stream) with `device` current; stream defaults to its current stream."""
+def _dense(name, t, dt, shape, dev) -> int:
+    """t's address, if it is dense, of that type and shape, on GPU `dev`."""
+    if t.dtype is not dt or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _wrong(name, t, dt, shape, dev)
+    return t.data_ptr()
+
+
+def _device_of(t) -> int:
+    """The index of the GPU that holds the output t."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be device tensors")
+    return dev
+
+
+def _run(dev, stream, fn, *args) -> None:
+    """fn(*args, raw stream) with GPU `dev` current; stream defaults to its current stream."""
     import torch
 
-    if device.type != "cuda":
-        raise ValueError("the tensors must be device tensors")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        _check(call(stream.cuda_stream))
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _run(dev, stream, fn, *args)
+    if stream is not None:
+        raw = stream.cuda_stream
     else:
-        with torch.cuda.device(device):
-            _check(call(stream.cuda_stream))
-
-
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+        # The handle alone where torch offers it: building the Stream object
+        # takes 1 us of the call's 6.
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        raw = get(dev) if get else torch.cuda.current_stream(dev).cuda_stream
+    st = fn(*args, raw)
+    if st:
+        _check(st)
 
 
 def quantize_rows(X, q=None, scale=None, stream=None):
@@ -499,14 +511,15 @@ def quantize_rows(X, q=None, scale=None, stream=None):
         q = torch.empty(X.shape, dtype=torch.int8, device=X.device)
     if scale is None:
         scale = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
-    _require((("X", X, X.dtype, X.shape), ("q", q, torch.int8, X.shape),
-              ("scale", scale, torch.float32, X.shape[:-1])), X.device)
+    dev = _device_of(X)
+    xp = _dense("X", X, X.dtype, X.shape, dev)
+    qp = _dense("q", q, torch.int8, X.shape, dev)
+    sp = _dense("scale", scale, torch.float32, X.shape[:-1], dev)
     cols = X.shape[-1]
     rows = 1
     for d in X.shape[:-1]:
         rows *= d
-    _launch(X.device, stream, lambda s: lib().mm_quantize_rows(X.data_ptr(), code, rows, cols, q.data_ptr(),
-                                                               scale.data_ptr(), s))
+    _run(dev, stream, lib().mm_quantize_rows, xp, code, rows, cols, qp, sp)
     return q, scale
 
 
@@ -531,6 +544,8 @@ class ScaledIntPlan(Plan):
                                            len(self.b_shape), ctypes.byref(desc), ctypes.byref(opt),
                                            ctypes.byref(self._handle)))
         self._lock = threading.Lock()
+        self._execute = L.mm_scaled_int_execute
+        self._i8, self._f32 = torch.int8, torch.float32
         self._a_dt, self._out_dt = torch_dtype(self.a_type), torch_dtype(self.dtype)
         self._y_shape = torch.Size(self.output_shape)
         n = 1 if len(self.b_shape) == 1 else self.b_shape[-2 if self.trans_b else -1]
@@ -545,9 +560,6 @@ class ScaledIntPlan(Plan):
     def execute(self, A, B, Y, a_scale=None, b_scale=None, bias=None, stream=None) -> None:
         """a_scale: FP32, A's shape without K (None where the plan quantizes
         A); b_scale: FP32, B's batch dimensions and N; bias: N values of Y's type."""
-        import torch
-
-        f32 = torch.float32
         if (a_scale is None) != (self.a_type != INT8):
             raise ValueError("a_scale: " + ("the plan quantizes A itself" if a_scale is not None
                                             else "an INT8 A needs its scales"))
@@ -555,16 +567,15 @@ class ScaledIntPlan(Plan):
             raise ValueError("b_scale is missing")
         if (bias is None) == self.bias:
             raise ValueError("bias: the plan has " + ("one" if self.bias else "none"))
-        checks = [("A", A, self._a_dt, self.a_shape), ("B", B, torch.int8, self.b_shape),
-                  ("Y", Y, self._out_dt, self._y_shape), ("b_scale", b_scale, f32, self.b_scale_shape)]
-        if a_scale is not None:
-            checks.append(("a_scale", a_scale, f32, self.a_scale_shape))
-        if bias is not None:
-            checks.append(("bias", bias, self._out_dt, self._bias_shape))
-        _require(checks, Y.device)
+        dev = _device_of(Y)
+        ap = _dense("A", A, self._a_dt, self.a_shape, dev)
+        bp = _dense("B", B, self._i8, self.b_shape, dev)
+        yp = _dense("Y", Y, self._out_dt, self._y_shape, dev)
+        bsp = _dense("b_scale", b_scale, self._f32, self.b_scale_shape, dev)
+        asp = None if a_scale is None else _dense("a_scale", a_scale, self._f32, self.a_scale_shape, dev)
+        biasp = None if bias is None else _dense("bias", bias, self._out_dt, self._bias_shape, dev)
         with self._lock:
-            _launch(Y.device, stream, lambda s: lib().mm_scaled_int_execute(
-                self._handle, A.data_ptr(), B.data_ptr(), _ptr(a_scale), b_scale.data_ptr(), _ptr(bias), Y.data_ptr(), s))
+            _run(dev, stream, self._execute, self._handle, ap, bp, asp, bsp, biasp, yp)
 
 
 class GluPlan(Plan):
@@ -592,17 +603,17 @@ class GluPlan(Plan):
         self._h = torch.Size((self.rows, self.hidden))
         self._w = torch.Size((self.hidden, self.in_features) if self.trans_w else (self.in_features, self.hidden))
         self._pitch = int(w_pitch) or self._w[1]
+        self._execute, self._backward = L.mm_glu_execute, L.mm_glu_backward
 
-    def _require_weights(self, tensors, device) -> None:
-        for name, t in tensors:
-            ok = t.dtype == self._dt and t.shape == self._w
-            if ok and t.numel():
-                ok = (t.stride(1) == 1 or t.shape[1] == 1) and (t.stride(0) == self._pitch or t.shape[0] == 1)
-            if not ok:
-                raise ValueError(f"{name} must be a {self._dt} tensor of shape {tuple(self._w)} with rows "
-                                 f"{self._pitch} elements apart")
-            if t.device != device:
-                raise ValueError(f"{name} is on {t.device}, the others on {device}")
+    def _weight(self, name, t, dev) -> int:
+        """t's address, if it is a weight of this plan on GPU `dev`."""
+        ok = t.dtype is self._dt and t.shape == self._w and t.get_device() == dev
+        if ok and not (t.is_contiguous() and self._pitch == self._w[1]) and t.numel():
+            ok = (t.stride(1) == 1 or t.shape[1] == 1) and (t.stride(0) == self._pitch or t.shape[0] == 1)
+        if not ok:
+            raise ValueError(f"{name} must be a {self._dt} tensor of shape {tuple(self._w)} with rows {self._pitch} "
+                             f"elements apart on the output's GPU")
+        return t.data_ptr()
 
     def execute_ptr(self, X: int, Wg: int, Wu: int, H: int, G: int = 0, U: int = 0, stream: int = 0) -> None:
         _check(lib().mm_glu_execute(self._handle, X, Wg, Wu, H, G, U, stream))
@@ -611,33 +622,29 @@ class GluPlan(Plan):
         """The forward pass; G and U (both or neither) keep X Wg and X Wu."""
         if (G is None) != (U is None):
             raise ValueError("G and U are given together or not at all")
-        dt = self._dt
-        checks = [("X", X, dt, self._x), ("H", H, dt, self._h)]
-        if G is not None:
-            checks += [("G", G, dt, self._h), ("U", U, dt, self._h)]
-        _require(checks, H.device)
-        self._require_weights((("Wg", Wg), ("Wu", Wu)), H.device)
+        dt, h = self._dt, self._h
+        dev = _device_of(H)
+        xp = _dense("X", X, dt, self._x, dev)
+        gp, up = self._weight("Wg", Wg, dev), self._weight("Wu", Wu, dev)
+        hp = _dense("H", H, dt, h, dev)
+        kg = None if G is None else _dense("G", G, dt, h, dev)
+        ku = None if U is None else _dense("U", U, dt, h, dev)
         with self._lock:
-            _launch(H.device, stream, lambda s: lib().mm_glu_execute(
-                self._handle, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), H.data_ptr(), _ptr(G), _ptr(U), s))
+            _run(dev, stream, self._execute, self._handle, xp, gp, up, hp, kg, ku)
 
     def backward(self, X, Wg, Wu, G, U, dH, dX=None, dWg=None, dWu=None, stream=None) -> None:
         """The backward pass into dX and / or dWg and dWu (overwritten)."""
         if (dWg is None) != (dWu is None):
             raise ValueError("dWg and dWu are given together or not at all")
-        dt = self._dt
-        checks = [("X", X, dt, self._x), ("G", G, dt, self._h), ("U", U, dt, self._h), ("dH", dH, dt, self._h)]
-        weights = [("Wg", Wg), ("Wu", Wu)]
-        if dX is not None:
-            checks.append(("dX", dX, dt, self._x))
-        if dWg is not None:
-            weights += [("dWg", dWg), ("dWu", dWu)]
-        _require(checks, dH.device)
-        self._require_weights(weights, dH.device)
+        dt, h = self._dt, self._h
+        dev = _device_of(dH)
+        ptrs = (_dense("X", X, dt, self._x, dev), self._weight("Wg", Wg, dev), self._weight("Wu", Wu, dev),
+                _dense("G", G, dt, h, dev), _dense("U", U, dt, h, dev), _dense("dH", dH, dt, h, dev),
+                None if dX is None else _dense("dX", dX, dt, self._x, dev),
+                None if dWg is None else self._weight("dWg", dWg, dev),
+                None if dWu is None else self._weight("dWu", dWu, dev))
         with self._lock:
-            _launch(dH.device, stream, lambda s: lib().mm_glu_backward(
-                self._handle, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), G.data_ptr(), U.data_ptr(), dH.data_ptr(),
-                _ptr(dX), _ptr(dWg), _ptr(dWu), s))
+            _run(dev, stream, self._backward, self._handle, *ptrs)
 
 
 _plan_cache = {}

@@ -1,7 +1,8 @@
 // activation.h -- the gated block's activations f and their derivatives, in
 // FP32.  Each is written so that neither tail cancels: the sigmoid and its
-// complement come from one exponential of -|x|, gelu from erfc, and the tanh
-// form of gelu from (1 + tanh z) / 2 = sigmoid(2 z).
+// complement come from one exponential of -|x|, the tanh form of gelu from
+// (1 + tanh z) / 2 = sigmoid(2 z), and gelu from the normal distribution's
+// tail, whose exponential is also the density that the derivative needs.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -24,6 +25,51 @@ __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &c) {
     if (x != x) s = c = x;
 }
 
+// Normal distribution at g: P = Phi(g) and its density D.  The tail is
+//   1 - Phi(|g|) = exp(-g^2 / 2) e(|g| / sqrt 2) / 2,  e(z) = exp(z^2) erfc(z),
+// and e is smooth in q = 1 / (1 + p z): e(z) = q (c0 + c1 q + ...), fitted here
+// by least squares on Chebyshev points, reweighted towards the least largest
+// relative error over 0 <= z <= 14 (past that the tail is below FP32):
+// 2.7e-6 with 7 coefficients, a hundredth of an FP16 half step; EXACT: 1.0e-8
+// with 10, and the rounding of g^2 is put back into the exponential.  (The
+// library's erfc cost about as much as the matrix work of a 1024-long K.)
+template <bool EXACT>
+__device__ __forceinline__ void normal_pair(float g, float &P, float &D) {
+    const float a = fminf(fabsf(g), 40.0f);
+    const float z = a * 0.70710678118654752f;
+    const float h = a * a;
+    float e, x;
+    if constexpr (EXACT) {
+        const float q = 1.0f / (1.0f + 0.35f * z);
+        e = 4.184608091e-02f;
+        e = e * q - 1.779090892e-01f;
+        e = e * q + 2.267881683e-01f;
+        e = e * q - 8.915867565e-02f;
+        e = e * q + 1.390371659e-01f;
+        e = e * q + 1.175938350e-01f;
+        e = e * q + 1.612167270e-01f;
+        e = e * q + 1.857080195e-01f;
+        e = e * q + 1.974081938e-01f;
+        e = e * q + 1.974695846e-01f;
+        e *= q;
+        x = expf(-0.5f * h) * (1.0f - 0.5f * fmaf(a, a, -h));
+    } else {
+        const float q = __builtin_amdgcn_rcpf(1.0f + 0.5f * z);
+        e = 8.212535751e-02f;
+        e = e * q - 3.356935106e-01f;
+        e = e * q + 3.603833506e-01f;
+        e = e * q + 5.776401879e-02f;
+        e = e * q + 2.743037532e-01f;
+        e = e * q + 2.788714043e-01f;
+        e = e * q + 2.822429085e-01f;
+        e *= q;
+        x = __expf(-0.5f * h);
+    }
+    const float tail = 0.5f * e * x;
+    P = g >= 0.0f ? 1.0f - tail : tail;
+    D = x * 0.3989422804014327f;
+}
+
 constexpr float kGeluC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
@@ -33,7 +79,8 @@ __device__ __forceinline__ float act_value(float g) {
     if constexpr (ACT == MM_ACT_RELU) {
         return g > 0.0f || g != g ? g : 0.0f;
     } else if constexpr (ACT == MM_ACT_GELU) {
-        return g * (0.5f * erfcf(g * -0.70710678118654752f));
+        normal_pair<EXACT>(g, s, c);
+        return g * s;
     } else if constexpr (ACT == MM_ACT_GELU_TANH) {
         sigmoid_pair<EXACT>(kGeluC * (g + kGeluA * g * g * g), s, c);
         return g * s;
@@ -52,10 +99,9 @@ __device__ __forceinline__ void act_grad(float g, float &f, float &d) {
         f = on || g != g ? g : 0.0f;
         d = on ? 1.0f : 0.0f;
     } else if constexpr (ACT == MM_ACT_GELU) {
-        const float p = 0.5f * erfcf(g * -0.70710678118654752f);
-        const float q = EXACT ? expf(-0.5f * g * g) : __expf(-0.5f * g * g);
-        f = g * p;
-        d = p + g * q * 0.3989422804014327f;
+        normal_pair<EXACT>(g, s, c);
+        f = g * s;
+        d = s + g * c;
     } else if constexpr (ACT == MM_ACT_GELU_TANH) {
         sigmoid_pair<EXACT>(kGeluC * (g + kGeluA * g * g * g), s, c);
         f = g * s;
@@ -73,9 +119,14 @@ __device__ __forceinline__ void act_grad(float g, float &f, float &d) {
 }
 
 // INT8 product's epilogue: the exact integer sum, rounded to FP32 once (the
-// sum can need 31 bits), times the scales, plus the bias.
+// sum can need 31 bits), times the scales, plus the bias.  The operations are
+// spelled out, and the FP32 result kept apart from the narrowing (which the
+// compiler else merges into the last operation here and there, rounding once
+// where other kernels round twice), so that every kernel gives the same bits.
 __device__ __forceinline__ float scaled_value(int acc, float sa, float sb, float bias) {
-    return (float)acc * sa * sb + bias;
+    float y = fmaf((float)acc * sa, sb, bias);
+    asm("" : "+v"(y));
+    return y;
 }
 
 }  // namespace mm

@@ -51,10 +51,14 @@ hipError_t launch_sum_reduce(int dtype, const FfnArgs &a, hipStream_t s);
 hipError_t launch_scaled(int out_dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);
 hipError_t launch_scaled_split(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);
 hipError_t launch_scaled_reduce(int out_dtype, const FfnArgs &a, hipStream_t s);
-// Few-row kernels (weights stored [N, K], any alignment, at most kFfnRows rows).
+// Few-row kernels (any alignment, at most kFfnRows rows, one product).
+// rows_quantize: whether the scaled one takes A in its own type and quantizes
+// it itself (`quant`); its INT8 rows then fit kFfnQuantLds bytes of LDS.
 constexpr int kFfnRows = 32;
-hipError_t launch_glu_rows(int dtype, const FfnArgs &a, hipStream_t s);
-hipError_t launch_scaled_rows(int out_dtype, const FfnArgs &a, hipStream_t s);
+constexpr int kFfnQuantLds = 48 * 1024;
+hipError_t launch_glu_rows(int dtype, bool tb, const FfnArgs &a, hipStream_t s);
+bool rows_quantize(int a_type, int out_dtype, int64_t M, int64_t K);
+hipError_t launch_scaled_rows(int out_dtype, bool tb, bool quant, const FfnArgs &a, hipStream_t s);
 // Row quantization of a dense [rows, cols] matrix into rows of ldq bytes; the
 // bytes past cols are set to zero.
 hipError_t launch_quantize_rows(int dtype, const void *X, int64_t rows, int64_t cols, void *Q, int64_t ldq, float *scale,

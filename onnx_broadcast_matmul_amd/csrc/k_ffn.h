@@ -29,6 +29,7 @@
 #include "activation.h"
 #include "device.h"
 #include "ffn.h"
+#include "pieces.h"
 
 namespace mm {
 
@@ -367,12 +368,11 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
         // read on into the next rows (where the matrix goes on for that long);
         // both reach only outputs that are not stored.  The last stage may
         // neither read past the matrix nor bring in values past K.
-        auto gather = [&](auto kc_t, auto cpr_t, auto count_t, const char *base, int64_t ld, int64_t left_mn, int64_t k0, uint4 *out) {
+        auto gather = [&](auto kc_t, auto cpr_t, auto count_t, const char *base, int64_t ld, int64_t left_mn,
+                          int64_t row_len, int64_t k0, uint4 *out) {
             constexpr bool KC = decltype(kc_t)::value;
             constexpr int CPR = decltype(cpr_t)::value, COUNT = decltype(count_t)::value;
-            typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
-            typedef const __attribute__((address_space(1))) S *gptr;
-            const gptr g = (gptr)base;
+            const GlobalPtr<S> g = (GlobalPtr<S>)base;
             const int64_t krem = kend - k0;
             const bool whole = krem >= BK && (KC || left_mn >= (int64_t)CPR * VE || (krem - BK) * ld >= VE);
             if (whole) {
@@ -389,7 +389,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
                         // Columns wholly past the matrix: its first ones.
                         at = (k0 + row) * ld + (c * VE < left_mn ? c * VE : 0);
                     }
-                    out[i] = __builtin_bit_cast(uint4, *(const __attribute__((address_space(1))) u32x4u *)(g + at));
+                    out[i] = whole_piece<S>(g + at);
                 }
             } else {
 #pragma unroll
@@ -399,15 +399,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
                     const int c = (y % CPR) ^ (KC ? aswz(row) : row_swizzle<ES>(row, CPR));
                     const int64_t left = KC ? (row < left_mn ? krem - c * VE : 0) : (row < krem ? left_mn - c * VE : 0);
                     const int64_t at = KC ? (int64_t)row * ld + k0 + c * VE : (k0 + row) * ld + c * VE;
-                    S tmp[VE];
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) tmp[e] = e < left ? g[at + e] : (S)0;
-                    uint4 v;
-                    __builtin_memcpy(&v, tmp, 16);
-                    // Bytes are packed here: otherwise the whole stages' words
-                    // are taken apart and packed again where the paths meet.
-                    if constexpr (ES == 1) asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
-                    out[i] = v;
+                    out[i] = row_piece<S>(g + at, left, row_len >= VE);
                 }
             }
         };
@@ -415,11 +407,11 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
             const int64_t k0 = stage_k0(st);
             const bool second = stage_second(st);
             gather(std::integral_constant<bool, !TA>(), std::integral_constant<int, TA ? CPRA : CA>(),
-                   std::integral_constant<int, AC>(), second ? At1 : At0, a.lda, M - m0, k0, rga);
+                   std::integral_constant<int, AC>(), second ? At1 : At0, a.lda, M - m0, TA ? M : K, k0, rga);
 #pragma unroll
             for (int p = 0; p < NPAN; ++p)
                 gather(std::integral_constant<bool, TB>(), std::integral_constant<int, TB ? CA : CPRB>(),
-                       std::integral_constant<int, BC>(), second || p == 1 ? Bt1 : Bt0, a.ldb, N - n0, k0, rgb[p]);
+                       std::integral_constant<int, BC>(), second || p == 1 ? Bt1 : Bt0, a.ldb, N - n0, TB ? K : N, k0, rgb[p]);
         };
         auto store = [&](int st) {
             char *sb = lds + (st % STAGES) * STAGE_BYTES;

@@ -69,6 +69,7 @@ struct mm_plan_s {
     // q_off), then its scales (at qs_off); split partials lie before it.
     bool is_scaled = false;
     bool has_bias = false;
+    bool fused_quant = false;  // the few-row kernel quantizes A itself
     int64_t a_rows = 0;  // rows of the whole A tensor
     int64_t q_pitch = 0, q_off = 0, qs_off = 0;
 

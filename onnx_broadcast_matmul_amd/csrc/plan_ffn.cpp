@@ -107,13 +107,22 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     if (sreq < 0) return fail(MM_ERR_BAD_OPTION, "split_k %d is negative", sreq);
     if (force != MM_ALGO_AUTO && force != MM_ALGO_SKINNY_M && force != MM_ALGO_GENERAL && force != MM_ALGO_SPLIT_K)
         return fail(MM_ERR_BAD_OPTION, "the scaled INT8 product runs on the skinny-M, general and split-K kernels only");
-    const bool rows_ok = p->tb && p->batch == 1 && M <= kFfnRows;
+    const bool rows_ok = p->batch == 1 && M <= kFfnRows;
     if (force == MM_ALGO_SKINNY_M && !rows_ok)
-        return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes one product of at most %d rows with trans_b", kFfnRows);
+        return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes one product of at most %d rows", kFfnRows);
     int only = -1;
     mm_status st = tile_option(opt, 0, &only);
     if (st != MM_OK) return st;
-    if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && treq == 0 && sreq == 0 && K > 0)) {
+    // Few rows: the rows kernel streams the weights once.  [K, N] weights
+    // give it a workgroup per 64 columns, each a chain of K at 18 GB/s, so a
+    // long K goes to split tiles unless the columns fill the CUs (M = 1, K =
+    // 11008, N = 4096: 38.8 against 18.3 us; K = 4096, N = 11008: 14.0 against
+    // 17.1 us).  Past 16 rows it
+    // re-reads X twice as much and wide products fill the tiles (M = 32, K =
+    // 4096: 21.3 against 18.7 us at N = 11008, 9.0 against 13.0 at 4096).
+    const bool rows_best = rows_ok && K > 0 && (p->tb || K <= 2048 || (K <= 4096 && N >= 8192)) &&
+                           (M <= 16 || N < 8192);
+    if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_best && treq == 0 && sreq == 0)) {
         p->algo = MM_ALGO_SKINNY_M;
         return MM_OK;
     }
@@ -181,7 +190,9 @@ mm_status mm_scaled_int_plan_create(const int64_t *a_shape, int a_rank, const in
         p->algo = MM_ALGO_EMPTY;
     } else if (st == MM_OK) {
         st = select_scaled(p, opt);
-        if (st == MM_OK && p->a_type != MM_INT8) {
+        p->fused_quant = p->a_type != MM_INT8 && p->algo == MM_ALGO_SKINNY_M &&
+                         rows_quantize(p->a_type, p->dtype, p->kernel_m, p->K);
+        if (st == MM_OK && p->a_type != MM_INT8 && !p->fused_quant) {
             p->a_rows = 1;
             for (int i = 0; i + 1 < a_rank; ++i) p->a_rows *= a_shape[i];
             p->q_pitch = round_up(p->K, 16);
@@ -218,7 +229,7 @@ mm_status mm_scaled_int_execute(mm_plan_t p, const void *A, const void *B, const
     if (!p) return fail(MM_ERR_NULL_ARG, "plan is NULL");
     if (!p->is_scaled) return fail(MM_ERR_BAD_OPTION, "not a scaled INT8 plan");
     if (p->algo == MM_ALGO_EMPTY) return MM_OK;
-    const bool quant = p->a_type != MM_INT8;
+    const bool quant = p->a_type != MM_INT8, pass = quant && !p->fused_quant;
     if (!Y) return fail(MM_ERR_NULL_ARG, "Y is NULL for a non-empty output");
     if (p->K > 0 && (!A || !B)) return fail(MM_ERR_NULL_ARG, "A or B is NULL");
     if (!b_scale || (!quant && !a_scale)) return fail(MM_ERR_NULL_ARG, "a scale is NULL");
@@ -233,29 +244,29 @@ mm_status mm_scaled_int_execute(mm_plan_t p, const void *A, const void *B, const
     char *ws = (char *)p->ws;
     FfnArgs a;
     memset(&a, 0, sizeof(a));
-    a.A[0] = quant ? ws + p->q_off : A;
+    a.A[0] = pass ? ws + p->q_off : A;
     a.B[0] = B;
     a.Y[0] = Y;
     a.M = p->kernel_m;
     a.N = p->N;
     a.K = p->K;
-    a.lda = std::max<int64_t>(quant ? p->q_pitch : p->K, 1);
+    a.lda = std::max<int64_t>(pass ? p->q_pitch : p->K, 1);
     a.ldb = p->tb ? p->K : p->N;
     a.ldy = p->N;
     a.batch = p->batch;
     a.y_vec = aligned16(Y) && (p->N * elem_size(p->dtype)) % 16 == 0;
-    a.sa = quant ? (const float *)(ws + p->qs_off) : a_scale;
+    a.sa = pass ? (const float *)(ws + p->qs_off) : a_scale;
     a.sb = b_scale;
     a.bias = bias;
     a.kstages = p->kstages;
     a.split = p->split;
     a.bd = p->bd;
-    if (quant) {
+    if (pass) {
         mm_status st = launched(launch_quantize_rows(p->a_type, A, p->a_rows, p->K, ws + p->q_off, p->q_pitch,
                                                      (float *)(ws + p->qs_off), s));
         if (st != MM_OK) return st;
     }
-    if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_scaled_rows(p->dtype, a, s));
+    if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_scaled_rows(p->dtype, p->tb != 0, p->fused_quant, a, s));
     const bool vec = aligned16(a.A[0]) && a.lda % 16 == 0 && aligned16(B) && a.ldb % 16 == 0;
     if (p->algo == MM_ALGO_SPLIT_K) {
         a.W = ws;
@@ -288,11 +299,11 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
     if (M > INT32_MAX || K > INT32_MAX || N > INT32_MAX || d->w_pitch > INT32_MAX)
         return fail(MM_ERR_TOO_LARGE, "rows, in_features, hidden and w_pitch must each be below 2^31");
     const int force = opt ? opt->force_algo : MM_ALGO_AUTO;
-    const bool rows_ok = d->trans_w && M <= kFfnRows;
+    const bool rows_ok = M <= kFfnRows;
     if (force != MM_ALGO_AUTO && force != MM_ALGO_GENERAL && force != MM_ALGO_SKINNY_M)
         return fail(MM_ERR_BAD_OPTION, "the gated block runs on the skinny-M and general kernels only");
     if (force == MM_ALGO_SKINNY_M && !rows_ok)
-        return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes at most %d rows with trans_w", kFfnRows);
+        return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes at most %d rows", kFfnRows);
     if (opt && opt->split_k != 0) return fail(MM_ERR_BAD_OPTION, "the gated block does not split K");
     mm_plan_s *p = new (std::nothrow) mm_plan_s();
     if (!p) return fail(MM_ERR_ALLOC, "host allocation failed");
@@ -320,8 +331,13 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         const bool aligned = (K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 && (p->tb || (N * es) % 16 == 0);
         p->tile = choose(type_class(dtype), aligned, 1, M, 2 * N, K * es, 1, tiles, false).tile;
         st = tile_option(opt, first, &p->tile);
-        p->algo = force != MM_ALGO_AUTO ? force
-                  : rows_ok && !(opt && opt->tile > 0) ? MM_ALGO_SKINNY_M : MM_ALGO_GENERAL;
+        // Few rows: the rows kernel, except where 32-row tiles fill most CUs
+        // with a long K and it has the dearer access: [K, N] weights (M = 1,
+        // K = 4096, N = 11008: 55.0 against 49.3 us) or more than 16 rows (M =
+        // 32: 56.9 against 48.0 us; at K = N = 4096 18.2 against 30.0 us).
+        const bool tiles_fill = cdiv(N, 64) >= 160 && K * es >= 8192;
+        const bool rows_best = rows_ok && !(tiles_fill && (!p->tb || M > 16));
+        p->algo = force != MM_ALGO_AUTO ? force : rows_best && !(opt && opt->tile > 0) ? MM_ALGO_SKINNY_M : MM_ALGO_GENERAL;
         if (p->algo == MM_ALGO_SKINNY_M) p->tile = -1;
     }
     if (st == MM_OK && p->training) {
@@ -378,7 +394,7 @@ mm_status mm_glu_execute(mm_plan_t p, const void *X, const void *Wg, const void 
     a.split = 1;
     a.act = p->act;
     a.y_vec = aligned16(H) && aligned16(G) && aligned16(U) && (p->N * es) % 16 == 0;
-    if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_glu_rows(p->dtype, a, s));
+    if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_glu_rows(p->dtype, p->tb != 0, a, s));
     const bool vec = aligned16(X) && aligned16(Wg) && aligned16(Wu) && (p->K * es) % 16 == 0 &&
                      (p->w_pitch * es) % 16 == 0 && (p->tb || (p->N * es) % 16 == 0);
     return launched(launch_glu_fwd(p->dtype, p->tb != 0, p->tile, vec, a, s));
