@@ -34,7 +34,7 @@ struct FfnArgs {
 struct FfnTile {
     int bm, bn, bkb;
 };
-constexpr FfnTile kFfnTiles[] = {{256, 256, 64}, {128, 128, 64}, {64, 128, 128}, {32, 128, 256}};
+constexpr FfnTile kFfnTiles[] = {{256, 256, 64}, {128, 128, 64}, {64, 128, 128}, {32, 128, 256}, {256, 128, 128}};
 constexpr int kNumFfnTiles = sizeof(kFfnTiles) / sizeof(kFfnTiles[0]);
 
 // Element-wise part of the gated block's backward pass: dG = dH * U * f'(G),

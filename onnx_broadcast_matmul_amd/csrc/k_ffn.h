@@ -631,6 +631,9 @@ static hipError_t launch_entry(int tile, bool vec, const FfnArgs &a, hipStream_t
         // A 32-row tile of a transposed 16-bit A has rows too short to stage.
         if constexpr (!TA || DT == MM_FLOAT) return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 32, 128, 1, 2, 4, 256, 3, 8>(vec, a, s);
         break;
+    case 4:
+        if constexpr (DT != MM_FLOAT) return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 256, 128, 4, 2, 1, 128, 3, 4>(vec, a, s);
+        break;
     }
     return hipErrorInvalidValue;
 }

@@ -28,16 +28,16 @@ static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == 
 // which lie within 10 % of each other; rows that are not 16-byte aligned run
 // the register-staged form (entry 0 has none and runs entry 1's).
 enum { kClass16 = 0, kClass8 = 1, kClass32 = 2 };
-static const int kOcc[kNumFfnTiles] = {1, 2, 2, 1};
-static const double kLaunch = 2.5;                                 // us
-static const double kFixed[kNumFfnTiles] = {7.0, 3.2, 2.5, 2.0};  // us
-static const double kStep[2][3][kNumFfnTiles][2] = {               // us: aligned, not aligned
-    {{{0.44, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}},
-     {{0.42, 0}, {0.17, 0.285}, {0.145, 0.160}, {0.095, 0}},
-     {{1e9, 0}, {0.54, 0.970}, {0.260, 0.490}, {0.148, 0}}},
-    {{{1e9, 0}, {0.29, 0.340}, {0.150, 0.195}, {0.110, 0}},
-     {{1e9, 0}, {0.30, 0.355}, {0.175, 0.195}, {0.090, 0}},
-     {{1e9, 0}, {0.78, 1.160}, {0.400, 0.610}, {0.200, 0}}}};
+static const int kOcc[kNumFfnTiles] = {1, 2, 2, 1, 1};
+static const double kLaunch = 2.5;                                      // us
+static const double kFixed[kNumFfnTiles] = {7.5, 3.2, 2.5, 2.0, 5.5};  // us
+static const double kStep[2][3][kNumFfnTiles][2] = {                    // us: aligned, not aligned
+    {{{0.41, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.240, 0}},
+     {{0.41, 0}, {0.17, 0.285}, {0.145, 0.160}, {0.095, 0}, {0.222, 0}},
+     {{1e9, 0}, {0.54, 0.970}, {0.260, 0.490}, {0.148, 0}, {1e9, 0}}},
+    {{{1e9, 0}, {0.29, 0.340}, {0.150, 0.195}, {0.110, 0}, {0.300, 0}},
+     {{1e9, 0}, {0.30, 0.355}, {0.175, 0.195}, {0.090, 0}, {0.300, 0}},
+     {{1e9, 0}, {0.78, 1.160}, {0.400, 0.610}, {0.200, 0}, {1e9, 0}}}};
 
 static int type_class(int dtype) { return dtype == MM_FLOAT ? kClass32 : dtype == MM_INT8 ? kClass8 : kClass16; }
 
@@ -90,11 +90,11 @@ static void set_split(FfnChoice *c, int64_t kbytes, int terms, int64_t split) {
     c->split = (int32_t)cdiv(stages, per);
 }
 
-static mm_status tile_option(const mm_plan_options *opt, int first, int *tile) {
+static mm_status tile_option(const mm_plan_options *opt, int *tile) {
     const int req = opt ? opt->tile : 0;
     if (req == 0) return MM_OK;
-    if (req - 1 < first || req > kNumFfnTiles)
-        return fail(MM_ERR_BAD_OPTION, "tile %d out of range %d..%d", req, first + 1, kNumFfnTiles);
+    if (req < 0 || req > kNumFfnTiles)
+        return fail(MM_ERR_BAD_OPTION, "tile %d out of range 1..%d", req, kNumFfnTiles);
     *tile = req - 1;
     return MM_OK;
 }
@@ -111,7 +111,7 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     if (force == MM_ALGO_SKINNY_M && !rows_ok)
         return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes one product of at most %d rows", kFfnRows);
     int only = -1;
-    mm_status st = tile_option(opt, 0, &only);
+    mm_status st = tile_option(opt, &only);
     if (st != MM_OK) return st;
     // Few rows: the rows kernel streams the weights once.  [K, N] weights
     // give it a workgroup per 64 columns, each a chain of K at 18 GB/s, so a
@@ -325,12 +325,12 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
     if (p->out_numel == 0) {
         p->algo = MM_ALGO_EMPTY;
     } else {
-        const int first = dtype == MM_FLOAT ? 1 : 0;  // no 256 x 256 FLOAT tile
-        const unsigned tiles = (1u << kNumFfnTiles) - (1u << first);
+                const unsigned tiles = dtype == MM_FLOAT ? 0xe : 0x1f;  // FLOAT has the three smaller entries
         const int64_t es = elem_size(dtype);
         const bool aligned = (K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 && (p->tb || (N * es) % 16 == 0);
         p->tile = choose(type_class(dtype), aligned, 1, M, 2 * N, K * es, 1, tiles, false).tile;
-        st = tile_option(opt, first, &p->tile);
+        st = tile_option(opt, &p->tile);
+        if (st == MM_OK && !(tiles >> p->tile & 1)) st = fail(MM_ERR_BAD_OPTION, "tile %d has no FLOAT kernel", p->tile + 1);
         // Few rows: the rows kernel, except where 32-row tiles fill most CUs
         // with a long K and it has the dearer access: [K, N] weights (M = 1,
         // K = 4096, N = 11008: 55.0 against 49.3 us) or more than 16 rows (M =
@@ -347,7 +347,7 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         const int64_t es = elem_size(dtype);
         // dW's reduction runs over the rows of X; a 16-bit 32-row tile of its
         // transposed operand has rows too short to stage.
-        const unsigned dx_tiles = dtype == MM_FLOAT ? 0xe : 0xf, dw_tiles = dtype == MM_FLOAT ? 0xe : 0x7;
+        const unsigned dx_tiles = dtype == MM_FLOAT ? 0xe : 0x1f, dw_tiles = dtype == MM_FLOAT ? 0xe : 0x17;
         const bool dx_al = (p->w_pitch * es) % 16 == 0 && ((p->tb ? K : N) * es) % 16 == 0, dw_al = (K * es) % 16 == 0;
         p->dx = choose(cls, dx_al, 1, M, K, N * es, 2, dx_tiles, true);
         p->dw = choose(cls, dw_al, 2, p->tb ? N : K, p->tb ? K : N, M * es, 1, dw_tiles, true);

@@ -37,8 +37,8 @@ def scaled(sa=(4, 64), sb=(64, 32), out=mm.BFLOAT16, **kw):
     (dict(rows=1 << 31), mm.ERR_TOO_LARGE), (dict(k=1 << 31), mm.ERR_TOO_LARGE), (dict(n=1 << 31), mm.ERR_TOO_LARGE),
     (dict(force_algo=mm.ALGO_SPLIT_K), mm.ERR_BAD_OPTION), (dict(force_algo=mm.ALGO_DIRECT), mm.ERR_BAD_OPTION),
     (dict(rows=33, force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
-    (dict(tile=5), mm.ERR_BAD_OPTION), (dict(tile=-1), mm.ERR_BAD_OPTION),
-    (dict(dtype=mm.FLOAT, tile=1), mm.ERR_BAD_OPTION),
+    (dict(tile=6), mm.ERR_BAD_OPTION), (dict(tile=-1), mm.ERR_BAD_OPTION),
+    (dict(dtype=mm.FLOAT, tile=1), mm.ERR_BAD_OPTION), (dict(dtype=mm.FLOAT, tile=5), mm.ERR_BAD_OPTION),
 ])
 def test_glu_refusals(kw, want):
     assert status(glu, **kw) == want
@@ -117,7 +117,7 @@ def test_glu_backward_workspace_holds_the_largest_split():
     (dict(force_algo=mm.ALGO_DIRECT), mm.ERR_BAD_OPTION), (dict(force_algo=mm.ALGO_SKINNY_N), mm.ERR_BAD_OPTION),
     (dict(sa=(33, 64), force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
     (dict(sa=(2, 4, 64), sb=(2, 64, 32), force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
-    (dict(tile=5), mm.ERR_BAD_OPTION), (dict(split_k=-1), mm.ERR_BAD_OPTION),
+    (dict(tile=6), mm.ERR_BAD_OPTION), (dict(split_k=-1), mm.ERR_BAD_OPTION),
     (dict(tile=1, split_k=2), mm.ERR_BAD_OPTION), (dict(tile=1, force_algo=mm.ALGO_SPLIT_K), mm.ERR_BAD_OPTION),
 ])
 def test_scaled_refusals(kw, want):

@@ -160,14 +160,11 @@ def test_glu_activations_over_a_wide_range(act, dt, dev):
     run_forward(dev, 9, 64, 96, TYPES[dt], True, act, seed=41, keep=True, scale=10.0)
 
 
-@pytest.mark.parametrize("tile", [1, 2, 3, 4])
 @pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
-@pytest.mark.parametrize("dt", TYPES, ids=str)
+@pytest.mark.parametrize("dt,tile", [(d, t) for d in TYPES for t in ((2, 3, 4) if d == "fp32" else (1, 2, 3, 4, 5))])
 def test_glu_every_tile(tile, nk, dt, dev):
     """Aligned and odd sizes over several tiles with a ragged edge, K of one
     stage, of less, and of many."""
-    if dt == "fp32" and tile == 1:
-        pytest.skip("FLOAT has no 256 x 256 entry")
     for j, (m, k, n) in enumerate(((530, 328, 400), (270, 16, 136), (300, 701, 281), (2, 35, 9))):
         run_forward(dev, m, k, n, TYPES[dt], nk, "silu", seed=50 + j, tile=tile, algo=mm.ALGO_GENERAL, keep=j == 0)
 
@@ -458,7 +455,8 @@ def test_scaled_every_kernel_gives_the_same_bits(nk, dt, dev):
     """Tiles, splits and the few-row kernel, aligned and odd, over one product."""
     for m, k, n in ((20, 1168, 304), (20, 1111, 301)):
         got = []
-        for kw in (dict(force_algo=mm.ALGO_SKINNY_M), dict(tile=1), dict(tile=2), dict(tile=3), dict(tile=4),
+        for kw in (dict(force_algo=mm.ALGO_SKINNY_M), dict(tile=1), dict(tile=2), dict(tile=3), dict(tile=4), dict(tile=5),
+                       dict(tile=5, split_k=2),
                    dict(tile=2, split_k=3), dict(tile=3, split_k=2), dict(tile=4, split_k=5),
                    dict(tile=4, split_k=1000), dict(force_algo=mm.ALGO_GENERAL)):
             got.append(run_scaled(dev, (m, k), (k, n), TYPES[dt], nk, bias=True, seed=700, **kw)[1])
