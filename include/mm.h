@@ -387,9 +387,10 @@ mm_status mm_quantize_rows(const void *X, int dtype, int64_t rows, int64_t cols,
  * cores.  relu's derivative at 0 is 0.  Infinities and NaN follow the
  * formulas.
  *
- * Options: force_algo SKINNY_M (at most 32 rows) or GENERAL; tile
+ * Options: force_algo SKINNY_M (at most 32 rows), GENERAL or SPLIT_K; tile
  * k >= 1 is entry k of 256 x 256, 128 x 128, 64 x 128, 32 x 128, 256 x 128
- * for the forward pass (columns count gate and up; FLOAT has 2, 3 and 4). */
+ * for the forward pass (columns count gate and up; FLOAT has 2, 3 and 4; 1 is
+ * not split); split_k is the forward pass's, as for MatMul. */
 typedef enum mm_activation {
     MM_ACT_SILU = 1,      /* g / (1 + exp(-g)) */
     MM_ACT_GELU = 2,      /* g Phi(g), by erf */
@@ -408,10 +409,12 @@ typedef struct mm_glu_desc {
 } mm_glu_desc;
 
 /* Create a gated-block plan.  MM_ERR_NEG_DIM, MM_ERR_DTYPE, MM_ERR_BAD_OPTION
- * (an invalid field or option), MM_ERR_TOO_LARGE, MM_ERR_ALLOC.  Forward
- * executions use no workspace and may overlap; backward executions of one
- * plan must not overlap.  The plan answers the introspection calls (output
- * shape [rows, hidden]). */
+ * (an invalid field or option), MM_ERR_TOO_LARGE, MM_ERR_ALLOC.  A plan that
+ * splits K in the forward pass (algorithm SPLIT_K) or is for training owns a
+ * workspace, allocated and bound to a device as described above; executions
+ * that use it (split forward passes, backward passes) must not overlap with
+ * their own kind.  Other forward passes may.  The plan answers the
+ * introspection calls (output shape [rows, hidden]). */
 mm_status mm_glu_plan_create(const mm_glu_desc *desc, int dtype, const mm_plan_options *opt, mm_plan_t *out);
 
 /* Enqueue H = f(X Wg) * (X Wu) on `stream`; G and U, both or neither (NULL),

@@ -585,7 +585,8 @@ class GluPlan(Plan):
     views of a merged matrix (rows w_pitch elements apart)."""
 
     def __init__(self, rows: int, in_features: int, hidden: int, dtype: int, activation: int = ACT_SILU,
-                 trans_w: bool = False, training: bool = False, w_pitch: int = 0, force_algo: int = 0, tile: int = 0):
+                 trans_w: bool = False, training: bool = False, w_pitch: int = 0, force_algo: int = 0, tile: int = 0,
+                 split_k: int = 0):
         import torch
 
         L = lib()
@@ -595,7 +596,7 @@ class GluPlan(Plan):
         self.trans_w, self.training = bool(trans_w), bool(training)
         desc = GluDesc(self.rows, self.in_features, self.hidden, int(w_pitch), int(self.trans_w), int(activation),
                        int(self.training), 0)
-        opt = PlanOptions(force_algo, tile, 0, 0)
+        opt = PlanOptions(force_algo, tile, split_k, 0)
         _check(L.mm_glu_plan_create(ctypes.byref(desc), self.dtype, ctypes.byref(opt), ctypes.byref(self._handle)))
         self._lock = threading.Lock()
         self._dt = torch_dtype(self.dtype)

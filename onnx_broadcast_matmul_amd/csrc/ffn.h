@@ -43,8 +43,10 @@ constexpr int kNumFfnTiles = sizeof(kFfnTiles) / sizeof(kFfnTiles[0]);
 hipError_t launch_glu_dact(int dtype, int act, const void *G, const void *U, const void *dH, void *dG, void *dU,
                            int64_t M, int64_t N, int64_t ldw, hipStream_t s);
 // Tiled products (vec: every operand row and base is 16-byte aligned; split:
-// partial sums to W, to be joined by launch_sum_reduce / launch_scaled_reduce).
-hipError_t launch_glu_fwd(int dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);
+// partial sums to W, to be joined by the matching reduction; the gated
+// block's are [split][G, U][M][N]).
+hipError_t launch_glu_fwd(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
+hipError_t launch_glu_reduce(int dtype, const FfnArgs &a, hipStream_t s);
 hipError_t launch_glu_dx(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
 hipError_t launch_glu_dw(int dtype, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
 hipError_t launch_sum_reduce(int dtype, const FfnArgs &a, hipStream_t s);

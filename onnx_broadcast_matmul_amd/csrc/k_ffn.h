@@ -539,7 +539,12 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
         }
     };
     auto plain = [](int, int, auto v) { return (float)v; };
-    if constexpr (SPLIT) {
+    if constexpr (SPLIT && MODE == kGlu) {
+        // Partials of G, then of U, for every partition.
+        float *w = (float *)a.W + sidx * 2 * M * N;
+        emit(0.0f, 0, plain, w, N, N % 4 == 0);
+        emit(0.0f, FNP, plain, w + M * N, N, N % 4 == 0);
+    } else if constexpr (SPLIT) {
         using T = typename std::conditional<INT, int32_t, float>::type;
         emit((T)0, 0, plain, (T *)a.W + (sidx * a.batch + b) * M * N, N, N % 4 == 0);
     } else if constexpr (MODE == kGlu) {
@@ -556,7 +561,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
                     for (int r = 0; r < 16; ++r)
                         acc[i][j][r] = act_value<decltype(kind)::value, DT == MM_FLOAT>(acc[i][j][r]) * acc[i][FNP + j][r];
         };
-        switch (a.act) {
+        if (kg == 0) switch (a.act) {  // the other groups' sums are already in group 0's
         case MM_ACT_SILU: apply(std::integral_constant<int, MM_ACT_SILU>()); break;
         case MM_ACT_GELU: apply(std::integral_constant<int, MM_ACT_GELU>()); break;
         case MM_ACT_GELU_TANH: apply(std::integral_constant<int, MM_ACT_GELU_TANH>()); break;

@@ -13,7 +13,10 @@
 namespace mm {
 
 #define MM_GLU_INSTANCE(DT, NAME)                                                                           \
-    hipError_t glu_fwd_##NAME(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s) {                \
+    hipError_t glu_fwd_##NAME(bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {    \
+        if (split)                                                                                          \
+            return tb ? launch_entry<DT, DT, kGlu, true, false, true>(tile, vec, a, s)                      \
+                      : launch_entry<DT, DT, kGlu, true, false, false>(tile, vec, a, s);                    \
         return tb ? launch_entry<DT, DT, kGlu, false, false, true>(tile, vec, a, s)                         \
                   : launch_entry<DT, DT, kGlu, false, false, false>(tile, vec, a, s);                       \
     }                                                                                                       \

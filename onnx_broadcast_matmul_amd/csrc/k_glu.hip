@@ -7,16 +7,16 @@
 namespace mm {
 
 #define MM_GLU_DECLARE(NAME)                                                                               \
-    hipError_t glu_fwd_##NAME(bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s);                \
+    hipError_t glu_fwd_##NAME(bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);    \
     hipError_t glu_dx_##NAME(bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);     \
     hipError_t glu_dw_##NAME(int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
 MM_GLU_DECLARE(f32)
 MM_GLU_DECLARE(f16)
 MM_GLU_DECLARE(bf16)
 
-hipError_t launch_glu_fwd(int dtype, bool tb, int tile, bool vec, const FfnArgs &a, hipStream_t s) {
-    return dtype == MM_FLOAT ? glu_fwd_f32(tb, tile, vec, a, s)
-           : dtype == MM_FLOAT16 ? glu_fwd_f16(tb, tile, vec, a, s) : glu_fwd_bf16(tb, tile, vec, a, s);
+hipError_t launch_glu_fwd(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {
+    return dtype == MM_FLOAT ? glu_fwd_f32(tb, tile, split, vec, a, s)
+           : dtype == MM_FLOAT16 ? glu_fwd_f16(tb, tile, split, vec, a, s) : glu_fwd_bf16(tb, tile, split, vec, a, s);
 }
 
 hipError_t launch_glu_dx(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {
@@ -27,6 +27,78 @@ hipError_t launch_glu_dx(int dtype, bool tb, int tile, bool split, bool vec, con
 hipError_t launch_glu_dw(int dtype, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {
     return dtype == MM_FLOAT ? glu_dw_f32(tile, split, vec, a, s)
            : dtype == MM_FLOAT16 ? glu_dw_f16(tile, split, vec, a, s) : glu_dw_bf16(tile, split, vec, a, s);
+}
+
+// f(g) for an activation known at run time.
+template <bool EXACT>
+__device__ __forceinline__ float act_switch(int act, float g) {
+    switch (act) {
+    case MM_ACT_SILU: return act_value<MM_ACT_SILU, EXACT>(g);
+    case MM_ACT_GELU: return act_value<MM_ACT_GELU, EXACT>(g);
+    case MM_ACT_GELU_TANH: return act_value<MM_ACT_GELU_TANH, EXACT>(g);
+    case MM_ACT_RELU: return act_value<MM_ACT_RELU, EXACT>(g);
+    default: return act_value<MM_ACT_SIGMOID, EXACT>(g);
+    }
+}
+
+// Forward pass over split K: the partitions' G and U added in partition order,
+// then the tiled kernel's epilogue.  A thread owns four consecutive elements
+// of the dense [M, N] outputs.
+template <int DT>
+__global__ __launch_bounds__(256) void k_glu_reduce(FfnArgs a) {
+    using E = Elem<DT>;
+    using S = typename E::S;
+    const int64_t total = a.M * a.N;
+    const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i0 >= total) return;
+    const int n = total - i0 < 4 ? (int)(total - i0) : 4;
+    const float *w = (const float *)a.W + i0;
+    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (total % 4 == 0) {
+#pragma unroll 4
+        for (int p = 0; p < a.split; ++p) {
+            const float4 x = *(const float4 *)(w + 2 * p * total), y = *(const float4 *)(w + (2 * p + 1) * total);
+            g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
+            u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+        }
+    } else {
+        for (int p = 0; p < a.split; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n) {
+                    g[e] += w[2 * p * total + e];
+                    u[e] += w[(2 * p + 1) * total + e];
+                }
+    }
+    S og[4], ou[4], oh[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        og[e] = E::from_f32(g[e]);
+        ou[e] = E::from_f32(u[e]);
+        oh[e] = E::from_f32(act_switch<DT == MM_FLOAT>(a.act, g[e]) * u[e]);
+    }
+    auto put = [&](void *p, const S *v) {
+        S *y = (S *)p + i0;
+        if (n == 4) __builtin_memcpy(y, v, sizeof(og));
+        else
+            for (int e = 0; e < n; ++e) y[e] = v[e];
+    };
+    if (a.G) {
+        put(a.G, og);
+        put(a.U, ou);
+    }
+    put(a.Y[0], oh);
+}
+
+hipError_t launch_glu_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
+    const int64_t g = ((a.M * a.N + 3) / 4 + 255) / 256;
+    if (g <= 0) return hipSuccess;
+    if (g > 0x7fffffff) return hipErrorInvalidValue;
+    const dim3 gr((unsigned)g), bl(256);
+    if (dtype == MM_FLOAT) hipLaunchKernelGGL(k_glu_reduce<MM_FLOAT>, gr, bl, 0, s, a);
+    else if (dtype == MM_FLOAT16) hipLaunchKernelGGL(k_glu_reduce<MM_FLOAT16>, gr, bl, 0, s, a);
+    else hipLaunchKernelGGL(k_glu_reduce<MM_BFLOAT16>, gr, bl, 0, s, a);
+    return hipGetLastError();
 }
 
 // Sum of the K partitions' FP32 partials in partition order, narrowed once;

@@ -74,14 +74,15 @@ struct mm_plan_s {
     int64_t q_pitch = 0, q_off = 0, qs_off = 0;
 
     // Gated feed-forward block (mm_glu_plan_create): tb is trans_w, M, N, K
-    // are rows, hidden, in_features.  The training workspace holds dG and dU
-    // with rows of d_pitch elements, d_bytes each.
+    // are rows, hidden, in_features.  The workspace holds a split forward
+    // pass's partials, then (training, at d_off) dG and dU with rows of
+    // d_pitch elements, d_bytes each, and a split backward product's partials.
     bool is_glu = false;
     int act = 0;
     bool training = false;
-    int64_t w_pitch = 0, d_pitch = 0, d_bytes = 0;
-    mm::FfnChoice dx, dw;  // the backward products; split partials follow dG and dU
-    int32_t kstages = 0;   // scaled INT8 product: K stages of a partition
+    int64_t w_pitch = 0, d_off = 0, d_pitch = 0, d_bytes = 0;
+    mm::FfnChoice dx, dw;  // the backward products
+    int32_t kstages = 0;   // K stages of a partition (scaled product, forward pass)
 
     // Plan-owned constant B (mm_plan_set_constant_b).
     std::mutex cb_mutex;

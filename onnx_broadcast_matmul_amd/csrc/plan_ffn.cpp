@@ -35,7 +35,7 @@ static const double kStep[2][3][kNumFfnTiles][2] = {                    // us: a
     {{{0.41, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.240, 0}},
      {{0.41, 0}, {0.17, 0.285}, {0.145, 0.160}, {0.095, 0}, {0.222, 0}},
      {{1e9, 0}, {0.54, 0.970}, {0.260, 0.490}, {0.148, 0}, {1e9, 0}}},
-    {{{1e9, 0}, {0.29, 0.340}, {0.150, 0.195}, {0.110, 0}, {0.300, 0}},
+    {{{1e9, 0}, {0.29, 0.340}, {0.150, 0.195}, {0.110, 0}, {0.260, 0}},
      {{1e9, 0}, {0.30, 0.355}, {0.175, 0.195}, {0.090, 0}, {0.300, 0}},
      {{1e9, 0}, {0.78, 1.160}, {0.400, 0.610}, {0.200, 0}, {1e9, 0}}}};
 
@@ -300,11 +300,20 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         return fail(MM_ERR_TOO_LARGE, "rows, in_features, hidden and w_pitch must each be below 2^31");
     const int force = opt ? opt->force_algo : MM_ALGO_AUTO;
     const bool rows_ok = M <= kFfnRows;
-    if (force != MM_ALGO_AUTO && force != MM_ALGO_GENERAL && force != MM_ALGO_SKINNY_M)
-        return fail(MM_ERR_BAD_OPTION, "the gated block runs on the skinny-M and general kernels only");
+    const int treq = opt ? opt->tile : 0, sreq = opt ? opt->split_k : 0;
+    if (force != MM_ALGO_AUTO && force != MM_ALGO_GENERAL && force != MM_ALGO_SKINNY_M && force != MM_ALGO_SPLIT_K)
+        return fail(MM_ERR_BAD_OPTION, "the gated block runs on the skinny-M, general and split-K kernels only");
     if (force == MM_ALGO_SKINNY_M && !rows_ok)
         return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes at most %d rows", kFfnRows);
-    if (opt && opt->split_k != 0) return fail(MM_ERR_BAD_OPTION, "the gated block does not split K");
+    if (sreq < 0) return fail(MM_ERR_BAD_OPTION, "split_k %d is negative", sreq);
+    int only = -1;
+    mm_status st = tile_option(opt, &only);
+    if (st != MM_OK) return st;
+    unsigned tiles = dtype == MM_FLOAT ? 0xe : 0x1f;  // FLOAT has the three smaller entries
+    if (only >= 0) tiles &= 1u << only;
+    if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile %d has no FLOAT kernel", treq);
+    if (force == MM_ALGO_SPLIT_K || sreq > 1) tiles &= ~1u;  // no 256 x 256 partials
+    if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile 1 does not split K");
     mm_plan_s *p = new (std::nothrow) mm_plan_s();
     if (!p) return fail(MM_ERR_ALLOC, "host allocation failed");
     p->dtype = dtype;
@@ -321,30 +330,38 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
     p->K = K;
     p->out_numel = M * N;
     p->total_batch = p->batch = 1;
-    mm_status st = MM_OK;
+    const int64_t es = elem_size(dtype);
+    const int cls = type_class(dtype);
     if (p->out_numel == 0) {
         p->algo = MM_ALGO_EMPTY;
     } else {
-                const unsigned tiles = dtype == MM_FLOAT ? 0xe : 0x1f;  // FLOAT has the three smaller entries
-        const int64_t es = elem_size(dtype);
-        const bool aligned = (K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 && (p->tb || (N * es) % 16 == 0);
-        p->tile = choose(type_class(dtype), aligned, 1, M, 2 * N, K * es, 1, tiles, false).tile;
-        st = tile_option(opt, &p->tile);
-        if (st == MM_OK && !(tiles >> p->tile & 1)) st = fail(MM_ERR_BAD_OPTION, "tile %d has no FLOAT kernel", p->tile + 1);
         // Few rows: the rows kernel, except where 32-row tiles fill most CUs
         // with a long K and it has the dearer access: [K, N] weights (M = 1,
         // K = 4096, N = 11008: 55.0 against 49.3 us) or more than 16 rows (M =
         // 32: 56.9 against 48.0 us; at K = N = 4096 18.2 against 30.0 us).
         const bool tiles_fill = cdiv(N, 64) >= 160 && K * es >= 8192;
         const bool rows_best = rows_ok && !(tiles_fill && (!p->tb || M > 16));
-        p->algo = force != MM_ALGO_AUTO ? force : rows_best && !(opt && opt->tile > 0) ? MM_ALGO_SKINNY_M : MM_ALGO_GENERAL;
-        if (p->algo == MM_ALGO_SKINNY_M) p->tile = -1;
+        if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_best && treq == 0 && sreq == 0)) {
+            p->algo = MM_ALGO_SKINNY_M;
+        } else {
+            const bool aligned = (K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 && (p->tb || (N * es) % 16 == 0);
+            const bool may_split = force != MM_ALGO_GENERAL && K > 0;
+            FfnChoice c = choose(cls, aligned, 1, M, 2 * N, K * es, 1, tiles, may_split && sreq == 0);
+            if (may_split && sreq > 0) set_split(&c, K * es, 1, sreq);
+            p->tile = c.tile;
+            p->split = c.split;
+            p->kstages = c.kstages;
+            p->algo = c.split > 1 ? MM_ALGO_SPLIT_K : MM_ALGO_GENERAL;
+            if (c.split > 1) {
+                p->kchunk = (int64_t)c.kstages * kFfnTiles[c.tile].bkb / es;
+                p->workspace_bytes = round_up((int64_t)c.split * 2 * M * N * 4, 256);
+            }
+        }
     }
-    if (st == MM_OK && p->training) {
-        p->d_pitch = round_up(N, 16 / elem_size(dtype));
-        p->d_bytes = round_up(M * p->d_pitch * elem_size(dtype), 256);
-        const int cls = type_class(dtype);
-        const int64_t es = elem_size(dtype);
+    if (p->training) {
+        p->d_off = p->workspace_bytes;
+        p->d_pitch = round_up(N, 16 / es);
+        p->d_bytes = round_up(M * p->d_pitch * es, 256);
         // dW's reduction runs over the rows of X; a 16-bit 32-row tile of its
         // transposed operand has rows too short to stage.
         const unsigned dx_tiles = dtype == MM_FLOAT ? 0xe : 0x1f, dw_tiles = dtype == MM_FLOAT ? 0xe : 0x17;
@@ -354,9 +371,9 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         int64_t part = 0;
         if (p->dx.split > 1) part = (int64_t)p->dx.split * M * K * 4;
         if (p->dw.split > 1) part = std::max(part, (int64_t)p->dw.split * 2 * K * N * 4);
-        p->workspace_bytes = 2 * p->d_bytes + part;
-        st = alloc_workspace(p, true);
+        p->workspace_bytes += 2 * p->d_bytes + part;
     }
+    st = alloc_workspace(p, true);
     if (st != MM_OK) {
         delete p;
         return st;
@@ -391,13 +408,20 @@ mm_status mm_glu_execute(mm_plan_t p, const void *X, const void *Wg, const void 
     a.ldb = p->w_pitch;
     a.ldy = p->N;
     a.batch = 1;
-    a.split = 1;
+    a.split = p->split;
+    a.kstages = p->kstages;
     a.act = p->act;
     a.y_vec = aligned16(H) && aligned16(G) && aligned16(U) && (p->N * es) % 16 == 0;
     if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_glu_rows(p->dtype, p->tb != 0, a, s));
     const bool vec = aligned16(X) && aligned16(Wg) && aligned16(Wu) && (p->K * es) % 16 == 0 &&
                      (p->w_pitch * es) % 16 == 0 && (p->tb || (p->N * es) % 16 == 0);
-    return launched(launch_glu_fwd(p->dtype, p->tb != 0, p->tile, vec, a, s));
+    if (p->algo != MM_ALGO_SPLIT_K) return launched(launch_glu_fwd(p->dtype, p->tb != 0, p->tile, false, vec, a, s));
+    mm_status st = alloc_workspace(p, false);
+    if (st != MM_OK) return st;
+    a.W = p->ws;
+    hipError_t e = launch_glu_fwd(p->dtype, p->tb != 0, p->tile, true, vec, a, s);
+    if (e == hipSuccess) e = launch_glu_reduce(p->dtype, a, s);
+    return launched(e);
 }
 
 mm_status mm_glu_backward(mm_plan_t p, const void *X, const void *Wg, const void *Wu, const void *G, const void *U,
@@ -418,12 +442,12 @@ mm_status mm_glu_backward(mm_plan_t p, const void *X, const void *Wg, const void
         mm_status st = alloc_workspace(p, false);
         if (st != MM_OK) return st;
     }
-    void *dG = p->ws, *dU = (char *)p->ws + p->d_bytes;
+    char *dG = (char *)p->ws + p->d_off, *dU = dG + p->d_bytes;
     if (p->out_numel > 0) {
         mm_status st = launched(launch_glu_dact(p->dtype, p->act, G, U, dH, dG, dU, M, N, p->d_pitch, s));
         if (st != MM_OK) return st;
     }
-    void *part = p->ws ? (char *)p->ws + 2 * p->d_bytes : nullptr;
+    void *part = dU + p->d_bytes;
     const bool w_vec = (p->w_pitch * es) % 16 == 0;
     if (want_x) {
         // dX [M, K] = dG Wg' + dU Wu', the reduction over the hidden features:

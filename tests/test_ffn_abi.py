@@ -35,8 +35,9 @@ def scaled(sa=(4, 64), sb=(64, 32), out=mm.BFLOAT16, **kw):
     (dict(w_pitch=31), mm.ERR_BAD_OPTION), (dict(w_pitch=63, trans_w=True), mm.ERR_BAD_OPTION),
     (dict(w_pitch=-1), mm.ERR_BAD_OPTION),
     (dict(rows=1 << 31), mm.ERR_TOO_LARGE), (dict(k=1 << 31), mm.ERR_TOO_LARGE), (dict(n=1 << 31), mm.ERR_TOO_LARGE),
-    (dict(force_algo=mm.ALGO_SPLIT_K), mm.ERR_BAD_OPTION), (dict(force_algo=mm.ALGO_DIRECT), mm.ERR_BAD_OPTION),
-    (dict(rows=33, force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
+    (dict(force_algo=mm.ALGO_SKINNY_N), mm.ERR_BAD_OPTION), (dict(force_algo=mm.ALGO_DIRECT), mm.ERR_BAD_OPTION),
+    (dict(split_k=-1), mm.ERR_BAD_OPTION), (dict(tile=1, split_k=2), mm.ERR_BAD_OPTION),
+    (dict(tile=1, force_algo=mm.ALGO_SPLIT_K), mm.ERR_BAD_OPTION), (dict(rows=33, force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
     (dict(tile=6), mm.ERR_BAD_OPTION), (dict(tile=-1), mm.ERR_BAD_OPTION),
     (dict(dtype=mm.FLOAT, tile=1), mm.ERR_BAD_OPTION), (dict(dtype=mm.FLOAT, tile=5), mm.ERR_BAD_OPTION),
 ])
@@ -55,7 +56,7 @@ def test_glu_descriptor_fields():
     assert L.mm_glu_plan_create(None, mm.FLOAT, None, ctypes.byref(h)) == mm.ERR_NULL_ARG
     d = mm.GluDesc(4, 64, 32, 0, 0, mm.ACT_SILU, 0, 0)
     assert L.mm_glu_plan_create(ctypes.byref(d), mm.FLOAT, None, None) == mm.ERR_NULL_ARG
-    opt = mm.PlanOptions(0, 0, 2, 0)
+    opt = mm.PlanOptions(0, 0, 0, 2)
     assert L.mm_glu_plan_create(ctypes.byref(d), mm.FLOAT, ctypes.byref(opt), ctypes.byref(h)) == mm.ERR_BAD_OPTION
 
 
@@ -68,6 +69,9 @@ def test_glu_info():
     assert p.workspace_bytes == 0 and i["algo_name"] == "general"
     assert glu(1, 4096, 512, trans_w=True).info()["algo_name"] == "skinny_m"
     assert glu(0, 64, 32).info()["algo_name"] == "empty"
+    s = glu(100, 4096, 64, split_k=4)
+    assert s.info()["algo_name"] == "split_k" and s.info()["split_k"] == 4
+    assert s.workspace_bytes == 4 * 2 * 100 * 64 * 4
     t = glu(100, 64, 33, training=True)
     assert t.workspace_bytes >= 2 * 100 * 40 * 2  # dG and dU with rows of 40 elements
 

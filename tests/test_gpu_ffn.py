@@ -111,7 +111,8 @@ def forward64(x, wg, wu, act, dt):
     return (h, th), (g, tg), (u, tu)
 
 
-def run_forward(dev, m, k, n, dt, nk, act, seed=0, keep=False, offset=0, merged=False, tile=0, algo=0, scale=1.0):
+def run_forward(dev, m, k, n, dt, nk, act, seed=0, keep=False, offset=0, merged=False, tile=0, algo=0, scale=1.0,
+                split=0):
     x, _ = guarded((m, k), dt, dev, offset)
     x.copy_(rand((m, k), dt, dev, seed, scale))
     wide = rand((2 * n, k) if nk else (k, 2 * n), dt, dev, seed + 1, max(k, 1) ** -0.5)
@@ -129,7 +130,7 @@ def run_forward(dev, m, k, n, dt, nk, act, seed=0, keep=False, offset=0, merged=
                 ws.append(t)
             wg, wu = ws
     plan = mm.GluPlan(m, k, n, mm.torch_dtype_code(dt), activation=mm.ACTIVATIONS[act], trans_w=nk, w_pitch=pitch,
-                      force_algo=algo, tile=tile)
+                      force_algo=algo, tile=tile, split_k=split)
     outs = [guarded((m, n), dt, dev, offset) for _ in range(3 if keep else 1)]
     plan.execute(x, wg, wu, *(t for t, _ in outs))
     torch.cuda.synchronize()
@@ -169,6 +170,14 @@ def test_glu_every_tile(tile, nk, dt, dev):
         run_forward(dev, m, k, n, TYPES[dt], nk, "silu", seed=50 + j, tile=tile, algo=mm.ALGO_GENERAL, keep=j == 0)
 
 
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("dt,tile", [(d, t) for d in TYPES for t in ((2, 3, 4) if d == "fp32" else (2, 3, 4, 5))])
+def test_glu_split(tile, nk, dt, dev):
+    for j, (m, k, n, split) in enumerate(((270, 1040, 136, 3), (50, 701, 281, 1000), (2, 35, 9, 2))):
+        p = run_forward(dev, m, k, n, TYPES[dt], nk, ACTS[j], seed=55 + j, tile=tile, split=split, keep=j != 1)
+        assert j == 2 or p.info()["algo_name"] == "split_k"
+
+
 @pytest.mark.parametrize("m", [1, 16, 17, 32])
 @pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
 @pytest.mark.parametrize("dt", TYPES, ids=str)
@@ -205,6 +214,16 @@ def test_glu_empty_reduction_and_nan_rows(m, dev):
     assert bool(dirty[1].isnan().all()) and not bool(dirty[2].isfinite().all())
     keep = [r for r in range(m) if r not in (1, 2)]
     assert torch.equal(clean[keep], dirty[keep])
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("keep", [False, True], ids=["h", "hgu"])
+def test_glu_more_large_tiles_than_cus(nk, keep, dev):
+    """Workgroups that walk several 256 x 256 tiles: ragged edges, K of the
+    fewest stages that they take, of a part of one more, and of a few."""
+    for j, (m, k, n) in enumerate(((4300, 128, 2312), (2900, 136, 3592), (4500, 328, 4104))):
+        run_forward(dev, m, k, n, (BF16, F16)[j % 2], nk, ACTS[(j + 2 * keep) % 5], seed=90 + j, tile=1,
+                    algo=mm.ALGO_GENERAL, keep=keep)
 
 
 # ---- gated block, backward
@@ -293,6 +312,12 @@ def test_glu_backward_variants(nk, dev):
     run_backward(dev, 40, 64, 96, BF16, nk, "silu", seed=430, offset=1)
     run_backward(dev, 40, 64, 96, BF16, nk, "silu", seed=440, merged=True)
     run_backward(dev, 41, 63, 95, F32, nk, "silu", seed=450, merged=True)
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+def test_glu_backward_more_large_tiles_than_cus(nk, dev):
+    run_backward(dev, 4360, 4616, 264, BF16, nk, "silu", seed=460)  # dX: 342 large tiles
+    run_backward(dev, 520, 4616, 2360, F16, nk, "gelu", seed=470)  # dW: 2 x 190
 
 
 def test_glu_backward_empty(dev):
@@ -422,19 +447,21 @@ def run_scaled(dev, sa, sb, dt, nk=False, bias=False, seed=0, offset=0, **kw):
     plan.execute(a, bt, y, a_scale=asc, b_scale=bsc, bias=bv)
     torch.cuda.synchronize()
     check_guard(buf, y, offset)
-    # batched products of 64-bit operands on the CPU
-    total = torch.matmul(a.cpu().double(), b.cpu().double())
-    av, bvv = asc.cpu().double(), bsc.cpu().double()
+    if len(sa) == 2 and len(sb) == 2:
+        total, av, bvv = a.double() @ b.double(), asc.double(), bsc.double()
+    else:  # batched products of 64-bit operands on the CPU
+        total = torch.matmul(a.cpu().double(), b.cpu().double()).to(dev)
+        av, bvv = asc.double(), bsc.double()
     if len(sa) > 1:
         av = av.unsqueeze(-1) if len(sb) > 1 else av
     want = total * av * (bvv.unsqueeze(-2) if len(sa) > 1 and len(sb) > 1 else bvv)
     t = 4 * 2.0 ** -24 * want.abs()
     if bias:
-        off = bv.cpu().double()
+        off = bv.double()
         want = want + (off if len(sb) > 1 else off.reshape(()))
         t = t + 2.0 ** -23 * (want.abs() + off.abs().max())
     tol = t * (1 + half_step(dt)) + half_step(dt) * want.abs() + tiny(dt)
-    within(y.cpu(), want, tol, f"{sa} x {sb}")
+    within(y, want, tol, f"{sa} x {sb}")
     return plan, y
 
 
@@ -462,6 +489,13 @@ def test_scaled_every_kernel_gives_the_same_bits(nk, dt, dev):
             got.append(run_scaled(dev, (m, k), (k, n), TYPES[dt], nk, bias=True, seed=700, **kw)[1])
         for y in got[1:]:
             assert torch.equal(y.view(torch.uint8), got[0].view(torch.uint8))
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("dt", TYPES, ids=str)
+def test_scaled_more_large_tiles_than_cus(dt, nk, dev):
+    run_scaled(dev, (4360, 272), (272, 4624), TYPES[dt], nk, bias=True, seed=705, tile=1)
+    run_scaled(dev, (3, 1400, 320), (3, 320, 4112), TYPES[dt], nk, seed=706, tile=1)
 
 
 @pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
@@ -623,7 +657,7 @@ def test_graph_replays_match_eager(m, dev):
 
 
 def test_two_streams_at_once(dev):
-    """Forward passes of one plan overlap freely; backward passes take a plan
+    """Unsplit forward passes of one plan overlap freely; the rest takes a plan
     per stream."""
     sets = [ffn_calls(dev, 300, 256, 512) for _ in range(2)]
     for call, _, _ in sets:
