@@ -14,6 +14,7 @@ struct FfnChoice {
     int tile = 0;
     int32_t split = 1;
     int32_t kstages = 0;  // K stages of a partition
+    double us = 0.0;      // estimated time
 };
 }  // namespace mm
 

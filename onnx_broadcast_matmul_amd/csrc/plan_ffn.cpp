@@ -51,6 +51,26 @@ static double est_us(int cls, bool aligned, int tile, double wgs, double steps) 
     return us;
 }
 
+// Time of the few-row kernel: a workgroup's chain of K (kChain us for each KiB
+// of a weight row, which memory latency sets), or the weights' stream once
+// the workgroups fill the GPU; [weights N x K, K x N][up to 16 rows, more].
+// Fitted to M = 1..32, K = 1000..11008, N = 128..11008.  [K, N] weights come at
+// 18 GB/s per workgroup from memory (3.6 us for each KiB) and twice as fast
+// when the last-level cache holds them from the call before: 2.8 between.
+static double rows_us(int cls, bool nk, int64_t M, int64_t kbytes, double wbytes) {
+    static const double kChain[3][2][2] = {{{1.0, 1.75}, {2.8, 3.2}}, {{0.6, 1.2}, {2.8, 3.2}}, {{1.2, 1.85}, {2.8, 3.2}}};
+    static const double kRate[3][2][2] = {{{4.9, 3.2}, {3.3, 2.9}}, {{3.5, 2.2}, {3.2, 2.5}}, {{4.9, 3.2}, {3.3, 2.9}}};  // TB/s
+    const int o = nk ? 0 : 1, r = M > 16 ? 1 : 0;
+    return std::max(3.0 + kChain[cls][o][r] * (double)kbytes / 1024.0, wbytes / (kRate[cls][o][r] * 1e6));
+}
+
+// The tiles' time over the same few rows: the weights stream at kStream
+// TB/s at best, and a second launch follows a split.
+static double tiles_us(int cls, const FfnChoice &c, double wbytes) {
+    static const double kStream[3] = {4.0, 2.7, 4.0};
+    return std::max(c.us + (c.split > 1 ? 3.0 : 0.0), wbytes / (kStream[cls] * 1e6));
+}
+
 // Entry and split with the least estimated time for `batch` products of
 // [M, cols] over `kbytes` bytes of K (terms: that many times in one K loop;
 // cols counts gate and up columns).  Partials cost their write, read and a
@@ -73,6 +93,7 @@ static FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t
             if (parts > 1) us += 3.0 + (double)parts * (double)batch * (double)M * (double)cols * 8.0 / 3.5e6;
             if (us < top) {
                 top = us;
+                best.us = us;
                 best.tile = i;
                 best.split = (int32_t)parts;
                 best.kstages = (int32_t)per;
@@ -113,19 +134,6 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     int only = -1;
     mm_status st = tile_option(opt, &only);
     if (st != MM_OK) return st;
-    // Few rows: the rows kernel streams the weights once.  [K, N] weights
-    // give it a workgroup per 64 columns, each a chain of K at 18 GB/s, so a
-    // long K goes to split tiles unless the columns fill the CUs (M = 1, K =
-    // 11008, N = 4096: 38.8 against 18.3 us; K = 4096, N = 11008: 14.0 against
-    // 17.1 us).  Past 16 rows it
-    // re-reads X twice as much and wide products fill the tiles (M = 32, K =
-    // 4096: 21.3 against 18.7 us at N = 11008, 9.0 against 13.0 at 4096).
-    const bool rows_best = rows_ok && K > 0 && (p->tb || K <= 2048 || (K <= 4096 && N >= 8192)) &&
-                           (M <= 16 || N < 8192);
-    if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_best && treq == 0 && sreq == 0)) {
-        p->algo = MM_ALGO_SKINNY_M;
-        return MM_OK;
-    }
     // Partials are added by a grid of at most 65535 products.
     const bool may_split = force != MM_ALGO_GENERAL && K > 0 && p->batch <= 65535;
     const unsigned all = (1u << kNumFfnTiles) - 1;
@@ -134,6 +142,12 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile 1 does not split K");
     const bool aligned = (p->tb ? K : N) % 16 == 0 && (p->a_type != MM_INT8 || K % 16 == 0);
     FfnChoice c = choose(kClass8, aligned, p->batch, M, N, K, 1, tiles, may_split && sreq == 0);
+    const double wbytes = (double)K * (double)N;
+    if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && K > 0 && treq == 0 && sreq == 0 &&
+                                      rows_us(kClass8, p->tb != 0, M, K, wbytes) <= tiles_us(kClass8, c, wbytes))) {
+        p->algo = MM_ALGO_SKINNY_M;
+        return MM_OK;
+    }
     if (may_split && sreq > 0) set_split(&c, K, 1, sreq);
     p->tile = c.tile;
     p->algo = c.split > 1 || (force == MM_ALGO_SPLIT_K && may_split) ? MM_ALGO_SPLIT_K : MM_ALGO_GENERAL;
@@ -335,18 +349,14 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
     if (p->out_numel == 0) {
         p->algo = MM_ALGO_EMPTY;
     } else {
-        // Few rows: the rows kernel, except where 32-row tiles fill most CUs
-        // with a long K and it has the dearer access: [K, N] weights (M = 1,
-        // K = 4096, N = 11008: 55.0 against 49.3 us) or more than 16 rows (M =
-        // 32: 56.9 against 48.0 us; at K = N = 4096 18.2 against 30.0 us).
-        const bool tiles_fill = cdiv(N, 64) >= 160 && K * es >= 8192;
-        const bool rows_best = rows_ok && !(tiles_fill && (!p->tb || M > 16));
-        if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_best && treq == 0 && sreq == 0)) {
+        const bool aligned = (K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 && (p->tb || (N * es) % 16 == 0);
+        const bool may_split = force != MM_ALGO_GENERAL && K > 0;
+        FfnChoice c = choose(cls, aligned, 1, M, 2 * N, K * es, 1, tiles, may_split && sreq == 0);
+        const double wbytes = 2.0 * (double)K * (double)N * (double)es;
+        if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && treq == 0 && sreq == 0 &&
+                                          rows_us(cls, p->tb != 0, M, K * es, wbytes) <= tiles_us(cls, c, wbytes))) {
             p->algo = MM_ALGO_SKINNY_M;
         } else {
-            const bool aligned = (K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 && (p->tb || (N * es) % 16 == 0);
-            const bool may_split = force != MM_ALGO_GENERAL && K > 0;
-            FfnChoice c = choose(cls, aligned, 1, M, 2 * N, K * es, 1, tiles, may_split && sreq == 0);
             if (may_split && sreq > 0) set_split(&c, K * es, 1, sreq);
             p->tile = c.tile;
             p->split = c.split;

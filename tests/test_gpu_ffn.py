@@ -677,6 +677,7 @@ def test_two_streams_at_once(dev):
             assert torch.equal(t.view(torch.uint8), v.view(torch.uint8))
     x, w = rand((300, 256), BF16, dev, 1), rand((512, 256), BF16, dev, 2, 0.1)
     plan = mm.GluPlan(300, 256, 512, mm.BFLOAT16, trans_w=True)
+    assert plan.workspace_bytes == 0
     hs = [torch.empty(300, 512, dtype=BF16, device=dev) for _ in range(2)]
     torch.cuda.synchronize()
     for st, h in zip(streams, hs):
