@@ -58,7 +58,11 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int64_t M = a.M, N = a.N, K = a.K;
-    const int64_t n0 = xcd_remap(blockIdx.x, gridDim.x) * COLS;
+    // Neighbouring columns on one XCD, except for wide gated blocks with [N, K]
+    // weights, whose two streams do better spread over the XCDs (M = 1, K =
+    // 4096, N = 11008: 41.4 us so, 38.9 spread; M = 13, K = 2048, N = 5461:
+    // 13.2 and 14.9; INT8, K = N = 4096: 6.6 and 7.6).
+    const int64_t n0 = (GLU && !KN && NWV == 4 ? (int64_t)blockIdx.x : xcd_remap(blockIdx.x, gridDim.x)) * COLS;
     const int64_t nb = K / BK;  // whole blocks
 
     // ---- weights
@@ -88,26 +92,34 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
             // Pieces that cross a row's end read on into the next rows, where
             // the matrix goes on for that long (see k_ffn.h).
             const bool whole = krem >= BK && (left_n >= COLS || (krem - BK) * a.ldb >= VE);
+            if (whole) {
 #pragma unroll
-            for (int p = 0; p < NPAN; ++p)
+                for (int p = 0; p < NPAN; ++p)
 #pragma unroll
-                for (int i = 0; i < PP; ++i) {
-                    const int y = lane + 64 * i, row = y / CPR, c = y % CPR;
-                    if (whole) {
+                    for (int i = 0; i < PP; ++i) {
+                        const int y = lane + 64 * i, row = y / CPR, c = y % CPR;
                         t[p * PP + i] = whole_piece<S>(w[p] + (k0 + row) * a.ldb + (c * VE < left_n ? c * VE : 0));
-                    } else {
+                    }
+            } else {
+#pragma unroll
+                for (int p = 0; p < NPAN; ++p)
+#pragma unroll
+                    for (int i = 0; i < PP; ++i) {
+                        const int y = lane + 64 * i, row = y / CPR, c = y % CPR;
                         t[p * PP + i] = row_piece<S>(w[p] + (k0 + row) * a.ldb + c * VE, row < krem ? left_n - c * VE : 0, back);
                     }
-                }
+            }
+        } else if (krem >= BK) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int f = 0; f < NF; ++f) t[u * NF + f] = whole_piece<S>(w[f] + k0 + u * SK);
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int f = 0; f < NF; ++f) {
-                    const gptr p = w[f] + k0 + u * SK;
-                    if (krem >= BK) t[u * NF + f] = whole_piece<S>(p);
-                    else t[u * NF + f] = row_piece<S>(p, krem - (u * 4 + g) * VE, back);
-                }
+                for (int f = 0; f < NF; ++f)
+                    t[u * NF + f] = row_piece<S>(w[f] + k0 + u * SK, krem - (u * 4 + g) * VE, back);
         }
     };
 
@@ -222,21 +234,28 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
     }
     auto load_x = [&](int64_t kb, uint4 *t) {
         const int64_t k0 = kb * BK, krem = K - k0;
+        if constexpr (XQ != 0) {
+            // Past K: zeros, or the (finite) bytes of a neighbour against
+            // weights that are zero there.
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                if constexpr (XQ != 0) {
-                    // Past K: zeros, or the (finite) bytes of a neighbour
-                    // against weights that are zero there.
+                for (int i = 0; i < MB; ++i) {
                     const int at = xr[i] + (int)k0 + u * SK;
                     t[u * MB + i] = *(const uint4 *)(xq + (at <= XCAP - 16 ? at : 0));
-                } else {
-                    const gptr p = x[i] + k0 + u * SK;
-                    if (krem >= BK) t[u * MB + i] = whole_piece<S>(p);
-                    else t[u * MB + i] = row_piece<S>(p, krem - (u * 4 + g) * VE, K >= VE);
                 }
-            }
+        } else if (krem >= BK) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < MB; ++i) t[u * MB + i] = whole_piece<S>(x[i] + k0 + u * SK);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+                    t[u * MB + i] = row_piece<S>(x[i] + k0 + u * SK, krem - (u * 4 + g) * VE, K >= VE);
+        }
     };
 
     AccT acc[NF][MB];
@@ -330,12 +349,21 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
 #endif
 }
 
+// Waves of a workgroup: 8, or 4 where the columns make more than the 512
+// workgroups of 8 that fit the GPU at once, so that all start together ([N, K]
+// weights, M = 1, K = 4096, N = 11008: INT8 13.9 against 11.9 us, gated BF16
+// 38.9 against 37.8; INT8 K = 11008, N = 4096: 12.8 with 8, 14.7 with 4).
+constexpr int64_t kRowsFit = 512;
+
 template <int DT, int OD, bool GLU, bool KN, int NF, int MB, int NWV, int XQ>
 static hipError_t launch_rows(const FfnArgs &a, hipStream_t s) {
     constexpr int COLS = 16 * NF / (GLU ? 2 : 1);
     const int64_t wgs = (a.N + COLS - 1) / COLS;
     if (wgs <= 0 || a.M <= 0) return hipSuccess;
     if (wgs > 0x7fffffff || a.M > 16 * MB) return hipErrorInvalidValue;
+    if constexpr (!KN && NWV == 8) {
+        if (wgs > kRowsFit) return launch_rows<DT, OD, GLU, KN, NF, MB, 4, XQ>(a, s);
+    }
     hipLaunchKernelGGL((k_ffn_rows<DT, OD, GLU, KN, NF, MB, NWV, XQ>), dim3((unsigned)wgs), dim3(64 * NWV), 0, s, a);
     return hipGetLastError();
 }
