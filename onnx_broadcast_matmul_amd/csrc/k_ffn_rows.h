@@ -185,9 +185,24 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
 
     uint4 cur[PIECES], nxt[PIECES];
     const int64_t nball = (K + BK - 1) / BK;
-    if (wave < nball) load_w(wave, cur);
 
     // ---- X
+    // XQ: the rows side by side, `group` threads each; a thread's first pieces
+    // stay in registers.  They are asked for before the first weights, whose
+    // longer way from memory the quantization then hides.
+    constexpr int XKEEP = 4;
+    int group = NT;
+    uint4 xkeep[XQ ? XKEEP : 1];
+    if constexpr (XQ != 0) {
+        using XS = typename Elem<XQ>::S;
+        while (NT / group < (int)M) group >>= 1;
+        if (tid / group < (int)M) {
+#pragma unroll
+            for (int j = 0; j < XKEEP; ++j)
+                xkeep[j] = quant_load<XQ>((const XS *)a.A[0] + tid / group * K, (int64_t)(tid % group + j * group) * Elem<XQ>::kVE, K);
+        }
+    }
+    if (wave < nball) load_w(wave, cur);
     constexpr int XCAP = XQ ? kFfnQuantLds : 16;
     __shared__ __attribute__((aligned(16))) char xq[XCAP];
     __shared__ uint32_t xtop[XQ ? 16 * MB : 1];
@@ -196,17 +211,16 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
         using XE = Elem<XQ>;
         using XS = typename XE::S;
         constexpr int XV = XE::kVE;
-        // The rows side by side, 64 or more threads each.
-        int group = NT;
-        while (group > 64 && NT / group < (int)M) group >>= 1;
-        const int t = tid % group;
+        static_assert(NT / 64 >= kFfnQuantRows, "a wave or more for each row");
+        const int t = tid % group, m = tid / group;
+        const XS *xm = (const XS *)a.A[0] + (int64_t)m * K;
         if (tid < 16 * MB) xtop[tid] = 0;
         __syncthreads();
-        for (int m = tid / group; m < (int)M; m += NT / group) {
+        if (m < (int)M) {
             uint32_t top = 0;
-#pragma unroll 4
-            for (int c = t; c * XV < (int)K; c += group)
-                top = quant_top<XQ>(quant_load<XQ>((const XS *)a.A[0] + m * K, c * XV, K), top);
+#pragma unroll
+            for (int j = 0; j < XKEEP; ++j) top = quant_top<XQ>(xkeep[j], top);
+            for (int c = t + XKEEP * group; c * XV < (int)K; c += group) top = quant_top<XQ>(quant_load<XQ>(xm, c * XV, K), top);
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) {
                 const uint32_t o = (uint32_t)__shfl_xor((int)top, d);
@@ -215,12 +229,13 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
             if (lane == 0) atomicMax(&xtop[m], top);
         }
         __syncthreads();
-        for (int m = tid / group; m < (int)M; m += NT / group) {
+        if (m < (int)M) {
             const float rr = quant_factor(xtop[m]);
-            // Zeros up to the pitch, which the last step may read.
-#pragma unroll 4
-            for (int c = t; c * XV < xp; c += group)
-                quant_store<XQ>(quant_load<XQ>((const XS *)a.A[0] + m * K, c * XV, K), rr, xq + m * xp + c * XV);
+            char *q = xq + m * xp;  // zeros up to the pitch, which the last step may read
+#pragma unroll
+            for (int j = 0; j < XKEEP; ++j)
+                if ((t + j * group) * XV < xp) quant_store<XQ>(xkeep[j], rr, q + (t + j * group) * XV);
+            for (int c = t + XKEEP * group; c * XV < xp; c += group) quant_store<XQ>(quant_load<XQ>(xm, c * XV, K), rr, q + c * XV);
         }
         __syncthreads();
     }

@@ -21,7 +21,7 @@ static hipError_t scaled(bool tb, bool quant, const FfnArgs &a, hipStream_t s) {
 // than the launch it saves (BF16, N = 4096: one row of 11008 15.4 us against
 // 12.8 + 5.8; eight rows of 4096 11.8 against 6.3 + 5).
 bool rows_quantize(int a_type, int out_dtype, int64_t M, int64_t K) {
-    return a_type == out_dtype && M <= 4 && M * ((K + 63) / 64 * 64 + 16) <= kFfnQuantLds;
+    return a_type == out_dtype && M <= kFfnQuantRows && M * ((K + 63) / 64 * 64 + 16) <= kFfnQuantLds;
 }
 
 hipError_t launch_scaled_rows(int od, bool tb, bool quant, const FfnArgs &a, hipStream_t s) {
