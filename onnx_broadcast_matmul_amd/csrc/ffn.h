@@ -58,9 +58,8 @@ hipError_t launch_scaled_reduce(int out_dtype, const FfnArgs &a, hipStream_t s);
 // it itself (`quant`); its INT8 rows then fit kFfnQuantLds bytes of LDS.
 constexpr int kFfnRows = 32;
 constexpr int kFfnQuantLds = 48 * 1024;
-constexpr int kFfnQuantRows = 4;  // most rows that it quantizes
 hipError_t launch_glu_rows(int dtype, bool tb, const FfnArgs &a, hipStream_t s);
-bool rows_quantize(int a_type, int out_dtype, int64_t M, int64_t K);
+bool rows_quantize(int a_type, int out_dtype, bool tb, int64_t M, int64_t K, int64_t N);
 hipError_t launch_scaled_rows(int out_dtype, bool tb, bool quant, const FfnArgs &a, hipStream_t s);
 // Row quantization of a dense [rows, cols] matrix into rows of ldq bytes; the
 // bytes past cols are set to zero.

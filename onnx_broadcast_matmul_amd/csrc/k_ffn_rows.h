@@ -195,7 +195,7 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
     uint4 xkeep[XQ ? XKEEP : 1];
     if constexpr (XQ != 0) {
         using XS = typename Elem<XQ>::S;
-        while (NT / group < (int)M) group >>= 1;
+        while (NT / group < (int)M) group >>= 1;  // at most NWV rows: a wave or more each
         if (tid / group < (int)M) {
 #pragma unroll
             for (int j = 0; j < XKEEP; ++j)
@@ -211,7 +211,6 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
         using XE = Elem<XQ>;
         using XS = typename XE::S;
         constexpr int XV = XE::kVE;
-        static_assert(NT / 64 >= kFfnQuantRows, "a wave or more for each row");
         const int t = tid % group, m = tid / group;
         const XS *xm = (const XS *)a.A[0] + (int64_t)m * K;
         if (tid < 16 * MB) xtop[tid] = 0;

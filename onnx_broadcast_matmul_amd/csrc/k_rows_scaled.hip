@@ -17,15 +17,17 @@ static hipError_t scaled(bool tb, bool quant, const FfnArgs &a, hipStream_t s) {
                      : launch_rows<MM_INT8, OD, false, true, 4, 2, 8, 0>(a, s);
 }
 
-// Each workgroup quantizes the rows for itself: up to 4 rows that costs less
-// than the launch it saves (BF16, N = 4096: one row of 11008 15.4 us against
-// 12.8 + 5.8; eight rows of 4096 11.8 against 6.3 + 5).
-bool rows_quantize(int a_type, int out_dtype, int64_t M, int64_t K) {
-    return a_type == out_dtype && M <= kFfnQuantRows && M * ((K + 63) / 64 * 64 + 16) <= kFfnQuantLds;
+// Each workgroup quantizes the rows for itself.  Up to 4 rows, or 8 short ones,
+// that costs less than the launch it saves (BF16, [N, K] weights: one row of
+// 11008, N = 4096 12.5 against 18.5 us; 8 rows of 1024 5.5 against 9.9, of 2048
+// 6.8 against 9.0, but of 4096 11.7 against 10.2).
+bool rows_quantize(int a_type, int out_dtype, bool tb, int64_t M, int64_t K, int64_t N) {
+    const int64_t waves = tb && (N + 15) / 16 > kRowsFit ? 4 : 8;  // see launch_rows
+    return a_type == out_dtype && M <= waves && (M <= 4 || K <= 2048) && M * ((K + 63) / 64 * 64 + 16) <= kFfnQuantLds;
 }
 
 hipError_t launch_scaled_rows(int od, bool tb, bool quant, const FfnArgs &a, hipStream_t s) {
-    if (quant && !rows_quantize(od, od, a.M, a.K)) return hipErrorInvalidValue;
+    if (quant && !rows_quantize(od, od, tb, a.M, a.K, a.N)) return hipErrorInvalidValue;
     switch (od) {
     case MM_FLOAT: return scaled<MM_FLOAT>(tb, quant, a, s);
     case MM_FLOAT16: return scaled<MM_FLOAT16>(tb, quant, a, s);

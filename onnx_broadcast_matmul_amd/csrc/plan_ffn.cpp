@@ -205,7 +205,7 @@ mm_status mm_scaled_int_plan_create(const int64_t *a_shape, int a_rank, const in
     } else if (st == MM_OK) {
         st = select_scaled(p, opt);
         p->fused_quant = p->a_type != MM_INT8 && p->algo == MM_ALGO_SKINNY_M &&
-                         rows_quantize(p->a_type, p->dtype, p->kernel_m, p->K);
+                         rows_quantize(p->a_type, p->dtype, p->tb != 0, p->kernel_m, p->K, p->N);
         if (st == MM_OK && p->a_type != MM_INT8 && !p->fused_quant) {
             p->a_rows = 1;
             for (int i = 0; i + 1 < a_rank; ++i) p->a_rows *= a_shape[i];

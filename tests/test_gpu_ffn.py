@@ -557,7 +557,8 @@ def test_dynamic_product_is_quantization_then_product(nk, dt, dev):
     t = TYPES[dt]
     other = F32 if t != F32 else BF16
     for j, (sa, sb, out) in enumerate((((1, 2048), (2048, 96), t), ((4, 100), (100, 33), t), ((4, 1), (1, 3), t),
-                                       ((9, 2000), (2000, 64), t), ((1, 64), (64, 48), other), ((200, 72), (72, 130), t),
+                                       ((9, 2000), (2000, 64), t), ((7, 1030), (1030, 70), t),
+                                       ((3, 9000), (9000, 20), t), ((4, 260), (260, 8300), t), ((1, 64), (64, 48), other), ((200, 72), (72, 130), t),
                                        ((130, 77), (77, 55), t), ((2, 3, 40, 65), (65, 48), t),
                                        ((2, 1, 40, 65), (3, 65, 33), t), ((64,), (64, 48), t), ((3, 0), (0, 9), t))):
         x = rand(sa, t, dev, 820 + j)
