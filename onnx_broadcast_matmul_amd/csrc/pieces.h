@@ -37,14 +37,16 @@ __device__ __forceinline__ uint4 row_piece(GlobalPtr<S> p, int64_t left, bool ba
             lo = lo >> sh | hi << (64 - sh);
             hi >>= sh;
         }
-        return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+        v = make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+        asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+        return v;
     }
     S tmp[VE];
 #pragma unroll
     for (int e = 0; e < VE; ++e) tmp[e] = e < left ? p[e] : (S)0;
     __builtin_memcpy(&v, tmp, 16);
-    // Packed here: otherwise a byte type's whole pieces are taken apart and
-    // packed again where the paths meet.
+    // Packed here (and shifted above): otherwise whole pieces are waited for,
+    // taken apart and packed again where the paths meet.
     if constexpr (ES == 1) asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
     return v;
 }

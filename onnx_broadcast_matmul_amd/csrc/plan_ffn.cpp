@@ -35,9 +35,9 @@ static const double kStep[2][3][kNumFfnTiles][2] = {                    // us: a
     {{{0.41, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.240, 0}},
      {{0.41, 0}, {0.17, 0.285}, {0.145, 0.160}, {0.095, 0}, {0.222, 0}},
      {{1e9, 0}, {0.54, 0.970}, {0.260, 0.490}, {0.148, 0}, {1e9, 0}}},
-    {{{1e9, 0}, {0.29, 0.340}, {0.150, 0.195}, {0.110, 0}, {0.260, 0}},
-     {{1e9, 0}, {0.30, 0.355}, {0.175, 0.195}, {0.090, 0}, {0.300, 0}},
-     {{1e9, 0}, {0.78, 1.160}, {0.400, 0.610}, {0.200, 0}, {1e9, 0}}}};
+    {{{1e9, 0}, {0.27, 0.345}, {0.200, 0.222}, {0.098, 0}, {0.345, 0}},
+     {{1e9, 0}, {0.23, 0.305}, {0.122, 0.182}, {0.080, 0}, {0.310, 0}},
+     {{1e9, 0}, {0.60, 1.050}, {0.355, 0.585}, {0.171, 0}, {1e9, 0}}}};
 
 static int type_class(int dtype) { return dtype == MM_FLOAT ? kClass32 : dtype == MM_INT8 ? kClass8 : kClass16; }
 
