@@ -19,6 +19,10 @@ static mm_status launched(hipError_t e) {
     return e == hipSuccess ? MM_OK : fail(MM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
 }
 
+// Matrices of at most 2^40 elements: their byte counts and the kernels' grids
+// then stay in range (and the memory of any device is smaller).
+static bool too_large(int64_t rows, int64_t cols) { return (double)rows * (double)cols > 1099511627776.0; }
+
 static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
 
 // Time model of the tiled products: a CU runs up to kOcc workgroups of an
@@ -200,6 +204,13 @@ mm_status mm_scaled_int_plan_create(const int64_t *a_shape, int a_rank, const in
     if (st == MM_OK) st = check_limits(p);
     if (st == MM_OK && p->K > 131071)
         st = fail(MM_ERR_TOO_LARGE, "K = %lld: INT32 sums hold at most 131071 INT8 products", (long long)p->K);
+    if (st == MM_OK) {
+        double a_rows = 1.0;
+        for (int i = 0; i + 1 < a_rank; ++i) a_rows *= (double)a_shape[i];
+        if (a_rows > INT32_MAX || too_large(p->batch * p->kernel_m, p->N) || too_large(p->K, p->N) ||
+            a_rows * (double)p->K > 1099511627776.0)
+            st = fail(MM_ERR_TOO_LARGE, "a matrix of more than 2^40 elements, or an A of 2^31 rows or more");
+    }
     if (st == MM_OK && p->out_numel == 0) {
         p->algo = MM_ALGO_EMPTY;
     } else if (st == MM_OK) {
@@ -231,7 +242,8 @@ mm_status mm_quantize_rows(const void *X, int dtype, int64_t rows, int64_t cols,
     clear_error();
     if (rows < 0 || cols < 0) return fail(MM_ERR_NEG_DIM, "rows and cols must not be negative");
     if (!float_type(dtype)) return fail(MM_ERR_DTYPE, "quantize_rows takes FLOAT, FLOAT16 or BFLOAT16 (got %d)", dtype);
-    if (rows > INT32_MAX || cols > INT32_MAX) return fail(MM_ERR_TOO_LARGE, "rows and cols must each be below 2^31");
+    if (rows > INT32_MAX || cols > INT32_MAX || too_large(rows, cols))
+        return fail(MM_ERR_TOO_LARGE, "rows and cols must each be below 2^31, their product at most 2^40");
     if (rows == 0) return MM_OK;
     if (!scale || (cols > 0 && (!X || !Q))) return fail(MM_ERR_NULL_ARG, "X, Q or scale is NULL");
     return launched(launch_quantize_rows(dtype, X, rows, cols, Q, cols, scale, (hipStream_t)stream));
@@ -312,6 +324,8 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
                     (long long)row);
     if (M > INT32_MAX || K > INT32_MAX || N > INT32_MAX || d->w_pitch > INT32_MAX)
         return fail(MM_ERR_TOO_LARGE, "rows, in_features, hidden and w_pitch must each be below 2^31");
+    if (too_large(M, K) || too_large(M, N) || too_large(K, N) || too_large(d->trans_w ? N : K, d->w_pitch))
+        return fail(MM_ERR_TOO_LARGE, "a matrix of more than 2^40 elements");
     const int force = opt ? opt->force_algo : MM_ALGO_AUTO;
     const bool rows_ok = M <= kFfnRows;
     const int treq = opt ? opt->tile : 0, sreq = opt ? opt->split_k : 0;

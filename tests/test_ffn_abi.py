@@ -35,6 +35,8 @@ def scaled(sa=(4, 64), sb=(64, 32), out=mm.BFLOAT16, **kw):
     (dict(w_pitch=31), mm.ERR_BAD_OPTION), (dict(w_pitch=63, trans_w=True), mm.ERR_BAD_OPTION),
     (dict(w_pitch=-1), mm.ERR_BAD_OPTION),
     (dict(rows=1 << 31), mm.ERR_TOO_LARGE), (dict(k=1 << 31), mm.ERR_TOO_LARGE), (dict(n=1 << 31), mm.ERR_TOO_LARGE),
+    (dict(rows=1 << 30, n=1 << 11), mm.ERR_TOO_LARGE), (dict(k=1 << 30, n=1 << 11, rows=1), mm.ERR_TOO_LARGE),
+    (dict(k=1 << 12, n=4, w_pitch=1 << 30), mm.ERR_TOO_LARGE),
     (dict(force_algo=mm.ALGO_SKINNY_N), mm.ERR_BAD_OPTION), (dict(force_algo=mm.ALGO_DIRECT), mm.ERR_BAD_OPTION),
     (dict(split_k=-1), mm.ERR_BAD_OPTION), (dict(tile=1, split_k=2), mm.ERR_BAD_OPTION),
     (dict(tile=1, force_algo=mm.ALGO_SPLIT_K), mm.ERR_BAD_OPTION), (dict(rows=33, force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
@@ -117,7 +119,8 @@ def test_glu_backward_workspace_holds_the_largest_split():
     (dict(out=mm.DOUBLE), mm.ERR_DTYPE), (dict(out=mm.INT32), mm.ERR_DTYPE),
     (dict(a_type=mm.UINT8), mm.ERR_DTYPE), (dict(a_type=mm.DOUBLE), mm.ERR_DTYPE), (dict(a_type=0), mm.ERR_DTYPE),
     (dict(sa=(64,), sb=(64,), trans_b=True), mm.ERR_BAD_OPTION),
-    (dict(sa=(1, 131072), sb=(131072, 1)), mm.ERR_TOO_LARGE),
+    (dict(sa=(1, 131072), sb=(131072, 1)), mm.ERR_TOO_LARGE), (dict(sa=(1 << 16, 1 << 15, 64)), mm.ERR_TOO_LARGE),
+    (dict(sa=(1 << 30, 64), sb=(64, 1 << 11)), mm.ERR_TOO_LARGE),
     (dict(force_algo=mm.ALGO_DIRECT), mm.ERR_BAD_OPTION), (dict(force_algo=mm.ALGO_SKINNY_N), mm.ERR_BAD_OPTION),
     (dict(sa=(33, 64), force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
     (dict(sa=(2, 4, 64), sb=(2, 64, 32), force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
@@ -184,6 +187,7 @@ def test_quantize_rows_refusals():
     assert f(8, mm.DOUBLE, 4, 4, 8, 8, None) == mm.ERR_DTYPE
     assert f(8, mm.INT8, 4, 4, 8, 8, None) == mm.ERR_DTYPE
     assert f(8, mm.FLOAT, 1 << 31, 4, 8, 8, None) == mm.ERR_TOO_LARGE
+    assert f(8, mm.FLOAT, 1 << 30, 1 << 12, 8, 8, None) == mm.ERR_TOO_LARGE
     for args in ((None, 8, 8), (8, None, 8), (8, 8, None)):
         assert f(args[0], mm.FLOAT, 4, 4, args[1], args[2], None) == mm.ERR_NULL_ARG
     assert f(None, mm.FLOAT, 0, 4, None, None, None) == 0
