@@ -3,20 +3,22 @@
 // shared by their plans and kernels.
 #pragma once
 
+#include <hip/hip_runtime.h>
+
 #include "internal.h"
 
 namespace mm {
 
-// Operands of the tiled products (k_ffn.h) and the few-row kernels
-// (k_ffn_rows.hip).  A and B hold two matrices where the mode has two.
+// One call's operands, as the plans give them to the launchers.  A and B hold
+// two matrices where the mode has two.
 struct FfnArgs {
     const void *A[2];
     const void *B[2];
     void *Y[2];
     void *G, *U;           // gated block: where to keep A B0 and A B1 (NULL: nowhere)
-    int64_t M, N, K;
+    int64_t M, N, K;       // below 2^31, like the pitches
     int64_t lda, ldb, ldy;  // row pitches of the stored operands and of Y, G, U
-    int64_t batch;         // products (kScaled), or 2 for a pair
+    int64_t batch;         // products (scaled), or 2 for a pair
     int32_t act;
     int32_t y_vec;         // output rows are whole, aligned 16-byte chunks
     // scaled INT8 product
@@ -28,6 +30,32 @@ struct FfnArgs {
     BatchDesc bd;
 };
 
+// The same as the kernels take it: in 88 bytes, because a launch with more
+// than about 100 bytes of arguments takes 0.8-1.1 us longer (2.8 us with 96,
+// 3.5 with 128, 3.8 with 384), which a decoded token's call feels.  Slots that
+// a mode leaves free hold what others need; the names below say which.
+struct FfnSlim {
+    const void *A[2];
+    const void *B[2];
+    void *Y[3];
+    int32_t M, N, K, lda, ldb, ldy;
+    int32_t kstages;
+    uint16_t split;
+    uint8_t act, y_vec;
+    __host__ __device__ void *G() const { return Y[1]; }  // gated block
+    __host__ __device__ void *U() const { return Y[2]; }
+    __host__ __device__ const float *sa() const { return (const float *)A[1]; }  // scaled product
+    __host__ __device__ const float *sb() const { return (const float *)B[1]; }
+    __host__ __device__ const void *bias() const { return Y[1]; }
+    __host__ __device__ void *part() const { return Y[0]; }     // split products write their partial sums instead of Y
+    __host__ __device__ const void *W() const { return A[0]; }  // reductions read them
+};
+static_assert(sizeof(FfnSlim) == 88, "FfnSlim");
+struct FfnSlimBatch : FfnSlim {  // scaled products over several batches
+    int64_t batch;
+    BatchDesc bd;
+};
+
 // Tile table of the tiled products: block rows and columns (the gated
 // block's columns count gate and up) and the bytes of K in a stage, see
 // k_ffn.h.
@@ -36,6 +64,46 @@ struct FfnTile {
 };
 constexpr FfnTile kFfnTiles[] = {{256, 256, 64}, {128, 128, 64}, {64, 128, 128}, {32, 128, 256}, {256, 128, 128}};
 constexpr int kNumFfnTiles = sizeof(kFfnTiles) / sizeof(kFfnTiles[0]);
+
+// Kernel arguments of a product (glu, scaled: which slots it needs), of a
+// split one (its partial sums) and of its reduction.
+enum FfnUse { kUsePlain, kUseGlu, kUseScaled };
+template <class T>
+inline T slim_args(const FfnArgs &a, FfnUse use, bool split, bool reduce) {
+    T s = {};
+    for (int i = 0; i < 2; ++i) {
+        s.A[i] = a.A[i];
+        s.B[i] = a.B[i];
+        s.Y[i] = a.Y[i];
+    }
+    s.M = (int32_t)a.M;
+    s.N = (int32_t)a.N;
+    s.K = (int32_t)a.K;
+    s.lda = (int32_t)a.lda;
+    s.ldb = (int32_t)a.ldb;
+    s.ldy = (int32_t)a.ldy;
+    s.kstages = a.kstages;
+    s.split = (uint16_t)a.split;
+    s.act = (uint8_t)a.act;
+    s.y_vec = (uint8_t)a.y_vec;
+    if (use == kUseGlu) {
+        s.Y[1] = a.G;
+        s.Y[2] = a.U;
+    } else if (use == kUseScaled) {
+        s.A[1] = a.sa;
+        s.B[1] = a.sb;
+        s.Y[1] = (void *)a.bias;
+    }
+    if (split) s.Y[0] = a.W;
+    if (reduce) s.A[0] = a.W;
+    return s;
+}
+inline FfnSlimBatch slim_batch(const FfnArgs &a, bool split, bool reduce) {
+    FfnSlimBatch s = slim_args<FfnSlimBatch>(a, kUseScaled, split, reduce);
+    s.batch = a.batch;
+    s.bd = a.bd;
+    return s;
+}
 
 // Element-wise part of the gated block's backward pass: dG = dH * U * f'(G),
 // dU = dH * f(G).  G, U, dH are dense [M, N]; dG, dU have rows of ldw elements

@@ -52,11 +52,12 @@ __device__ __forceinline__ int row_swizzle(int k, int cpr) {
 // operands: INT32) partial sums to the workspace.
 // KG groups of WGM x WGN waves share the tile; group g takes every KG-th MFMA
 // step of a stage, and their sums are added in group order at the end.
+// BATCH (kScaled): more than one product.
 enum FfnMode { kGlu = 0, kSum2 = 1, kPair = 2, kScaled = 3 };
 
 template <int DT, int OD, int MODE, bool SPLIT, bool TA, bool TB, int BM, int BN, int WGM, int WGN, int KG, int BKB,
-          int STAGES, int PW, bool DMA>
-__global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
+          int STAGES, int PW, bool DMA, bool BATCH>
+__global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::conditional<BATCH, FfnSlimBatch, FfnSlim>::type a) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using E = Elem<DT>;
     using S = typename E::S;
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
     const int64_t m0 = tm * BM, n0 = tn * PN;
 
     int64_t oa = 0, ob = 0;
-    if constexpr (INT) batch_offsets(a.bd, b, oa, ob);
+    if constexpr (BATCH) batch_offsets(a.bd, b, oa, ob);
     // Tile origins of the two A and B operands (the modes that have one use [0]).
     const int64_t ta_off = oa + (TA ? m0 : m0 * a.lda), tb_off = ob + (TB ? n0 * a.ldb : n0);
     const int pick = MODE == kPair ? (int)b : 0;
@@ -567,16 +568,18 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
     auto plain = [](int, int, auto v) { return (float)v; };
     if constexpr (SPLIT && MODE == kGlu) {
         // Partials of G, then of U, for every partition.
-        float *w = (float *)a.W + sidx * 2 * M * N;
+        float *w = (float *)a.part() + sidx * 2 * M * N;
         emit(0.0f, 0, plain, w, N, N % 4 == 0);
         emit(0.0f, FNP, plain, w + M * N, N, N % 4 == 0);
     } else if constexpr (SPLIT) {
         using T = typename std::conditional<INT, int32_t, float>::type;
-        emit((T)0, 0, plain, (T *)a.W + (sidx * a.batch + b) * M * N, N, N % 4 == 0);
+        int64_t nprod = MODE == kPair ? 2 : 1;
+        if constexpr (BATCH) nprod = a.batch;
+        emit((T)0, 0, plain, (T *)a.part() + (sidx * nprod + b) * M * N, N, N % 4 == 0);
     } else if constexpr (MODE == kGlu) {
-        if (a.G) {
-            emit((typename OE::S)0, 0, plain, a.G, a.ldy, a.y_vec != 0);
-            emit((typename OE::S)0, FNP, plain, a.U, a.ldy, a.y_vec != 0);
+        if (a.G()) {
+            emit((typename OE::S)0, 0, plain, a.G(), a.ldy, a.y_vec != 0);
+            emit((typename OE::S)0, FNP, plain, a.U(), a.ldy, a.y_vec != 0);
         }
         auto apply = [&](auto kind) {
 #pragma unroll
@@ -603,14 +606,14 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(FfnArgs a) {
         const int64_t sb0 = ob / kd + n0;  // scale of column n of B matrix i: i N + n
         for (int x = tid; x < PN; x += NT) {
             const bool in = n0 + x < N;
-            cs[x] = in ? a.sb[sb0 + x] : 0.0f;
-            cb[x] = in && a.bias ? OE::to_f32(((const typename OE::S *)a.bias)[n0 + x]) : 0.0f;
+            cs[x] = in ? a.sb()[sb0 + x] : 0.0f;
+            cb[x] = in && a.bias() ? OE::to_f32(((const typename OE::S *)a.bias())[n0 + x]) : 0.0f;
         }
         float rs[FM];
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int64_t row = m0 + wr * WM + i * 32 + (lane & 31);
-            rs[i] = row < M ? a.sa[oa / a.lda + row] : 0.0f;
+            rs[i] = row < M ? a.sa()[oa / a.lda + row] : 0.0f;
         }
         __syncthreads();
         emit((typename OE::S)0, 0, [&](int i, int cl, int v) { return scaled_value(v, rs[i], cs[cl], cb[cl]); },
@@ -635,13 +638,24 @@ static hipError_t launch_ffn(bool vec, const FfnArgs &a, hipStream_t s) {
     const int64_t b_span = (TB ? (int64_t)PN : (int64_t)(BKB / ES)) * a.ldb;
     const bool fits = a_span * ES < 0x7fff0000LL && b_span * ES < 0x7fff0000LL;
     const dim3 g((unsigned)tiles), blk(64 * WGM * WGN * KG);
-    if (vec && fits)
-        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, SPLIT, TA, TB, BM, BN, WGM, WGN, KG, BKB, STAGES, PW, true>), g, blk, 0, s, a);
-    else if constexpr (BM * BN < 256 * 256)
-        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, SPLIT, TA, TB, BM, BN, WGM, WGN, KG, BKB, STAGES, PW, false>), g, blk, 0, s, a);
-    else  // the register-staged form would not fit the registers of this tile
-        return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 128, 128, 2, 2, 1, 64, 4, 4>(false, a, s);
-    return hipGetLastError();
+    auto go = [&](auto dma) {
+        constexpr bool D = decltype(dma)::value;
+        if constexpr (MODE == kScaled) {
+            if (a.batch != 1) {
+                hipLaunchKernelGGL((k_ffn<DT, OD, MODE, SPLIT, TA, TB, BM, BN, WGM, WGN, KG, BKB, STAGES, PW, D, true>), g,
+                                   blk, 0, s, slim_batch(a, SPLIT, false));
+                return hipGetLastError();
+            }
+        }
+        const FfnUse use = MODE == kGlu ? kUseGlu : MODE == kScaled ? kUseScaled : kUsePlain;
+        hipLaunchKernelGGL((k_ffn<DT, OD, MODE, SPLIT, TA, TB, BM, BN, WGM, WGN, KG, BKB, STAGES, PW, D, false>), g, blk,
+                           0, s, slim_args<FfnSlim>(a, use, SPLIT, false));
+        return hipGetLastError();
+    };
+    if (vec && fits) return go(std::true_type());
+    if constexpr (BM * BN < 256 * 256) return go(std::false_type());
+    // The register-staged form would not fit the registers of this tile.
+    return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 128, 128, 2, 2, 1, 64, 4, 4>(false, a, s);
 }
 
 // The entries of kFfnTiles for one kind of product.

@@ -34,7 +34,7 @@ namespace mm {
 typedef int i32x4v __attribute__((ext_vector_type(4)));
 
 template <int DT, int OD, bool GLU, bool KN, int NF, int MB, int NWV, int XQ>
-__global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn_rows(FfnArgs a) {
+__global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 4 ? 3 : 4) void k_ffn_rows(FfnSlim a) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using E = Elem<DT>;
     using S = typename E::S;
@@ -63,7 +63,6 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
     // 4096, N = 11008: 41.4 us so, 38.9 spread; M = 13, K = 2048, N = 5461:
     // 13.2 and 14.9; INT8, K = N = 4096: 6.6 and 7.6).
     const int64_t n0 = (GLU && !KN && NWV == 4 ? (int64_t)blockIdx.x : xcd_remap(blockIdx.x, gridDim.x)) * COLS;
-    const int64_t nb = K / BK;  // whole blocks
 
     // ---- weights
     // [N, K]: fragment f of a lane is row n0 + 16 (f % CF) + r of its panel;
@@ -337,9 +336,9 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
                 sg += red[v][c >> 4][i][at];
                 su += red[v][CF + (c >> 4)][i][at];
             }
-            if (a.G) {
-                ((OS *)a.G)[o] = OE::from_f32(sg);
-                ((OS *)a.U)[o] = OE::from_f32(su);
+            if (a.G()) {
+                ((OS *)a.G())[o] = OE::from_f32(sg);
+                ((OS *)a.U())[o] = OE::from_f32(su);
             }
             constexpr bool X = DT == MM_FLOAT;
             float f;
@@ -355,9 +354,9 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : 4) void k_ffn
             int sum = 0;
 #pragma unroll
             for (int v = 0; v < NWV; ++v) sum += (int)red[v][c >> 4][i][at];
-            const float bias = a.bias ? OE::to_f32(((const OS *)a.bias)[n]) : 0.0f;
-            const float sa = XQ ? quant_scale(xtop[XQ ? m16 : 0]) : a.sa[m];
-            ((OS *)a.Y[0])[o] = OE::from_f32(scaled_value(sum, sa, a.sb[n], bias));
+            const float bias = a.bias() ? OE::to_f32(((const OS *)a.bias())[n]) : 0.0f;
+            const float sa = XQ ? quant_scale(xtop[XQ ? m16 : 0]) : a.sa()[m];
+            ((OS *)a.Y[0])[o] = OE::from_f32(scaled_value(sum, sa, a.sb()[n], bias));
         }
     }
 #endif
@@ -378,7 +377,8 @@ static hipError_t launch_rows(const FfnArgs &a, hipStream_t s) {
     if constexpr (!KN && NWV == 8) {
         if (wgs > kRowsFit) return launch_rows<DT, OD, GLU, KN, NF, MB, 4, XQ>(a, s);
     }
-    hipLaunchKernelGGL((k_ffn_rows<DT, OD, GLU, KN, NF, MB, NWV, XQ>), dim3((unsigned)wgs), dim3(64 * NWV), 0, s, a);
+    hipLaunchKernelGGL((k_ffn_rows<DT, OD, GLU, KN, NF, MB, NWV, XQ>), dim3((unsigned)wgs), dim3(64 * NWV), 0, s,
+                       slim_args<FfnSlim>(a, GLU ? kUseGlu : kUseScaled, false, false));
     return hipGetLastError();
 }
 

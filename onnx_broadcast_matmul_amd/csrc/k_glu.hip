@@ -45,14 +45,14 @@ __device__ __forceinline__ float act_switch(int act, float g) {
 // then the tiled kernel's epilogue.  A thread owns four consecutive elements
 // of the dense [M, N] outputs.
 template <int DT>
-__global__ __launch_bounds__(256) void k_glu_reduce(FfnArgs a) {
+__global__ __launch_bounds__(256) void k_glu_reduce(FfnSlim a) {
     using E = Elem<DT>;
     using S = typename E::S;
-    const int64_t total = a.M * a.N;
+    const int64_t total = (int64_t)a.M * a.N;
     const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i0 >= total) return;
     const int n = total - i0 < 4 ? (int)(total - i0) : 4;
-    const float *w = (const float *)a.W + i0;
+    const float *w = (const float *)a.W() + i0;
     float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (total % 4 == 0) {
 #pragma unroll 4
@@ -83,9 +83,9 @@ __global__ __launch_bounds__(256) void k_glu_reduce(FfnArgs a) {
         else
             for (int e = 0; e < n; ++e) y[e] = v[e];
     };
-    if (a.G) {
-        put(a.G, og);
-        put(a.U, ou);
+    if (a.G()) {
+        put(a.G(), og);
+        put(a.U(), ou);
     }
     put(a.Y[0], oh);
 }
@@ -95,26 +95,27 @@ hipError_t launch_glu_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
     if (g <= 0) return hipSuccess;
     if (g > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 gr((unsigned)g), bl(256);
-    if (dtype == MM_FLOAT) hipLaunchKernelGGL(k_glu_reduce<MM_FLOAT>, gr, bl, 0, s, a);
-    else if (dtype == MM_FLOAT16) hipLaunchKernelGGL(k_glu_reduce<MM_FLOAT16>, gr, bl, 0, s, a);
-    else hipLaunchKernelGGL(k_glu_reduce<MM_BFLOAT16>, gr, bl, 0, s, a);
+    const FfnSlim r = slim_args<FfnSlim>(a, kUseGlu, false, true);
+    if (dtype == MM_FLOAT) hipLaunchKernelGGL(k_glu_reduce<MM_FLOAT>, gr, bl, 0, s, r);
+    else if (dtype == MM_FLOAT16) hipLaunchKernelGGL(k_glu_reduce<MM_FLOAT16>, gr, bl, 0, s, r);
+    else hipLaunchKernelGGL(k_glu_reduce<MM_BFLOAT16>, gr, bl, 0, s, r);
     return hipGetLastError();
 }
 
 // Sum of the K partitions' FP32 partials in partition order, narrowed once;
-// product b (blockIdx.y) of a.batch goes to Y[b], rows ldy elements apart.  A
+// product b (blockIdx.y of gridDim.y) goes to Y[b], rows ldy elements apart.  A
 // thread owns four consecutive columns of one row.
 template <int DT>
-__global__ __launch_bounds__(256) void k_sum_reduce(FfnArgs a) {
+__global__ __launch_bounds__(256) void k_sum_reduce(FfnSlim a) {
     using E = Elem<DT>;
     using S = typename E::S;
     const uint32_t N = (uint32_t)a.N, cpr = (N + 3) / 4;
     const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (x >= a.M * cpr) return;
+    if (x >= (int64_t)a.M * cpr) return;
     const int64_t row = x < 0x7fffffff ? (int64_t)((uint32_t)x / cpr) : x / cpr;
     const uint32_t col = (uint32_t)(x - row * cpr) * 4;
-    const int64_t stride = a.batch * a.M * N;
-    const float *w = (const float *)a.W + (int64_t)blockIdx.y * a.M * N + row * N + col;
+    const int64_t stride = (int64_t)gridDim.y * a.M * N;
+    const float *w = (const float *)a.W() + (int64_t)blockIdx.y * a.M * N + row * N + col;
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     S *y = (S *)a.Y[blockIdx.y] + row * a.ldy + col;
     if (N % 4 == 0) {
@@ -144,9 +145,10 @@ hipError_t launch_sum_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
     if (g <= 0 || a.batch <= 0) return hipSuccess;
     if (g > 0x7fffffff) return hipErrorInvalidValue;
     const dim3 gr((unsigned)g, (unsigned)a.batch), bl(256);
-    if (dtype == MM_FLOAT) hipLaunchKernelGGL(k_sum_reduce<MM_FLOAT>, gr, bl, 0, s, a);
-    else if (dtype == MM_FLOAT16) hipLaunchKernelGGL(k_sum_reduce<MM_FLOAT16>, gr, bl, 0, s, a);
-    else hipLaunchKernelGGL(k_sum_reduce<MM_BFLOAT16>, gr, bl, 0, s, a);
+    const FfnSlim r = slim_args<FfnSlim>(a, kUsePlain, false, true);
+    if (dtype == MM_FLOAT) hipLaunchKernelGGL(k_sum_reduce<MM_FLOAT>, gr, bl, 0, s, r);
+    else if (dtype == MM_FLOAT16) hipLaunchKernelGGL(k_sum_reduce<MM_FLOAT16>, gr, bl, 0, s, r);
+    else hipLaunchKernelGGL(k_sum_reduce<MM_BFLOAT16>, gr, bl, 0, s, r);
     return hipGetLastError();
 }
 

@@ -23,6 +23,9 @@ static mm_status launched(hipError_t e) {
 // then stay in range (and the memory of any device is smaller).
 static bool too_large(int64_t rows, int64_t cols) { return (double)rows * (double)cols > 1099511627776.0; }
 
+// Sizes and pitches, rounded up to whole chunks, are 32-bit in the kernels.
+constexpr int64_t kMaxSize = (int64_t)INT32_MAX - 64;
+
 static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
 
 // Time model of the tiled products: a CU runs up to kOcc workgroups of an
@@ -110,7 +113,7 @@ static FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t
 // A requested number of partitions for an entry, as whole stages.
 static void set_split(FfnChoice *c, int64_t kbytes, int terms, int64_t split) {
     const int64_t stages = std::max<int64_t>(1, terms * cdiv(kbytes, kFfnTiles[c->tile].bkb));
-    const int64_t per = cdiv(stages, std::max<int64_t>(1, std::min<int64_t>(split, stages)));
+    const int64_t per = cdiv(stages, std::max<int64_t>(1, std::min<int64_t>({split, stages, 4096})));
     c->kstages = (int32_t)per;
     c->split = (int32_t)cdiv(stages, per);
 }
@@ -208,8 +211,8 @@ mm_status mm_scaled_int_plan_create(const int64_t *a_shape, int a_rank, const in
         double a_rows = 1.0;
         for (int i = 0; i + 1 < a_rank; ++i) a_rows *= (double)a_shape[i];
         if (a_rows > INT32_MAX || too_large(p->batch * p->kernel_m, p->N) || too_large(p->K, p->N) ||
-            a_rows * (double)p->K > 1099511627776.0)
-            st = fail(MM_ERR_TOO_LARGE, "a matrix of more than 2^40 elements, or an A of 2^31 rows or more");
+            a_rows * (double)p->K > 1099511627776.0 || p->kernel_m > kMaxSize || p->N > kMaxSize)
+            st = fail(MM_ERR_TOO_LARGE, "a matrix of more than 2^40 elements, or a size of 2^31 - 64 or more");
     }
     if (st == MM_OK && p->out_numel == 0) {
         p->algo = MM_ALGO_EMPTY;
@@ -322,8 +325,8 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
     if (d->w_pitch != 0 && d->w_pitch < row)
         return fail(MM_ERR_BAD_OPTION, "w_pitch %lld is below the weights' row length %lld", (long long)d->w_pitch,
                     (long long)row);
-    if (M > INT32_MAX || K > INT32_MAX || N > INT32_MAX || d->w_pitch > INT32_MAX)
-        return fail(MM_ERR_TOO_LARGE, "rows, in_features, hidden and w_pitch must each be below 2^31");
+    if (M > kMaxSize || K > kMaxSize || N > kMaxSize || d->w_pitch > kMaxSize)
+        return fail(MM_ERR_TOO_LARGE, "rows, in_features, hidden and w_pitch must each be below 2^31 - 64");
     if (too_large(M, K) || too_large(M, N) || too_large(K, N) || too_large(d->trans_w ? N : K, d->w_pitch))
         return fail(MM_ERR_TOO_LARGE, "a matrix of more than 2^40 elements");
     const int force = opt ? opt->force_algo : MM_ALGO_AUTO;
