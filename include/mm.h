@@ -330,12 +330,12 @@ mm_status mm_int_execute(mm_plan_t plan, const void *A, const void *B, const voi
  *
  * Options: force_algo SKINNY_M (one product, after folding, of at most 32
  * rows), GENERAL or SPLIT_K; tile k >= 1 is entry k of 256 x 256 (not
- * split), 128 x 128, 64 x 128, 32 x 128, 256 x 128; split_k as for MatMul.  A plan with an A to
- * quantize or a split K may own a workspace (mm_plan_workspace_bytes > 0):
- * its executions must then not overlap, and it is allocated and bound to a
- * device as described above.  Matrices hold at most 2^40 elements, and sizes
- * lie below 2^31 - 64 (MM_ERR_TOO_LARGE).  Other errors
- * are those of mm_plan_create. */
+ * split), 128 x 128, 64 x 128, 32 x 128, 256 x 128; split_k as for MatMul.  A
+ * plan with an A to quantize or a split K may own a workspace
+ * (mm_plan_workspace_bytes > 0): its executions must then not overlap, and it
+ * is allocated and bound to a device as described above.  Matrices hold at
+ * most 2^40 elements, sizes lie below 2^31 - 64, and a launch has less than
+ * 2^32 threads (MM_ERR_TOO_LARGE).  Other errors are those of mm_plan_create. */
 typedef struct mm_scaled_int_desc {
     int32_t a_type;   /* MM_INT8, or the type of an A to be quantized */
     int32_t out_type; /* MM_FLOAT, MM_FLOAT16 or MM_BFLOAT16 */
@@ -411,7 +411,7 @@ typedef struct mm_glu_desc {
 
 /* Create a gated-block plan.  MM_ERR_NEG_DIM, MM_ERR_DTYPE, MM_ERR_BAD_OPTION
  * (an invalid field or option), MM_ERR_TOO_LARGE (a size of 2^31 - 64 or more,
- * or a matrix of more than 2^40 elements), MM_ERR_ALLOC.  A plan that splits K
+ * a matrix of more than 2^40 elements, or a launch of 2^32 threads), MM_ERR_ALLOC.  A plan that splits K
  * in the forward pass (algorithm SPLIT_K) or is for training owns a
  * workspace, allocated and bound to a device as described above; executions
  * that use it (split forward passes, backward passes) must not overlap with

@@ -16,7 +16,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows(const void *X, int64_t ro
     constexpr int VE = E::kVE;
     constexpr int RPW = 256 / TPR;
     const int t = threadIdx.x % TPR;
-    const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
+    const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RPW + threadIdx.x / TPR;
     const bool live = row < rows;  // all threads reach the barrier
     const S *x = (const S *)X + (live ? row : 0) * cols;
     uint4 keep[CH];
@@ -63,8 +63,10 @@ static hipError_t quantize(const void *X, int64_t rows, int64_t cols, void *Q, i
     const bool narrow = ldq <= 64 * 4 * VE;
     const int64_t g = narrow ? (rows + 3) / 4 : rows;
     if (g <= 0) return hipSuccess;
-    if (g > 0x7fffffff) return hipErrorInvalidValue;
-    const dim3 gr((unsigned)g), bl(256);
+    // One dimension of a grid holds less than 2^32 threads.
+    const int64_t gx = g < (1 << 23) ? g : (1 << 23), gy = (g + gx - 1) / gx;
+    if (gy > 65535) return hipErrorInvalidValue;
+    const dim3 gr((unsigned)gx, (unsigned)gy), bl(256);
     if (narrow) hipLaunchKernelGGL((k_quantize_rows<DT, 64, 4>), gr, bl, 0, s, X, rows, cols, (int8_t *)Q, ldq, scale);
     else if (ldq <= 256 * 2 * VE) hipLaunchKernelGGL((k_quantize_rows<DT, 256, 2>), gr, bl, 0, s, X, rows, cols, (int8_t *)Q, ldq, scale);
     else hipLaunchKernelGGL((k_quantize_rows<DT, 256, 8>), gr, bl, 0, s, X, rows, cols, (int8_t *)Q, ldq, scale);

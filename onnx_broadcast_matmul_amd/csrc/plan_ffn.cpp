@@ -26,6 +26,18 @@ static bool too_large(int64_t rows, int64_t cols) { return (double)rows * (doubl
 // Sizes and pitches, rounded up to whole chunks, are 32-bit in the kernels.
 constexpr int64_t kMaxSize = (int64_t)INT32_MAX - 64;
 
+// A launch has at most 2^32 - 1 threads.
+static bool launchable(double wgs, int threads) { return wgs * threads < 4294967296.0; }
+
+// Whether an entry's grid for `batch` products of M x cols can be launched.
+// Operands that are not 16-byte aligned run entry 1 in entry 0's place: four
+// times its workgroups, of half its size.
+static bool tile_launchable(const FfnChoice &c, int64_t batch, int64_t M, int64_t cols) {
+    const FfnTile &t = kFfnTiles[c.tile];
+    const double wgs = (double)batch * (double)cdiv(M, t.bm) * (double)cdiv(cols, t.bn) * c.split;
+    return launchable(c.tile == 0 ? 4.0 * wgs : wgs, c.tile <= 1 ? 256 : 512);
+}
+
 static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
 
 // Time model of the tiled products: a CU runs up to kOcc workgroups of an
@@ -153,6 +165,7 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && K > 0 && treq == 0 && sreq == 0 &&
                                       rows_us(kClass8, p->tb != 0, M, K, wbytes) <= tiles_us(kClass8, c, wbytes))) {
         p->algo = MM_ALGO_SKINNY_M;
+        if (!launchable((double)cdiv(N, 16), 512)) return fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
         return MM_OK;
     }
     if (may_split && sreq > 0) set_split(&c, K, 1, sreq);
@@ -164,8 +177,7 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
         p->kchunk = (int64_t)c.kstages * kFfnTiles[c.tile].bkb;
         p->workspace_bytes = round_up((int64_t)p->split * p->batch * M * N * 4, 256);
     }
-    const int64_t wgs = p->batch * cdiv(M, kFfnTiles[p->tile].bm) * cdiv(N, kFfnTiles[p->tile].bn);
-    if (wgs * p->split > INT32_MAX) return fail(MM_ERR_TOO_LARGE, "too many workgroups (%lld)", (long long)wgs);
+    if (!tile_launchable(c, p->batch, M, N)) return fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
     return MM_OK;
 }
 
@@ -373,19 +385,21 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && treq == 0 && sreq == 0 &&
                                           rows_us(cls, p->tb != 0, M, K * es, wbytes) <= tiles_us(cls, c, wbytes))) {
             p->algo = MM_ALGO_SKINNY_M;
+            if (!launchable((double)cdiv(N, 8), 512)) st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
         } else {
             if (may_split && sreq > 0) set_split(&c, K * es, 1, sreq);
             p->tile = c.tile;
             p->split = c.split;
             p->kstages = c.kstages;
             p->algo = c.split > 1 ? MM_ALGO_SPLIT_K : MM_ALGO_GENERAL;
+            if (!tile_launchable(c, 1, M, 2 * N)) st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
             if (c.split > 1) {
                 p->kchunk = (int64_t)c.kstages * kFfnTiles[c.tile].bkb / es;
                 p->workspace_bytes = round_up((int64_t)c.split * 2 * M * N * 4, 256);
             }
         }
     }
-    if (p->training) {
+    if (st == MM_OK && p->training) {
         p->d_off = p->workspace_bytes;
         p->d_pitch = round_up(N, 16 / es);
         p->d_bytes = round_up(M * p->d_pitch * es, 256);
@@ -395,12 +409,15 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         const bool dx_al = (p->w_pitch * es) % 16 == 0 && ((p->tb ? K : N) * es) % 16 == 0, dw_al = (K * es) % 16 == 0;
         p->dx = choose(cls, dx_al, 1, M, K, N * es, 2, dx_tiles, true);
         p->dw = choose(cls, dw_al, 2, p->tb ? N : K, p->tb ? K : N, M * es, 1, dw_tiles, true);
+        if (!tile_launchable(p->dx, 1, M, K) || !tile_launchable(p->dw, 2, p->tb ? N : K, p->tb ? K : N) ||
+            !launchable((double)M * (double)cdiv(p->d_pitch * es, 16), 1))
+            st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
         int64_t part = 0;
         if (p->dx.split > 1) part = (int64_t)p->dx.split * M * K * 4;
         if (p->dw.split > 1) part = std::max(part, (int64_t)p->dw.split * 2 * K * N * 4);
         p->workspace_bytes += 2 * p->d_bytes + part;
     }
-    st = alloc_workspace(p, true);
+    if (st == MM_OK) st = alloc_workspace(p, true);
     if (st != MM_OK) {
         delete p;
         return st;

@@ -37,6 +37,10 @@ def scaled(sa=(4, 64), sb=(64, 32), out=mm.BFLOAT16, **kw):
     (dict(rows=1 << 31), mm.ERR_TOO_LARGE), (dict(k=1 << 31), mm.ERR_TOO_LARGE), (dict(n=1 << 31), mm.ERR_TOO_LARGE),
     (dict(rows=1 << 30, n=1 << 11), mm.ERR_TOO_LARGE), (dict(k=1 << 30, n=1 << 11, rows=1), mm.ERR_TOO_LARGE),
     (dict(k=1 << 12, n=4, w_pitch=1 << 30), mm.ERR_TOO_LARGE),
+    # grids of more than 2^32 threads: few rows, tiles, the two gradients
+    (dict(rows=1, k=1, n=1 << 30), mm.ERR_TOO_LARGE), (dict(rows=100, k=1, n=1 << 30), mm.ERR_TOO_LARGE),
+    (dict(rows=1 << 30, k=1 << 9, n=1, training=True), mm.ERR_TOO_LARGE),
+    (dict(rows=1, k=1 << 20, n=1 << 20, training=True), mm.ERR_TOO_LARGE),
     (dict(force_algo=mm.ALGO_SKINNY_N), mm.ERR_BAD_OPTION), (dict(force_algo=mm.ALGO_DIRECT), mm.ERR_BAD_OPTION),
     (dict(split_k=-1), mm.ERR_BAD_OPTION), (dict(tile=1, split_k=2), mm.ERR_BAD_OPTION),
     (dict(tile=1, force_algo=mm.ALGO_SPLIT_K), mm.ERR_BAD_OPTION), (dict(rows=33, force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
@@ -121,6 +125,9 @@ def test_glu_backward_workspace_holds_the_largest_split():
     (dict(sa=(64,), sb=(64,), trans_b=True), mm.ERR_BAD_OPTION),
     (dict(sa=(1, 131072), sb=(131072, 1)), mm.ERR_TOO_LARGE), (dict(sa=(1 << 16, 1 << 15, 64)), mm.ERR_TOO_LARGE),
     (dict(sa=(1 << 30, 64), sb=(64, 1 << 11)), mm.ERR_TOO_LARGE),
+    # grids of more than 2^32 threads: few rows, tiles, products of a batch
+    (dict(sa=(1, 1), sb=(1, 1 << 30)), mm.ERR_TOO_LARGE), (dict(sa=(1000, 1), sb=(1, 1 << 30)), mm.ERR_TOO_LARGE),
+    (dict(sa=(1 << 25, 4, 64), sb=(1 << 25, 64, 32)), mm.ERR_TOO_LARGE),
     (dict(force_algo=mm.ALGO_DIRECT), mm.ERR_BAD_OPTION), (dict(force_algo=mm.ALGO_SKINNY_N), mm.ERR_BAD_OPTION),
     (dict(sa=(33, 64), force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),
     (dict(sa=(2, 4, 64), sb=(2, 64, 32), force_algo=mm.ALGO_SKINNY_M), mm.ERR_BAD_OPTION),

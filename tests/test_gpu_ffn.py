@@ -417,6 +417,15 @@ def test_quantize_rows_special_values(dt, dev):
     assert mm.quantize_rows(torch.empty(0, 5, dtype=t, device=dev))[1].shape == (0,)
 
 
+def test_quantize_more_rows_than_one_grid_dimension_covers(dev):
+    """2^26 rows and some: more than 2^32 threads."""
+    n = (1 << 26) // 7 + 3
+    x = torch.tensor([[0.0], [1.0], [-2.5], [float("inf")], [0.1], [-100.0], [2.0 ** -14]], dtype=F16, device=dev)
+    q, s = mm.quantize_rows(x)
+    many_q, many_s = mm.quantize_rows(x.repeat(n, 1))
+    assert torch.equal(many_q, q.repeat(n, 1)) and torch.equal(many_s.view(torch.int32), s.view(torch.int32).repeat(n))
+
+
 # ---- scaled INT8 product
 
 
