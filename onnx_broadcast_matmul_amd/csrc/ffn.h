@@ -126,6 +126,14 @@ hipError_t launch_scaled_reduce(int out_dtype, const FfnArgs &a, hipStream_t s);
 // it itself (`quant`); its INT8 rows then fit kFfnQuantLds bytes of LDS.
 constexpr int kFfnRows = 32;
 constexpr int kFfnQuantLds = 48 * 1024;
+// Workgroups of [K, N] weights take 64 columns (the gated block: 32 of each
+// matrix), and half as many as long as all still start at once: a workgroup
+// reads its columns at what one CU gets from memory, which more CUs multiply,
+// but row pieces below 64 bytes cost more than they bring once every CU has
+// one (M = 1, K = 4096, INT8: N = 4096 with 64, 32 and 16 columns 10.9, 9.4 and
+// 7.8 us, N = 1024 9.5, 7.9 and 6.1, N = 11008 10.8, 14.7 and 18.3; BF16 gated,
+// N = 4096 with 32 and 16: 31.3 and 27.5, N = 11008: 52.9 and 62.3).
+inline bool rows_halve(int64_t wgs) { return 2 * wgs <= kNumCUs; }
 hipError_t launch_glu_rows(int dtype, bool tb, const FfnArgs &a, hipStream_t s);
 bool rows_quantize(int a_type, int out_dtype, bool tb, int64_t M, int64_t K, int64_t N);
 hipError_t launch_scaled_rows(int out_dtype, bool tb, bool quant, const FfnArgs &a, hipStream_t s);

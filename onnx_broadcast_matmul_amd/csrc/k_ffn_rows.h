@@ -377,6 +377,9 @@ static hipError_t launch_rows(const FfnArgs &a, hipStream_t s) {
     if constexpr (!KN && NWV == 8) {
         if (wgs > kRowsFit) return launch_rows<DT, OD, GLU, KN, NF, MB, 4, XQ>(a, s);
     }
+    if constexpr (KN && NF > (GLU ? 2 : 1)) {
+        if (rows_halve(wgs)) return launch_rows<DT, OD, GLU, KN, NF / 2, MB, NWV, XQ>(a, s);
+    }
     hipLaunchKernelGGL((k_ffn_rows<DT, OD, GLU, KN, NF, MB, NWV, XQ>), dim3((unsigned)wgs), dim3(64 * NWV), 0, s,
                        slim_args<FfnSlim>(a, GLU ? kUseGlu : kUseScaled, false, false));
     return hipGetLastError();

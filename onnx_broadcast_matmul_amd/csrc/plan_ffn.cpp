@@ -71,16 +71,22 @@ static double est_us(int cls, bool aligned, int tile, double wgs, double steps) 
 }
 
 // Time of the few-row kernel: a workgroup's chain of K (kChain us for each KiB
-// of a weight row, which memory latency sets), or the weights' stream once
-// the workgroups fill the GPU; [weights N x K, K x N][up to 16 rows, more].
-// Fitted to M = 1..32, K = 1000..11008, N = 128..11008.  [K, N] weights come at
-// 18 GB/s per workgroup from memory (3.6 us for each KiB) and twice as fast
-// when the last-level cache holds them from the call before: 2.8 between.
-static double rows_us(int cls, bool nk, int64_t M, int64_t kbytes, double wbytes) {
-    static const double kChain[3][2][2] = {{{1.0, 1.75}, {2.8, 3.2}}, {{0.6, 1.2}, {2.8, 3.2}}, {{1.2, 1.85}, {2.8, 3.2}}};
-    static const double kRate[3][2][2] = {{{4.9, 3.2}, {3.3, 2.9}}, {{3.5, 2.2}, {3.2, 2.5}}, {{4.9, 3.2}, {3.3, 2.9}}};  // TB/s
-    const int o = nk ? 0 : 1, r = M > 16 ? 1 : 0;
-    return std::max(3.0 + kChain[cls][o][r] * (double)kbytes / 1024.0, wbytes / (kRate[cls][o][r] * 1e6));
+// of a weight row, which memory latency sets), or the weights' stream at kRate
+// TB/s once the workgroups fill the GPU; each [up to 16 rows, more].  [K, N]
+// weights: by how often rows_halve halves a workgroup's columns, for the
+// gated block and the INT8 product.  Fitted to M = 1..32, K = 1000..11008, N =
+// 128..11008, weights that come from memory.
+static double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, double wbytes) {
+    static const double kChain[3][2] = {{1.0, 1.75}, {0.6, 1.2}, {1.2, 1.85}}, kRate[3][2] = {{4.9, 3.2}, {3.5, 2.2}, {4.9, 3.2}};
+    static const double kChainKn[2][3][2] = {{{2.8, 3.2}, {1.4, 1.85}, {1.4, 1.85}}, {{2.0, 2.45}, {1.5, 2.0}, {1.35, 1.75}}};
+    static const double kRateKn[2][3][2] = {{{3.6, 3.1}, {2.75, 2.45}, {2.75, 2.45}}, {{5.0, 4.4}, {4.5, 4.0}, {3.5, 3.0}}};
+    const int r = M > 16 ? 1 : 0;
+    const double kib = (double)kbytes / 1024.0;
+    if (nk) return std::max(3.0 + kChain[cls][r] * kib, wbytes / (kRate[cls][r] * 1e6));
+    const int i8 = cls == kClass8 ? 1 : 0;
+    int h = 0;
+    for (int64_t cols = i8 ? 64 : 32; h < 1 + i8 && rows_halve(cdiv(N, cols)); cols /= 2) ++h;
+    return 3.0 + std::max(kChainKn[i8][h][r] * kib, wbytes / (kRateKn[i8][h][r] * 1e6));
 }
 
 // The tiles' time over the same few rows: the weights stream at kStream
@@ -162,8 +168,11 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     const bool aligned = (p->tb ? K : N) % 16 == 0 && (p->a_type != MM_INT8 || K % 16 == 0);
     FfnChoice c = choose(kClass8, aligned, p->batch, M, N, K, 1, tiles, may_split && sreq == 0);
     const double wbytes = (double)K * (double)N;
-    if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && K > 0 && treq == 0 && sreq == 0 &&
-                                      rows_us(kClass8, p->tb != 0, M, K, wbytes) <= tiles_us(kClass8, c, wbytes))) {
+    // The few-row kernel may save the quantization's own launch.
+    const double saved = p->a_type != MM_INT8 && rows_quantize(p->a_type, p->dtype, p->tb != 0, M, K, N) ? 3.0 : 0.0;
+    if (force == MM_ALGO_SKINNY_M ||
+        (force == MM_ALGO_AUTO && rows_ok && K > 0 && treq == 0 && sreq == 0 &&
+         rows_us(kClass8, p->tb != 0, M, N, K, wbytes) <= tiles_us(kClass8, c, wbytes) + saved)) {
         p->algo = MM_ALGO_SKINNY_M;
         if (!launchable((double)cdiv(N, 16), 512)) return fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
         return MM_OK;
@@ -383,7 +392,7 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         FfnChoice c = choose(cls, aligned, 1, M, 2 * N, K * es, 1, tiles, may_split && sreq == 0);
         const double wbytes = 2.0 * (double)K * (double)N * (double)es;
         if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && treq == 0 && sreq == 0 &&
-                                          rows_us(cls, p->tb != 0, M, K * es, wbytes) <= tiles_us(cls, c, wbytes))) {
+                                          rows_us(cls, p->tb != 0, M, N, K * es, wbytes) <= tiles_us(cls, c, wbytes))) {
             p->algo = MM_ALGO_SKINNY_M;
             if (!launchable((double)cdiv(N, 8), 512)) st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
         } else {
