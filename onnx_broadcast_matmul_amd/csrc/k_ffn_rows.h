@@ -15,6 +15,12 @@
 // multiplied.  Rows of any alignment are read in 16-byte pieces; only the end
 // of K goes element by element.
 //
+// UA ([N, K] weights or X with rows off 4-byte alignment, an odd K): 16-byte
+// loads off a dword boundary run at half the rate, so pieces are read from the
+// dword they begin in, with the one behind, and shifted where they are used
+// (M = 3, K = 2561, N = 5530: INT8 14.2 -> 7.8 us, BF16 gated 37.4 -> 26.6; at
+// K = 2560 6.4 and 15.8).
+//
 // XQ (INT8 product): X comes in that float type, and every workgroup
 // quantizes its rows into LDS by mm_quantize_rows' rule while its first
 // weights are on their way.  Two reads of a few rows from cache cost less than
@@ -33,7 +39,7 @@ namespace mm {
 
 typedef int i32x4v __attribute__((ext_vector_type(4)));
 
-template <int DT, int OD, bool GLU, bool KN, int NF, int MB, int NWV, int XQ>
+template <int DT, int OD, bool GLU, bool KN, int NF, int MB, int NWV, int XQ, bool UA>
 __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 4 ? 3 : 4) void k_ffn_rows(FfnSlim a) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using E = Elem<DT>;
@@ -48,7 +54,7 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
     constexpr int NPAN = GLU ? 2 : 1;
     constexpr int CF = NF / NPAN;          // fragments (of 16 columns) of one panel
     constexpr int COLS = 16 * CF;          // output columns of the workgroup
-    constexpr int U = KN ? 2 : 4;          // MFMA steps of a block
+    constexpr int U = KN || (UA && GLU) ? 2 : 4;  // MFMA steps of a block
     constexpr int SK = 4 * VE;             // k of one step: 16 bytes in each of 4 lane groups
     constexpr int BK = U * SK;             // k of a block
     using AccT = typename std::conditional<INT, i32x4v, f32x4>::type;
@@ -71,7 +77,9 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
     constexpr int CPR = COLS / VE;
     constexpr int PIECES = KN ? BK * CPR * NPAN / 64 : NF * U;  // 16-byte pieces per lane and block
     static_assert(!KN || (BK * CPR) % 64 == 0, "whole pieces per lane");
+    static_assert(!UA || (!KN && ES < 4), "only [N, K] rows of narrow types are shifted");
     gptr w[KN ? NPAN : NF];
+    int wsh[UA ? NF : 1];  // UA: bytes from the dword that w points to to the piece
     if constexpr (KN) {
 #pragma unroll
         for (int p = 0; p < NPAN; ++p) w[p] = (gptr)a.B[p] + n0;
@@ -80,11 +88,25 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
         for (int f = 0; f < NF; ++f) {
             const int64_t n = n0 + 16 * (f % CF) + r;
             w[f] = (gptr)a.B[f / CF] + (n < N ? n : N - 1) * a.ldb + g * VE;
+            if constexpr (UA) {
+                wsh[f] = (int)((uintptr_t)w[f] & 3);
+                w[f] -= wsh[f] / ES;
+            }
         }
     }
     const bool back = (KN ? N : K) >= VE;  // weight rows are at least a piece long
     const int64_t left_n = N - n0;
-    auto load_w = [&](int64_t kb, uint4 *t) {
+    // The dword behind a shifted piece's 16 bytes, or (nothing to shift) its
+    // own last one: never beyond the dwords that hold the piece.
+    auto next_dword = [&](gptr p, int sh) {
+        return *(const __attribute__((address_space(1))) uint32_t *)((const __attribute__((address_space(1))) char *)p +
+                                                                    (sh ? 16 : 12));
+    };
+    auto shifted = [&](const uint4 &v, uint32_t e, int sh) {
+        return make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, sh), __builtin_amdgcn_alignbyte(v.z, v.y, sh),
+                          __builtin_amdgcn_alignbyte(v.w, v.z, sh), __builtin_amdgcn_alignbyte(e, v.w, sh));
+    };
+    auto load_w = [&](int64_t kb, uint4 *t, uint32_t *te) {
         const int64_t k0 = kb * BK, krem = K - k0;
         if constexpr (KN) {
             constexpr int PP = PIECES / NPAN;
@@ -112,13 +134,16 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int f = 0; f < NF; ++f) t[u * NF + f] = whole_piece<S>(w[f] + k0 + u * SK);
+                for (int f = 0; f < NF; ++f) {
+                    t[u * NF + f] = whole_piece<S>(w[f] + k0 + u * SK);
+                    if constexpr (UA) te[u * NF + f] = next_dword(w[f] + k0 + u * SK, wsh[f]);
+                }
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int f = 0; f < NF; ++f)
-                    t[u * NF + f] = row_piece<S>(w[f] + k0 + u * SK, krem - (u * 4 + g) * VE, back);
+                    t[u * NF + f] = row_piece<S>(w[f] + (UA ? wsh[f] / ES : 0) + k0 + u * SK, krem - (u * 4 + g) * VE, back);
         }
     };
 
@@ -143,8 +168,10 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
         }
     };
     // Fragment f of step u: 16 bytes of consecutive k of column 16 (f % CF) + r.
-    auto frag_w = [&](const uint4 *t, int u, int f) -> uint4 {
-        if constexpr (!KN) {
+    auto frag_w = [&](const uint4 *t, const uint32_t *te, bool whole, int u, int f) -> uint4 {
+        if constexpr (UA) {
+            return shifted(t[u * NF + f], te[u * NF + f], whole ? wsh[f] : 0);
+        } else if constexpr (!KN) {
             return t[u * NF + f];
         } else {
             const char *P = mine + (f / CF) * BK * RB;
@@ -183,6 +210,7 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
     };
 
     uint4 cur[PIECES], nxt[PIECES];
+    uint32_t cur_e[UA ? PIECES : 1] = {}, nxt_e[UA ? PIECES : 1] = {};  // UA: the dwords behind them
     const int64_t nball = (K + BK - 1) / BK;
 
     // ---- X
@@ -201,7 +229,7 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
                 xkeep[j] = quant_load<XQ>((const XS *)a.A[0] + tid / group * K, (int64_t)(tid % group + j * group) * Elem<XQ>::kVE, K);
         }
     }
-    if (wave < nball) load_w(wave, cur);
+    if (wave < nball) load_w(wave, cur, cur_e);
     constexpr int XCAP = XQ ? kFfnQuantLds : 16;
     __shared__ __attribute__((aligned(16))) char xq[XCAP];
     __shared__ uint32_t xtop[XQ ? 16 * MB : 1];
@@ -237,15 +265,20 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
         }
         __syncthreads();
     }
+    constexpr bool XUA = UA && XQ == 0;
     gptr x[MB];
-    int xr[MB];
+    int xr[MB], xsh[MB];
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
         const int64_t m = 16 * i + r < M ? 16 * i + r : M - 1;  // rows past the end are not stored
         x[i] = (gptr)a.A[0] + m * a.lda + g * VE;
         xr[i] = (int)m * xp + g * 16;
+        if constexpr (XUA) {
+            xsh[i] = (int)((uintptr_t)x[i] & 3);
+            x[i] -= xsh[i] / ES;
+        }
     }
-    auto load_x = [&](int64_t kb, uint4 *t) {
+    auto load_x = [&](int64_t kb, uint4 *t, uint32_t *te) {
         const int64_t k0 = kb * BK, krem = K - k0;
         if constexpr (XQ != 0) {
             // Past K: zeros, or the (finite) bytes of a neighbour against
@@ -261,13 +294,16 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < MB; ++i) t[u * MB + i] = whole_piece<S>(x[i] + k0 + u * SK);
+                for (int i = 0; i < MB; ++i) {
+                    t[u * MB + i] = whole_piece<S>(x[i] + k0 + u * SK);
+                    if constexpr (XUA) te[u * MB + i] = next_dword(x[i] + k0 + u * SK, xsh[i]);
+                }
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < MB; ++i)
-                    t[u * MB + i] = row_piece<S>(x[i] + k0 + u * SK, krem - (u * 4 + g) * VE, K >= VE);
+                    t[u * MB + i] = row_piece<S>(x[i] + (XUA ? xsh[i] / ES : 0) + k0 + u * SK, krem - (u * 4 + g) * VE, K >= VE);
         }
     };
 
@@ -278,15 +314,16 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
         for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[f][i][e] = 0;
-    auto mul = [&](const uint4 *tw, const uint4 *tx) {
+    auto mul = [&](const uint4 *tw, const uint32_t *twe, const uint4 *tx, const uint32_t *txe, bool whole) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
-                const uint4 y = frag_w(tw, u, f);
+                const uint4 y = frag_w(tw, twe, whole, u, f);
 #pragma unroll
                 for (int i = 0; i < MB; ++i) {
-                    const uint4 &z = tx[u * MB + i];
+                    uint4 z = tx[u * MB + i];
+                    if constexpr (XUA) z = shifted(z, txe[u * MB + i], whole ? xsh[i] : 0);
                     AccT &c = acc[f][i];
                     if constexpr (INT) {
                         c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4v, y), __builtin_bit_cast(i32x4v, z), c, 0, 0, 0);
@@ -305,12 +342,15 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
     };
     for (int64_t kb = wave; kb < nball; kb += NWV) {
         uint4 tx[U * MB];
-        load_x(kb, tx);
+        uint32_t txe[XUA ? U * MB : 1] = {};
+        load_x(kb, tx, txe);
         stage_w(cur);
-        if (kb + NWV < nball) load_w(kb + NWV, nxt);
-        mul(cur, tx);
+        if (kb + NWV < nball) load_w(kb + NWV, nxt, nxt_e);
+        mul(cur, cur_e, tx, txe, K - kb * BK >= BK);
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) cur[i] = nxt[i];
+#pragma unroll
+        for (int i = 0; i < (UA ? PIECES : 1); ++i) cur_e[i] = nxt_e[i];
     }
 
     // ---- the waves' sums, in wave order
@@ -368,19 +408,25 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
 // 38.9 against 37.8; INT8 K = 11008, N = 4096: 12.8 with 8, 14.7 with 4).
 constexpr int64_t kRowsFit = 512;
 
-template <int DT, int OD, bool GLU, bool KN, int NF, int MB, int NWV, int XQ>
+template <int DT, int OD, bool GLU, bool KN, int NF, int MB, int NWV, int XQ, bool UA = false>
 static hipError_t launch_rows(const FfnArgs &a, hipStream_t s) {
     constexpr int COLS = 16 * NF / (GLU ? 2 : 1);
     const int64_t wgs = (a.N + COLS - 1) / COLS;
     if (wgs <= 0 || a.M <= 0) return hipSuccess;
     if (wgs > 0x7fffffff || a.M > 16 * MB) return hipErrorInvalidValue;
     if constexpr (!KN && NWV == 8) {
-        if (wgs > kRowsFit) return launch_rows<DT, OD, GLU, KN, NF, MB, 4, XQ>(a, s);
+        if (wgs > kRowsFit) return launch_rows<DT, OD, GLU, KN, NF, MB, 4, XQ, UA>(a, s);
+    }
+    constexpr int ES = (int)sizeof(typename Elem<DT>::S);
+    if constexpr (!KN && ES < 4 && !UA) {
+        uintptr_t low = (uintptr_t)a.B[0] | (uintptr_t)a.B[1] | (uintptr_t)(a.ldb * ES);
+        if (XQ == 0) low |= (uintptr_t)a.A[0] | (uintptr_t)(a.lda * ES);
+        if (low & 3) return launch_rows<DT, OD, GLU, KN, NF, MB, NWV, XQ, true>(a, s);
     }
     if constexpr (KN && NF > (GLU ? 2 : 1)) {
         if (rows_halve(wgs)) return launch_rows<DT, OD, GLU, KN, NF / 2, MB, NWV, XQ>(a, s);
     }
-    hipLaunchKernelGGL((k_ffn_rows<DT, OD, GLU, KN, NF, MB, NWV, XQ>), dim3((unsigned)wgs), dim3(64 * NWV), 0, s,
+    hipLaunchKernelGGL((k_ffn_rows<DT, OD, GLU, KN, NF, MB, NWV, XQ, UA>), dim3((unsigned)wgs), dim3(64 * NWV), 0, s,
                        slim_args<FfnSlim>(a, GLU ? kUseGlu : kUseScaled, false, false));
     return hipGetLastError();
 }

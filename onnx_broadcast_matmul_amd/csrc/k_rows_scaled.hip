@@ -17,13 +17,14 @@ static hipError_t scaled(bool tb, bool quant, const FfnArgs &a, hipStream_t s) {
                      : launch_rows<MM_INT8, OD, false, true, 4, 2, 8, 0>(a, s);
 }
 
-// Each workgroup quantizes the rows for itself.  Up to 4 rows, or 8 short ones,
-// that costs less than the launch it saves (BF16, [N, K] weights: one row of
-// 11008, N = 4096 12.5 against 18.5 us; 8 rows of 1024 5.5 against 9.9, of 2048
-// 6.8 against 9.0, but of 4096 11.7 against 10.2).
+// Each workgroup quantizes the rows for itself.  Up to 2 rows, or 8 short ones,
+// that costs less than the launch it saves (BF16, [N, K] weights from memory,
+// N = 4096: 1 x 11008 15.1 against 19.3 us, 2 x 11008 17.3 against 19.5, 8 x 2048
+// 6.8 against 8.6; but 4 x 4096 9.3 against 9.1, 4 x 11008 21.8 against 19.9 and,
+// with N = 11008, 45.9 against 36.5).
 bool rows_quantize(int a_type, int out_dtype, bool tb, int64_t M, int64_t K, int64_t N) {
     const int64_t waves = tb && (N + 15) / 16 > kRowsFit ? 4 : 8;  // see launch_rows
-    return a_type == out_dtype && M <= waves && (M <= 4 || K <= 2048) && M * ((K + 63) / 64 * 64 + 16) <= kFfnQuantLds;
+    return a_type == out_dtype && M <= waves && (M <= 2 || K <= 2048) && M * ((K + 63) / 64 * 64 + 16) <= kFfnQuantLds;
 }
 
 hipError_t launch_scaled_rows(int od, bool tb, bool quant, const FfnArgs &a, hipStream_t s) {

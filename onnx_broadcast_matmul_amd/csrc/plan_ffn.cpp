@@ -76,13 +76,15 @@ static double est_us(int cls, bool aligned, int tile, double wgs, double steps) 
 // weights: by how often rows_halve halves a workgroup's columns, for the
 // gated block and the INT8 product.  Fitted to M = 1..32, K = 1000..11008, N =
 // 128..11008, weights that come from memory.
+// 16-bit rows off 4-byte alignment stream at half of it.
 static double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, double wbytes) {
     static const double kChain[3][2] = {{1.0, 1.75}, {0.6, 1.2}, {1.2, 1.85}}, kRate[3][2] = {{4.9, 3.2}, {3.5, 2.2}, {4.9, 3.2}};
     static const double kChainKn[2][3][2] = {{{2.8, 3.2}, {1.4, 1.85}, {1.4, 1.85}}, {{2.0, 2.45}, {1.5, 2.0}, {1.35, 1.75}}};
     static const double kRateKn[2][3][2] = {{{3.6, 3.1}, {2.75, 2.45}, {2.75, 2.45}}, {{5.0, 4.4}, {4.5, 4.0}, {3.5, 3.0}}};
     const int r = M > 16 ? 1 : 0;
     const double kib = (double)kbytes / 1024.0;
-    if (nk) return std::max(3.0 + kChain[cls][r] * kib, wbytes / (kRate[cls][r] * 1e6));
+    const double half = cls == kClass16 && kbytes % 4 != 0 ? 0.5 : 1.0;
+    if (nk) return std::max(3.0 + kChain[cls][r] * kib, wbytes / (kRate[cls][r] * half * 1e6));
     const int i8 = cls == kClass8 ? 1 : 0;
     int h = 0;
     for (int64_t cols = i8 ? 64 : 32; h < 1 + i8 && rows_halve(cdiv(N, cols)); cols /= 2) ++h;
@@ -169,7 +171,7 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     FfnChoice c = choose(kClass8, aligned, p->batch, M, N, K, 1, tiles, may_split && sreq == 0);
     const double wbytes = (double)K * (double)N;
     // The few-row kernel may save the quantization's own launch.
-    const double saved = p->a_type != MM_INT8 && rows_quantize(p->a_type, p->dtype, p->tb != 0, M, K, N) ? 3.0 : 0.0;
+    const double saved = p->a_type != MM_INT8 && rows_quantize(p->a_type, p->dtype, p->tb != 0, M, K, N) ? 2.5 : 0.0;
     if (force == MM_ALGO_SKINNY_M ||
         (force == MM_ALGO_AUTO && rows_ok && K > 0 && treq == 0 && sreq == 0 &&
          rows_us(kClass8, p->tb != 0, M, N, K, wbytes) <= tiles_us(kClass8, c, wbytes) + saved)) {

@@ -186,6 +186,15 @@ def test_glu_few_rows(m, nk, dt, dev):
         run_forward(dev, m, k, n, TYPES[dt], nk, "gelu", seed=60 + j, algo=mm.ALGO_SKINNY_M, keep=j == 1)
 
 
+@pytest.mark.parametrize("m", [1, 13, 32])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_glu_few_rows_off_dword_alignment(m, dt, dev):
+    """Rows of every alignment (odd K) and a base off a dword (even K), blocks
+    of K whole and partial, few columns and more than 512 workgroups."""
+    for j, (k, n, offset) in enumerate(((1301, 35, 0), (64, 20, 1), (1300, 40, 1), (67, 8209, 0))):
+        run_forward(dev, m, k, n, TYPES[dt], True, "silu", seed=90 + j, algo=mm.ALGO_SKINNY_M, offset=offset, keep=j == 0)
+
+
 @pytest.mark.parametrize("m", [4, 150])
 @pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
 def test_glu_unaligned_and_merged_operands(m, nk, dev):
@@ -485,6 +494,17 @@ def test_scaled(i, nk, dev):
     run_scaled(dev, (m, k), (k, n), list(TYPES.values())[i % 3], nk, bias=i % 2 == 0, seed=600 + 5 * i)
 
 
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("m", [1, 16, 29])
+def test_scaled_few_rows_of_any_alignment_and_width(m, nk, dev):
+    """Row lengths and bases off 4-byte alignment, and column counts on both
+    sides of each width of the few-row kernel's workgroups."""
+    for j, (k, n, offset) in enumerate(((1301, 35, 0), (1302, 16, 0), (1303, 4097, 0), (256, 40, 1), (1024, 24, 2),
+                                        (260, 4096, 3), (515, 8192, 0), (300, 8193, 0), (257, 8208, 1))):
+        run_scaled(dev, (m, k), (k, n), BF16, nk, bias=j % 2 == 0, seed=760 + 5 * j, offset=offset,
+                   force_algo=mm.ALGO_SKINNY_M)
+
+
 @pytest.mark.parametrize("dt", TYPES, ids=str)
 @pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
 def test_scaled_every_kernel_gives_the_same_bits(nk, dt, dev):
@@ -567,7 +587,7 @@ def test_dynamic_product_is_quantization_then_product(nk, dt, dev):
     other = F32 if t != F32 else BF16
     for j, (sa, sb, out) in enumerate((((1, 2048), (2048, 96), t), ((4, 100), (100, 33), t), ((4, 1), (1, 3), t),
                                        ((9, 2000), (2000, 64), t), ((7, 1030), (1030, 70), t),
-                                       ((3, 9000), (9000, 20), t), ((4, 260), (260, 8300), t), ((1, 64), (64, 48), other), ((200, 72), (72, 130), t),
+                                       ((3, 9000), (9000, 20), t), ((4, 1301), (1301, 70), t), ((2, 1303), (1303, 8300), t), ((4, 260), (260, 8300), t), ((1, 64), (64, 48), other), ((200, 72), (72, 130), t),
                                        ((130, 77), (77, 55), t), ((2, 3, 40, 65), (65, 48), t),
                                        ((2, 1, 40, 65), (3, 65, 33), t), ((64,), (64, 48), t), ((3, 0), (0, 9), t))):
         x = rand(sa, t, dev, 820 + j)
