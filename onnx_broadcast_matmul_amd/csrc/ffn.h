@@ -58,7 +58,13 @@ struct FfnSlimBatch : FfnSlim {  // scaled products over several batches
 
 // Tile table of the tiled products: block rows and columns (the gated
 // block's columns count gate and up) and the bytes of K in a stage, see
-// k_ffn.h.
+// k_ffn.h.  A smaller tile gives few-row and narrow products more workgroups
+// and costs more LDS and cache reads for each MFMA: 32 bytes of K take 0.41 us
+// on 256 x 256 (8 waves of 128 x 64), 0.24 on 256 x 128, 0.17 on 128 x 128 (0.285
+// for two of them on a CU), 0.147 on 64 x 128 (two K groups) and 0.095 on 32 x 128
+// (four), so plans choose by the time model in plan_ffn.cpp.  Four waves of 128 x
+// 64 on 256 x 128 need fewer LDS reads than the eight of 64 x 64 but leave a
+// SIMD one wave: 265 against 201 us at 4096 x 2048 x 5504, gated.
 struct FfnTile {
     int bm, bn, bkb;
 };

@@ -1,7 +1,9 @@
 // k_ffn_rows.h -- the gated block and the scaled INT8 product over few rows
 // (one decoded token to kFfnRows of them).
 //
-// The weights are the traffic: each is read once.  A workgroup owns NF x 16
+// The weights are the traffic, and memory's rate the bound: each is read once
+// (one token, [N, K]: gated BF16 4096 x 11008 35 us, 5.1 TB/s; INT8 11008 x 4096
+// 12 us, of which 3 are the launch and the rest a workgroup's chain of K).  A workgroup owns NF x 16
 // weight columns (the gated block: half gate, half up of the same features);
 // its waves take every NWV-th block of K and their sums meet in LDS in wave
 // order, so the result does not depend on timing.  X (a few rows) is re-read

@@ -104,7 +104,8 @@ hipError_t launch_glu_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
 
 // Sum of the K partitions' FP32 partials in partition order, narrowed once;
 // product b (blockIdx.y of gridDim.y) goes to Y[b], rows ldy elements apart.  A
-// thread owns four consecutive columns of one row.
+// thread owns four consecutive columns of one row.  The launch bounds it
+// (300 x 512, 6 partitions: 4.0 us, of which 3 are an empty kernel's).
 template <int DT>
 __global__ __launch_bounds__(256) void k_sum_reduce(FfnSlim a) {
     using E = Elem<DT>;
@@ -153,7 +154,10 @@ hipError_t launch_sum_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
 }
 
 // dG = dH U f'(G) and dU = dH f(G), a thread per 16 bytes of each tensor's
-// row.  Three tensors are read and two written once.  G and U come in the
+// row.  Three tensors are read and two written once, which bounds it (8192 x
+// 11008 BF16: 0.90 GB in 151 us, 6.0 TB/s; 4096 x 5504 41 us).  A kernel of its
+// own because dX reduces over N and dW over M: formed inside those products it
+// would be formed once for every tile column.  G and U come in the
 // element type (the forward pass rounded them once) and dG, dU are rounded to
 // it because the matrix cores take them in it: the roundings, half a step
 // each, that an unfused block in this type makes too.  dG and dU have rows of
