@@ -487,14 +487,18 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
     // larger than the stage buffers go in row passes.
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     using OE = Elem<OD>;
-    if constexpr (KG > 1) {
-        // Groups 1 .. KG - 1 hand their sums to group 0 through LDS.
-        static_assert((KG - 1) * BM * BN * 4 <= STAGES * STAGE_BYTES, "K group exchange");
+    // K groups meet through LDS, their sums added in group order.  Of four
+    // groups each takes a quarter of every accumulator (QG quarters of four
+    // columns) and carries it through the epilogue, so that all eight waves
+    // work there and not two (300 x 512 x 1364 FP32, gelu: 15.5 -> 14.7 us); of two
+    // groups the first takes all (halves gained nothing).
+    constexpr int QG = KG > 2 ? 4 / KG : 4;
+    auto mine = [&](int q) { return KG <= 2 || q / QG == kg; };
+    static_assert((KG - 1) * BM * BN * 4 <= STAGES * STAGE_BYTES, "K group exchange");
+    if constexpr (KG == 2) {
         using T = typename std::conditional<INT, int, float>::type;
         T *xch = (T *)lds;
-        auto at = [&](int g, int i, int j, int r) {
-            return ((((g - 1) * NWG + wave % NWG) * FM + i) * FN * 16 + j * 16 + r) * 64 + lane;
-        };
+        auto at = [&](int i, int j, int r) { return (((wave % NWG) * FM + i) * FN * 16 + j * 16 + r) * 64 + lane; };
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (kg > 0) {
 #pragma unroll
@@ -502,19 +506,61 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) xch[at(kg, i, j, r)] = acc[i][j][r];
+                    for (int r = 0; r < 16; ++r) xch[at(i, j, r)] = acc[i][j][r];
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (kg == 0) {
 #pragma unroll
-            for (int g = 1; g < KG; ++g)
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] += xch[at(i, j, r)];
+        }
+    } else if constexpr (KG > 2) {
+        using T = typename std::conditional<INT, int, float>::type;
+        uint4 *xch = (uint4 *)lds;
+        // What group s holds of group d's quarter q.
+        auto at = [&](int d, int s, int i, int j, int q) {
+            return (((((d * (KG - 1) + (s < d ? s : s - 1)) * NWG + wave % NWG) * FM + i) * FN + j) * QG + q % QG) * 64 + lane;
+        };
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (!mine(q)) {
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
-                    for (int j = 0; j < FN; ++j)
+                    for (int j = 0; j < FN; ++j) {
+                        const T part[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                        uint4 x;
+                        __builtin_memcpy(&x, part, 16);
+                        xch[at(q / QG, kg, i, j, q)] = x;
+                    }
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) acc[i][j][r] += xch[at(g, i, j, r)];
-        }
+        for (int q = 0; q < 4; ++q)
+            if (mine(q)) {
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) {
+                        T sum[4];
+#pragma unroll
+                        for (int g = 0; g < KG; ++g) {
+                            T part[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                            if (g != kg) {
+                                const uint4 x = xch[at(kg, g, i, j, q)];
+                                __builtin_memcpy(part, &x, 16);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum[e] = g ? sum[e] + part[e] : part[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] = sum[e];
+                    }
+            }
     }
     auto emit = [&](auto zero, int jbase, auto value, void *outp, int64_t ldo, bool vec) {
         using O = decltype(zero);
@@ -530,12 +576,13 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const int rl = wr * WM + i * 32 + (lane & 31) - pass * PR;
-                if (kg == 0 && (NP == 1 || (rl >= 0 && rl < PR))) {
+                if ((KG > 2 || kg == 0) && (NP == 1 || (rl >= 0 && rl < PR))) {
                     char *trow = lds + rl * (PN * OS);
 #pragma unroll
                     for (int j = 0; j < FNP; ++j)
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
+                            if (!mine(q)) continue;
                             const int cl = wc * WNP + j * 32 + 8 * q + 4 * (lane >> 5);
                             char *dst = trow + ((cl / OV) ^ (rl & (OCPR - 1))) * 16 + (cl % OV) * OS;
                             const AccT &v = acc[i][jbase + j];
@@ -599,9 +646,10 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
                 for (int j = 0; j < FNP; ++j)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        acc[i][j][r] = act_value<decltype(kind)::value, DT == MM_FLOAT>(acc[i][j][r]) * acc[i][FNP + j][r];
+                        if (mine(r / 4))
+                            acc[i][j][r] = act_value<decltype(kind)::value, DT == MM_FLOAT>(acc[i][j][r]) * acc[i][FNP + j][r];
         };
-        if (kg == 0) switch (a.act) {  // the other groups' sums are already in group 0's
+        if (KG > 2 || kg == 0) switch (a.act) {
         case MM_ACT_SILU: apply(std::integral_constant<int, MM_ACT_SILU>()); break;
         case MM_ACT_GELU: apply(std::integral_constant<int, MM_ACT_GELU>()); break;
         case MM_ACT_GELU_TANH: apply(std::integral_constant<int, MM_ACT_GELU_TANH>()); break;
