@@ -49,7 +49,7 @@ static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == 
 enum { kClass16 = 0, kClass8 = 1, kClass32 = 2 };
 static const int kOcc[kNumFfnTiles] = {1, 2, 2, 1, 1};
 static const double kLaunch = 2.5;                                      // us
-static const double kFixed[kNumFfnTiles] = {7.5, 3.2, 2.5, 2.0, 5.5};  // us
+static const double kFixed[kNumFfnTiles] = {7.5, 3.2, 2.5, 1.4, 5.5};  // us
 static const double kStep[2][3][kNumFfnTiles][2] = {                    // us: aligned, not aligned
     {{{0.41, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.240, 0}},
      {{0.41, 0}, {0.17, 0.285}, {0.145, 0.160}, {0.095, 0}, {0.222, 0}},
