@@ -428,7 +428,8 @@ mm_status mm_glu_execute(mm_plan_t plan, const void *X, const void *Wg, const vo
 /* Enqueue the backward pass of a plan with `training` (else MM_ERR_BAD_OPTION)
  * on `stream`, from the G and U of the forward pass on the same X and
  * weights.  dX may be NULL (inputs without a gradient), and dWg and dWu may
- * both be NULL (frozen weights); what is computed is written, not added.
+ * both be NULL (frozen weights); what is computed is written, not added.  No
+ * output may overlap an input or another output.
  * rows == 0 writes zero weight gradients, hidden == 0 a zero dX. */
 mm_status mm_glu_backward(mm_plan_t plan, const void *X, const void *Wg, const void *Wu, const void *G, const void *U,
                           const void *dH, void *dX, void *dWg, void *dWu, void *stream);
