@@ -72,30 +72,36 @@ static double est_us(int cls, bool aligned, int tile, double wgs, double steps) 
 
 // Time of the few-row kernel: a workgroup's chain of K (kChain us for each KiB
 // of a weight row, which memory latency sets), or the weights' stream at kRate
-// TB/s once the workgroups fill the GPU; each [up to 16 rows, more].  [K, N]
-// weights: by how often rows_halve halves a workgroup's columns, for the
-// gated block and the INT8 product.  Fitted to M = 1..32, K = 1000..11008, N =
-// 128..11008, weights that come from memory.
-// 16-bit rows off 4-byte alignment stream at half of it.
-static double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, double wbytes) {
+// TB/s once the workgroups fill the GPU; each [up to 16 rows, more].  Fitted to
+// M = 1..32, K = 500..11008, N = 128..11008, weights that come from memory.
+// [K, N] weights: by how often rows_halve halves a workgroup's columns.  The
+// gated block's workgroups of 32 columns take as long again where a CU has
+// two, those of 16 longer the more of them share the cache lines.  Rows (of
+// `row` bytes) off 4-byte alignment cost 16-bit types more.
+static double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, int64_t row, double wbytes) {
     static const double kChain[3][2] = {{1.0, 1.75}, {0.6, 1.2}, {1.2, 1.85}}, kRate[3][2] = {{4.9, 3.2}, {3.5, 2.2}, {4.9, 3.2}};
-    static const double kChainKn[2][3][2] = {{{2.8, 3.2}, {1.4, 1.85}, {1.4, 1.85}}, {{2.0, 2.45}, {1.5, 2.0}, {1.35, 1.75}}};
-    static const double kRateKn[2][3][2] = {{{3.6, 3.1}, {2.75, 2.45}, {2.75, 2.45}}, {{5.0, 4.4}, {4.5, 4.0}, {3.5, 3.0}}};
+    static const double kChain8[3][2] = {{2.0, 2.45}, {1.5, 2.0}, {1.35, 1.75}}, kRate8[3][2] = {{5.0, 4.4}, {4.5, 4.0}, {3.5, 3.0}};
     const int r = M > 16 ? 1 : 0;
     const double kib = (double)kbytes / 1024.0;
-    const double half = cls == kClass16 && kbytes % 4 != 0 ? 0.5 : 1.0;
-    if (nk) return std::max(3.0 + kChain[cls][r] * kib, wbytes / (kRate[cls][r] * half * 1e6));
-    const int i8 = cls == kClass8 ? 1 : 0;
+    const bool odd = cls == kClass16 && row % 4 != 0;
+    if (nk) return std::max(3.0 + kChain[cls][r] * kib, wbytes / (kRate[cls][r] * (odd ? 0.5 : 1.0) * 1e6));
+    const bool i8 = cls == kClass8;
     int h = 0;
-    for (int64_t cols = i8 ? 64 : 32; h < 1 + i8 && rows_halve(cdiv(N, cols)); cols /= 2) ++h;
-    return 3.0 + std::max(kChainKn[i8][h][r] * kib, wbytes / (kRateKn[i8][h][r] * 1e6));
+    int64_t cols = i8 ? 64 : 32;
+    for (; h < (i8 ? 2 : 1) && rows_halve(cdiv(N, cols)); cols /= 2) ++h;
+    if (i8) return 3.0 + std::max(kChain8[h][r] * kib, wbytes / (kRate8[h][r] * 1e6));
+    const double wgs = (double)cdiv(N, cols);
+    const double chain = h ? (r ? 1.3 + 0.0085 * wgs : 1.2 + 0.0075 * wgs) : (r ? 3.5 : 2.8) * ceil(wgs / kNumCUs);
+    return 3.0 + chain * kib * (odd ? 1.25 : 1.0);
 }
 
 // The tiles' time over the same few rows: the weights stream at kStream
-// TB/s at best, and a second launch follows a split.
-static double tiles_us(int cls, const FfnChoice &c, double wbytes) {
+// TB/s at best ([K, N] ones at 0.72 of it in the register-staged form, at half
+// with rows off 4-byte alignment), and a second launch follows a split.
+static double tiles_us(int cls, const FfnChoice &c, bool nk, bool aligned, int64_t row, double wbytes) {
     static const double kStream[3] = {4.0, 2.7, 4.0};
-    return std::max(c.us + (c.split > 1 ? 3.0 : 0.0), wbytes / (kStream[cls] * 1e6));
+    const double part = aligned || nk ? 1.0 : row % 4 == 0 ? 0.72 : 0.5;
+    return std::max(c.us + (c.split > 1 ? 3.0 : 0.0), wbytes / (kStream[cls] * part * 1e6));
 }
 
 // Entry and split with the least estimated time for `batch` products of
@@ -174,7 +180,8 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     const double saved = p->a_type != MM_INT8 && rows_quantize(p->a_type, p->dtype, p->tb != 0, M, K, N) ? 2.5 : 0.0;
     if (force == MM_ALGO_SKINNY_M ||
         (force == MM_ALGO_AUTO && rows_ok && K > 0 && treq == 0 && sreq == 0 &&
-         rows_us(kClass8, p->tb != 0, M, N, K, wbytes) <= tiles_us(kClass8, c, wbytes) + saved)) {
+         rows_us(kClass8, p->tb != 0, M, N, K, p->tb ? K : N, wbytes) <=
+             tiles_us(kClass8, c, p->tb != 0, aligned, p->tb ? K : N, wbytes) + saved)) {
         p->algo = MM_ALGO_SKINNY_M;
         if (!launchable((double)cdiv(N, 16), 512)) return fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
         return MM_OK;
@@ -394,7 +401,8 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         FfnChoice c = choose(cls, aligned, 1, M, 2 * N, K * es, 1, tiles, may_split && sreq == 0);
         const double wbytes = 2.0 * (double)K * (double)N * (double)es;
         if (force == MM_ALGO_SKINNY_M || (force == MM_ALGO_AUTO && rows_ok && treq == 0 && sreq == 0 &&
-                                          rows_us(cls, p->tb != 0, M, N, K * es, wbytes) <= tiles_us(cls, c, wbytes))) {
+                                          rows_us(cls, p->tb != 0, M, N, K * es, p->w_pitch * es, wbytes) <=
+                                              tiles_us(cls, c, p->tb != 0, aligned, p->w_pitch * es, wbytes))) {
             p->algo = MM_ALGO_SKINNY_M;
             if (!launchable((double)cdiv(N, 8), 512)) st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
         } else {
