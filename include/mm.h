@@ -326,7 +326,7 @@ mm_status mm_int_execute(mm_plan_t plan, const void *A, const void *B, const voi
  * FP32, and the result is narrowed once.  Results do not depend on the
  * algorithm or on a split of K.  A scale that is NaN or infinite makes its
  * row or column what IEEE arithmetic makes of it; K == 0 gives the bias (or
- * zeros).
+ * zeros) whatever the scales hold.
  *
  * Options: force_algo SKINNY_M (one product, after folding, of at most 32
  * rows), GENERAL or SPLIT_K; tile k >= 1 is entry k of 256 x 256 (not

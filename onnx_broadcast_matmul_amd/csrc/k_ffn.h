@@ -659,20 +659,21 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
         emit((typename OE::S)0, 0, plain, a.Y[0], a.ldy, a.y_vec != 0);
     } else if constexpr (MODE == kScaled) {
         // Scales of this lane's rows, and of the tile's columns in LDS after
-        // the main loop's last reads.
+        // the main loop's last reads.  K == 0: the matrices are empty, their
+        // batch offsets tell no scales apart, and zeros in the scales' place
+        // leave the bias alone.
         __shared__ __attribute__((aligned(16))) float cs[PN], cb[PN];
-        const int64_t kd = K > 0 ? K : 1;      // K == 0: one empty matrix, offsets 0
-        const int64_t sb0 = ob / kd + n0;  // scale of column n of B matrix i: i N + n
+        const int64_t sb0 = K > 0 ? ob / K + n0 : 0;  // scale of column n of B matrix i: i N + n
         for (int x = tid; x < PN; x += NT) {
             const bool in = n0 + x < N;
-            cs[x] = in ? a.sb()[sb0 + x] : 0.0f;
+            cs[x] = in && K > 0 ? a.sb()[sb0 + x] : 0.0f;
             cb[x] = in && a.bias() ? OE::to_f32(((const typename OE::S *)a.bias())[n0 + x]) : 0.0f;
         }
         float rs[FM];
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int64_t row = m0 + wr * WM + i * 32 + (lane & 31);
-            rs[i] = row < M ? a.sa()[oa / a.lda + row] : 0.0f;
+            rs[i] = row < M && K > 0 ? a.sa()[oa / a.lda + row] : 0.0f;
         }
         __syncthreads();
         emit((typename OE::S)0, 0, [&](int i, int cl, int v) { return scaled_value(v, rs[i], cs[cl], cb[cl]); },

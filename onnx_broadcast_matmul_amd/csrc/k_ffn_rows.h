@@ -397,8 +397,9 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
 #pragma unroll
             for (int v = 0; v < NWV; ++v) sum += (int)red[v][c >> 4][i][at];
             const float bias = a.bias() ? OE::to_f32(((const OS *)a.bias())[n]) : 0.0f;
-            const float sa = XQ ? quant_scale(xtop[XQ ? m16 : 0]) : a.sa()[m];
-            ((OS *)a.Y[0])[o] = OE::from_f32(scaled_value(sum, sa, a.sb()[n], bias));
+            // K == 0 takes no scales: the result is the bias.
+            const float sa = XQ ? quant_scale(xtop[XQ ? m16 : 0]) : K > 0 ? a.sa()[m] : 0.0f;
+            ((OS *)a.Y[0])[o] = OE::from_f32(scaled_value(sum, sa, K > 0 ? a.sb()[n] : 0.0f, bias));
         }
     }
 #endif

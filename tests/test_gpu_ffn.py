@@ -770,3 +770,31 @@ def test_offsets_past_32_bits(dev):
     plan.backward(x, w, w, g, g, dh, dx)
     wx, tx = backward64(x[-9:], w.t(), w.t(), g[-9:], g[-9:], dh[-9:], "silu", BF16)[0]
     within(dx[-9:], wx, tx, "dX")
+
+
+# ---- empty reductions, rounding, far ends of the activations
+
+
+@pytest.mark.parametrize("bias", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("a_type", ["int8", "quantized"])
+def test_scaled_empty_reduction_takes_no_scales(a_type, bias, dev):
+    """K == 0 gives the bias or zeros, whatever the scales hold: few rows,
+    tiles, and batches with scales of their own."""
+    for j, (sa, sb, kw) in enumerate((((5, 0), (0, 24), dict(force_algo=mm.ALGO_SKINNY_M)), ((5, 0), (0, 24), {}),
+                                      ((70, 0), (0, 33), {}), ((3, 5, 0), (3, 0, 24), {}),
+                                      ((2, 1, 40, 0), (3, 0, 24), {}), ((0,), (0,), {}))):
+        dt = list(TYPES.values())[j % 3]
+        at = torch.int8 if a_type == "int8" else dt
+        p = mm.ScaledIntPlan(sa, sb, mm.torch_dtype_code(dt), a_type=mm.torch_dtype_code(dt) if a_type != "int8" else mm.INT8,
+                             bias=bias, **kw)
+        asc, bsc = torch.ones(p.a_scale_shape, device=dev), torch.ones(p.b_scale_shape, device=dev)
+        asc.view(-1)[-1] = float("nan")
+        bsc.view(-1)[0] = float("inf")
+        bv = rand((1 if len(sb) == 1 else sb[-1],), dt, dev, 1000 + j) if bias else None
+        y, buf = guarded(p.output_shape, dt, dev)
+        p.execute(torch.empty(sa, dtype=at, device=dev), torch.empty(sb, dtype=torch.int8, device=dev), y,
+                  a_scale=asc if a_type == "int8" else None, b_scale=bsc, bias=bv)
+        torch.cuda.synchronize()
+        want = torch.zeros((), dtype=dt, device=dev) if bv is None else bv if len(sb) > 1 else bv[0]
+        assert torch.equal(y, want.expand(y.shape)), (sa, sb)
+        check_guard(buf, y)
