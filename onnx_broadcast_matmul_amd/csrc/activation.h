@@ -105,7 +105,9 @@ __device__ __forceinline__ void act_grad(float g, float &f, float &d) {
     } else if constexpr (ACT == MM_ACT_GELU_TANH) {
         sigmoid_pair<EXACT>(kGeluC * (g + kGeluA * g * g * g), s, c);
         f = g * s;
-        d = s + g * s * c * kGeluC * (1.0f + 3.0f * kGeluA * g * g);
+        // s c is 0 long before g^2 leaves FP32, which the limit keeps finite:
+        // the far finite gates' second term is 0 and not 0 times infinity.
+        d = s + g * s * c * kGeluC * (1.0f + 3.0f * kGeluA * fminf(g * g, 1e30f));
     } else {
         sigmoid_pair<EXACT>(g, s, c);
         if constexpr (ACT == MM_ACT_SILU) {

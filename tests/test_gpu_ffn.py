@@ -798,3 +798,23 @@ def test_scaled_empty_reduction_takes_no_scales(a_type, bias, dev):
         want = torch.zeros((), dtype=dt, device=dev) if bv is None else bv if len(sb) > 1 else bv[0]
         assert torch.equal(y, want.expand(y.shape)), (sa, sb)
         check_guard(buf, y)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dt", TYPES, ids=str)
+def test_glu_gradient_of_far_finite_gates(act, dt, dev):
+    """f' of finite gates up to the type's largest is its limit: 1 above and 0
+    below, 0 on both sides for the sigmoid.  Wg is the identity, Wu zero and U
+    one, so that dX is dH f'(G) itself."""
+    t = TYPES[dt]
+    top = torch.finfo(t).max
+    row = [v for a in (200.0, 6.0e4, 1.0e13, 1.0e19, 3.0e19, 1.0e25, 1.0e38, top) if a <= top for v in (a, -a)]
+    n = len(row)
+    g = torch.tensor(row, dtype=t, device=dev).repeat(5, 1)
+    u, dh = torch.ones_like(g), torch.full_like(g, 0.5)
+    wg, wu = torch.eye(n, dtype=t, device=dev), torch.zeros(n, n, dtype=t, device=dev)
+    dx = torch.empty(5, n, dtype=t, device=dev)
+    p = mm.GluPlan(5, n, n, mm.torch_dtype_code(t), activation=mm.ACTIVATIONS[act], training=True)
+    p.backward(torch.zeros_like(dx), wg, wu, g, u, dh, dx)
+    want = dh * ((g > 0) & (act != "sigmoid")).to(t)
+    assert torch.equal(dx, want), dx[0]
