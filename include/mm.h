@@ -329,8 +329,11 @@ mm_status mm_int_execute(mm_plan_t plan, const void *A, const void *B, const voi
  * zeros) whatever the scales hold.
  *
  * Options: force_algo SKINNY_M (one product, after folding, of at most 32
- * rows), GENERAL or SPLIT_K; tile k >= 1 is entry k of 256 x 256 (not
- * split), 128 x 128, 64 x 128, 32 x 128, 256 x 128; split_k as for MatMul.  A
+ * rows), GENERAL or SPLIT_K (at most 65535 products); tile k >= 1 is entry k of
+ * 256 x 256 (not split), 128 x 128, 64 x 128, 32 x 128, 256 x 128; split_k is
+ * the number of partitions (clamped so that none is empty).  GENERAL and
+ * SKINNY_M with a split_k above 1, and SKINNY_M with a tile, give
+ * MM_ERR_BAD_OPTION.  A
  * plan with an A to quantize or a split K may own a workspace
  * (mm_plan_workspace_bytes > 0): its executions must then not overlap, and it
  * is allocated and bound to a device as described above.  Matrices hold at
@@ -391,7 +394,8 @@ mm_status mm_quantize_rows(const void *X, int dtype, int64_t rows, int64_t cols,
  * Options: force_algo SKINNY_M (at most 32 rows), GENERAL or SPLIT_K; tile
  * k >= 1 is entry k of 256 x 256, 128 x 128, 64 x 128, 32 x 128, 256 x 128
  * for the forward pass (columns count gate and up; FLOAT has 2, 3 and 4; 1 is
- * not split); split_k is the forward pass's, as for MatMul. */
+ * not split); split_k is the forward pass's.  What the scaled product refuses
+ * beside a forced algorithm, the block refuses too. */
 typedef enum mm_activation {
     MM_ACT_SILU = 1,      /* g / (1 + exp(-g)) */
     MM_ACT_GELU = 2,      /* g Phi(g), by erf */

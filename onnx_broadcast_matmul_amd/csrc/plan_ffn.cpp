@@ -153,6 +153,17 @@ static mm_status tile_option(const mm_plan_options *opt, int *tile) {
     return MM_OK;
 }
 
+// Options that a forced algorithm would drop: partitions of the unsplit ones,
+// a tile entry of the few-row kernel.
+static mm_status forced_alone(const mm_plan_options *opt) {
+    if (!opt) return MM_OK;
+    const bool rows = opt->force_algo == MM_ALGO_SKINNY_M;
+    if ((rows || opt->force_algo == MM_ALGO_GENERAL) && opt->split_k > 1)
+        return fail(MM_ERR_BAD_OPTION, "%s does not split K (split_k %d)", rows ? "SKINNY_M" : "GENERAL", opt->split_k);
+    if (rows && opt->tile != 0) return fail(MM_ERR_BAD_OPTION, "SKINNY_M has no tiles (tile %d)", opt->tile);
+    return MM_OK;
+}
+
 // Algorithm, tile and split of a scaled product whose output is not empty.
 static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
     const int64_t M = p->kernel_m, N = p->N, K = p->K;
@@ -166,8 +177,11 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
         return fail(MM_ERR_BAD_OPTION, "SKINNY_M takes one product of at most %d rows", kFfnRows);
     int only = -1;
     mm_status st = tile_option(opt, &only);
+    if (st == MM_OK) st = forced_alone(opt);
     if (st != MM_OK) return st;
     // Partials are added by a grid of at most 65535 products.
+    if (p->batch > 65535 && K > 0 && (force == MM_ALGO_SPLIT_K || sreq > 1))
+        return fail(MM_ERR_BAD_OPTION, "split K takes at most 65535 products (got %lld)", (long long)p->batch);
     const bool may_split = force != MM_ALGO_GENERAL && K > 0 && p->batch <= 65535;
     const unsigned all = (1u << kNumFfnTiles) - 1;
     unsigned tiles = only >= 0 ? 1u << only : all;
@@ -369,6 +383,7 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
     if (sreq < 0) return fail(MM_ERR_BAD_OPTION, "split_k %d is negative", sreq);
     int only = -1;
     mm_status st = tile_option(opt, &only);
+    if (st == MM_OK && M > 0 && N > 0) st = forced_alone(opt);
     if (st != MM_OK) return st;
     unsigned tiles = dtype == MM_FLOAT ? 0xe : 0x1f;  // FLOAT has the three smaller entries
     if (only >= 0) tiles &= 1u << only;
@@ -410,9 +425,9 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
             p->tile = c.tile;
             p->split = c.split;
             p->kstages = c.kstages;
-            p->algo = c.split > 1 ? MM_ALGO_SPLIT_K : MM_ALGO_GENERAL;
+            p->algo = c.split > 1 || (force == MM_ALGO_SPLIT_K && may_split) ? MM_ALGO_SPLIT_K : MM_ALGO_GENERAL;
             if (!tile_launchable(c, 1, M, 2 * N)) st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
-            if (c.split > 1) {
+            if (p->algo == MM_ALGO_SPLIT_K) {
                 p->kchunk = (int64_t)c.kstages * kFfnTiles[c.tile].bkb / es;
                 p->workspace_bytes = round_up((int64_t)c.split * 2 * M * N * 4, 256);
             }

@@ -243,3 +243,47 @@ def test_binding_refuses_host_tensors():
         s.execute(a, b, h, b_scale=torch.zeros(32))
     with pytest.raises(ValueError):
         mm.quantize_rows(x)
+
+
+# ---- forced algorithms
+
+
+@pytest.mark.parametrize("rows,k,n", [(300, 64, 64), (4096, 64, 4096), (2, 35, 9)])
+def test_forced_split_is_kept(rows, k, n):
+    """SPLIT_K runs as SPLIT_K, with one partition where the plan prefers it."""
+    for dtype in (mm.FLOAT, mm.BFLOAT16):
+        for kw in ({}, dict(split_k=1), dict(split_k=3), dict(tile=3), dict(tile=4, split_k=2)):
+            p = glu(rows, k, n, dtype, force_algo=mm.ALGO_SPLIT_K, **kw)
+            i = p.info()
+            assert i["algo_name"] == "split_k" and i["split_k"] >= 1, kw
+            assert p.workspace_bytes == (i["split_k"] * 2 * rows * n * 4 + 255) // 256 * 256
+            assert i["k_chunk"] > 0
+    p = scaled((rows, k), (k, n), force_algo=mm.ALGO_SPLIT_K)
+    assert p.info()["algo_name"] == "split_k"
+
+
+@pytest.mark.parametrize("kw", [
+    dict(force_algo=mm.ALGO_GENERAL, split_k=2), dict(force_algo=mm.ALGO_SKINNY_M, split_k=2),
+    dict(force_algo=mm.ALGO_SKINNY_M, tile=2),
+])
+def test_options_that_the_forced_algorithm_lacks_are_refused(kw):
+    assert status(glu, **kw) == mm.ERR_BAD_OPTION
+    assert status(scaled, **kw) == mm.ERR_BAD_OPTION
+    # as everywhere, nothing is forced on an empty output
+    assert glu(0, 64, 32, **kw).info()["algo_name"] == "empty"
+    assert scaled((0, 64), **kw).info()["algo_name"] == "empty"
+
+
+def test_options_of_one_partition_and_forced_tiles_still_run():
+    assert glu(force_algo=mm.ALGO_GENERAL, split_k=1, tile=3).info()["algo_name"] == "general"
+    assert scaled(force_algo=mm.ALGO_GENERAL, split_k=1, tile=3).info()["algo_name"] == "general"
+    assert glu(force_algo=mm.ALGO_SKINNY_M, split_k=1).info()["algo_name"] == "skinny_m"
+    assert scaled(force_algo=mm.ALGO_SKINNY_M, split_k=1).info()["algo_name"] == "skinny_m"
+
+
+def test_split_of_more_products_than_its_reduction_takes_is_refused():
+    """Partial sums are added by a grid of at most 65535 products."""
+    many = dict(sa=(65536, 1, 64), sb=(65536, 64, 2))
+    assert status(scaled, **many) == 0
+    assert status(scaled, **many, force_algo=mm.ALGO_SPLIT_K) == mm.ERR_BAD_OPTION
+    assert status(scaled, **many, split_k=2) == mm.ERR_BAD_OPTION

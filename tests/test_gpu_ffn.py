@@ -818,3 +818,11 @@ def test_glu_gradient_of_far_finite_gates(act, dt, dev):
     p.backward(torch.zeros_like(dx), wg, wu, g, u, dh, dx)
     want = dh * ((g > 0) & (act != "sigmoid")).to(t)
     assert torch.equal(dx, want), dx[0]
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+def test_glu_forced_split_of_one_partition(nk, dev):
+    for j, (m, k, n) in enumerate(((300, 64, 64), (2, 35, 9), (40, 264, 130))):
+        p = run_forward(dev, m, k, n, list(TYPES.values())[j], nk, "silu", seed=1100 + j, algo=mm.ALGO_SPLIT_K, split=1,
+                        keep=j != 1)
+        assert p.info()["algo_name"] == "split_k" and p.info()["split_k"] == 1
