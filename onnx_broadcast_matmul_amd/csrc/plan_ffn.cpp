@@ -38,6 +38,13 @@ static bool tile_launchable(const FfnChoice &c, int64_t batch, int64_t M, int64_
     return launchable(c.tile == 0 ? 4.0 * wgs : wgs, c.tile <= 1 ? 256 : 512);
 }
 
+// The same for kernels of 256 threads that take `pieces` of each of M rows: the
+// joining of partial sums (four columns a thread) and the backward pass's
+// element-wise part.
+static bool pieces_launchable(int64_t M, int64_t pieces) {
+    return launchable(ceil((double)M * (double)pieces / 256.0), 256);
+}
+
 static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
 
 // Time model of the tiled products: a CU runs up to kOcc workgroups of an
@@ -209,7 +216,8 @@ static mm_status select_scaled(mm_plan_s *p, const mm_plan_options *opt) {
         p->kchunk = (int64_t)c.kstages * kFfnTiles[c.tile].bkb;
         p->workspace_bytes = round_up((int64_t)p->split * p->batch * M * N * 4, 256);
     }
-    if (!tile_launchable(c, p->batch, M, N)) return fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
+    if (!tile_launchable(c, p->batch, M, N) || (p->algo == MM_ALGO_SPLIT_K && !pieces_launchable(M, cdiv(N, 4))))
+        return fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
     return MM_OK;
 }
 
@@ -426,7 +434,8 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
             p->split = c.split;
             p->kstages = c.kstages;
             p->algo = c.split > 1 || (force == MM_ALGO_SPLIT_K && may_split) ? MM_ALGO_SPLIT_K : MM_ALGO_GENERAL;
-            if (!tile_launchable(c, 1, M, 2 * N)) st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
+            if (!tile_launchable(c, 1, M, 2 * N) || (p->algo == MM_ALGO_SPLIT_K && !pieces_launchable(M, cdiv(N, 4))))
+                st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
             if (p->algo == MM_ALGO_SPLIT_K) {
                 p->kchunk = (int64_t)c.kstages * kFfnTiles[c.tile].bkb / es;
                 p->workspace_bytes = round_up((int64_t)c.split * 2 * M * N * 4, 256);
@@ -444,7 +453,8 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         p->dx = choose(cls, dx_al, 1, M, K, N * es, 2, dx_tiles, true);
         p->dw = choose(cls, dw_al, 2, p->tb ? N : K, p->tb ? K : N, M * es, 1, dw_tiles, true);
         if (!tile_launchable(p->dx, 1, M, K) || !tile_launchable(p->dw, 2, p->tb ? N : K, p->tb ? K : N) ||
-            !launchable((double)M * (double)cdiv(p->d_pitch * es, 16), 1))
+            !pieces_launchable(M, cdiv(p->d_pitch * es, 16)) || (p->dx.split > 1 && !pieces_launchable(M, cdiv(K, 4))) ||
+            (p->dw.split > 1 && !pieces_launchable(p->tb ? N : K, cdiv(p->tb ? K : N, 4))))
             st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
         int64_t part = 0;
         if (p->dx.split > 1) part = (int64_t)p->dx.split * M * K * 4;

@@ -287,3 +287,17 @@ def test_split_of_more_products_than_its_reduction_takes_is_refused():
     assert status(scaled, **many) == 0
     assert status(scaled, **many, force_algo=mm.ALGO_SPLIT_K) == mm.ERR_BAD_OPTION
     assert status(scaled, **many, split_k=2) == mm.ERR_BAD_OPTION
+
+
+# ---- second launches (the joining of partial sums, the element-wise pass)
+
+
+@pytest.mark.parametrize("call,kw", [
+    (scaled, dict(sa=(1 << 17, 4096), sb=(4096, 1 << 17), split_k=2)),
+    (scaled, dict(sa=(1 << 17, 4096), sb=(4096, (1 << 17) - 3), split_k=2)),
+    (glu, dict(rows=1 << 17, k=4096, n=1 << 17, split_k=2)),
+    # 2^32 - 1 pieces of dG's rows, whole workgroups of them 2^32 threads
+    (glu, dict(rows=65537, k=1, n=65535 * 8, training=True)),
+])
+def test_second_launches_of_2_32_threads_are_refused(call, kw):
+    assert status(call, **kw) == mm.ERR_TOO_LARGE
