@@ -321,10 +321,10 @@ mm_status mm_int_execute(mm_plan_t plan, const void *A, const void *B, const voi
  * (out_type: FLOAT, FLOAT16 or BFLOAT16), shared by every batch.
  *
  * The integer sum is exact: K is at most 131071 (MM_ERR_TOO_LARGE above), so
- * INT32 holds any sum of INT8 products.  It is rounded to FP32 once,
- * multiplied by the row's, then the column's scale, the bias is added in
- * FP32, and the result is narrowed once.  Results do not depend on the
- * algorithm or on a split of K.  A scale that is NaN or infinite makes its
+ * INT32 holds any sum of INT8 products.  It is rounded to FP32 and multiplied
+ * by the row's scale; that product times the column's scale plus the bias is
+ * one fused multiply-add (rounded once, to FP32), and the result is narrowed
+ * to out_type.  Results do not depend on the algorithm or on a split of K.  A scale that is NaN or infinite makes its
  * row or column what IEEE arithmetic makes of it; K == 0 gives the bias (or
  * zeros) whatever the scales hold.
  *

@@ -120,9 +120,9 @@ __device__ __forceinline__ void act_grad(float g, float &f, float &d) {
     }
 }
 
-// INT8 product's epilogue: the exact integer sum, rounded to FP32 once (the
-// sum can need 31 bits), times the scales, plus the bias.  The operations are
-// spelled out, and the FP32 result kept apart from the narrowing (which the
+// INT8 product's epilogue: the exact integer sum, rounded to FP32 (it can need
+// 31 bits), times the row's scale, rounded; that times the column's scale plus
+// the bias, rounded once.  The operations are spelled out, and the FP32 result kept apart from the narrowing (which the
 // compiler else merges into the last operation here and there, rounding once
 // where other kernels round twice), so that every kernel gives the same bits.
 __device__ __forceinline__ float scaled_value(int acc, float sa, float sb, float bias) {

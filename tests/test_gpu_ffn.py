@@ -826,3 +826,20 @@ def test_glu_forced_split_of_one_partition(nk, dev):
         p = run_forward(dev, m, k, n, list(TYPES.values())[j], nk, "silu", seed=1100 + j, algo=mm.ALGO_SPLIT_K, split=1,
                         keep=j != 1)
         assert p.info()["algo_name"] == "split_k" and p.info()["split_k"] == 1
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+def test_scaled_column_scale_and_bias_round_once(nk, dev):
+    """(sum sa) is rounded, then sb times it and the bias together: with sum 1,
+    both scales 1 + 2^-23 and the bias -(1 + 2^-22) that leaves 2^-46, where a
+    rounded product would leave 0."""
+    s = 1.0 + 2.0 ** -23
+    for m, kw in ((3, dict(force_algo=mm.ALGO_SKINNY_M)), (50, dict(tile=3)), (50, dict(tile=4, split_k=2))):
+        a, b = torch.ones(m, 512, dtype=torch.int8, device=dev), torch.zeros(512, 24, dtype=torch.int8, device=dev)
+        b[77] = 1
+        b = b.t().contiguous() if nk else b
+        p = mm.ScaledIntPlan(a.shape, b.shape, mm.FLOAT, trans_b=nk, bias=True, **kw)
+        y = torch.empty(m, 24, device=dev)
+        p.execute(a, b, y, a_scale=torch.full((m,), s, device=dev), b_scale=torch.full((24,), s, device=dev),
+                  bias=torch.full((24,), -1.0 - 2.0 ** -22, device=dev))
+        assert bool((y == 2.0 ** -46).all())
