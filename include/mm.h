@@ -423,6 +423,26 @@ typedef struct mm_glu_desc {
  * introspection calls (output shape [rows, hidden]). */
 mm_status mm_glu_plan_create(const mm_glu_desc *desc, int dtype, const mm_plan_options *opt, mm_plan_t *out);
 
+/* Tile entry (1 .. 5, as in mm_plan_options.tile) and number of K partitions
+ * of a training plan's two backward products: dX (its reduction runs over
+ * hidden, twice) and the pair dWg, dWu (over rows). */
+typedef struct mm_glu_backward_tiling {
+    int32_t dx_tile, dx_split_k;
+    int32_t dw_tile, dw_split_k;
+} mm_glu_backward_tiling;
+
+/* As mm_glu_plan_create, with overrides for the backward pass (NULL, or 0 in a
+ * field: the plan's choice; a split is clamped so that no partition is empty).
+ * MM_ERR_BAD_OPTION: a value out of range, one without a kernel (FLOAT has
+ * entries 2, 3 and 4; dW of FLOAT16 and BFLOAT16 has all but 4; 1 is not
+ * split), or any in a plan without training. */
+mm_status mm_glu_plan_create_ex(const mm_glu_desc *desc, int dtype, const mm_plan_options *opt,
+                                const mm_glu_backward_tiling *backward, mm_plan_t *out);
+
+/* What a training plan's backward pass runs on (MM_ERR_BAD_OPTION for another
+ * plan).  Entry 1 runs as entry 2 where an operand is not 16-byte aligned. */
+mm_status mm_glu_backward_info(mm_plan_t plan, mm_glu_backward_tiling *info);
+
 /* Enqueue H = f(X Wg) * (X Wu) on `stream`; G and U, both or neither (NULL),
  * receive X Wg and X Wu for the backward pass.  H, G and U may not overlap
  * each other or an input.  in_features == 0 gives zeros without reading. */

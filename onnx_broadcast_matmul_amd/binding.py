@@ -84,6 +84,11 @@ class GluDesc(ctypes.Structure):
                 ("training", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class GluBackwardTiling(ctypes.Structure):
+    _fields_ = [("dx_tile", ctypes.c_int32), ("dx_split_k", ctypes.c_int32), ("dw_tile", ctypes.c_int32),
+                ("dw_split_k", ctypes.c_int32)]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 
@@ -152,6 +157,11 @@ def lib() -> ctypes.CDLL:
         L.mm_glu_plan_create.argtypes = [ctypes.POINTER(GluDesc), ctypes.c_int, ctypes.POINTER(PlanOptions),
                                          ctypes.POINTER(vp)]
         L.mm_glu_plan_create.restype = ctypes.c_int
+        L.mm_glu_plan_create_ex.argtypes = [ctypes.POINTER(GluDesc), ctypes.c_int, ctypes.POINTER(PlanOptions),
+                                            ctypes.POINTER(GluBackwardTiling), ctypes.POINTER(vp)]
+        L.mm_glu_plan_create_ex.restype = ctypes.c_int
+        L.mm_glu_backward_info.argtypes = [vp, ctypes.POINTER(GluBackwardTiling)]
+        L.mm_glu_backward_info.restype = ctypes.c_int
         L.mm_glu_execute.argtypes = [vp] * 8
         L.mm_glu_execute.restype = ctypes.c_int
         L.mm_glu_backward.argtypes = [vp] * 11
@@ -579,14 +589,15 @@ class ScaledIntPlan(Plan):
 
 
 class GluPlan(Plan):
-    """mm_glu_plan_create / mm_glu_execute / mm_glu_backward: the gated
+    """mm_glu_plan_create_ex / mm_glu_execute / mm_glu_backward: the gated
     feed-forward block H = f(X Wg) * (X Wu) and its gradients.  The weights are
     [in_features, hidden], or [hidden, in_features] with trans_w; they may be
-    views of a merged matrix (rows w_pitch elements apart)."""
+    views of a merged matrix (rows w_pitch elements apart).  tile and split_k
+    override the forward pass's choices, dx_* and dw_* the backward pass's."""
 
     def __init__(self, rows: int, in_features: int, hidden: int, dtype: int, activation: int = ACT_SILU,
                  trans_w: bool = False, training: bool = False, w_pitch: int = 0, force_algo: int = 0, tile: int = 0,
-                 split_k: int = 0):
+                 split_k: int = 0, dx_tile: int = 0, dx_split_k: int = 0, dw_tile: int = 0, dw_split_k: int = 0):
         import torch
 
         L = lib()
@@ -597,7 +608,9 @@ class GluPlan(Plan):
         desc = GluDesc(self.rows, self.in_features, self.hidden, int(w_pitch), int(self.trans_w), int(activation),
                        int(self.training), 0)
         opt = PlanOptions(force_algo, tile, split_k, 0)
-        _check(L.mm_glu_plan_create(ctypes.byref(desc), self.dtype, ctypes.byref(opt), ctypes.byref(self._handle)))
+        back = GluBackwardTiling(dx_tile, dx_split_k, dw_tile, dw_split_k)
+        _check(L.mm_glu_plan_create_ex(ctypes.byref(desc), self.dtype, ctypes.byref(opt), ctypes.byref(back),
+                                       ctypes.byref(self._handle)))
         self._lock = threading.Lock()
         self._dt = torch_dtype(self.dtype)
         self._x = torch.Size((self.rows, self.in_features))
@@ -605,6 +618,12 @@ class GluPlan(Plan):
         self._w = torch.Size((self.hidden, self.in_features) if self.trans_w else (self.in_features, self.hidden))
         self._pitch = int(w_pitch) or self._w[1]
         self._execute, self._backward = L.mm_glu_execute, L.mm_glu_backward
+
+    def backward_info(self) -> dict:
+        """Tile entry and K partitions of a training plan's dX and of dWg, dWu."""
+        t = GluBackwardTiling()
+        _check(lib().mm_glu_backward_info(self._handle, ctypes.byref(t)))
+        return {name: getattr(t, name) for name, _ in t._fields_}
 
     def _weight(self, name, t, dev) -> int:
         """t's address, if it is a weight of this plan on GPU `dev`."""

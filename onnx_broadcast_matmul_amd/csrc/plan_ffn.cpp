@@ -160,6 +160,22 @@ static mm_status tile_option(const mm_plan_options *opt, int *tile) {
     return MM_OK;
 }
 
+// A backward product's entry and split: the requested ones, the time model's
+// where they are 0.
+static mm_status choose_backward(const char *name, int cls, bool aligned, int64_t batch, int64_t M, int64_t cols,
+                                 int64_t kbytes, int terms, unsigned tiles, int treq, int sreq, FfnChoice *c) {
+    if (treq < 0 || treq > kNumFfnTiles)
+        return fail(MM_ERR_BAD_OPTION, "%s tile %d out of range 1..%d", name, treq, kNumFfnTiles);
+    if (sreq < 0) return fail(MM_ERR_BAD_OPTION, "%s split_k %d is negative", name, sreq);
+    if (treq > 0) tiles &= 1u << (treq - 1);
+    if (!tiles) return fail(MM_ERR_BAD_OPTION, "%s has no kernel of tile %d in this type", name, treq);
+    if (sreq > 1) tiles &= ~1u;  // no 256 x 256 partials
+    if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile 1 does not split K");
+    *c = choose(cls, aligned, batch, M, cols, kbytes, terms, tiles, sreq == 0);
+    if (sreq > 0) set_split(c, kbytes, terms, sreq);
+    return MM_OK;
+}
+
 // Options that a forced algorithm would drop: partitions of the unsplit ones,
 // a tile entry of the few-row kernel.
 static mm_status forced_alone(const mm_plan_options *opt) {
@@ -359,6 +375,11 @@ mm_status mm_scaled_int_execute(mm_plan_t p, const void *A, const void *B, const
 }
 
 mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_options *opt, mm_plan_t *out) {
+    return mm_glu_plan_create_ex(d, dtype, opt, nullptr, out);
+}
+
+mm_status mm_glu_plan_create_ex(const mm_glu_desc *d, int dtype, const mm_plan_options *opt,
+                                const mm_glu_backward_tiling *backward, mm_plan_t *out) {
     clear_error();
     if (!out) return fail(MM_ERR_NULL_ARG, "out is NULL");
     *out = nullptr;
@@ -398,6 +419,9 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
     if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile %d has no FLOAT kernel", treq);
     if (force == MM_ALGO_SPLIT_K || sreq > 1) tiles &= ~1u;  // no 256 x 256 partials
     if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile 1 does not split K");
+    const mm_glu_backward_tiling bt = backward ? *backward : mm_glu_backward_tiling{};
+    if (!d->training && (bt.dx_tile || bt.dx_split_k || bt.dw_tile || bt.dw_split_k))
+        return fail(MM_ERR_BAD_OPTION, "backward tiling of a plan without training");
     mm_plan_s *p = new (std::nothrow) mm_plan_s();
     if (!p) return fail(MM_ERR_ALLOC, "host allocation failed");
     p->dtype = dtype;
@@ -450,8 +474,12 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         // transposed operand has rows too short to stage.
         const unsigned dx_tiles = dtype == MM_FLOAT ? 0xe : 0x1f, dw_tiles = dtype == MM_FLOAT ? 0xe : 0x17;
         const bool dx_al = (p->w_pitch * es) % 16 == 0 && ((p->tb ? K : N) * es) % 16 == 0, dw_al = (K * es) % 16 == 0;
-        p->dx = choose(cls, dx_al, 1, M, K, N * es, 2, dx_tiles, true);
-        p->dw = choose(cls, dw_al, 2, p->tb ? N : K, p->tb ? K : N, M * es, 1, dw_tiles, true);
+        st = choose_backward("dX", cls, dx_al, 1, M, K, N * es, 2, dx_tiles, bt.dx_tile, bt.dx_split_k, &p->dx);
+        if (st == MM_OK)
+            st = choose_backward("dW", cls, dw_al, 2, p->tb ? N : K, p->tb ? K : N, M * es, 1, dw_tiles, bt.dw_tile,
+                                 bt.dw_split_k, &p->dw);
+    }
+    if (st == MM_OK && p->training) {
         if (!tile_launchable(p->dx, 1, M, K) || !tile_launchable(p->dw, 2, p->tb ? N : K, p->tb ? K : N) ||
             !pieces_launchable(M, cdiv(p->d_pitch * es, 16)) || (p->dx.split > 1 && !pieces_launchable(M, cdiv(K, 4))) ||
             (p->dw.split > 1 && !pieces_launchable(p->tb ? N : K, cdiv(p->tb ? K : N, 4))))
@@ -467,6 +495,14 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
         return st;
     }
     *out = p;
+    return MM_OK;
+}
+
+mm_status mm_glu_backward_info(mm_plan_t p, mm_glu_backward_tiling *info) {
+    clear_error();
+    if (!p || !info) return fail(MM_ERR_NULL_ARG, "plan or info is NULL");
+    if (!p->is_glu || !p->training) return fail(MM_ERR_BAD_OPTION, "not a gated-block plan with training");
+    *info = mm_glu_backward_tiling{p->dx.tile + 1, p->dx.split, p->dw.tile + 1, p->dw.split};
     return MM_OK;
 }
 

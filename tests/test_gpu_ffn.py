@@ -843,3 +843,88 @@ def test_scaled_column_scale_and_bias_round_once(nk, dev):
         p.execute(a, b, y, a_scale=torch.full((m,), s, device=dev), b_scale=torch.full((24,), s, device=dev),
                   bias=torch.full((24,), -1.0 - 2.0 ** -22, device=dev))
         assert bool((y == 2.0 ** -46).all())
+
+
+# ---- operands of any place, every entry of the backward products
+
+
+def placed(values, offset=0, gap=0, fill=float("nan")):
+    """A copy of the matrix `values` with rows `gap` elements apart, `offset`
+    elements off 16-byte alignment, and a check that nothing around it changed
+    (`fill` everywhere: a value read from there would spoil the result)."""
+    r, c = values.shape
+    buf = torch.full((256 + offset + r * (c + gap) + 256,), fill, dtype=values.dtype, device=values.device)
+    at = ((r, c), (c + gap, 1), 256 + offset)
+    view = buf.as_strided(*at)
+    view.copy_(values)
+    rest = torch.ones_like(buf, dtype=torch.bool)
+    rest.as_strided(*at).fill_(False)
+    before = buf[rest].clone().view(torch.uint8)
+
+    def check(what):
+        assert torch.equal(buf[rest].view(torch.uint8), before), f"wrote outside {what}"
+
+    return view, check
+
+
+def run_step(dev, m, k, n, dt, nk, act, seed=0, offset=0, gap=0, forward=True, **tiling):
+    """A training step whose eleven operands all lie at `offset`, the weights
+    and their gradients with rows `gap` apart, compared with 64 bits."""
+    shape = (n, k) if nk else (k, n)
+    values = {"x": rand((m, k), dt, dev, seed), "dh": rand((m, n), dt, dev, seed + 1, 0.5)}
+    for i, w in enumerate(("wg", "wu", "dwg", "dwu")):
+        values[w] = rand(shape, dt, dev, seed + 2 + i, 0.2)
+    for i, name in enumerate(("h", "g", "u")):
+        values[name] = rand((m, n), dt, dev, seed + 6 + i, 1.5)
+    values["dx"] = rand((m, k), dt, dev, seed + 9)
+    t, checks = {}, []
+    for name, v in values.items():
+        t[name], check = placed(v, offset, gap if "w" in name else 0)
+        checks.append((name, check))
+    plan = mm.GluPlan(m, k, n, mm.torch_dtype_code(dt), activation=mm.ACTIVATIONS[act], trans_w=nk, training=True,
+                      w_pitch=shape[1] + gap if gap else 0, **tiling)
+    w = [t[i].t() if nk else t[i] for i in ("wg", "wu")]
+    if forward:
+        plan.execute(t["x"], t["wg"], t["wu"], t["h"], t["g"], t["u"])
+        torch.cuda.synchronize()
+        for name, (want, tol) in zip("hgu", forward64(t["x"], *w, act, dt)):
+            within(t[name], want, tol, f"{name} {m}x{k}x{n}")
+    plan.backward(t["x"], t["wg"], t["wu"], t["g"], t["u"], t["dh"], t["dx"], t["dwg"], t["dwu"])
+    torch.cuda.synchronize()
+    for name, (want, tol) in zip(("dx", "dwg", "dwu"), backward64(t["x"], *w, t["g"], t["u"], t["dh"], act, dt)):
+        within(t[name].t() if nk and "w" in name else t[name], want, tol, f"{name} {m}x{k}x{n}")
+    for name, check in checks:
+        check(name)
+    return plan
+
+
+BACK_TILES = [(d, t) for d in TYPES for t in ((2, 3, 4) if d == "fp32" else (1, 2, 3, 4, 5))]
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("dt,tile", BACK_TILES)
+def test_glu_backward_every_tile(tile, nk, dt, dev):
+    """dX and the pair dWg, dWu on each entry, whole and split K, over several
+    tiles with a ragged edge: aligned and odd sizes, operands off alignment,
+    reductions of many stages, of part of one and of one element."""
+    dw = tile if dt == "fp32" or tile != 4 else 3  # dW of 16-bit types has no entry 4
+    for split in (1, 3) if tile > 1 else (1,):
+        for j, (m, k, n, offset, gap) in enumerate(((530, 328, 400, 0, 0), (300, 701, 281, 0, 0), (270, 136, 16, 0, 8),
+                                                    (16, 264, 530, 1, 0), (2, 35, 9, 0, 0), (1, 300, 1, 0, 1))):
+            p = run_step(dev, m, k, n, TYPES[dt], nk, ACTS[j % 5], seed=1300 + 10 * j, offset=offset, gap=gap,
+                         forward=False, dx_tile=tile, dw_tile=dw, dx_split_k=split, dw_split_k=split)
+            i = p.backward_info()
+            assert (i["dx_tile"], i["dw_tile"]) == (tile, dw)
+            assert j > 1 or (i["dx_split_k"] == split and i["dw_split_k"] in (2, split))
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_glu_backward_more_tiles_of_each_large_entry_than_cus(dt, nk, dev):
+    """dX of the first size has 18 x 19 tiles of 256 x 256, dW of the second twice
+    10 x 19; with 256 x 128 about twice as many."""
+    for tile in (1, 5):
+        for j, (m, k, n) in enumerate(((4360, 4616, 264), (520, 4616, 2360))):
+            p = run_step(dev, m, k, n, TYPES[dt], nk, "silu", seed=1400 + 10 * j, forward=False, dx_tile=tile, dw_tile=tile,
+                         dx_split_k=1, dw_split_k=1)
+            assert p.backward_info() == {"dx_tile": tile, "dx_split_k": 1, "dw_tile": tile, "dw_split_k": 1}
