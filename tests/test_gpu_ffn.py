@@ -898,6 +898,16 @@ def run_step(dev, m, k, n, dt, nk, act, seed=0, offset=0, gap=0, forward=True, *
     return plan
 
 
+@pytest.mark.parametrize("offset,gap", [(0, 0), (0, 16), (0, 3), (1, 0), (1, 16), (3, 5)])
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("dt", TYPES, ids=str)
+def test_glu_step_on_operands_of_any_place(dt, nk, offset, gap, dev):
+    """Bases and pitches on and off 16-byte alignment, aligned and odd sizes,
+    on the few-row kernel and the tiles."""
+    for j, (m, k, n) in enumerate(((5, 64, 96), (3, 65, 33), (150, 64, 96), (150, 65, 97), (300, 200, 136))):
+        run_step(dev, m, k, n, TYPES[dt], nk, ACTS[j], seed=1200 + 10 * j, offset=offset, gap=gap)
+
+
 BACK_TILES = [(d, t) for d in TYPES for t in ((2, 3, 4) if d == "fp32" else (1, 2, 3, 4, 5))]
 
 
