@@ -509,19 +509,32 @@ def _run(dev, stream, fn, *args) -> None:
         _check(st)
 
 
+def _empty(shape, dt, device, stream):
+    """A result that is made on `stream` (None: the current one)."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dt, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dt, device=device)
+
+
 def quantize_rows(X, q=None, scale=None, stream=None):
     """mm_quantize_rows: (q, scale) of X's rows (its last dimension), q INT8 of
-    X's shape, scale FP32 of X's shape without the last dimension."""
+    X's shape, scale FP32 of X's shape without the last dimension.  Those that
+    are not given are made on ``stream`` (default: the current stream), as if
+    it were current: memory that another stream's queued work still uses does
+    not come into them."""
     import torch
 
     code = torch_dtype_code(X.dtype)
     if X.dim() < 1:
         raise ValueError("X needs at least one dimension")
-    if q is None:
-        q = torch.empty(X.shape, dtype=torch.int8, device=X.device)
-    if scale is None:
-        scale = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
     dev = _device_of(X)
+    if q is None:
+        q = _empty(X.shape, torch.int8, X.device, stream)
+    if scale is None:
+        scale = _empty(X.shape[:-1], torch.float32, X.device, stream)
     xp = _dense("X", X, X.dtype, X.shape, dev)
     qp = _dense("q", q, torch.int8, X.shape, dev)
     sp = _dense("scale", scale, torch.float32, X.shape[:-1], dev)

@@ -938,3 +938,19 @@ def test_glu_backward_more_tiles_of_each_large_entry_than_cus(dt, nk, dev):
             p = run_step(dev, m, k, n, TYPES[dt], nk, "silu", seed=1400 + 10 * j, forward=False, dx_tile=tile, dw_tile=tile,
                          dx_split_k=1, dw_split_k=1)
             assert p.backward_info() == {"dx_tile": tile, "dx_split_k": 1, "dw_tile": tile, "dw_split_k": 1}
+
+
+def test_quantize_rows_makes_its_results_on_its_stream(dev):
+    """Memory freed on the current stream, whose queued work may still use it,
+    is not what a call on another stream writes to."""
+    x = rand((700, 3001), BF16, dev, 1500)
+    wq, ws = quantize64(x)
+    side = torch.cuda.Stream()
+    old = [torch.empty(700, 3001, dtype=torch.int8, device=dev), torch.empty(700, device=dev)]
+    at = {t.data_ptr() for t in old}
+    torch.cuda.synchronize()
+    del old
+    q, s = mm.quantize_rows(x, stream=side)
+    torch.cuda.synchronize()
+    assert q.data_ptr() not in at and s.data_ptr() not in at
+    assert np.array_equal(q.cpu().numpy(), wq) and np.array_equal(s.cpu().numpy(), ws)
