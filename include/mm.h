@@ -383,12 +383,13 @@ mm_status mm_quantize_rows(const void *X, int dtype, int64_t rows, int64_t cols,
  * in_features], with rows w_pitch elements apart (0: dense; the gate and up
  * halves of one merged matrix are two pointers with its pitch).  dWg and dWu
  * have the weights' layout and pitch.  Everything has the plan's type (FLOAT,
- * FLOAT16 or BFLOAT16); X, H, G, U, dH and dX are dense.
+ * FLOAT16 or BFLOAT16), except that G and U may be kept in FLOAT
+ * (mm_glu_plan_create_ex); X, H, G, U, dH and dX are dense.
  *
  * Products accumulate in FP32, f and the element-wise products are computed
  * in FP32, H, G and U are each rounded once.  The backward pass starts from
- * the rounded G and U and rounds dG and dU to the plan's type for the matrix
- * cores.  relu's derivative at 0 is 0.  Infinities and NaN follow the
+ * G and U as they are kept and rounds dG and dU to the plan's type for the
+ * matrix cores.  relu's derivative at 0 is 0.  Infinities and NaN follow the
  * formulas.
  *
  * Options: force_algo SKINNY_M (at most 32 rows), GENERAL or SPLIT_K; tile
@@ -423,25 +424,32 @@ typedef struct mm_glu_desc {
  * introspection calls (output shape [rows, hidden]). */
 mm_status mm_glu_plan_create(const mm_glu_desc *desc, int dtype, const mm_plan_options *opt, mm_plan_t *out);
 
-/* Tile entry (1 .. 5, as in mm_plan_options.tile) and number of K partitions
- * of a training plan's two backward products: dX (its reduction runs over
- * hidden, twice) and the pair dWg, dWu (over rows). */
-typedef struct mm_glu_backward_tiling {
+/* What a gated-block plan's G and U are kept in, and its backward products'
+ * tile entry (1 .. 5, as in mm_plan_options.tile) and number of K partitions:
+ * of dX (its reduction runs over hidden, twice) and of the pair dWg, dWu (over
+ * rows).
+ *
+ * kept_type MM_FLOAT keeps G and U as the FP32 sums they are, for twice their
+ * bytes in a 16-bit plan: the backward pass then rounds dG, dU and its results
+ * only, and its gradients are off by 0.0024 of their norm in BFLOAT16, where a G
+ * and U rounded to 16 bits make it 0.0031. */
+typedef struct mm_glu_options {
+    int32_t kept_type; /* 0 (the plan's type), the plan's type, or MM_FLOAT */
     int32_t dx_tile, dx_split_k;
     int32_t dw_tile, dw_split_k;
-} mm_glu_backward_tiling;
+} mm_glu_options;
 
-/* As mm_glu_plan_create, with overrides for the backward pass (NULL, or 0 in a
- * field: the plan's choice; a split is clamped so that no partition is empty).
- * MM_ERR_BAD_OPTION: a value out of range, one without a kernel (FLOAT has
- * entries 2, 3 and 4; dW of FLOAT16 and BFLOAT16 has all but 4; 1 is not
- * split), or any in a plan without training. */
+/* As mm_glu_plan_create, with these options (NULL, or 0 in a field: as
+ * mm_glu_plan_create; a split is clamped so that no partition is empty).
+ * MM_ERR_DTYPE: another kept_type.  MM_ERR_BAD_OPTION: a tile or split out of
+ * range, one without a kernel (FLOAT has entries 2, 3 and 4; dW of FLOAT16 and
+ * BFLOAT16 has all but 4; 1 is not split), or any in a plan without training. */
 mm_status mm_glu_plan_create_ex(const mm_glu_desc *desc, int dtype, const mm_plan_options *opt,
-                                const mm_glu_backward_tiling *backward, mm_plan_t *out);
+                                const mm_glu_options *glu, mm_plan_t *out);
 
-/* What a training plan's backward pass runs on (MM_ERR_BAD_OPTION for another
+/* The options that a training plan runs with (MM_ERR_BAD_OPTION for another
  * plan).  Entry 1 runs as entry 2 where an operand is not 16-byte aligned. */
-mm_status mm_glu_backward_info(mm_plan_t plan, mm_glu_backward_tiling *info);
+mm_status mm_glu_get_options(mm_plan_t plan, mm_glu_options *glu);
 
 /* Enqueue H = f(X Wg) * (X Wu) on `stream`; G and U, both or neither (NULL),
  * receive X Wg and X Wu for the backward pass.  H, G and U may not overlap

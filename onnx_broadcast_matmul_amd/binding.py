@@ -84,9 +84,9 @@ class GluDesc(ctypes.Structure):
                 ("training", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-class GluBackwardTiling(ctypes.Structure):
-    _fields_ = [("dx_tile", ctypes.c_int32), ("dx_split_k", ctypes.c_int32), ("dw_tile", ctypes.c_int32),
-                ("dw_split_k", ctypes.c_int32)]
+class GluOptions(ctypes.Structure):
+    _fields_ = [("kept_type", ctypes.c_int32), ("dx_tile", ctypes.c_int32), ("dx_split_k", ctypes.c_int32),
+                ("dw_tile", ctypes.c_int32), ("dw_split_k", ctypes.c_int32)]
 
 
 _lib = None
@@ -158,10 +158,10 @@ def lib() -> ctypes.CDLL:
                                          ctypes.POINTER(vp)]
         L.mm_glu_plan_create.restype = ctypes.c_int
         L.mm_glu_plan_create_ex.argtypes = [ctypes.POINTER(GluDesc), ctypes.c_int, ctypes.POINTER(PlanOptions),
-                                            ctypes.POINTER(GluBackwardTiling), ctypes.POINTER(vp)]
+                                            ctypes.POINTER(GluOptions), ctypes.POINTER(vp)]
         L.mm_glu_plan_create_ex.restype = ctypes.c_int
-        L.mm_glu_backward_info.argtypes = [vp, ctypes.POINTER(GluBackwardTiling)]
-        L.mm_glu_backward_info.restype = ctypes.c_int
+        L.mm_glu_get_options.argtypes = [vp, ctypes.POINTER(GluOptions)]
+        L.mm_glu_get_options.restype = ctypes.c_int
         L.mm_glu_execute.argtypes = [vp] * 8
         L.mm_glu_execute.restype = ctypes.c_int
         L.mm_glu_backward.argtypes = [vp] * 11
@@ -605,12 +605,15 @@ class GluPlan(Plan):
     """mm_glu_plan_create_ex / mm_glu_execute / mm_glu_backward: the gated
     feed-forward block H = f(X Wg) * (X Wu) and its gradients.  The weights are
     [in_features, hidden], or [hidden, in_features] with trans_w; they may be
-    views of a merged matrix (rows w_pitch elements apart).  tile and split_k
-    override the forward pass's choices, dx_* and dw_* the backward pass's."""
+    views of a merged matrix (rows w_pitch elements apart).  kept_type is the
+    type of G and U (0: the plan's; FLOAT keeps their FP32 sums).  tile and
+    split_k override the forward pass's choices, dx_* and dw_* the backward
+    pass's."""
 
     def __init__(self, rows: int, in_features: int, hidden: int, dtype: int, activation: int = ACT_SILU,
                  trans_w: bool = False, training: bool = False, w_pitch: int = 0, force_algo: int = 0, tile: int = 0,
-                 split_k: int = 0, dx_tile: int = 0, dx_split_k: int = 0, dw_tile: int = 0, dw_split_k: int = 0):
+                 split_k: int = 0, kept_type: int = 0, dx_tile: int = 0, dx_split_k: int = 0, dw_tile: int = 0,
+                 dw_split_k: int = 0):
         import torch
 
         L = lib()
@@ -621,21 +624,23 @@ class GluPlan(Plan):
         desc = GluDesc(self.rows, self.in_features, self.hidden, int(w_pitch), int(self.trans_w), int(activation),
                        int(self.training), 0)
         opt = PlanOptions(force_algo, tile, split_k, 0)
-        back = GluBackwardTiling(dx_tile, dx_split_k, dw_tile, dw_split_k)
-        _check(L.mm_glu_plan_create_ex(ctypes.byref(desc), self.dtype, ctypes.byref(opt), ctypes.byref(back),
+        glu = GluOptions(int(kept_type), dx_tile, dx_split_k, dw_tile, dw_split_k)
+        _check(L.mm_glu_plan_create_ex(ctypes.byref(desc), self.dtype, ctypes.byref(opt), ctypes.byref(glu),
                                        ctypes.byref(self._handle)))
         self._lock = threading.Lock()
         self._dt = torch_dtype(self.dtype)
+        self._kept = torch_dtype(int(kept_type) or self.dtype)
         self._x = torch.Size((self.rows, self.in_features))
         self._h = torch.Size((self.rows, self.hidden))
         self._w = torch.Size((self.hidden, self.in_features) if self.trans_w else (self.in_features, self.hidden))
         self._pitch = int(w_pitch) or self._w[1]
         self._execute, self._backward = L.mm_glu_execute, L.mm_glu_backward
 
-    def backward_info(self) -> dict:
-        """Tile entry and K partitions of a training plan's dX and of dWg, dWu."""
-        t = GluBackwardTiling()
-        _check(lib().mm_glu_backward_info(self._handle, ctypes.byref(t)))
+    def options(self) -> dict:
+        """mm_glu_get_options: the type of G and U, and the tile entry and K
+        partitions of a training plan's dX and of dWg, dWu."""
+        t = GluOptions()
+        _check(lib().mm_glu_get_options(self._handle, ctypes.byref(t)))
         return {name: getattr(t, name) for name, _ in t._fields_}
 
     def _weight(self, name, t, dev) -> int:
@@ -660,8 +665,8 @@ class GluPlan(Plan):
         xp = _dense("X", X, dt, self._x, dev)
         gp, up = self._weight("Wg", Wg, dev), self._weight("Wu", Wu, dev)
         hp = _dense("H", H, dt, h, dev)
-        kg = None if G is None else _dense("G", G, dt, h, dev)
-        ku = None if U is None else _dense("U", U, dt, h, dev)
+        kg = None if G is None else _dense("G", G, self._kept, h, dev)
+        ku = None if U is None else _dense("U", U, self._kept, h, dev)
         with self._lock:
             _run(dev, stream, self._execute, self._handle, xp, gp, up, hp, kg, ku)
 
@@ -672,7 +677,7 @@ class GluPlan(Plan):
         dt, h = self._dt, self._h
         dev = _device_of(dH)
         ptrs = (_dense("X", X, dt, self._x, dev), self._weight("Wg", Wg, dev), self._weight("Wu", Wu, dev),
-                _dense("G", G, dt, h, dev), _dense("U", U, dt, h, dev), _dense("dH", dH, dt, h, dev),
+                _dense("G", G, self._kept, h, dev), _dense("U", U, self._kept, h, dev), _dense("dH", dH, dt, h, dev),
                 None if dX is None else _dense("dX", dX, dt, self._x, dev),
                 None if dWg is None else self._weight("dWg", dWg, dev),
                 None if dWu is None else self._weight("dWu", dWu, dev))

@@ -21,6 +21,8 @@ struct FfnArgs {
     int64_t batch;         // products (scaled), or 2 for a pair
     int32_t act;
     int32_t y_vec;         // output rows are whole, aligned 16-byte chunks
+    int32_t kept_vec;      // gated block: so are those of G and U,
+    int32_t kept32;        // which are FP32 in a 16-bit plan
     // scaled INT8 product
     const float *sa, *sb;
     const void *bias;      // of the output type, or NULL
@@ -41,7 +43,10 @@ struct FfnSlim {
     int32_t M, N, K, lda, ldb, ldy;
     int32_t kstages;
     uint16_t split;
-    uint8_t act, y_vec;
+    uint8_t act, flags;
+    __host__ __device__ bool y_vec() const { return flags & 1; }
+    __host__ __device__ bool kept_vec() const { return flags & 2; }
+    __host__ __device__ bool kept32() const { return flags & 4; }
     __host__ __device__ void *G() const { return Y[1]; }  // gated block
     __host__ __device__ void *U() const { return Y[2]; }
     __host__ __device__ const float *sa() const { return (const float *)A[1]; }  // scaled product
@@ -91,7 +96,7 @@ inline T slim_args(const FfnArgs &a, FfnUse use, bool split, bool reduce) {
     s.kstages = a.kstages;
     s.split = (uint16_t)a.split;
     s.act = (uint8_t)a.act;
-    s.y_vec = (uint8_t)a.y_vec;
+    s.flags = (uint8_t)((a.y_vec ? 1 : 0) | (a.kept_vec ? 2 : 0) | (a.kept32 ? 4 : 0));
     if (use == kUseGlu) {
         s.Y[1] = a.G;
         s.Y[2] = a.U;
@@ -112,9 +117,10 @@ inline FfnSlimBatch slim_batch(const FfnArgs &a, bool split, bool reduce) {
 }
 
 // Element-wise part of the gated block's backward pass: dG = dH * U * f'(G),
-// dU = dH * f(G).  G, U, dH are dense [M, N]; dG, dU have rows of ldw elements
-// (whole 16-byte chunks, 16-byte aligned), zero past N.
-hipError_t launch_glu_dact(int dtype, int act, const void *G, const void *U, const void *dH, void *dG, void *dU,
+// dU = dH * f(G).  G, U (of type `kept`: dtype or MM_FLOAT) and dH are dense
+// [M, N]; dG, dU have rows of ldw elements (whole 16-byte chunks, 16-byte
+// aligned), zero past N.
+hipError_t launch_glu_dact(int dtype, int kept, int act, const void *G, const void *U, const void *dH, void *dG, void *dU,
                            int64_t M, int64_t N, int64_t ldw, hipStream_t s);
 // Tiled products (vec: every operand row and base is 16-byte aligned; split:
 // partial sums to W, to be joined by the matching reduction; the gated

@@ -636,8 +636,13 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
         emit((T)0, 0, plain, (T *)a.part() + (sidx * nprod + b) * M * N, N, N % 4 == 0);
     } else if constexpr (MODE == kGlu) {
         if (a.G()) {
-            emit((typename OE::S)0, 0, plain, a.G(), a.ldy, a.y_vec != 0);
-            emit((typename OE::S)0, FNP, plain, a.U(), a.ldy, a.y_vec != 0);
+            if (OD != MM_FLOAT && a.kept32()) {
+                emit(0.0f, 0, plain, a.G(), a.ldy, a.kept_vec());
+                emit(0.0f, FNP, plain, a.U(), a.ldy, a.kept_vec());
+            } else {
+                emit((typename OE::S)0, 0, plain, a.G(), a.ldy, a.kept_vec());
+                emit((typename OE::S)0, FNP, plain, a.U(), a.ldy, a.kept_vec());
+            }
         }
         auto apply = [&](auto kind) {
 #pragma unroll
@@ -656,7 +661,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
         case MM_ACT_RELU: apply(std::integral_constant<int, MM_ACT_RELU>()); break;
         default: apply(std::integral_constant<int, MM_ACT_SIGMOID>()); break;
         }
-        emit((typename OE::S)0, 0, plain, a.Y[0], a.ldy, a.y_vec != 0);
+        emit((typename OE::S)0, 0, plain, a.Y[0], a.ldy, a.y_vec());
     } else if constexpr (MODE == kScaled) {
         // Scales of this lane's rows, and of the tile's columns in LDS after
         // the main loop's last reads.  K == 0: the matrices are empty, their
@@ -677,9 +682,9 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
         }
         __syncthreads();
         emit((typename OE::S)0, 0, [&](int i, int cl, int v) { return scaled_value(v, rs[i], cs[cl], cb[cl]); },
-             (typename OE::S *)a.Y[0] + b * M * a.ldy, a.ldy, a.y_vec != 0);
+             (typename OE::S *)a.Y[0] + b * M * a.ldy, a.ldy, a.y_vec());
     } else {
-        emit((typename OE::S)0, 0, plain, MODE == kPair ? a.Y[pick] : a.Y[0], a.ldy, a.y_vec != 0);
+        emit((typename OE::S)0, 0, plain, MODE == kPair ? a.Y[pick] : a.Y[0], a.ldy, a.y_vec());
     }
 #endif
 }

@@ -379,8 +379,13 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
                 su += red[v][CF + (c >> 4)][i][at];
             }
             if (a.G()) {
-                ((OS *)a.G())[o] = OE::from_f32(sg);
-                ((OS *)a.U())[o] = OE::from_f32(su);
+                if (OD != MM_FLOAT && a.kept32()) {
+                    ((float *)a.G())[o] = sg;
+                    ((float *)a.U())[o] = su;
+                } else {
+                    ((OS *)a.G())[o] = OE::from_f32(sg);
+                    ((OS *)a.U())[o] = OE::from_f32(su);
+                }
             }
             constexpr bool X = DT == MM_FLOAT;
             float f;

@@ -1,5 +1,7 @@
 // k_glu.hip -- gated feed-forward block: dispatch of the tiled products by
 // element type, and the element-wise part of the backward pass.
+#include <type_traits>
+
 #include "activation.h"
 #include "device.h"
 #include "ffn.h"
@@ -77,15 +79,20 @@ __global__ __launch_bounds__(256) void k_glu_reduce(FfnSlim a) {
         ou[e] = E::from_f32(u[e]);
         oh[e] = E::from_f32(act_switch<DT == MM_FLOAT>(a.act, g[e]) * u[e]);
     }
-    auto put = [&](void *p, const S *v) {
-        S *y = (S *)p + i0;
-        if (n == 4) __builtin_memcpy(y, v, sizeof(og));
+    auto put = [&](void *p, const auto *v) {
+        auto *y = (typename std::remove_const<typename std::remove_pointer<decltype(v)>::type>::type *)p + i0;
+        if (n == 4) __builtin_memcpy(y, v, 4 * sizeof(*v));
         else
             for (int e = 0; e < n; ++e) y[e] = v[e];
     };
     if (a.G()) {
-        put(a.G(), og);
-        put(a.U(), ou);
+        if (DT != MM_FLOAT && a.kept32()) {
+            put(a.G(), g);
+            put(a.U(), u);
+        } else {
+            put(a.G(), og);
+            put(a.U(), ou);
+        }
     }
     put(a.Y[0], oh);
 }
@@ -155,19 +162,23 @@ hipError_t launch_sum_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
 
 // dG = dH U f'(G) and dU = dH f(G), a thread per 16 bytes of each tensor's
 // row.  Three tensors are read and two written once, which bounds it (8192 x
-// 11008 BF16: 0.90 GB in 151 us, 6.0 TB/s; 4096 x 5504 41 us).  A kernel of its
+// 11008 BF16: 0.90 GB in 151 us, 6.0 TB/s, and 1.26 GB in 210 us with FP32 G and
+// U; 4096 x 5504 41 and 48 us).  A kernel of its
 // own because dX reduces over N and dW over M: formed inside those products it
-// would be formed once for every tile column.  G and U come in the
-// element type (the forward pass rounded them once) and dG, dU are rounded to
-// it because the matrix cores take them in it: the roundings, half a step
-// each, that an unfused block in this type makes too.  dG and dU have rows of
-// ldw elements, whole 16-byte chunks; the columns past N hold zeros, so the
+// would be formed once for every tile column.  G and U come as the forward
+// pass kept them (KT): FP32 sums, or rounded to the element type, which halves
+// their bytes and makes BF16 gradients off by 0.0031 of their norm, not 0.0024.
+// dG and dU are rounded to
+// the element type because the matrix cores take them in it.  They have rows
+// of ldw elements, whole 16-byte chunks; the columns past N hold zeros, so the
 // products may read them.
-template <int DT, int ACT>
+template <int DT, int KT, int ACT>
 __global__ __launch_bounds__(256) void k_glu_dact(const void *G, const void *U, const void *dH, void *dG, void *dU,
                                                   int64_t M, int64_t N, int64_t ldw) {
     using E = Elem<DT>;
     using S = typename E::S;
+    using KE = Elem<KT>;
+    using KS = typename KE::S;
     constexpr int VE = E::kVE;
     const int64_t cpr = ldw / VE;
     const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -175,26 +186,27 @@ __global__ __launch_bounds__(256) void k_glu_dact(const void *G, const void *U, 
     // cpr < 2^31: one 32-bit division where the index allows it.
     const int64_t row = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
     const int64_t col = (x - row * cpr) * VE, i0 = row * N + col;
-    S g[VE], u[VE], h[VE], og[VE], ou[VE];
+    KS g[VE], u[VE];
+    S h[VE], og[VE], ou[VE];
     if (col + VE <= N) {
-        __builtin_memcpy(g, (const S *)G + i0, 16);
-        __builtin_memcpy(u, (const S *)U + i0, 16);
+        __builtin_memcpy(g, (const KS *)G + i0, sizeof(g));
+        __builtin_memcpy(u, (const KS *)U + i0, sizeof(u));
         __builtin_memcpy(h, (const S *)dH + i0, 16);
     } else {
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             const bool in = col + e < N;
-            g[e] = in ? ((const S *)G)[i0 + e] : (S)0;
-            u[e] = in ? ((const S *)U)[i0 + e] : (S)0;
+            g[e] = in ? ((const KS *)G)[i0 + e] : (KS)0;
+            u[e] = in ? ((const KS *)U)[i0 + e] : (KS)0;
             h[e] = in ? ((const S *)dH)[i0 + e] : (S)0;
         }
     }
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
         float f, d;
-        act_grad<ACT, DT == MM_FLOAT>(E::to_f32(g[e]), f, d);
+        act_grad<ACT, DT == MM_FLOAT>(KE::to_f32(g[e]), f, d);
         const float dh = E::to_f32(h[e]);
-        og[e] = E::from_f32(dh * E::to_f32(u[e]) * d);
+        og[e] = E::from_f32(dh * KE::to_f32(u[e]) * d);
         ou[e] = E::from_f32(dh * f);
     }
     uint4 vg, vu;
@@ -204,34 +216,41 @@ __global__ __launch_bounds__(256) void k_glu_dact(const void *G, const void *U, 
     *(uint4 *)((S *)dU + row * ldw + col) = vu;
 }
 
-template <int DT, int ACT>
+template <int DT, int KT, int ACT>
 static hipError_t dact(const void *G, const void *U, const void *dH, void *dG, void *dU, int64_t M, int64_t N,
                        int64_t ldw, hipStream_t s) {
     const int64_t g = (M * (ldw / Elem<DT>::kVE) + 255) / 256;
     if (g <= 0) return hipSuccess;
     if (g > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_glu_dact<DT, ACT>), dim3((unsigned)g), dim3(256), 0, s, G, U, dH, dG, dU, M, N, ldw);
+    hipLaunchKernelGGL((k_glu_dact<DT, KT, ACT>), dim3((unsigned)g), dim3(256), 0, s, G, U, dH, dG, dU, M, N, ldw);
     return hipGetLastError();
 }
 
-template <int DT>
+template <int DT, int KT>
 static hipError_t dact(int act, const void *G, const void *U, const void *dH, void *dG, void *dU, int64_t M, int64_t N,
                        int64_t ldw, hipStream_t s) {
     switch (act) {
-    case MM_ACT_SILU: return dact<DT, MM_ACT_SILU>(G, U, dH, dG, dU, M, N, ldw, s);
-    case MM_ACT_GELU: return dact<DT, MM_ACT_GELU>(G, U, dH, dG, dU, M, N, ldw, s);
-    case MM_ACT_GELU_TANH: return dact<DT, MM_ACT_GELU_TANH>(G, U, dH, dG, dU, M, N, ldw, s);
-    case MM_ACT_RELU: return dact<DT, MM_ACT_RELU>(G, U, dH, dG, dU, M, N, ldw, s);
-    case MM_ACT_SIGMOID: return dact<DT, MM_ACT_SIGMOID>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_SILU: return dact<DT, KT, MM_ACT_SILU>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_GELU: return dact<DT, KT, MM_ACT_GELU>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_GELU_TANH: return dact<DT, KT, MM_ACT_GELU_TANH>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_RELU: return dact<DT, KT, MM_ACT_RELU>(G, U, dH, dG, dU, M, N, ldw, s);
+    case MM_ACT_SIGMOID: return dact<DT, KT, MM_ACT_SIGMOID>(G, U, dH, dG, dU, M, N, ldw, s);
     }
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_glu_dact(int dtype, int act, const void *G, const void *U, const void *dH, void *dG, void *dU,
+template <int DT>
+static hipError_t dact(int kept, int act, const void *G, const void *U, const void *dH, void *dG, void *dU, int64_t M,
+                       int64_t N, int64_t ldw, hipStream_t s) {
+    return kept == DT ? dact<DT, DT>(act, G, U, dH, dG, dU, M, N, ldw, s)
+                      : dact<DT, MM_FLOAT>(act, G, U, dH, dG, dU, M, N, ldw, s);
+}
+
+hipError_t launch_glu_dact(int dtype, int kept, int act, const void *G, const void *U, const void *dH, void *dG, void *dU,
                            int64_t M, int64_t N, int64_t ldw, hipStream_t s) {
-    return dtype == MM_FLOAT ? dact<MM_FLOAT>(act, G, U, dH, dG, dU, M, N, ldw, s)
-           : dtype == MM_FLOAT16 ? dact<MM_FLOAT16>(act, G, U, dH, dG, dU, M, N, ldw, s)
-                                 : dact<MM_BFLOAT16>(act, G, U, dH, dG, dU, M, N, ldw, s);
+    return dtype == MM_FLOAT ? dact<MM_FLOAT>(kept, act, G, U, dH, dG, dU, M, N, ldw, s)
+           : dtype == MM_FLOAT16 ? dact<MM_FLOAT16>(kept, act, G, U, dH, dG, dU, M, N, ldw, s)
+                                 : dact<MM_BFLOAT16>(kept, act, G, U, dH, dG, dU, M, N, ldw, s);
 }
 
 }  // namespace mm

@@ -81,6 +81,7 @@ struct mm_plan_s {
     bool is_glu = false;
     int act = 0;
     bool training = false;
+    int kept = 0;          // type of G and U
     int64_t w_pitch = 0, d_off = 0, d_pitch = 0, d_bytes = 0;
     mm::FfnChoice dx, dw;  // the backward products
     int32_t kstages = 0;   // K stages of a partition (scaled product, forward pass)

@@ -379,7 +379,7 @@ mm_status mm_glu_plan_create(const mm_glu_desc *d, int dtype, const mm_plan_opti
 }
 
 mm_status mm_glu_plan_create_ex(const mm_glu_desc *d, int dtype, const mm_plan_options *opt,
-                                const mm_glu_backward_tiling *backward, mm_plan_t *out) {
+                                const mm_glu_options *glu, mm_plan_t *out) {
     clear_error();
     if (!out) return fail(MM_ERR_NULL_ARG, "out is NULL");
     *out = nullptr;
@@ -419,7 +419,9 @@ mm_status mm_glu_plan_create_ex(const mm_glu_desc *d, int dtype, const mm_plan_o
     if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile %d has no FLOAT kernel", treq);
     if (force == MM_ALGO_SPLIT_K || sreq > 1) tiles &= ~1u;  // no 256 x 256 partials
     if (!tiles) return fail(MM_ERR_BAD_OPTION, "tile 1 does not split K");
-    const mm_glu_backward_tiling bt = backward ? *backward : mm_glu_backward_tiling{};
+    const mm_glu_options bt = glu ? *glu : mm_glu_options{};
+    if (bt.kept_type != 0 && bt.kept_type != dtype && bt.kept_type != MM_FLOAT)
+        return fail(MM_ERR_DTYPE, "G and U are kept in the plan's type or in FLOAT (got %d)", bt.kept_type);
     if (!d->training && (bt.dx_tile || bt.dx_split_k || bt.dw_tile || bt.dw_split_k))
         return fail(MM_ERR_BAD_OPTION, "backward tiling of a plan without training");
     mm_plan_s *p = new (std::nothrow) mm_plan_s();
@@ -429,6 +431,7 @@ mm_status mm_glu_plan_create_ex(const mm_glu_desc *d, int dtype, const mm_plan_o
     p->tb = d->trans_w;
     p->act = d->activation;
     p->training = d->training != 0;
+    p->kept = bt.kept_type ? bt.kept_type : dtype;
     p->w_pitch = d->w_pitch ? d->w_pitch : row;
     p->out_rank = 2;
     p->out_shape[0] = M;
@@ -498,11 +501,11 @@ mm_status mm_glu_plan_create_ex(const mm_glu_desc *d, int dtype, const mm_plan_o
     return MM_OK;
 }
 
-mm_status mm_glu_backward_info(mm_plan_t p, mm_glu_backward_tiling *info) {
+mm_status mm_glu_get_options(mm_plan_t p, mm_glu_options *glu) {
     clear_error();
-    if (!p || !info) return fail(MM_ERR_NULL_ARG, "plan or info is NULL");
+    if (!p || !glu) return fail(MM_ERR_NULL_ARG, "plan or glu is NULL");
     if (!p->is_glu || !p->training) return fail(MM_ERR_BAD_OPTION, "not a gated-block plan with training");
-    *info = mm_glu_backward_tiling{p->dx.tile + 1, p->dx.split, p->dw.tile + 1, p->dw.split};
+    *glu = mm_glu_options{p->kept, p->dx.tile + 1, p->dx.split, p->dw.tile + 1, p->dw.split};
     return MM_OK;
 }
 
@@ -535,7 +538,9 @@ mm_status mm_glu_execute(mm_plan_t p, const void *X, const void *Wg, const void 
     a.split = p->split;
     a.kstages = p->kstages;
     a.act = p->act;
-    a.y_vec = aligned16(H) && aligned16(G) && aligned16(U) && (p->N * es) % 16 == 0;
+    a.y_vec = aligned16(H) && (p->N * es) % 16 == 0;
+    a.kept_vec = aligned16(G) && aligned16(U) && (p->N * elem_size(p->kept)) % 16 == 0;
+    a.kept32 = p->kept != p->dtype;
     if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_glu_rows(p->dtype, p->tb != 0, a, s));
     const bool vec = aligned16(X) && aligned16(Wg) && aligned16(Wu) && (p->K * es) % 16 == 0 &&
                      (p->w_pitch * es) % 16 == 0 && (p->tb || (p->N * es) % 16 == 0);
@@ -568,7 +573,7 @@ mm_status mm_glu_backward(mm_plan_t p, const void *X, const void *Wg, const void
     }
     char *dG = (char *)p->ws + p->d_off, *dU = dG + p->d_bytes;
     if (p->out_numel > 0) {
-        mm_status st = launched(launch_glu_dact(p->dtype, p->act, G, U, dH, dG, dU, M, N, p->d_pitch, s));
+        mm_status st = launched(launch_glu_dact(p->dtype, p->kept, p->act, G, U, dH, dG, dU, M, N, p->d_pitch, s));
         if (st != MM_OK) return st;
     }
     void *part = dU + p->d_bytes;

@@ -312,23 +312,23 @@ def test_backward_tiling_is_shown_and_kept():
         for t in entries:
             for s in (1, 3) if t > 1 else (1,):
                 p = glu(dtype=dtype, **d, dx_tile=t, dw_tile=t, dx_split_k=s, dw_split_k=s)
-                i = p.backward_info()
+                i = p.options()
                 assert i["dx_tile"] == i["dw_tile"] == t
                 # three partitions of dW's reduction over 530 rows may be two of whole stages
                 assert i["dx_split_k"] == s and i["dw_split_k"] in (min(s, 2), s)
                 parts = max(i["dx_split_k"] * 530 * 328 * (s > 1), i["dw_split_k"] * 2 * 328 * 400 * (s > 1))
                 assert p.workspace_bytes >= 2 * 530 * 400 * 2 + 4 * parts
-    assert glu(**d, dx_tile=4).backward_info()["dx_tile"] == 4
-    i = glu(**d).backward_info()  # the plan's choice
+    assert glu(**d, dx_tile=4).options()["dx_tile"] == 4
+    i = glu(**d).options()  # the plan's choice
     assert 1 <= i["dx_tile"] <= 5 and 1 <= i["dw_tile"] <= 5 and i["dx_split_k"] >= 1 and i["dw_split_k"] >= 1
 
 
 def test_large_training_steps_run_on_the_large_entries():
     """The entries that the forced-tile tests compare are those that large
     steps run on."""
-    i = glu(8192, 4096, 11008, trans_w=True, training=True).backward_info()
+    i = glu(8192, 4096, 11008, trans_w=True, training=True).options()
     assert (i["dx_tile"], i["dw_tile"]) == (1, 1)
-    i = glu(4096, 2048, 5504, trans_w=True, training=True).backward_info()
+    i = glu(4096, 2048, 5504, trans_w=True, training=True).options()
     assert (i["dx_tile"], i["dw_tile"]) == (5, 5)
 
 
@@ -344,19 +344,29 @@ def test_backward_tiling_refusals(kw):
 
 def test_backward_tiling_calls():
     L = mm.lib()
-    t = mm.GluBackwardTiling()
-    assert L.mm_glu_backward_info(None, ctypes.byref(t)) == mm.ERR_NULL_ARG
-    assert L.mm_glu_backward_info(glu(training=True).handle, None) == mm.ERR_NULL_ARG
-    assert L.mm_glu_backward_info(glu().handle, ctypes.byref(t)) == mm.ERR_BAD_OPTION
-    assert L.mm_glu_backward_info(scaled().handle, ctypes.byref(t)) == mm.ERR_BAD_OPTION
+    t = mm.GluOptions()
+    assert L.mm_glu_get_options(None, ctypes.byref(t)) == mm.ERR_NULL_ARG
+    assert L.mm_glu_get_options(glu(training=True).handle, None) == mm.ERR_NULL_ARG
+    assert L.mm_glu_get_options(glu().handle, ctypes.byref(t)) == mm.ERR_BAD_OPTION
+    assert L.mm_glu_get_options(scaled().handle, ctypes.byref(t)) == mm.ERR_BAD_OPTION
     d = mm.GluDesc(4, 64, 32, 0, 0, mm.ACT_SILU, 1, 0)
     h = ctypes.c_void_p()
     assert L.mm_glu_plan_create_ex(ctypes.byref(d), mm.FLOAT, None, None, ctypes.byref(h)) == 0
-    assert L.mm_glu_backward_info(h, ctypes.byref(t)) == 0 and t.dx_split_k >= 1
+    assert L.mm_glu_get_options(h, ctypes.byref(t)) == 0 and t.dx_split_k >= 1
     L.mm_plan_destroy(h)
     assert L.mm_glu_plan_create_ex(None, mm.FLOAT, None, None, ctypes.byref(h)) == mm.ERR_NULL_ARG and not h.value
     # empty steps take the options too
     for size in ((0, 64, 32), (4, 0, 32), (4, 64, 0)):
         p = glu(*size, training=True, dx_tile=3, dx_split_k=2, dw_tile=2, dw_split_k=5)
-        i = p.backward_info()
+        i = p.options()
         assert i["dx_tile"] == 3 and i["dw_tile"] == 2 and i["dx_split_k"] >= 1 and i["dw_split_k"] >= 1
+
+
+@pytest.mark.parametrize("dtype", [mm.FLOAT, mm.FLOAT16, mm.BFLOAT16])
+def test_kept_type(dtype):
+    for training in (False, True):
+        for kept in (0, dtype, mm.FLOAT):
+            p = glu(dtype=dtype, training=training, kept_type=kept)
+            assert not training or p.options()["kept_type"] == (kept or dtype)
+        for kept in {mm.FLOAT16, mm.BFLOAT16, mm.DOUBLE, mm.INT8, -1, 99} - {dtype}:
+            assert status(glu, dtype=dtype, training=training, kept_type=kept) == mm.ERR_DTYPE

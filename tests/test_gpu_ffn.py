@@ -867,27 +867,29 @@ def placed(values, offset=0, gap=0, fill=float("nan")):
     return view, check
 
 
-def run_step(dev, m, k, n, dt, nk, act, seed=0, offset=0, gap=0, forward=True, **tiling):
+def run_step(dev, m, k, n, dt, nk, act, seed=0, offset=0, gap=0, forward=True, kept=None, **options):
     """A training step whose eleven operands all lie at `offset`, the weights
-    and their gradients with rows `gap` apart, compared with 64 bits."""
+    and their gradients with rows `gap` apart, G and U of type `kept`, compared
+    with 64 bits."""
+    kept = kept or dt
     shape = (n, k) if nk else (k, n)
     values = {"x": rand((m, k), dt, dev, seed), "dh": rand((m, n), dt, dev, seed + 1, 0.5)}
     for i, w in enumerate(("wg", "wu", "dwg", "dwu")):
         values[w] = rand(shape, dt, dev, seed + 2 + i, 0.2)
     for i, name in enumerate(("h", "g", "u")):
-        values[name] = rand((m, n), dt, dev, seed + 6 + i, 1.5)
+        values[name] = rand((m, n), dt if name == "h" else kept, dev, seed + 6 + i, 1.5)
     values["dx"] = rand((m, k), dt, dev, seed + 9)
     t, checks = {}, []
     for name, v in values.items():
         t[name], check = placed(v, offset, gap if "w" in name else 0)
         checks.append((name, check))
     plan = mm.GluPlan(m, k, n, mm.torch_dtype_code(dt), activation=mm.ACTIVATIONS[act], trans_w=nk, training=True,
-                      w_pitch=shape[1] + gap if gap else 0, **tiling)
+                      w_pitch=shape[1] + gap if gap else 0, kept_type=mm.torch_dtype_code(kept), **options)
     w = [t[i].t() if nk else t[i] for i in ("wg", "wu")]
     if forward:
         plan.execute(t["x"], t["wg"], t["wu"], t["h"], t["g"], t["u"])
         torch.cuda.synchronize()
-        for name, (want, tol) in zip("hgu", forward64(t["x"], *w, act, dt)):
+        for name, (want, tol) in zip("hgu", forward64(t["x"], *w, act, dt)[:1] + forward64(t["x"], *w, act, kept)[1:]):
             within(t[name], want, tol, f"{name} {m}x{k}x{n}")
     plan.backward(t["x"], t["wg"], t["wu"], t["g"], t["u"], t["dh"], t["dx"], t["dwg"], t["dwu"])
     torch.cuda.synchronize()
@@ -923,7 +925,7 @@ def test_glu_backward_every_tile(tile, nk, dt, dev):
                                                     (16, 264, 530, 1, 0), (2, 35, 9, 0, 0), (1, 300, 1, 0, 1))):
             p = run_step(dev, m, k, n, TYPES[dt], nk, ACTS[j % 5], seed=1300 + 10 * j, offset=offset, gap=gap,
                          forward=False, dx_tile=tile, dw_tile=dw, dx_split_k=split, dw_split_k=split)
-            i = p.backward_info()
+            i = p.options()
             assert (i["dx_tile"], i["dw_tile"]) == (tile, dw)
             assert j > 1 or (i["dx_split_k"] == split and i["dw_split_k"] in (2, split))
 
@@ -937,7 +939,8 @@ def test_glu_backward_more_tiles_of_each_large_entry_than_cus(dt, nk, dev):
         for j, (m, k, n) in enumerate(((4360, 4616, 264), (520, 4616, 2360))):
             p = run_step(dev, m, k, n, TYPES[dt], nk, "silu", seed=1400 + 10 * j, forward=False, dx_tile=tile, dw_tile=tile,
                          dx_split_k=1, dw_split_k=1)
-            assert p.backward_info() == {"dx_tile": tile, "dx_split_k": 1, "dw_tile": tile, "dw_split_k": 1}
+            assert p.options() == {"kept_type": mm.torch_dtype_code(TYPES[dt]), "dx_tile": tile, "dx_split_k": 1,
+                                   "dw_tile": tile, "dw_split_k": 1}
 
 
 def test_quantize_rows_makes_its_results_on_its_stream(dev):
@@ -954,3 +957,78 @@ def test_quantize_rows_makes_its_results_on_its_stream(dev):
     torch.cuda.synchronize()
     assert q.data_ptr() not in at and s.data_ptr() not in at
     assert np.array_equal(q.cpu().numpy(), wq) and np.array_equal(s.cpu().numpy(), ws)
+
+
+# ---- G and U kept in FP32
+
+
+@pytest.mark.parametrize("offset,gap", [(0, 0), (1, 5)])
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("dt", TYPES, ids=str)
+def test_glu_step_with_g_and_u_in_fp32(dt, nk, offset, gap, dev):
+    """The few-row kernel, every tile, whole and split K, aligned and odd."""
+    t = TYPES[dt]
+    for j, (m, k, n) in enumerate(((1, 64, 96), (3, 65, 33), (20, 264, 130), (150, 65, 97), (300, 200, 136))):
+        run_step(dev, m, k, n, t, nk, ACTS[j], seed=1600 + 10 * j, offset=offset, gap=gap, kept=F32)
+    for tile in (2, 3, 4) if dt == "fp32" else (1, 2, 3, 4, 5):
+        for split in (1, 2) if tile > 1 else (1,):
+            for j, (m, k, n) in enumerate(((270, 528, 136), (300, 701, 281), (2, 35, 9))):
+                run_step(dev, m, k, n, t, nk, ACTS[(tile + j) % 5], seed=1650 + 10 * j, offset=offset, gap=gap, kept=F32,
+                         tile=tile, split_k=split)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_glu_gradients_round_twice_when_g_and_u_are_fp32(act, dt, dev):
+    """From X and the weights to the gradients, dG and dU and the results are
+    the only values rounded to 16 bits: the error is that of 64-bit gradients
+    with these two roundings, to 2 %.  (dG and dU are off by some 2^-16 of
+    theirs before they are rounded, which moves one in a hundred over a tie,
+    where either neighbour is half a step off: the norm of the error keeps.)"""
+    t = TYPES[dt]
+    m, k, n = 700, 192, 320
+    x, dh = rand((m, k), t, dev, 1700), rand((m, n), t, dev, 1701, 0.1)
+    wg, wu = rand((n, k), t, dev, 1702, k ** -0.5), rand((n, k), t, dev, 1703, k ** -0.5)
+    p = mm.GluPlan(m, k, n, mm.torch_dtype_code(t), activation=mm.ACTIVATIONS[act], trans_w=True, training=True,
+                   kept_type=mm.FLOAT)
+    h, g, u = torch.empty(m, n, dtype=t, device=dev), torch.empty(m, n, device=dev), torch.empty(m, n, device=dev)
+    got = [torch.empty_like(v) for v in (x, wg, wu)]
+    p.execute(x, wg, wu, h, g, u)
+    p.backward(x, wg, wu, g, u, dh, *got)
+    x, wg, wu, dh = (v.double() for v in (x, wg, wu, dh))
+    f, d = act64(act, x @ wg.t())
+    dg, du = dh * (x @ wu.t()) * d, dh * f
+    products = lambda a, b: (a @ wg + b @ wu, a.t() @ x, b.t() @ x)  # noqa: E731
+    for v, exact, two in zip(got, products(dg, du), products(dg.to(t).double(), du.to(t).double())):
+        error, least = (float((w.double() - exact).norm() / exact.norm()) for w in (v, two.to(t)))
+        assert error <= 1.02 * least, (error, least)
+
+
+def test_glu_fp32_g_and_u_replayed_from_a_graph(dev):
+    m, k, n = 300, 128, 200
+    x, dh = rand((m, k), BF16, dev, 1800), rand((m, n), BF16, dev, 1801)
+    wg, wu = rand((n, k), BF16, dev, 1802, 0.1), rand((n, k), BF16, dev, 1803, 0.1)
+    p = mm.GluPlan(m, k, n, mm.BFLOAT16, trans_w=True, training=True, split_k=2, kept_type=mm.FLOAT)
+    outs = [torch.zeros(m, n, dtype=BF16, device=dev), torch.zeros(m, n, device=dev), torch.zeros(m, n, device=dev),
+            torch.zeros_like(x), torch.zeros_like(wg), torch.zeros_like(wu)]
+
+    def call():
+        p.execute(x, wg, wu, *outs[:3])
+        p.backward(x, wg, wu, outs[1], outs[2], dh, *outs[3:])
+
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t.view(torch.uint8), w.view(torch.uint8)) for t, w in zip(outs, want))
+        call()
+        torch.cuda.synchronize()
+    with pytest.raises(ValueError):  # G and U of the plan's type, where it keeps FP32
+        p.execute(x, wg, wu, outs[0], outs[1].to(BF16), outs[2].to(BF16))
