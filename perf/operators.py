@@ -139,11 +139,13 @@ def _plan(case, st, dev):
     if case["kind"] in ("glu", "glu_train"):
         dt = DTYPES[case["dtype"]]
         train = case["kind"] == "glu_train"
+        # A training step keeps G and U in 32 bits, as the plain form does:
+        # rounded to 16 they would make the gradients a third less exact.
         st["plan"] = mm.GluPlan(m, k, n, mm.torch_dtype_code(dt), activation=mm.ACTIVATIONS[case["act"]],
-                                trans_w=case["nk"], training=train)
+                                trans_w=case["nk"], training=train, kept_type=mm.FLOAT if train else 0)
         st["h"] = torch.empty(m, n, dtype=dt, device=dev)
         if train:
-            st["g"], st["u"] = torch.empty_like(st["h"]), torch.empty_like(st["h"])
+            st["g"], st["u"] = (torch.empty(m, n, dtype=torch.float32, device=dev) for _ in range(2))
             st["dx"] = torch.empty_like(st["x"])
             st["dwg"], st["dwu"] = torch.empty_like(st["wg"]), torch.empty_like(st["wu"])
     else:
