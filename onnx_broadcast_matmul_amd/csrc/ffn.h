@@ -144,7 +144,10 @@ constexpr int kFfnQuantLds = 48 * 1024;
 // but row pieces below 64 bytes cost more than they bring once every CU has
 // one (M = 1, K = 4096, INT8: N = 4096 with 64, 32 and 16 columns 10.9, 9.4 and
 // 7.8 us, N = 1024 9.5, 7.9 and 6.1, N = 11008 10.8, 14.7 and 18.3; BF16 gated,
-// N = 4096 with 32 and 16: 31.3 and 27.5, N = 11008: 52.9 and 62.3).
+// forced, N = 4096 with 32 and 16: 31.3 and 27.4, N = 11008: 53.5 and 62.3, where
+// plans take split tiles, 22.6 us, and tiles, 50.3).  A lane's pieces shrink with
+// the columns (8, 4, 2 in flight): the narrow forms are bound by latency, 24 x
+// 4096 x 4096 INT8 9.6 us at 1.85 TB/s.
 inline bool rows_halve(int64_t wgs) { return 2 * wgs <= kNumCUs; }
 hipError_t launch_glu_rows(int dtype, bool tb, const FfnArgs &a, hipStream_t s);
 bool rows_quantize(int a_type, int out_dtype, bool tb, int64_t M, int64_t K, int64_t N);

@@ -55,7 +55,9 @@ __device__ __forceinline__ int row_swizzle(int k, int cpr) {
 }
 
 // Which products a kernel computes.
-//   kGlu:    H = act(A B0) * (A B1), optionally also A B0 and A B1
+//   kGlu:    H = act(A B0) * (A B1), optionally also A B0 and A B1, in OD or
+//            (flags) as their FP32 sums: 4096 x 2048 x 5504 BF16 171 us without
+//            them, 181 and 196 with (8192 x 4096 x 11008: 1199, 1241, 1287)
 //   kSum2:   Y0 = A0 B0 + A1 B1 (the K loop runs over both terms)
 //   kPair:   Y0 = A0 B0 and Y1 = A1 B1 (half of the grid each)
 //   kScaled: Y = sa[m] sb[n] (A B) + bias[n], INT8 operands
@@ -460,6 +462,10 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
                 scatter(BKC(), BCPR(), std::integral_constant<int, BC>(), second || p == 1 ? Bt1 : Bt0, a.ldb, N - n0,
                         TB ? K : N, k0, rgb[p], sb + A_BYTES + p * P_BYTES);
         };
+        // Stages 0 and 1 go through the same registers one after the other: two
+        // memory latencies before the first MFMA, and a partial last stage's
+        // own where it is stored, which products of few stages feel (333 x 1000
+        // x 1501 INT8, four stages: 8.5 us, of which the bytes take 0.7).
         if (nk > 0) {
             load(0);
             store(0);
@@ -490,7 +496,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
     // K groups meet through LDS, their sums added in group order.  Of four
     // groups each takes a quarter of every accumulator (QG quarters of four
     // columns) and carries it through the epilogue, so that all eight waves
-    // work there and not two (300 x 512 x 1364 FP32, gelu: 15.5 -> 14.7 us); of two
+    // work there and not two (300 x 512 x 1364 FP32, gelu: 15.4 -> 14.3 us); of two
     // groups the first takes all (halves gained nothing).
     constexpr int QG = KG > 2 ? 4 / KG : 4;
     auto mine = [&](int q) { return KG <= 2 || q / QG == kg; };
