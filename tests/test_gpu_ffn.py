@@ -1032,3 +1032,29 @@ def test_glu_fp32_g_and_u_replayed_from_a_graph(dev):
         torch.cuda.synchronize()
     with pytest.raises(ValueError):  # G and U of the plan's type, where it keeps FP32
         p.execute(x, wg, wu, outs[0], outs[1].to(BF16), outs[2].to(BF16))
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("kept", ["same", "fp32"])
+def test_glu_gradients_into_the_halves_of_one_matrix(kept, nk, dev):
+    """Weights and gradients as gate and up halves of merged matrices, on a
+    stream of the caller's."""
+    for j, (m, k, n, dt) in enumerate(((40, 64, 96, BF16), (150, 65, 97, F16), (33, 31, 7, BF16), (70, 40, 33, F32))):
+        x, dh = rand((m, k), dt, dev, 1900 + j), rand((m, n), dt, dev, 1910 + j, 0.5)
+        w = rand((2 * n, k) if nk else (k, 2 * n), dt, dev, 1920 + j, 0.2)
+        dw = torch.full_like(w, -7.0)
+        halves = lambda t: (t[:n], t[n:]) if nk else (t[:, :n], t[:, n:])  # noqa: E731
+        kt = F32 if kept == "fp32" else dt
+        p = mm.GluPlan(m, k, n, mm.torch_dtype_code(dt), trans_w=nk, training=True, w_pitch=0 if nk else 2 * n,
+                       kept_type=mm.torch_dtype_code(kt))
+        h, g, u, dx = (torch.empty(s, dtype=t, device=dev) for s, t in (((m, n), dt), ((m, n), kt), ((m, n), kt), ((m, k), dt)))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        p.execute(x, *halves(w), h, g, u, stream=side)
+        p.backward(x, *halves(w), g, u, dh, dx, *halves(dw), stream=side)
+        torch.cuda.synchronize()
+        wg, wu = (t.t() if nk else t for t in halves(w))
+        within(h, *forward64(x, wg, wu, "silu", dt)[0], "H")
+        ref = backward64(x, wg, wu, g, u, dh, "silu", dt)
+        for t, r, name in zip((dx, *(v.t() if nk else v for v in halves(dw))), ref, ("dX", "dWg", "dWu")):
+            within(t, *r, f"{name} {m}x{k}x{n}")
