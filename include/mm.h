@@ -324,19 +324,19 @@ mm_status mm_int_execute(mm_plan_t plan, const void *A, const void *B, const voi
  * INT32 holds any sum of INT8 products.  It is rounded to FP32 and multiplied
  * by the row's scale; that product times the column's scale plus the bias is
  * one fused multiply-add (rounded once, to FP32), and the result is narrowed
- * to out_type.  Results do not depend on the algorithm or on a split of K.  A scale that is NaN or infinite makes its
- * row or column what IEEE arithmetic makes of it; K == 0 gives the bias (or
- * zeros) whatever the scales hold.
+ * to out_type.  Results do not depend on the algorithm or on a split of K.  A
+ * scale that is NaN or infinite makes its row or column what IEEE arithmetic
+ * makes of it; K == 0 gives the bias (or zeros) whatever the scales hold.
  *
  * Options: force_algo SKINNY_M (one product, after folding, of at most 32
  * rows), GENERAL or SPLIT_K (at most 65535 products); tile k >= 1 is entry k of
  * 256 x 256 (not split), 128 x 128, 64 x 128, 32 x 128, 256 x 128; split_k is
  * the number of partitions (clamped so that none is empty).  GENERAL and
  * SKINNY_M with a split_k above 1, and SKINNY_M with a tile, give
- * MM_ERR_BAD_OPTION.  A
- * plan with an A to quantize or a split K may own a workspace
- * (mm_plan_workspace_bytes > 0): its executions must then not overlap, and it
- * is allocated and bound to a device as described above.  Matrices hold at
+ * MM_ERR_BAD_OPTION.  A plan with an A to quantize or a split K may own a
+ * workspace (mm_plan_workspace_bytes > 0): its executions must then not
+ * overlap, and it is allocated and bound to a device as described above.
+ * Matrices hold at
  * most 2^40 elements, sizes lie below 2^31 - 64, and a launch has less than
  * 2^32 threads (MM_ERR_TOO_LARGE).  Other errors are those of mm_plan_create. */
 typedef struct mm_scaled_int_desc {

@@ -122,9 +122,10 @@ __device__ __forceinline__ void act_grad(float g, float &f, float &d) {
 
 // INT8 product's epilogue: the exact integer sum, rounded to FP32 (it can need
 // 31 bits), times the row's scale, rounded; that times the column's scale plus
-// the bias, rounded once.  The operations are spelled out, and the FP32 result kept apart from the narrowing (which the
-// compiler else merges into the last operation here and there, rounding once
-// where other kernels round twice), so that every kernel gives the same bits.
+// the bias, rounded once.  The operations are spelled out, and the FP32 result
+// kept apart from the narrowing (which the compiler else merges into the last
+// operation here and there, rounding once where other kernels round twice), so
+// that every kernel gives the same bits.
 __device__ __forceinline__ float scaled_value(int acc, float sa, float sb, float bias) {
     float y = fmaf((float)acc * sa, sb, bias);
     asm("" : "+v"(y));

@@ -168,10 +168,9 @@ hipError_t launch_sum_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
 // would be formed once for every tile column.  G and U come as the forward
 // pass kept them (KT): FP32 sums, or rounded to the element type, which halves
 // their bytes and makes BF16 gradients off by 0.0031 of their norm, not 0.0024.
-// dG and dU are rounded to
-// the element type because the matrix cores take them in it.  They have rows
-// of ldw elements, whole 16-byte chunks; the columns past N hold zeros, so the
-// products may read them.
+// dG and dU are rounded to the element type because the matrix cores take them
+// in it.  They have rows of ldw elements, whole 16-byte chunks; the columns past
+// N hold zeros, so the products may read them.
 template <int DT, int KT, int ACT>
 __global__ __launch_bounds__(256) void k_glu_dact(const void *G, const void *U, const void *dH, void *dG, void *dU,
                                                   int64_t M, int64_t N, int64_t ldw) {
