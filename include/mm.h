@@ -336,9 +336,9 @@ mm_status mm_int_execute(mm_plan_t plan, const void *A, const void *B, const voi
  * MM_ERR_BAD_OPTION.  A plan with an A to quantize or a split K may own a
  * workspace (mm_plan_workspace_bytes > 0): its executions must then not
  * overlap, and it is allocated and bound to a device as described above.
- * Matrices hold at
- * most 2^40 elements, sizes lie below 2^31 - 64, and a launch has less than
- * 2^32 threads (MM_ERR_TOO_LARGE).  Other errors are those of mm_plan_create. */
+ * Matrices hold at most 2^40 elements, sizes lie below 2^31 - 64, and a
+ * launch has less than 2^32 threads (MM_ERR_TOO_LARGE).  Other errors are
+ * those of mm_plan_create. */
 typedef struct mm_scaled_int_desc {
     int32_t a_type;   /* MM_INT8, or the type of an A to be quantized */
     int32_t out_type; /* MM_FLOAT, MM_FLOAT16 or MM_BFLOAT16 */
