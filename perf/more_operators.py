@@ -1,0 +1,498 @@
+"""Measured cases of the linear layer with its epilogue, of 8-bit activation
+checkpoints and of the norms around a residual block.
+
+Kinds of case:
+
+* ``linear``: ``Y = f(X W + b) + R`` (inference; b, f and R may be absent).
+* ``linear_train``: the same forward pass, then the backward pass from ``dY``
+  to ``dX``, ``dW`` and ``db``.  ``kept`` says what the backward pass starts
+  from: ``full``, X itself and ``Z = X W + b`` in 32 bits; ``int8``, 8-bit
+  checkpoints of X and Z that the forward pass makes.
+* ``checkpoint``: a tensor to its 8-bit checkpoint and back.  Blocks of 32
+  elements along a row share ``s = 2^(E - 6)``, ``E = floor(log2(max|x|))``
+  (of at least 2^-100), ``q = clamp(rint(x / s), -127, 127)``; the value is q s.
+* ``norm``: ``R = X + alpha g n(B)`` and ``Y = norm(R) w + b`` where ``n(B)`` is
+  B or its own norm with weight and bias, and the gate g is absent or has one
+  row for each ``gate_rows`` rows of X.
+* ``norm_train``: the same, then the backward pass from ``dY`` and from ``dR``,
+  the gradient that reaches R along the residual path, to X, B, the gate, the
+  weights and the biases.  ``kept`` as above: B and R themselves, or their
+  checkpoints.
+
+``own`` selects what ``run`` does: false, the plain form in elementary torch
+operations; true, this library's calls.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+EPS = 1e-5
+BLOCK = 32  # elements of a checkpoint that share a scale
+
+
+def listed():
+    """The listed cases.  m: tokens, k: input features, n: output features (of
+    norms: features); nk: weights stored [n, k], as linear layers keep them,
+    else [k, n]."""
+    return [
+        # One decoded token through the attention's output projection, added
+        # to the residual stream.
+        {"name": "linear_token", "kind": "linear", "dtype": "bf16", "act": "none", "bias": False, "residual": True, "nk": True, "m": 1, "k": 4096, "n": 4096},
+        # A decode batch of 13 sequences of a smaller model whose hidden width
+        # (8/3 of 2048) is odd, weights in the [k, n] order of an ONNX MatMul.
+        {"name": "linear_batch13_odd", "kind": "linear", "dtype": "fp16", "act": "gelu", "bias": True, "residual": False, "nk": False, "m": 13, "k": 2048, "n": 5461},
+        # 16 prompts of 512 tokens through a plain feed-forward layer.
+        {"name": "linear_prefill", "kind": "linear", "dtype": "bf16", "act": "gelu_tanh", "bias": True, "residual": False, "nk": True, "m": 8192, "k": 4096, "n": 11008},
+        # Training in 32 bits of a small model on a ragged batch (the kind of
+        # run that gradients are checked on).
+        {"name": "linear_train_fp32", "kind": "linear_train", "dtype": "fp32", "act": "gelu", "bias": True, "residual": True, "nk": False, "kept": "full", "m": 300, "k": 512, "n": 1364},
+        # A training microbatch of 2 x 2048 tokens of a 2048-wide model: the
+        # block's last layer with its residual.
+        {"name": "linear_train", "kind": "linear_train", "dtype": "bf16", "act": "none", "bias": True, "residual": True, "nk": True, "kept": "full", "m": 4096, "k": 5504, "n": 2048},
+        # A training batch of the 4096-wide model, activations kept in 8 bits.
+        {"name": "linear_train_int8", "kind": "linear_train", "dtype": "bf16", "act": "gelu_tanh", "bias": True, "residual": False, "nk": True, "kept": "int8", "m": 8192, "k": 4096, "n": 11008},
+        # Checkpoints: a ragged tensor in 32 bits; a hidden activation of a
+        # training batch.
+        {"name": "checkpoint_ragged", "kind": "checkpoint", "dtype": "fp32", "m": 1000, "n": 1501},
+        {"name": "checkpoint_hidden", "kind": "checkpoint", "dtype": "bf16", "m": 8192, "n": 11008},
+        # One decoded token: residual added, next block's norm.
+        {"name": "norm_token", "kind": "norm", "dtype": "bf16", "norm": "rms", "post": False, "gate_rows": 0, "alpha": 1.0, "m": 1, "n": 4096},
+        # 16 prompts of 512 tokens, norms on both sides of the block and a
+        # scale for each channel.
+        {"name": "norm_prefill", "kind": "norm", "dtype": "bf16", "norm": "rms", "post": True, "gate_rows": 8192, "alpha": 1.0, "m": 8192, "n": 4096},
+        # Training with layer norms and a gate for each of five sequences; odd
+        # sizes.
+        {"name": "norm_train_odd", "kind": "norm_train", "dtype": "fp16", "norm": "layer", "post": False, "gate_rows": 333, "alpha": 1.0, "kept": "full", "m": 1600, "n": 2047},
+        # A training batch, norms on both sides, residual scale, activations
+        # kept in 8 bits.
+        {"name": "norm_train_int8", "kind": "norm_train", "dtype": "bf16", "norm": "rms", "post": True, "gate_rows": 8192, "alpha": 0.5, "kept": "int8", "m": 8192, "n": 4096},
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.5)))))))
+
+
+def draw(rng):
+    """One more case of the same ranges: every kind, type, weight order,
+    activation and norm, one token to 8192, odd and ragged sizes among them,
+    no costlier than the largest listed case."""
+    kind = rng.choice(["linear", "linear", "linear_train", "linear_train", "checkpoint", "norm", "norm_train", "norm_train"])
+    m = _log(rng, 1, 8192)
+    case = {"kind": kind, "dtype": rng.choice(["bf16", "bf16", "fp16", "fp32"]), "m": m}
+    if kind in ("linear", "linear_train"):
+        k, n = _log(rng, 64, 8192), _log(rng, 64, 11008)
+        if rng.random() < 0.5:  # widths of real layers are mostly whole multiples; the rest stay as drawn
+            k, n = (k + 63) // 64 * 64, (n + 63) // 64 * 64
+        case.update(k=k, n=n, nk=rng.random() < 0.6, bias=rng.random() < 0.6, residual=rng.random() < 0.5)
+        case["act"] = rng.choice(["none", "silu", "gelu", "gelu_tanh", "relu", "sigmoid"])
+        if case["dtype"] == "fp32":
+            case["m"] = max(1, m // 4)  # 32-bit layers are the small ones
+        if kind == "linear_train":
+            case["m"] = max(case["m"], 16)
+            # relu's slope jumps at 0, where 8 bits round small Z to: no two
+            # ways of summing agree on it.
+            case["kept"] = "full" if case["act"] == "relu" else rng.choice(["full", "int8"])
+        return case
+    n = _log(rng, 64, 11008)
+    case["n"] = (n + 63) // 64 * 64 if rng.random() < 0.5 else n
+    if kind == "checkpoint":
+        return case
+    case["norm"] = rng.choice(["rms", "rms", "layer"])
+    case["post"] = rng.random() < 0.5
+    case["alpha"] = rng.choice([1.0, 0.5])
+    # No gate, one for all rows, or one for each sequence.
+    case["gate_rows"] = rng.choice([0, m, max(1, m // rng.randint(2, 8))])
+    if kind == "norm_train":
+        case["m"] = max(m, 16)
+        case["kept"] = rng.choice(["full", "int8"])
+    return case
+
+
+# ---- inputs
+
+
+def prepare(case, seed):
+    """Inputs on the GPU (and the plan and result buffers where ``own``)."""
+    dev = torch.device("cuda")
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    dt = DTYPES[case["dtype"]]
+    m, n = case["m"], case["n"]
+
+    def normal(*shape, scale=1.0):
+        return (torch.randn(*shape, generator=gen, device=dev) * scale).to(dt)
+
+    def stream(rows, cols):  # a residual stream: a few channels of large magnitude
+        loud = torch.rand(cols, generator=gen, device=dev) < 0.01
+        x = torch.randn(rows, cols, generator=gen, device=dev)
+        return torch.where(loud, x * 12.0, x).to(dt)
+
+    st = {"case": case}
+    if case["kind"] in ("linear", "linear_train"):
+        k = case["k"]
+        st["x"] = normal(m, k)
+        st["w"] = normal(*((n, k) if case["nk"] else (k, n)), scale=k ** -0.5)
+        st["b"] = normal(n, scale=0.1) if case["bias"] else None
+        st["r"] = stream(m, n) if case["residual"] else None
+        if case["kind"] == "linear_train":
+            st["dy"] = normal(m, n, scale=0.1)
+    elif case["kind"] == "checkpoint":
+        st["x"] = stream(m, n)
+    else:
+        st["x"], st["block"] = stream(m, n), normal(m, n)
+        bias = case["norm"] == "layer"
+        st["w2"], st["b2"] = 1.0 + normal(n, scale=0.1), normal(n, scale=0.1) if bias else None
+        st["w1"] = 1.0 + normal(n, scale=0.1) if case["post"] else None
+        st["b1"] = normal(n, scale=0.1) if case["post"] and bias else None
+        gr = case["gate_rows"]
+        st["gate"] = normal((m + gr - 1) // gr, n, scale=0.5) if gr else None
+        if case["kind"] == "norm_train":
+            st["dy"], st["dr"] = normal(m, n, scale=0.1), normal(m, n, scale=0.1)
+    if own:
+        _plan(case, st, dev, dt)
+    return st
+
+
+def _plan(case, st, dev, dt):
+    from onnx_broadcast_matmul_amd import binding as mm
+
+    m, n, code = case["m"], case["n"], mm.torch_dtype_code(dt)
+    train = case["kind"].endswith("_train")
+    small = train and case["kept"] == "int8"
+
+    def packed(rows, cols):  # a checkpoint's buffers
+        return (torch.empty(rows, cols, dtype=torch.int8, device=dev),
+                torch.empty(rows, mm.checkpoint_blocks(cols), dtype=torch.uint8, device=dev))
+
+    st["mm"] = mm
+    if case["kind"] in ("linear", "linear_train"):
+        k, act = case["k"], 0 if case["act"] == "none" else mm.ACTIVATIONS[case["act"]]
+        # A training step keeps Z in 32 bits, as the plain form does, or in 8.
+        st["plan"] = mm.LinearPlan(m, k, n, code, activation=act, trans_w=case["nk"], bias=case["bias"],
+                                   residual=case["residual"], training=train,
+                                   z_type=(mm.INT8 if small else mm.FLOAT) if train and act else 0,
+                                   x_type=mm.INT8 if small else 0)
+        st["y"] = torch.empty(m, n, dtype=dt, device=dev)
+        st["z"], st["zs"], st["xq"], st["xs"] = None, None, None, None
+        if train:
+            if act and small:
+                st["z"], st["zs"] = packed(m, n)
+            elif act:
+                st["z"] = torch.empty(m, n, dtype=torch.float32, device=dev)
+            if small:
+                st["xq"], st["xs"] = packed(m, k)
+            st["dx"], st["dw"] = torch.empty_like(st["x"]), torch.empty_like(st["w"])
+            st["db"] = torch.empty_like(st["b"]) if case["bias"] else None
+    elif case["kind"] == "checkpoint":
+        st["q"], st["s"] = packed(m, n)
+        st["back"] = torch.empty_like(st["x"])
+    else:
+        norm = mm.NORM_RMS if case["norm"] == "rms" else mm.NORM_LAYER
+        st["plan"] = mm.NormPlan(m, n, code, pre=norm, post=norm if case["post"] else mm.NORM_NONE, pre_eps=EPS,
+                                 post_eps=EPS, pre_weight=True, pre_bias=st["b2"] is not None,
+                                 post_weight=st["w1"] is not None, post_bias=st["b1"] is not None,
+                                 gate_rows=case["gate_rows"], residual_scale=case["alpha"], training=train,
+                                 kept_type=mm.INT8 if small else 0)
+        st["sum"], st["out"] = torch.empty_like(st["x"]), torch.empty_like(st["x"])
+        if train:
+            st["stats"] = torch.empty(m, 4, dtype=torch.float32, device=dev)
+            st["kept"] = (packed(m, n), packed(m, n)) if small else (None, None)
+            like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+            st["grads"] = {name: like(st[of]) for name, of in
+                           (("dX", "x"), ("dblock", "block"), ("dgate", "gate"), ("dpre_weight", "w2"),
+                            ("dpre_bias", "b2"), ("dpost_weight", "w1"), ("dpost_bias", "b1"))}
+
+
+# ---- one pass
+
+
+def run(state):
+    """One pass: the outputs, and the gradients of a training step."""
+    kind = state["case"]["kind"]
+    if own:
+        if kind in ("linear", "linear_train"):
+            return _own_linear(state)
+        if kind == "checkpoint":
+            state["mm"].checkpoint_pack(state["x"], state["q"], state["s"])
+            state["mm"].checkpoint_unpack(state["q"], state["s"], state["back"])
+            return state["back"]
+        return _own_norm(state)
+    if kind in ("linear", "linear_train"):
+        return _plain_linear(state)
+    if kind == "checkpoint":
+        return _through_8_bits(state["x"].float()).to(state["x"].dtype)
+    return _plain_norm(state)
+
+
+def _own_linear(st):
+    plan = st["plan"]
+    plan.execute(st["x"], st["w"], st["y"], bias=st["b"], residual=st["r"], Z=st["z"], z_scale=st["zs"])
+    if st["case"]["kind"] == "linear":
+        return st["y"]
+    x = st["x"]
+    if st["xq"] is not None:
+        st["mm"].checkpoint_pack(x, st["xq"], st["xs"])
+        x = st["xq"]
+    plan.backward(x, st["w"], st["dy"], Z=st["z"], z_scale=st["zs"], x_scale=st["xs"], dX=st["dx"], dW=st["dw"],
+                  dbias=st["db"])
+    return {"y": st["y"], "dx": st["dx"], "dw": st["dw"], "db": st["db"]}
+
+
+def _own_norm(st):
+    plan, args = st["plan"], {"gate": st["gate"], "pre_weight": st["w2"], "post_weight": st["w1"]}
+    if st["case"]["kind"] == "norm":
+        plan.execute(st["x"], st["out"], block=st["block"], sum=st["sum"], pre_bias=st["b2"], post_bias=st["b1"], **args)
+        return {"sum": st["sum"], "out": st["out"]}
+    ksum, kblock = st["kept"]
+    plan.execute(st["x"], st["out"], block=st["block"], sum=st["sum"], pre_bias=st["b2"], post_bias=st["b1"],
+                 stats=st["stats"], sum_checkpoint=ksum, block_checkpoint=kblock, **args)
+    plan.backward(st["stats"], sum=ksum or st["sum"], block=kblock or st["block"], dout=st["dy"], dsum=st["dr"],
+                  post_bias=st["b1"], **args, **st["grads"])
+    return {"sum": st["sum"], "out": st["out"], **st["grads"]}
+
+
+# ---- plain forms
+
+
+def _act(name, z):
+    """f(z) and its derivative, in z's type."""
+    if name == "none":
+        return z, None
+    if name == "relu":
+        on = (z > 0).to(z.dtype)
+        return z * on, on
+    if name == "gelu":
+        cdf = 0.5 * (1.0 + torch.erf(z * (0.5 ** 0.5)))
+        return z * cdf, cdf + z * torch.exp(-0.5 * z * z) * (2.0 * math.pi) ** -0.5
+    if name == "gelu_tanh":
+        c = (2.0 / math.pi) ** 0.5
+        t = torch.tanh(c * (z + 0.044715 * z * z * z))
+        return 0.5 * z * (1.0 + t), 0.5 * (1.0 + t) + 0.5 * z * (1.0 - t * t) * c * (1.0 + 3.0 * 0.044715 * z * z)
+    s = 1.0 / (1.0 + torch.exp(-z))
+    if name == "sigmoid":
+        return s, s * (1.0 - s)
+    return z * s, s * (1.0 + z * (1.0 - s))  # silu
+
+
+def _through_8_bits(x):
+    """The values that x's checkpoint stands for, in x's type (32 bits)."""
+    m, n = x.shape
+    blocks = torch.nn.functional.pad(x, (0, -n % BLOCK)).reshape(m, -1, BLOCK)
+    top = blocks.abs().amax(dim=2, keepdim=True).clamp_min(2.0 ** -100)
+    s = torch.ldexp(torch.ones_like(top), torch.frexp(top)[1] - 7)  # top = f 2^e, f in [1/2, 1)
+    q = torch.round(blocks / s).clamp(-127.0, 127.0)
+    return (q * s).reshape(m, -1)[:, :n]
+
+
+def _plain_linear(st):
+    case, dt = st["case"], st["x"].dtype
+    x, w = st["x"].float(), st["w"].float()
+    if case["nk"]:
+        w = w.t()
+    z = x @ w
+    if st["b"] is not None:
+        z = z + st["b"].float()
+    y = _act(case["act"], z)[0]
+    if st["r"] is not None:
+        y = y + st["r"].float()
+    y = y.to(dt)
+    if case["kind"] == "linear":
+        return y
+    if case["kept"] == "int8":
+        x, z = _through_8_bits(x), _through_8_bits(z)
+    dz, slope = st["dy"].float(), _act(case["act"], z)[1]
+    if slope is not None:
+        dz = dz * slope
+    dw = dz.t() @ x if case["nk"] else x.t() @ dz
+    db = dz.sum(dim=0).to(dt) if case["bias"] else None
+    return {"y": y, "dx": (dz @ w.t()).to(dt), "dw": dw.to(dt), "db": db}
+
+
+def _statistics(case, v):
+    """Mean (0 for rms) and reciprocal deviation of v's rows."""
+    mean = v.mean(dim=1, keepdim=True) if case["norm"] == "layer" else torch.zeros_like(v[:, :1])
+    return mean, torch.rsqrt((v - mean).square().mean(dim=1, keepdim=True) + EPS)
+
+
+def _into_norm(case, d, hat, r):
+    """Gradient of a norm's input from that of its normalised values."""
+    into = d - hat * (d * hat).mean(dim=1, keepdim=True)
+    if case["norm"] == "layer":
+        into = into - d.mean(dim=1, keepdim=True)
+    return into * r
+
+
+def _plain_norm(st):
+    case, dt = st["case"], st["x"].dtype
+    m, n, gr, alpha = case["m"], case["n"], case["gate_rows"], case["alpha"]
+    x, b = st["x"].float(), st["block"].float()
+    f = {name: None if st[name] is None else st[name].float() for name in ("w1", "b1", "w2", "b2", "gate")}
+    gate = f["gate"].repeat_interleave(gr, dim=0)[:m] * alpha if gr else alpha
+    mean1 = r1 = None
+    n1 = b
+    if case["post"]:
+        mean1, r1 = _statistics(case, b)
+        n1 = (b - mean1) * r1 * f["w1"]
+        if f["b1"] is not None:
+            n1 = n1 + f["b1"]
+    total = x + gate * n1
+    mean2, r2 = _statistics(case, total)
+    y = (total - mean2) * r2 * f["w2"]
+    if f["b2"] is not None:
+        y = y + f["b2"]
+    found = {"sum": total.to(dt), "out": y.to(dt)}
+    if case["kind"] == "norm":
+        return found
+    if case["kept"] == "int8":
+        total, b = _through_8_bits(found["sum"].float()), _through_8_bits(b)
+    dy = st["dy"].float()
+    hat2 = (total - mean2) * r2
+    dr = st["dr"].float() + _into_norm(case, dy * f["w2"], hat2, r2)
+    found["dX"] = dr.to(dt)
+    found["dpre_weight"] = (dy * hat2).sum(dim=0).to(dt)
+    found["dpre_bias"] = None if f["b2"] is None else dy.sum(dim=0).to(dt)
+    dn1, n1 = dr * gate, b
+    hat1 = None
+    if case["post"]:
+        hat1 = (b - mean1) * r1
+        n1 = hat1 * f["w1"]
+        if f["b1"] is not None:
+            n1 = n1 + f["b1"]
+    found["dgate"] = found["dpost_weight"] = found["dpost_bias"] = None
+    if gr:
+        per = torch.nn.functional.pad(dr * n1 * alpha, (0, 0, 0, -m % gr)).reshape(-1, gr, n)
+        found["dgate"] = per.sum(dim=1).to(dt)
+    if case["post"]:
+        found["dpost_weight"] = (dn1 * hat1).sum(dim=0).to(dt)
+        found["dpost_bias"] = None if f["b1"] is None else dn1.sum(dim=0).to(dt)
+        found["dblock"] = _into_norm(case, dn1 * f["w1"], hat1, r1).to(dt)
+    else:
+        found["dblock"] = dn1.to(dt)
+    return found
+
+
+# ---- what a pass cannot do without
+
+
+def work(case):
+    m, n = case["m"], case["n"]
+    es = 4 if case["dtype"] == "fp32" else 2
+    if case["kind"] in ("linear", "linear_train"):
+        k = case["k"]
+        elements = m * k + k * n + m * n + (n if case["bias"] else 0) + (m * n if case["residual"] else 0)
+        if case["kind"] == "linear":
+            return {"bytes": es * elements, "flops": 2 * m * k * n}
+        # dY in; dX, dW and db out
+        elements += m * n + m * k + k * n + (n if case["bias"] else 0)
+        return {"bytes": es * elements, "flops": 6 * m * k * n}
+    if case["kind"] == "checkpoint":  # the tensor, its checkpoint, the tensor read back
+        return {"bytes": (2 * es + 1) * m * n, "flops": 4 * m * n}
+    rows = 1 + (case["norm"] == "layer") + (1 + (case["norm"] == "layer") if case["post"] else 0)
+    rows += (m + case["gate_rows"] - 1) // case["gate_rows"] if case["gate_rows"] else 0
+    elements = 4 * m * n + rows * n  # X and B in, R and Y out
+    if case["kind"] == "norm":
+        return {"bytes": es * elements, "flops": 12 * m * n}
+    # dY and dR in; dX, dB and the parameters' gradients out
+    return {"bytes": es * (elements + 4 * m * n + rows * n), "flops": 40 * m * n}
+
+
+# ---- the definitions in 64 bits
+
+
+def _values_of_blocks(x):
+    """x (in 64 bits) as 8-bit checkpoints hold it: the exponent of each block's
+    largest magnitude is read from its bits."""
+    out = torch.zeros(x.shape[0], -(-x.shape[1] // BLOCK) * BLOCK, dtype=torch.float64, device=x.device)
+    out[:, : x.shape[1]] = x
+    parts = out.view(x.shape[0], -1, BLOCK)
+    top = torch.clamp(parts.abs().max(dim=-1)[0], min=2.0 ** -100)
+    exponent = (top.view(torch.int64) >> 52) - 1023
+    step = ((exponent - 6 + 1023) << 52).view(torch.float64)[..., None]
+    whole = torch.minimum(torch.maximum(torch.round(parts / step), torch.full_like(step, -127.0)), torch.full_like(step, 127.0))
+    return (whole * step).view(out.shape)[:, : x.shape[1]].contiguous()
+
+
+def exact(case, seed):
+    """run's results in 64 bits.  Kept checkpoints are formed from the values
+    that the tensors hold: X as it is, Z from its 64-bit sum, R as rounded."""
+    st = prepare(case, seed)
+    wide = lambda t: None if t is None else t.double()  # noqa: E731
+    if case["kind"] == "checkpoint":
+        return _values_of_blocks(st["x"].double())
+    if case["kind"] in ("linear", "linear_train"):
+        return _exact_linear(case, {name: wide(st.get(name)) for name in ("x", "w", "b", "r", "dy")})
+
+    x, b, w1, b1, w2, b2, gate, dy, dr = (wide(st.get(k)) for k in ("x", "block", "w1", "b1", "w2", "b2", "gate", "dy", "dr"))
+    m, n, layer = case["m"], case["n"], case["norm"] == "layer"
+
+    def moments(v):
+        mu = torch.sum(v, 1, keepdim=True) / n if layer else 0.0
+        return mu, 1.0 / torch.sqrt(torch.sum((v - mu) ** 2, 1, keepdim=True) / n + EPS)
+
+    owner = torch.arange(m, device=x.device) // case["gate_rows"] if case["gate_rows"] else None
+    g = torch.full_like(x, case["alpha"]) if owner is None else case["alpha"] * gate[owner]
+    branch = lambda hat: hat if w1 is None else hat * w1 + (0.0 if b1 is None else b1)  # noqa: E731
+    mu1, r1 = moments(b) if case["post"] else (0.0, 1.0)
+    total = x + g * branch((b - mu1) * r1)
+    mu2, r2 = moments(total)
+    found = {"sum": total, "out": (total - mu2) * r2 * w2 + (0.0 if b2 is None else b2)}
+    if case["kind"] == "norm":
+        return found
+    if case["kept"] == "int8":
+        total, b = _values_of_blocks(total.to(st["x"].dtype).double()), _values_of_blocks(b)
+
+    def back(d, hat, r):
+        p = torch.sum(d * hat, 1, keepdim=True) / n
+        return r * (d - p * hat - (torch.sum(d, 1, keepdim=True) / n if layer else 0.0))
+
+    hat1, hat2 = (b - mu1) * r1, (total - mu2) * r2
+    dt = dr + back(dy * w2, hat2, r2)
+    dn = dt * g
+    found.update(dX=dt, dblock=back(dn * w1, hat1, r1) if case["post"] else dn, dgate=None, dpost_weight=None,
+                 dpost_bias=None, dpre_weight=torch.sum(dy * hat2, 0), dpre_bias=None if b2 is None else torch.sum(dy, 0))
+    if owner is not None:
+        found["dgate"] = torch.zeros_like(gate).index_add_(0, owner, case["alpha"] * dt * branch(hat1))
+    if case["post"]:
+        found["dpost_weight"] = torch.sum(dn * hat1, 0)
+        if b1 is not None:
+            found["dpost_bias"] = torch.sum(dn, 0)
+    return found
+
+
+def _exact_linear(case, t):
+    w = t["w"].T.contiguous() if case["nk"] else t["w"]
+    z = torch.matmul(t["x"], w)
+    if t["b"] is not None:
+        z += t["b"]
+
+    def f_and_slope(v):
+        act = case["act"]
+        if act == "none":
+            return v, torch.ones_like(v)
+        if act == "relu":
+            return torch.clamp(v, min=0.0), (v > 0).double()
+        if act == "gelu":
+            p = 0.5 * torch.erfc(-v / math.sqrt(2.0))
+            return v * p, p + v * torch.exp(-v * v / 2.0) / math.sqrt(2.0 * math.pi)
+        if act == "gelu_tanh":
+            p = torch.sigmoid(math.sqrt(8.0 / math.pi) * (v + 0.044715 * v ** 3))  # (1 + tanh(./2)) / 2
+            return v * p, p + v * p * (1.0 - p) * math.sqrt(8.0 / math.pi) * (1.0 + 0.134145 * v ** 2)
+        p = torch.sigmoid(v)
+        return (p, p * torch.sigmoid(-v)) if act == "sigmoid" else (v * p, p + v * p * torch.sigmoid(-v))
+
+    y = f_and_slope(z)[0]
+    if t["r"] is not None:
+        y = y + t["r"]
+    if case["kind"] == "linear":
+        return y
+    x = t["x"]
+    if case["kept"] == "int8":
+        x, z = _values_of_blocks(x), _values_of_blocks(z)
+    dz = t["dy"] * f_and_slope(z)[1]
+    dw = torch.matmul(x.T, dz)
+    return {"y": y, "dx": torch.matmul(dz, w.T), "dw": dw.T.contiguous() if case["nk"] else dw,
+            "db": torch.sum(dz, 0) if case["bias"] else None}
