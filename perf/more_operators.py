@@ -93,9 +93,11 @@ def draw(rng):
             case["m"] = max(1, m // 4)  # 32-bit layers are the small ones
         if kind == "linear_train":
             case["m"] = max(case["m"], 16)
-            # relu's slope jumps at 0, where 8 bits round small Z to: no two
-            # ways of summing agree on it.
-            case["kept"] = "full" if case["act"] == "relu" else rng.choice(["full", "int8"])
+            # A sum next to a border between two 8-bit values falls on either
+            # side.  Gradients in 32 bits show that, and relu's slope, which
+            # jumps where 8 bits round small Z to, in every type.
+            border = case["act"] == "relu" or (case["dtype"] == "fp32" and case["act"] != "none")
+            case["kept"] = "full" if border else rng.choice(["full", "int8"])
         return case
     n = _log(rng, 64, 11008)
     case["n"] = (n + 63) // 64 * 64 if rng.random() < 0.5 else n
@@ -108,7 +110,7 @@ def draw(rng):
     case["gate_rows"] = rng.choice([0, m, max(1, m // rng.randint(2, 8))])
     if kind == "norm_train":
         case["m"] = max(m, 16)
-        case["kept"] = rng.choice(["full", "int8"])
+        case["kept"] = "full" if case["dtype"] == "fp32" else rng.choice(["full", "int8"])
     return case
 
 
