@@ -466,6 +466,117 @@ mm_status mm_glu_execute(mm_plan_t plan, const void *X, const void *Wg, const vo
 mm_status mm_glu_backward(mm_plan_t plan, const void *X, const void *Wg, const void *Wu, const void *G, const void *U,
                           const void *dH, void *dX, void *dWg, void *dWu, void *stream);
 
+/* Activation checkpoints in 8 bits, beside mm_quantize_rows: what a training
+ * step keeps of its activations in 1.03 bytes an element.  Blocks of
+ * MM_CHECKPOINT_BLOCK consecutive elements of a row (the last block of a row
+ * may be shorter) share a power of two:
+ *
+ *   a = max(max |x|, 2^-100)    E = floor(log2(a))    s = 2^(E - 6)
+ *   q = rint(x / s), ties to even, limited to -127 .. 127
+ *
+ * which stands for the value q s, off by at most s / 2 (by less than s where |x|
+ * is above 127.5 s), so by at most a / 64.  q is INT8 [rows, cols], dense; the scale
+ * array holds E + 127 as one byte for each block, [rows,
+ * mm_checkpoint_blocks(cols)], dense.  A block with an infinity or a NaN has
+ * the byte 255 and stands for NaN.  (This is the MXINT8 format of the OCP
+ * Microscaling specification.)  Because the scale is a power of two, the
+ * values of a FLOAT, BFLOAT16 or FLOAT16 tensor's checkpoint are numbers of its
+ * type (BFLOAT16's and FLOAT16's are FLOAT's too): reading one back rounds
+ * nothing, and products take its values on the matrix cores as they are. */
+#define MM_CHECKPOINT_BLOCK 32
+
+/* Scale bytes of a row of cols elements (-1: cols is negative). */
+int64_t mm_checkpoint_blocks(int64_t cols);
+
+/* Enqueue the checkpoint of a dense [rows, cols] tensor X (FLOAT, FLOAT16 or
+ * BFLOAT16) on `stream`.  Errors as for mm_quantize_rows. */
+mm_status mm_checkpoint_pack(const void *X, int dtype, int64_t rows, int64_t cols, void *q, void *scale, void *stream);
+
+/* Enqueue the values of a checkpoint as a dense tensor of type dtype, rounded
+ * to nearest even where the type does not hold them (values of a wider
+ * tensor's checkpoint). */
+mm_status mm_checkpoint_unpack(const void *q, const void *scale, int64_t rows, int64_t cols, int dtype, void *X,
+                               void *stream);
+
+/* Linear layer with its epilogue, beside Gemm and the gated block: with X
+ * [rows, in_features],
+ *
+ *   Z = X W + bias      Y = f(Z) + residual
+ *
+ * in one kernel (two where K is split), and its backward pass from dY:
+ *
+ *   dZ = dY * f'(Z)    dX = dZ W^T    dW = X^T dZ    dbias[n] = sum_m dZ[m][n]
+ *
+ * (the residual's gradient is dY itself).  W is stored [in_features,
+ * out_features] or, with trans_w, [out_features, in_features], with rows
+ * w_pitch elements apart (0: dense); dW has its layout and pitch.  bias (N
+ * values), the residual and the activation may be absent.  Everything has
+ * the plan's type (FLOAT, FLOAT16 or BFLOAT16), except Z (z_type) and
+ * checkpoints; X, residual, Y, Z, dY and dX are dense.
+ *
+ * Products accumulate in FP32; bias, f and the residual are applied to the
+ * FP32 sum and Y is rounded once.  dZ is rounded to the plan's type for the
+ * matrix cores; dbias sums it before that, in FP32.  relu's derivative at 0
+ * is 0.  Infinities and NaN follow the formulas.  Results do not vary from
+ * run to run.
+ *
+ * For the backward pass a plan with an activation keeps Z in its own type,
+ * in FLOAT (its FP32 sums) or as a checkpoint (MM_INT8: formed from the FP32
+ * sums in the product's epilogue).  X may be given as a checkpoint (x_type
+ * MM_INT8); x_activation then is applied to its values: the checkpoint of a
+ * layer's Z serves as the next layer's X = f(Z), which is rounded to the
+ * plan's type.
+ *
+ * Options: as for the gated block (one matrix: tile columns are output
+ * columns). */
+#define MM_ACT_NONE 0
+
+typedef struct mm_linear_desc {
+    int64_t rows, in_features, out_features;
+    int64_t w_pitch;        /* 0, or at least the length of a stored weight row */
+    int32_t trans_w;        /* 0 or 1 */
+    int32_t activation;     /* MM_ACT_NONE or an mm_activation value */
+    int32_t has_bias;       /* 0 or 1 */
+    int32_t has_residual;   /* 0 or 1 */
+    int32_t training;       /* 1: the plan owns the backward pass's workspace */
+    int32_t z_type;         /* training with an activation: 0 (the plan's type), the plan's type, MM_FLOAT or MM_INT8 */
+    int32_t x_type;         /* training: 0 or the plan's type (X itself), or MM_INT8 */
+    int32_t x_activation;   /* x_type MM_INT8: applied to the checkpoint's values */
+    int32_t dx_tile, dx_split_k; /* backward products' tile entry and K partitions, 0: the plan's choice; of dX */
+    int32_t dw_tile, dw_split_k; /* (its reduction runs over out_features) and of dW (over rows) */
+    int32_t reserved;       /* must be 0 */
+} mm_linear_desc;
+
+/* Create a linear-layer plan.  MM_ERR_NEG_DIM, MM_ERR_DTYPE, MM_ERR_BAD_OPTION
+ * (an invalid field or option), MM_ERR_TOO_LARGE (as for the gated block),
+ * MM_ERR_ALLOC.  A plan that splits K in the forward pass or is for training
+ * owns a workspace, allocated and bound to a device as described above;
+ * executions that use it must not overlap with their own kind.  The plan
+ * answers the introspection calls (output shape [rows, out_features]). */
+mm_status mm_linear_plan_create(const mm_linear_desc *desc, int dtype, const mm_plan_options *opt, mm_plan_t *out);
+
+/* The descriptor of a linear-layer plan, its type and option fields as
+ * resolved (a training plan's backward tiling; z_type 0 where nothing is
+ * kept). */
+mm_status mm_linear_get_desc(mm_plan_t plan, mm_linear_desc *desc);
+
+/* Enqueue the forward pass on `stream`.  bias and residual are non-NULL exactly
+ * when the plan has them (MM_ERR_NULL_ARG / MM_ERR_BAD_OPTION).  Z, of a training
+ * plan with an activation only, receives what the backward pass needs, or is
+ * NULL; z_scale goes with a checkpoint Z.  Y may be the residual (the layer is
+ * then added to it in place); otherwise no output may overlap an input or
+ * another output.  in_features == 0: the product is zero, X and W are not read. */
+mm_status mm_linear_execute(mm_plan_t plan, const void *X, const void *W, const void *bias, const void *residual,
+                            void *Y, void *Z, void *z_scale, void *stream);
+
+/* Enqueue the backward pass of a training plan on `stream`.  X (x_scale for a
+ * checkpoint) is needed for dW, Z (z_scale) with an activation, W for dX.  Each
+ * of dX, dW and dbias (of a plan with a bias) may be NULL; what is computed is
+ * written, not added.  No output may overlap an input or another output.  rows
+ * == 0 writes zero gradients of W and bias, out_features == 0 a zero dX. */
+mm_status mm_linear_backward(mm_plan_t plan, const void *X, const void *x_scale, const void *W, const void *Z,
+                             const void *z_scale, const void *dY, void *dX, void *dW, void *dbias, void *stream);
+
 /* Output shape: writes up to MM_MAX_RANK entries to `shape` and the rank to
  * *rank (0 when both inputs are rank one). */
 mm_status mm_plan_output_shape(mm_plan_t plan, int64_t *shape, int *rank);

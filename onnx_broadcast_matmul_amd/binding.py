@@ -8,6 +8,7 @@ fallback: if ``libmm.so`` is missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional, Sequence, Tuple
@@ -18,6 +19,7 @@ LIB_PATH = os.path.join(PKG, "libmm.so")
 FLOAT, FLOAT16, DOUBLE, BFLOAT16 = 1, 10, 11, 16
 UINT8, INT8, INT32 = 2, 3, 6
 ZP_NONE, ZP_SCALAR, ZP_VECTOR = 0, 1, 2
+ACT_NONE = 0
 ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SIGMOID = 1, 2, 3, 4, 5
 ACTIVATIONS = {"silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU,
                "sigmoid": ACT_SIGMOID}
@@ -87,6 +89,15 @@ class GluDesc(ctypes.Structure):
 class GluOptions(ctypes.Structure):
     _fields_ = [("kept_type", ctypes.c_int32), ("dx_tile", ctypes.c_int32), ("dx_split_k", ctypes.c_int32),
                 ("dw_tile", ctypes.c_int32), ("dw_split_k", ctypes.c_int32)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_features", ctypes.c_int64), ("out_features", ctypes.c_int64),
+                ("w_pitch", ctypes.c_int64), ("trans_w", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("has_bias", ctypes.c_int32), ("has_residual", ctypes.c_int32), ("training", ctypes.c_int32),
+                ("z_type", ctypes.c_int32), ("x_type", ctypes.c_int32), ("x_activation", ctypes.c_int32),
+                ("dx_tile", ctypes.c_int32), ("dx_split_k", ctypes.c_int32), ("dw_tile", ctypes.c_int32),
+                ("dw_split_k", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -166,6 +177,21 @@ def lib() -> ctypes.CDLL:
         L.mm_glu_execute.restype = ctypes.c_int
         L.mm_glu_backward.argtypes = [vp] * 11
         L.mm_glu_backward.restype = ctypes.c_int
+        L.mm_checkpoint_blocks.argtypes = [ctypes.c_int64]
+        L.mm_checkpoint_blocks.restype = ctypes.c_int64
+        L.mm_checkpoint_pack.argtypes = [vp, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, vp, vp, vp]
+        L.mm_checkpoint_pack.restype = ctypes.c_int
+        L.mm_checkpoint_unpack.argtypes = [vp, vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, vp, vp]
+        L.mm_checkpoint_unpack.restype = ctypes.c_int
+        L.mm_linear_plan_create.argtypes = [ctypes.POINTER(LinearDesc), ctypes.c_int, ctypes.POINTER(PlanOptions),
+                                            ctypes.POINTER(vp)]
+        L.mm_linear_plan_create.restype = ctypes.c_int
+        L.mm_linear_get_desc.argtypes = [vp, ctypes.POINTER(LinearDesc)]
+        L.mm_linear_get_desc.restype = ctypes.c_int
+        L.mm_linear_execute.argtypes = [vp] * 9
+        L.mm_linear_execute.restype = ctypes.c_int
+        L.mm_linear_backward.argtypes = [vp] * 11
+        L.mm_linear_backward.restype = ctypes.c_int
         L.mm_status_string.argtypes = [ctypes.c_int]
         L.mm_status_string.restype = ctypes.c_char_p
         L.mm_last_error.argtypes = []
@@ -681,6 +707,178 @@ class GluPlan(Plan):
                 None if dX is None else _dense("dX", dX, dt, self._x, dev),
                 None if dWg is None else self._weight("dWg", dWg, dev),
                 None if dWu is None else self._weight("dWu", dWu, dev))
+        with self._lock:
+            _run(dev, stream, self._backward, self._handle, *ptrs)
+
+
+CHECKPOINT_BLOCK = 32
+
+
+def checkpoint_blocks(cols: int) -> int:
+    """Scale bytes of a checkpoint row of ``cols`` elements."""
+    return -(-int(cols) // CHECKPOINT_BLOCK)
+
+
+def _checkpoint(name, q, scale, shape, dev):
+    """The addresses of a checkpoint of a tensor of `shape` on GPU `dev`."""
+    import torch
+
+    qp = _dense(name, q, torch.int8, shape, dev)
+    return qp, _dense(f"{name}'s scale", scale, torch.uint8, shape[:-1] + (checkpoint_blocks(shape[-1]),), dev)
+
+
+def _rows_cols(shape) -> Tuple[int, int]:
+    if len(shape) < 1:
+        raise ValueError("a tensor of at least one dimension is needed")
+    return math.prod(shape[:-1]), shape[-1]
+
+
+def checkpoint_pack(X, q=None, scale=None, stream=None):
+    """mm_checkpoint_pack: (q, scale), the 8-bit checkpoint of X's rows (its
+    last dimension): q INT8 of X's shape, scale UINT8 with a byte for each block
+    of CHECKPOINT_BLOCK elements.  Those that are not given are made on ``stream``
+    (default: the current stream), as if it were current."""
+    import torch
+
+    code = torch_dtype_code(X.dtype)
+    rows, cols = _rows_cols(X.shape)
+    dev = _device_of(X)
+    if q is None:
+        q = _empty(X.shape, torch.int8, X.device, stream)
+    if scale is None:
+        scale = _empty(X.shape[:-1] + (checkpoint_blocks(cols),), torch.uint8, X.device, stream)
+    xp = _dense("X", X, X.dtype, X.shape, dev)
+    qp, sp = _checkpoint("q", q, scale, X.shape, dev)
+    _run(dev, stream, lib().mm_checkpoint_pack, xp, code, rows, cols, qp, sp)
+    return q, scale
+
+
+def checkpoint_unpack(q, scale, out, stream=None):
+    """mm_checkpoint_unpack: the checkpoint's values into ``out`` (q's shape), or
+    into a new tensor of ``out`` if that is a torch dtype."""
+    import torch
+
+    rows, cols = _rows_cols(q.shape)
+    dev = _device_of(q)
+    if isinstance(out, torch.dtype):
+        torch_dtype_code(out)
+        out = _empty(q.shape, out, q.device, stream)
+    code = torch_dtype_code(out.dtype)
+    qp, sp = _checkpoint("q", q, scale, q.shape, dev)
+    op = _dense("out", out, out.dtype, q.shape, dev)
+    _run(dev, stream, lib().mm_checkpoint_unpack, qp, sp, rows, cols, code, op)
+    return out
+
+
+class LinearPlan(Plan):
+    """mm_linear_plan_create / mm_linear_execute / mm_linear_backward: the linear
+    layer Y = f(X W + bias) + residual and its gradients.  The weights are
+    [in_features, out_features], or [out_features, in_features] with trans_w;
+    they may be a view of a wider matrix (rows w_pitch elements apart).  A
+    training plan with an activation keeps Z = X W + bias in z_type (0: the
+    plan's type; FLOAT; INT8: a checkpoint) and takes X for the backward pass as
+    x_type says (INT8: a checkpoint, to whose values x_activation is applied).
+    tile and split_k override the forward pass's choices, dx_* and dw_* the
+    backward pass's."""
+
+    def __init__(self, rows: int, in_features: int, out_features: int, dtype: int, activation: int = ACT_NONE,
+                 trans_w: bool = False, bias: bool = False, residual: bool = False, training: bool = False,
+                 z_type: int = 0, x_type: int = 0, x_activation: int = ACT_NONE, w_pitch: int = 0, force_algo: int = 0,
+                 tile: int = 0, split_k: int = 0, dx_tile: int = 0, dx_split_k: int = 0, dw_tile: int = 0,
+                 dw_split_k: int = 0):
+        import torch
+
+        L = lib()
+        self._handle = ctypes.c_void_p()
+        self.dtype = int(dtype)
+        self.rows, self.in_features, self.out_features = int(rows), int(in_features), int(out_features)
+        self.trans_w, self.bias, self.residual = bool(trans_w), bool(bias), bool(residual)
+        self.training, self.activation = bool(training), int(activation)
+        desc = LinearDesc(self.rows, self.in_features, self.out_features, int(w_pitch), int(self.trans_w),
+                          self.activation, int(self.bias), int(self.residual), int(self.training), int(z_type),
+                          int(x_type), int(x_activation), dx_tile, dx_split_k, dw_tile, dw_split_k, 0)
+        opt = PlanOptions(force_algo, tile, split_k, 0)
+        _check(L.mm_linear_plan_create(ctypes.byref(desc), self.dtype, ctypes.byref(opt), ctypes.byref(self._handle)))
+        self._lock = threading.Lock()
+        self._dt = torch_dtype(self.dtype)
+        kept = self.training and self.activation != ACT_NONE
+        self._z_dt = torch_dtype(int(z_type) or self.dtype) if kept else None
+        self._z8, self._x8 = kept and int(z_type) == INT8, int(x_type) == INT8
+        self._x = torch.Size((self.rows, self.in_features))
+        self._y = torch.Size((self.rows, self.out_features))
+        self._b = torch.Size((self.out_features,))
+        self._w = torch.Size((self.out_features, self.in_features) if self.trans_w else
+                             (self.in_features, self.out_features))
+        self._pitch = int(w_pitch) or self._w[1]
+        self._execute, self._backward = L.mm_linear_execute, L.mm_linear_backward
+
+    def desc(self) -> dict:
+        """mm_linear_get_desc: what the plan resolved, the backward products'
+        tile entries and K partitions among it."""
+        d = LinearDesc()
+        _check(lib().mm_linear_get_desc(self._handle, ctypes.byref(d)))
+        return {name: getattr(d, name) for name, _ in d._fields_ if name != "reserved"}
+
+    _weight = GluPlan._weight
+
+    def _kept(self, Z, z_scale, dev):
+        """The addresses of Z and of its scale."""
+        if Z is None:
+            if z_scale is not None:
+                raise ValueError("z_scale is given without Z")
+            return None, None
+        if self._z_dt is None:
+            raise ValueError("the plan keeps no Z")
+        if self._z8:
+            if z_scale is None:
+                raise ValueError("Z is a checkpoint: z_scale is missing")
+            return _checkpoint("Z", Z, z_scale, self._y, dev)
+        if z_scale is not None:
+            raise ValueError("z_scale: the plan keeps Z whole")
+        return _dense("Z", Z, self._z_dt, self._y, dev), None
+
+    def execute_ptr(self, X: int, W: int, Y: int, stream: int = 0, bias: int = 0, residual: int = 0, Z: int = 0,
+                    z_scale: int = 0) -> None:
+        _check(lib().mm_linear_execute(self._handle, X, W, bias, residual, Y, Z, z_scale, stream))
+
+    def execute(self, X, W, Y, bias=None, residual=None, Z=None, z_scale=None, stream=None) -> None:
+        """The forward pass; Z (and z_scale, for a checkpoint) keeps what the
+        backward pass needs.  Y may be the residual itself."""
+        if (bias is None) == self.bias:
+            raise ValueError("bias: the plan has " + ("one" if self.bias else "none"))
+        if (residual is None) == self.residual:
+            raise ValueError("residual: the plan has " + ("one" if self.residual else "none"))
+        dt = self._dt
+        dev = _device_of(Y)
+        xp = _dense("X", X, dt, self._x, dev)
+        wp = self._weight("W", W, dev)
+        yp = _dense("Y", Y, dt, self._y, dev)
+        bp = None if bias is None else _dense("bias", bias, dt, self._b, dev)
+        rp = None if residual is None else _dense("residual", residual, dt, self._y, dev)
+        zp, sp = self._kept(Z, z_scale, dev)
+        with self._lock:
+            _run(dev, stream, self._execute, self._handle, xp, wp, bp, rp, yp, zp, sp)
+
+    def backward(self, X, W, dY, Z=None, z_scale=None, x_scale=None, dX=None, dW=None, dbias=None, stream=None) -> None:
+        """The backward pass into those of dX, dW and dbias that are given
+        (overwritten).  X may be None without dW, W without dX."""
+        dt = self._dt
+        dev = _device_of(dY)
+        if X is not None and self._x8:
+            if x_scale is None:
+                raise ValueError("X is a checkpoint: x_scale is missing")
+            xp, xsp = _checkpoint("X", X, x_scale, self._x, dev)
+        else:
+            if x_scale is not None:
+                raise ValueError("x_scale: " + ("X is missing" if self._x8 else "the plan takes X whole"))
+            xp, xsp = None if X is None else _dense("X", X, dt, self._x, dev), None
+        zp, zsp = self._kept(Z, z_scale, dev)
+        if dbias is not None and not self.bias:
+            raise ValueError("dbias: the plan has no bias")
+        ptrs = (xp, xsp, None if W is None else self._weight("W", W, dev), zp, zsp, _dense("dY", dY, dt, self._y, dev),
+                None if dX is None else _dense("dX", dX, dt, self._x, dev),
+                None if dW is None else self._weight("dW", dW, dev),
+                None if dbias is None else _dense("dbias", dbias, dt, self._b, dev))
         with self._lock:
             _run(dev, stream, self._backward, self._handle, *ptrs)
 

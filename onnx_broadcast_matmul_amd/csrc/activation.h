@@ -1,4 +1,4 @@
-// activation.h -- the gated block's activations f and their derivatives, in
+// activation.h -- the feed-forward operators' activations f and their derivatives, in
 // FP32.  Each is written so that neither tail cancels: the sigmoid and its
 // complement come from one exponential of -|x|, the tanh form of gelu from
 // (1 + tanh z) / 2 = sigmoid(2 z), and gelu from the normal distribution's
@@ -88,6 +88,19 @@ __device__ __forceinline__ float act_value(float g) {
         sigmoid_pair<EXACT>(g, s, c);
         return ACT == MM_ACT_SILU ? g * s : s;
     }
+}
+
+// f(z) for an activation known at run time (MM_ACT_NONE: z).
+template <bool EXACT>
+__device__ __forceinline__ float act_run(int act, float z) {
+    switch (act) {
+    case MM_ACT_SILU: return act_value<MM_ACT_SILU, EXACT>(z);
+    case MM_ACT_GELU: return act_value<MM_ACT_GELU, EXACT>(z);
+    case MM_ACT_GELU_TANH: return act_value<MM_ACT_GELU_TANH, EXACT>(z);
+    case MM_ACT_RELU: return act_value<MM_ACT_RELU, EXACT>(z);
+    case MM_ACT_SIGMOID: return act_value<MM_ACT_SIGMOID, EXACT>(z);
+    }
+    return z;
 }
 
 // f(g) and f'(g).

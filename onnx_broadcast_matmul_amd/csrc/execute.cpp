@@ -58,6 +58,8 @@ mm_status mm::require_matmul(const mm_plan_s *p) {
     if (p->is_int) return fail(MM_ERR_BAD_OPTION, "a MatMulInteger plan runs through mm_int_execute");
     if (p->is_scaled) return fail(MM_ERR_BAD_OPTION, "a scaled INT8 plan runs through mm_scaled_int_execute");
     if (p->is_glu) return fail(MM_ERR_BAD_OPTION, "a gated-block plan runs through mm_glu_execute");
+    if (p->is_linear) return fail(MM_ERR_BAD_OPTION, "a linear-layer plan runs through mm_linear_execute");
+    if (p->is_norm) return fail(MM_ERR_BAD_OPTION, "a norm plan runs through mm_norm_execute");
     return MM_OK;
 }
 
@@ -365,7 +367,7 @@ mm_status mm_gemm_execute(mm_plan_t p, const void *A, const void *B, const void 
 mm_status mm_plan_set_constant_b(mm_plan_t p, const void *B, int64_t numel, void *stream) {
     clear_error();
     if (!p) return fail(MM_ERR_NULL_ARG, "plan is NULL");
-    if (p->is_gemm || p->is_int || p->is_scaled || p->is_glu)
+    if (p->is_gemm || p->is_int || p->is_scaled || p->is_glu || p->is_linear || p->is_norm)
         return fail(MM_ERR_BAD_OPTION, "constant B is for MatMul plans (it runs through mm_execute)");
     if (numel != p->b_numel)
         return fail(MM_ERR_SIZE, "constant B has %lld elements; the planned B has %lld", (long long)numel,
@@ -425,7 +427,7 @@ mm_status mm_execute_constant_b(mm_plan_t p, const void *A, void *Y, void *strea
         B = p->cb;
         packed = p->cbp_ok;
     }
-    if (p->is_gemm || p->is_int || p->is_scaled || p->is_glu)
+    if (p->is_gemm || p->is_int || p->is_scaled || p->is_glu || p->is_linear || p->is_norm)
         return fail(MM_ERR_BAD_OPTION, "constant B serves MatMul plans");
     return execute_plan(p, A, B, nullptr, Y, stream, nullptr, packed);
 }

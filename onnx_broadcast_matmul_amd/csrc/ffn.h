@@ -25,11 +25,17 @@ struct FfnArgs {
     int32_t kept32;        // which are FP32 in a 16-bit plan
     // scaled INT8 product
     const float *sa, *sb;
-    const void *bias;      // of the output type, or NULL
+    const void *bias;      // of the output type, or NULL (the linear layer's too)
     void *W;               // partial sums [split][batch][M][N], INT32 (INT8 operands) or FP32
     int32_t split;
     int32_t kstages;       // K stages of a partition
     BatchDesc bd;
+    // linear layer: Z goes to G (kept32: FP32; q8: a checkpoint with its scale
+    // bytes in zs), the residual is read from R
+    const void *R;
+    void *zs;
+    int32_t q8;
+    int32_t r_vec;         // four columns of R are an aligned vector
 };
 
 // The same as the kernels take it: in 88 bytes, because a launch with more
@@ -49,6 +55,11 @@ struct FfnSlim {
     __host__ __device__ bool kept32() const { return flags & 4; }
     __host__ __device__ void *G() const { return Y[1]; }  // gated block
     __host__ __device__ void *U() const { return Y[2]; }
+    __host__ __device__ bool q8() const { return flags & 8; }  // linear layer: Z in G()
+    __host__ __device__ bool r_vec() const { return flags & 16; }
+    __host__ __device__ const void *R() const { return Y[2]; }
+    __host__ __device__ void *zs() const { return (void *)A[1]; }
+    __host__ __device__ const void *lin_bias() const { return B[1]; }
     __host__ __device__ const float *sa() const { return (const float *)A[1]; }  // scaled product
     __host__ __device__ const float *sb() const { return (const float *)B[1]; }
     __host__ __device__ const void *bias() const { return Y[1]; }
@@ -76,9 +87,9 @@ struct FfnTile {
 constexpr FfnTile kFfnTiles[] = {{256, 256, 64}, {128, 128, 64}, {64, 128, 128}, {32, 128, 256}, {256, 128, 128}};
 constexpr int kNumFfnTiles = sizeof(kFfnTiles) / sizeof(kFfnTiles[0]);
 
-// Kernel arguments of a product (glu, scaled: which slots it needs), of a
+// Kernel arguments of a product (glu, scaled, linear: which slots it needs), of a
 // split one (its partial sums) and of its reduction.
-enum FfnUse { kUsePlain, kUseGlu, kUseScaled };
+enum FfnUse { kUsePlain, kUseGlu, kUseScaled, kUseLinear };
 template <class T>
 inline T slim_args(const FfnArgs &a, FfnUse use, bool split, bool reduce) {
     T s = {};
@@ -96,7 +107,8 @@ inline T slim_args(const FfnArgs &a, FfnUse use, bool split, bool reduce) {
     s.kstages = a.kstages;
     s.split = (uint16_t)a.split;
     s.act = (uint8_t)a.act;
-    s.flags = (uint8_t)((a.y_vec ? 1 : 0) | (a.kept_vec ? 2 : 0) | (a.kept32 ? 4 : 0));
+    s.flags = (uint8_t)((a.y_vec ? 1 : 0) | (a.kept_vec ? 2 : 0) | (a.kept32 ? 4 : 0) | (a.q8 ? 8 : 0) |
+                        (a.r_vec ? 16 : 0));
     if (use == kUseGlu) {
         s.Y[1] = a.G;
         s.Y[2] = a.U;
@@ -104,6 +116,11 @@ inline T slim_args(const FfnArgs &a, FfnUse use, bool split, bool reduce) {
         s.A[1] = a.sa;
         s.B[1] = a.sb;
         s.Y[1] = (void *)a.bias;
+    } else if (use == kUseLinear) {
+        s.A[1] = a.zs;
+        s.B[1] = a.bias;
+        s.Y[1] = a.G;
+        s.Y[2] = (void *)a.R;
     }
     if (split) s.Y[0] = a.W;
     if (reduce) s.A[0] = a.W;
@@ -152,6 +169,46 @@ inline bool rows_halve(int64_t wgs) { return 2 * wgs <= kNumCUs; }
 hipError_t launch_glu_rows(int dtype, bool tb, const FfnArgs &a, hipStream_t s);
 bool rows_quantize(int a_type, int out_dtype, bool tb, int64_t M, int64_t K, int64_t N);
 hipError_t launch_scaled_rows(int out_dtype, bool tb, bool quant, const FfnArgs &a, hipStream_t s);
+// Linear layer: the forward products (also dX's, which has no epilogue), the
+// joining of a split one with the epilogue, the few-row kernel.  dW is a pair of
+// one (launch_glu_dw with batch 1).
+hipError_t launch_linear(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
+hipError_t launch_linear_reduce(int dtype, const FfnArgs &a, hipStream_t s);
+hipError_t launch_linear_rows(int dtype, bool tb, const FfnArgs &a, hipStream_t s);
+
+// What a linear layer's backward products need first: dZ = dY f'(Z) (act; rows
+// of ldz elements, zeros past N), the column sums of dZ over each block of
+// kPrepRows rows (part, rows of ldp floats), and a checkpoint's values f(q s) as
+// rows of ldx elements (zeros past K).  NULL dZ, part, X: not wanted.
+constexpr int kPrepRows = 64;
+struct LinearPrep {
+    const void *dY, *Z, *zs;
+    void *dZ;
+    float *part;
+    const void *xq, *xs;
+    void *X;
+    int64_t M, N, ldz, ldp, K, ldx;
+    int32_t act, z_type, x_act;
+};
+hipError_t launch_linear_prep(int dtype, const LinearPrep &a, hipStream_t s);
+int64_t linear_prep_blocks(const LinearPrep &a, int dtype);
+
+// out[j][n] = sum over p of part[p * stride + j * ldp + n], n < N, j < jobs, in
+// order of p within each of 32 slices and then of the slices; ldp and stride are
+// multiples of four.  NULL out[j]: job left out.
+constexpr int kJoinJobs = 5;
+struct JoinArgs {
+    const float *part;
+    int64_t P, stride, ldp, N;
+    void *out[kJoinJobs];
+};
+hipError_t launch_join(int dtype, const JoinArgs &a, int jobs, hipStream_t s);
+
+// Checkpoints (the format stands in checkpoint.h).
+hipError_t launch_checkpoint_pack(int dtype, const void *X, int64_t rows, int64_t cols, void *q, void *scale, hipStream_t s);
+hipError_t launch_checkpoint_unpack(int dtype, const void *q, const void *scale, int64_t rows, int64_t cols, void *X,
+                                    hipStream_t s);
+
 // Row quantization of a dense [rows, cols] matrix into rows of ldq bytes; the
 // bytes past cols are set to zero.
 hipError_t launch_quantize_rows(int dtype, const void *X, int64_t rows, int64_t cols, void *Q, int64_t ldq, float *scale,

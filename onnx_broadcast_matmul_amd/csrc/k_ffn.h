@@ -1,7 +1,8 @@
 // k_ffn.h -- tiled products of the feed-forward operators on the gfx950
 // matrix cores: the gated block (two weight matrices, one fused epilogue), the
-// two-term input gradient, the pair of weight gradients, and the INT8 product
-// with row and column scales.
+// two-term input gradient, the pair of weight gradients (or one), the linear
+// layer with bias, activation and residual, and the INT8 product with row and
+// column scales.
 //
 // One workgroup owns a BM x BN tile (for the gated block BN counts the gate
 // and the up columns: BN / 2 hidden features).  K moves through STAGES LDS
@@ -38,6 +39,7 @@
 #include <type_traits>
 
 #include "activation.h"
+#include "checkpoint.h"
 #include "device.h"
 #include "ffn.h"
 #include "pieces.h"
@@ -61,12 +63,14 @@ __device__ __forceinline__ int row_swizzle(int k, int cpr) {
 //   kSum2:   Y0 = A0 B0 + A1 B1 (the K loop runs over both terms)
 //   kPair:   Y0 = A0 B0 and Y1 = A1 B1 (half of the grid each)
 //   kScaled: Y = sa[m] sb[n] (A B) + bias[n], INT8 operands
+//   kLinear: Y = act(Z) + R, Z = A B + bias; optionally also Z, in OD, as its
+//            FP32 sums or (flags) as an 8-bit checkpoint
 // SPLIT: a workgroup takes a range of K stages and writes FP32 (INT8
 // operands: INT32) partial sums to the workspace.
 // KG groups of WGM x WGN waves share the tile; group g takes every KG-th MFMA
 // step of a stage, and their sums are added in group order at the end.
 // BATCH (kScaled): more than one product.
-enum FfnMode { kGlu = 0, kSum2 = 1, kPair = 2, kScaled = 3 };
+enum FfnMode { kGlu = 0, kSum2 = 1, kPair = 2, kScaled = 3, kLinear = 4 };
 
 template <int DT, int OD, int MODE, bool SPLIT, bool TA, bool TB, int BM, int BN, int WGM, int WGN, int KG, int BKB,
           int STAGES, int PW, bool DMA, bool BATCH>
@@ -592,13 +596,17 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
                             const int cl = wc * WNP + j * 32 + 8 * q + 4 * (lane >> 5);
                             char *dst = trow + ((cl / OV) ^ (rl & (OCPR - 1))) * 16 + (cl % OV) * OS;
                             const AccT &v = acc[i][jbase + j];
-                            if constexpr (std::is_same<O, int32_t>::value) {
+                            if constexpr (std::is_same<O, int8_t>::value) {
+                                // Whole numbers of -127 .. 127.
+                                *(uint32_t *)dst = pack_bytes(value(i, j, cl, v[4 * q]), value(i, j, cl + 1, v[4 * q + 1]),
+                                                              value(i, j, cl + 2, v[4 * q + 2]), value(i, j, cl + 3, v[4 * q + 3]));
+                            } else if constexpr (std::is_same<O, int32_t>::value) {
                                 *(uint4 *)dst = make_uint4((uint32_t)v[4 * q], (uint32_t)v[4 * q + 1],
                                                            (uint32_t)v[4 * q + 2], (uint32_t)v[4 * q + 3]);
                             } else {
                                 float w[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) w[e] = value(i, cl + e, v[4 * q + e]);
+                                for (int e = 0; e < 4; ++e) w[e] = value(i, j, cl + e, v[4 * q + e]);
                                 using PK = Elem<OS == 4 ? MM_BFLOAT16 : OD>;
                                 if constexpr (OS == 4) *(float4 *)dst = make_float4(w[0], w[1], w[2], w[3]);
                                 else *(uint2 *)dst = make_uint2(PK::pack2(w[0], w[1]), PK::pack2(w[2], w[3]));
@@ -629,7 +637,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
             }
         }
     };
-    auto plain = [](int, int, auto v) { return (float)v; };
+    auto plain = [](int, int, int, auto v) { return (float)v; };
     if constexpr (SPLIT && MODE == kGlu) {
         // Partials of G, then of U, for every partition.
         float *w = (float *)a.part() + sidx * 2 * M * N;
@@ -637,7 +645,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
         emit(0.0f, FNP, plain, w + M * N, N, N % 4 == 0);
     } else if constexpr (SPLIT) {
         using T = typename std::conditional<INT, int32_t, float>::type;
-        int64_t nprod = MODE == kPair ? 2 : 1;
+        int64_t nprod = MODE == kPair ? (int64_t)gridDim.x / (per * nsplit) : 1;
         if constexpr (BATCH) nprod = a.batch;
         emit((T)0, 0, plain, (T *)a.part() + (sidx * nprod + b) * M * N, N, N % 4 == 0);
     } else if constexpr (MODE == kGlu) {
@@ -668,6 +676,98 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
         default: apply(std::integral_constant<int, MM_ACT_SIGMOID>()); break;
         }
         emit((typename OE::S)0, 0, plain, a.Y[0], a.ldy, a.y_vec());
+    } else if constexpr (MODE == kLinear) {
+        // The tile's bias in LDS; the residual straight into the accumulators'
+        // places, four columns a lane, so that everything is added in FP32 and
+        // Y rounded once.  (row, col) of a lane's quarter q of block (i, j):
+        __shared__ __attribute__((aligned(16))) float cb[PN];
+        const bool holds = KG > 2 || kg == 0;
+        auto row_of = [&](int i) { return m0 + wr * WM + i * 32 + (lane & 31); };
+        auto col_of = [&](int j, int q) { return wc * WNP + j * 32 + 8 * q + 4 * (lane >> 5); };
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FNP; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (mine(q)) f(i, j, q);
+        };
+        if (a.lin_bias()) {
+            for (int x = tid; x < PN; x += NT)
+                cb[x] = n0 + x < N ? OE::to_f32(((const typename OE::S *)a.lin_bias())[n0 + x]) : 0.0f;
+            __syncthreads();
+            if (holds) each([&](int i, int j, int q) {
+                const float4 b = *(const float4 *)(cb + col_of(j, q));
+                acc[i][j][4 * q] += b.x;
+                acc[i][j][4 * q + 1] += b.y;
+                acc[i][j][4 * q + 2] += b.z;
+                acc[i][j][4 * q + 3] += b.w;
+            });
+        }
+        if (a.G()) {
+            // A 32 x 32 block of the accumulators is a checkpoint block for each
+            // of 32 rows, half of it in lane l and half in lane l + 32.  (The
+            // entry whose K groups share the epilogue does not hold it whole:
+            // plans do not use it here.)
+            if (a.q8()) {
+                if constexpr (KG <= 2) {
+                    float inv[FM][FNP];
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+#pragma unroll
+                        for (int j = 0; j < FNP; ++j) {
+                            uint32_t top = 0;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) {
+                                const uint32_t b = ck_magnitude(acc[i][j][r]);
+                                if (n0 + col_of(j, r / 4) + r % 4 < N) top = b > top ? b : top;
+                            }
+                            const uint32_t o = (uint32_t)__shfl_xor((int)top, 32);
+                            const uint32_t ex = ck_exponent(o > top ? o : top);
+                            inv[i][j] = ck_inverse(ex);
+                            const int64_t row = row_of(i), col = n0 + wc * WNP + j * 32;
+                            if (kg == 0 && lane < 32 && row < M && col < N)
+                                ((uint8_t *)a.zs())[row * ((N + 31) / 32) + col / 32] = (uint8_t)ex;
+                        }
+                    emit((int8_t)0, 0, [&](int i, int j, int, float v) { return ck_number(v, inv[i][j]); }, a.G(), a.ldy,
+                         a.kept_vec());
+                }
+            } else if (OD != MM_FLOAT && a.kept32()) {
+                emit(0.0f, 0, plain, a.G(), a.ldy, a.kept_vec());
+            } else {
+                emit((typename OE::S)0, 0, plain, a.G(), a.ldy, a.kept_vec());
+            }
+        }
+        auto apply = [&](auto kind) {
+            each([&](int i, int j, int q) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][4 * q + e] = act_value<decltype(kind)::value, DT == MM_FLOAT>(acc[i][j][4 * q + e]);
+            });
+        };
+        if (holds) switch (a.act) {
+        case MM_ACT_SILU: apply(std::integral_constant<int, MM_ACT_SILU>()); break;
+        case MM_ACT_GELU: apply(std::integral_constant<int, MM_ACT_GELU>()); break;
+        case MM_ACT_GELU_TANH: apply(std::integral_constant<int, MM_ACT_GELU_TANH>()); break;
+        case MM_ACT_RELU: apply(std::integral_constant<int, MM_ACT_RELU>()); break;
+        case MM_ACT_SIGMOID: apply(std::integral_constant<int, MM_ACT_SIGMOID>()); break;
+        }
+        if (holds && a.R()) each([&](int i, int j, int q) {
+            using RS = typename OE::S;
+            const int64_t row = row_of(i), col = n0 + col_of(j, q);
+            if (row >= M || col >= N) return;
+            const RS *r = (const RS *)a.R() + row * a.ldy + col;
+            RS v[4] = {};
+            if (a.r_vec()) __builtin_memcpy(v, __builtin_assume_aligned(r, 4 * sizeof(RS)), sizeof(v));
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < N) v[e] = r[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] += OE::to_f32(v[e]);
+        });
+        emit((typename OE::S)0, 0, plain, a.Y[0], a.ldy, a.y_vec());
     } else if constexpr (MODE == kScaled) {
         // Scales of this lane's rows, and of the tile's columns in LDS after
         // the main loop's last reads.  K == 0: the matrices are empty, their
@@ -687,7 +787,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
             rs[i] = row < M && K > 0 ? a.sa()[oa / a.lda + row] : 0.0f;
         }
         __syncthreads();
-        emit((typename OE::S)0, 0, [&](int i, int cl, int v) { return scaled_value(v, rs[i], cs[cl], cb[cl]); },
+        emit((typename OE::S)0, 0, [&](int i, int, int cl, int v) { return scaled_value(v, rs[i], cs[cl], cb[cl]); },
              (typename OE::S *)a.Y[0] + b * M * a.ldy, a.ldy, a.y_vec());
     } else {
         emit((typename OE::S)0, 0, plain, MODE == kPair ? a.Y[pick] : a.Y[0], a.ldy, a.y_vec());
@@ -718,7 +818,7 @@ static hipError_t launch_ffn(bool vec, const FfnArgs &a, hipStream_t s) {
                 return hipGetLastError();
             }
         }
-        const FfnUse use = MODE == kGlu ? kUseGlu : MODE == kScaled ? kUseScaled : kUsePlain;
+        const FfnUse use = MODE == kGlu ? kUseGlu : MODE == kScaled ? kUseScaled : MODE == kLinear ? kUseLinear : kUsePlain;
         hipLaunchKernelGGL((k_ffn<DT, OD, MODE, SPLIT, TA, TB, BM, BN, WGM, WGN, KG, BKB, STAGES, PW, D, false>), g, blk,
                            0, s, slim_args<FfnSlim>(a, use, SPLIT, false));
         return hipGetLastError();

@@ -1,4 +1,4 @@
-// k_ffn_rows.h -- the gated block and the scaled INT8 product over few rows
+// k_ffn_rows.h -- the gated block, the linear layer and the scaled INT8 product over few rows
 // (one decoded token to kFfnRows of them).
 //
 // The weights are the traffic, and memory's rate the bound: each is read once
@@ -397,6 +397,19 @@ __global__ __launch_bounds__(64 * NWV, MB == 2 || (XQ && KN) ? 2 : XQ && NWV == 
             default: f = act_value<MM_ACT_SIGMOID, X>(sg); break;
             }
             ((OS *)a.Y[0])[o] = OE::from_f32(f * su);
+        } else if constexpr (!INT) {
+            // Linear layer (no checkpoint of Z: plans for one run the tiles).
+            float z = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NWV; ++v) z += red[v][c >> 4][i][at];
+            if (a.lin_bias()) z += OE::to_f32(((const OS *)a.lin_bias())[n]);
+            if (a.G()) {
+                if (OD != MM_FLOAT && a.kept32()) ((float *)a.G())[o] = z;
+                else ((OS *)a.G())[o] = OE::from_f32(z);
+            }
+            z = act_run<DT == MM_FLOAT>(a.act, z);
+            if (a.R()) z += OE::to_f32(((const OS *)a.R())[o]);
+            ((OS *)a.Y[0])[o] = OE::from_f32(z);
         } else {
             int sum = 0;
 #pragma unroll
@@ -435,7 +448,7 @@ static hipError_t launch_rows(const FfnArgs &a, hipStream_t s) {
         if (rows_halve(wgs)) return launch_rows<DT, OD, GLU, KN, NF / 2, MB, NWV, XQ>(a, s);
     }
     hipLaunchKernelGGL((k_ffn_rows<DT, OD, GLU, KN, NF, MB, NWV, XQ, UA>), dim3((unsigned)wgs), dim3(64 * NWV), 0, s,
-                       slim_args<FfnSlim>(a, GLU ? kUseGlu : kUseScaled, false, false));
+                       slim_args<FfnSlim>(a, GLU ? kUseGlu : DT == MM_INT8 ? kUseScaled : kUseLinear, false, false));
     return hipGetLastError();
 }
 

@@ -1,0 +1,6 @@
+// k_linear_bf16.hip -- the linear layer's tiled products in BFLOAT16.
+#include "k_linear.h"
+
+namespace mm {
+MM_LINEAR_INSTANCE(MM_BFLOAT16, bf16)
+}  // namespace mm

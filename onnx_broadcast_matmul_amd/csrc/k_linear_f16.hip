@@ -1,0 +1,6 @@
+// k_linear_f16.hip -- the linear layer's tiled products in FLOAT16.
+#include "k_linear.h"
+
+namespace mm {
+MM_LINEAR_INSTANCE(MM_FLOAT16, f16)
+}  // namespace mm

@@ -1,0 +1,6 @@
+// k_linear_f32.hip -- the linear layer's tiled products in FLOAT.
+#include "k_linear.h"
+
+namespace mm {
+MM_LINEAR_INSTANCE(MM_FLOAT, f32)
+}  // namespace mm

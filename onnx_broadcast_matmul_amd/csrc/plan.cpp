@@ -1106,6 +1106,12 @@ mm_status mm_plan_get_info(mm_plan_t p, mm_plan_info *info) {
                           ((double)p->M * (double)p->K + 2.0 * (double)p->K * (double)p->N + (double)p->M * (double)p->N);
         return MM_OK;
     }
+    if (p->is_linear) {  // forward pass: X, W, bias, residual and Y once
+        info->min_bytes = (double)elem_size(p->dtype) *
+                          ((double)p->M * (double)p->K + (double)p->K * (double)p->N + (p->has_bias ? (double)p->N : 0.0) +
+                           (p->has_residual ? 2.0 : 1.0) * (double)p->M * (double)p->N);
+        return MM_OK;
+    }
     int64_t na = 1, nb = 1;
     for (int i = 0; i < p->a_rank; ++i) na *= p->a_shape[i];
     for (int i = 0; i < p->b_rank; ++i) nb *= p->b_shape[i];

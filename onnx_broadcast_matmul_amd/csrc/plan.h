@@ -86,6 +86,18 @@ struct mm_plan_s {
     mm::FfnChoice dx, dw;  // the backward products
     int32_t kstages = 0;   // K stages of a partition (scaled product, forward pass)
 
+    // Linear layer (mm_linear_plan_create): M, N, K are rows, out_features,
+    // in_features; tb, act, training, kept (of Z; 0: nothing is kept), w_pitch
+    // and the backward choices as for the gated block.  A training workspace
+    // holds, at d_off, dZ (with an activation: rows of d_pitch elements), then at
+    // x_off the values of an X checkpoint (rows of x_pitch elements), at p_off the
+    // column sums of dZ (rows of p_pitch floats), at s_off partial sums.
+    bool is_norm = false;
+    bool is_linear = false;
+    bool has_residual = false;
+    int x_type = 0, x_act = 0;
+    int64_t x_pitch = 0, x_off = 0, p_pitch = 0, p_off = 0, s_off = 0;
+
     // Plan-owned constant B (mm_plan_set_constant_b).
     std::mutex cb_mutex;
     bool cb_set = false;

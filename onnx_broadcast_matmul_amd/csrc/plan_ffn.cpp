@@ -6,46 +6,9 @@
 #include <algorithm>
 #include <new>
 
-#include "ffn.h"
-#include "plan.h"
+#include "ffn_choice.h"
 
 namespace mm {
-
-static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-static int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
-static bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-static mm_status launched(hipError_t e) {
-    return e == hipSuccess ? MM_OK : fail(MM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
-}
-
-// Matrices of at most 2^40 elements: their byte counts and the kernels' grids
-// then stay in range (and the memory of any device is smaller).
-static bool too_large(int64_t rows, int64_t cols) { return (double)rows * (double)cols > 1099511627776.0; }
-
-// Sizes and pitches, rounded up to whole chunks, are 32-bit in the kernels.
-constexpr int64_t kMaxSize = (int64_t)INT32_MAX - 64;
-
-// A launch has at most 2^32 - 1 threads.
-static bool launchable(double wgs, int threads) { return wgs * threads < 4294967296.0; }
-
-// Whether an entry's grid for `batch` products of M x cols can be launched.
-// Operands that are not 16-byte aligned run entry 1 in entry 0's place: four
-// times its workgroups, of half its size.
-static bool tile_launchable(const FfnChoice &c, int64_t batch, int64_t M, int64_t cols) {
-    const FfnTile &t = kFfnTiles[c.tile];
-    const double wgs = (double)batch * (double)cdiv(M, t.bm) * (double)cdiv(cols, t.bn) * c.split;
-    return launchable(c.tile == 0 ? 4.0 * wgs : wgs, c.tile <= 1 ? 256 : 512);
-}
-
-// The same for kernels of 256 threads that take `pieces` of each of M rows: the
-// joining of partial sums (four columns a thread) and the backward pass's
-// element-wise part.
-static bool pieces_launchable(int64_t M, int64_t pieces) {
-    return launchable(ceil((double)M * (double)pieces / 256.0), 256);
-}
-
-static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
 
 // Time model of the tiled products: a CU runs up to kOcc workgroups of an
 // entry together, and a round of o workgroups per CU takes kFixed + kStep[o - 1]
@@ -53,7 +16,6 @@ static bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == 
 // 512 workgroups, 1 and 8 KiB of K, over the forward, dX, dW and INT8 kinds,
 // which lie within 10 % of each other; rows that are not 16-byte aligned run
 // the register-staged form (entry 0 has none and runs entry 1's).
-enum { kClass16 = 0, kClass8 = 1, kClass32 = 2 };
 static const int kOcc[kNumFfnTiles] = {1, 2, 2, 1, 1};
 static const double kLaunch = 2.5;                                      // us
 static const double kFixed[kNumFfnTiles] = {7.5, 3.2, 2.5, 1.4, 5.5};  // us
@@ -65,7 +27,7 @@ static const double kStep[2][3][kNumFfnTiles][2] = {                    // us: a
      {{1e9, 0}, {0.23, 0.305}, {0.122, 0.182}, {0.080, 0}, {0.310, 0}},
      {{1e9, 0}, {0.60, 1.050}, {0.355, 0.585}, {0.171, 0}, {1e9, 0}}}};
 
-static int type_class(int dtype) { return dtype == MM_FLOAT ? kClass32 : dtype == MM_INT8 ? kClass8 : kClass16; }
+int type_class(int dtype) { return dtype == MM_FLOAT ? kClass32 : dtype == MM_INT8 ? kClass8 : kClass16; }
 
 static double est_us(int cls, bool aligned, int tile, double wgs, double steps) {
     const double *step = kStep[aligned ? 0 : 1][cls][tile];
@@ -85,7 +47,7 @@ static double est_us(int cls, bool aligned, int tile, double wgs, double steps) 
 // gated block's workgroups of 32 columns take as long again where a CU has
 // two, those of 16 longer the more of them share the cache lines.  Rows (of
 // `row` bytes) off 4-byte alignment cost 16-bit types more.
-static double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, int64_t row, double wbytes) {
+double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, int64_t row, double wbytes) {
     static const double kChain[3][2] = {{1.0, 1.75}, {0.6, 1.2}, {1.2, 1.85}}, kRate[3][2] = {{4.9, 3.2}, {3.5, 2.2}, {4.9, 3.2}};
     static const double kChain8[3][2] = {{2.0, 2.45}, {1.5, 2.0}, {1.35, 1.75}}, kRate8[3][2] = {{5.0, 4.4}, {4.5, 4.0}, {3.5, 3.0}};
     const int r = M > 16 ? 1 : 0;
@@ -102,10 +64,14 @@ static double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, in
     return 3.0 + chain * kib * (odd ? 1.25 : 1.0);
 }
 
+double linear_rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, int64_t row, double wbytes) {
+    return rows_us(cls, nk, M, N, kbytes, row, wbytes);
+}
+
 // The tiles' time over the same few rows: the weights stream at kStream
 // TB/s at best ([K, N] ones at 0.72 of it in the register-staged form, at half
 // with rows off 4-byte alignment), and a second launch follows a split.
-static double tiles_us(int cls, const FfnChoice &c, bool nk, bool aligned, int64_t row, double wbytes) {
+double tiles_us(int cls, const FfnChoice &c, bool nk, bool aligned, int64_t row, double wbytes) {
     static const double kStream[3] = {4.0, 2.7, 4.0};
     const double part = aligned || nk ? 1.0 : row % 4 == 0 ? 0.72 : 0.5;
     return std::max(c.us + (c.split > 1 ? 3.0 : 0.0), wbytes / (kStream[cls] * part * 1e6));
@@ -115,7 +81,7 @@ static double tiles_us(int cls, const FfnChoice &c, bool nk, bool aligned, int64
 // [M, cols] over `kbytes` bytes of K (terms: that many times in one K loop;
 // cols counts gate and up columns).  Partials cost their write, read and a
 // launch.
-static FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t cols, int64_t kbytes, int terms,
+FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t cols, int64_t kbytes, int terms,
                         unsigned tiles, bool may_split) {
     FfnChoice best;
     double top = 1e30;
@@ -144,14 +110,14 @@ static FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t
 }
 
 // A requested number of partitions for an entry, as whole stages.
-static void set_split(FfnChoice *c, int64_t kbytes, int terms, int64_t split) {
+void set_split(FfnChoice *c, int64_t kbytes, int terms, int64_t split) {
     const int64_t stages = std::max<int64_t>(1, terms * cdiv(kbytes, kFfnTiles[c->tile].bkb));
     const int64_t per = cdiv(stages, std::max<int64_t>(1, std::min<int64_t>({split, stages, 4096})));
     c->kstages = (int32_t)per;
     c->split = (int32_t)cdiv(stages, per);
 }
 
-static mm_status tile_option(const mm_plan_options *opt, int *tile) {
+mm_status tile_option(const mm_plan_options *opt, int *tile) {
     const int req = opt ? opt->tile : 0;
     if (req == 0) return MM_OK;
     if (req < 0 || req > kNumFfnTiles)
@@ -162,7 +128,7 @@ static mm_status tile_option(const mm_plan_options *opt, int *tile) {
 
 // A backward product's entry and split: the requested ones, the time model's
 // where they are 0.
-static mm_status choose_backward(const char *name, int cls, bool aligned, int64_t batch, int64_t M, int64_t cols,
+mm_status choose_backward(const char *name, int cls, bool aligned, int64_t batch, int64_t M, int64_t cols,
                                  int64_t kbytes, int terms, unsigned tiles, int treq, int sreq, FfnChoice *c) {
     if (treq < 0 || treq > kNumFfnTiles)
         return fail(MM_ERR_BAD_OPTION, "%s tile %d out of range 1..%d", name, treq, kNumFfnTiles);
@@ -178,7 +144,7 @@ static mm_status choose_backward(const char *name, int cls, bool aligned, int64_
 
 // Options that a forced algorithm would drop: partitions of the unsplit ones,
 // a tile entry of the few-row kernel.
-static mm_status forced_alone(const mm_plan_options *opt) {
+mm_status forced_alone(const mm_plan_options *opt) {
     if (!opt) return MM_OK;
     const bool rows = opt->force_algo == MM_ALGO_SKINNY_M;
     if ((rows || opt->force_algo == MM_ALGO_GENERAL) && opt->split_k > 1)
