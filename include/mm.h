@@ -577,6 +577,106 @@ mm_status mm_linear_execute(mm_plan_t plan, const void *X, const void *W, const 
 mm_status mm_linear_backward(mm_plan_t plan, const void *X, const void *x_scale, const void *W, const void *Z,
                              const void *z_scale, const void *dY, void *dX, void *dW, void *dbias, void *stream);
 
+/* Norms before and after a block, fused with its gate and residual scale: a
+ * row operator beside mm_quantize_rows, on both sides of the layers above.
+ * With X (the residual stream) and B (the block's output) [rows, cols],
+ *
+ *   n1 = post_norm(B) * post_weight + post_bias    (or B)
+ *   R  = X + residual_scale * gate * n1            (sum; or X)
+ *   Y  = pre_norm(R) * pre_weight + pre_bias       (out; absent without pre_norm)
+ *
+ * where a norm of a row v is v * r, r = 1 / sqrt(mean(v^2) + eps) (MM_NORM_RMS), or
+ * (v - mean(v)) * r, r = 1 / sqrt(var(v) + eps) (MM_NORM_LAYER), and gate is absent (1)
+ * or [ceil(rows / gate_rows), cols]: row m takes gate row m / gate_rows (one
+ * gate for everything, for each sequence, or with gate_rows 1 for each token).
+ * The backward pass, from dY = dout and dsum, the gradient that reaches R along the
+ * residual stream (x1, x2 are the normalised rows of B and R):
+ *
+ *   d2 = dY * pre_weight          dR  = dsum + r2 (d2 - [mean(d2)] - x2 mean(d2 x2))
+ *   dX = dR                       dn1 = residual_scale * gate * dR
+ *   dgate = residual_scale * sum over its rows of dR n1
+ *   d1 = dn1 * post_weight        dB  = r1 (d1 - [mean(d1)] - x1 mean(d1 x1))   (or dn1)
+ *   dpre_weight = sum dY x2, dpre_bias = sum dY, dpost_weight = sum dn1 x1, dpost_bias = sum dn1
+ *
+ * ([..]: layer norm only).  Everything has the plan's type (FLOAT, FLOAT16 or
+ * BFLOAT16) and is dense; statistics and sums are FP32, every result is
+ * rounded once (Y is formed from the R before its rounding).  Infinities and
+ * NaN stay in their rows (and in sums over them).  Results do not vary from run
+ * to run.  cols is at most MM_NORM_MAX_COLS.
+ *
+ * Training plans: the forward pass writes `stats`, FP32 [rows, 4]: mean and r of
+ * B's norm, mean and r of R's (0 and 1 where there is none).  kept_type says
+ * what the backward pass is given of R and B: the tensors; (MM_FLOAT) the FP32 R
+ * before its rounding, which the forward pass then writes to sum_f32 (in
+ * 16-bit types R's rounding else makes dpre_weight off by 1.4 times its own
+ * rounding), and B; or (MM_INT8) their checkpoints, whose values then take
+ * their places in the formulas, with the statistics as they were.  The
+ * forward pass forms checkpoints of R, B and Y (of what it writes or reads,
+ * that is of the rounded R and Y) in the same launch. */
+#define MM_NORM_NONE 0
+#define MM_NORM_RMS 1
+#define MM_NORM_LAYER 2
+#define MM_NORM_MAX_COLS 16384
+
+typedef struct mm_norm_desc {
+    int64_t rows, cols;
+    int64_t gate_rows;       /* 0: no gate */
+    int32_t post_norm, pre_norm; /* MM_NORM_*; not both MM_NORM_NONE */
+    float post_eps, pre_eps; /* not negative */
+    float residual_scale;
+    int32_t has_block;       /* 1; 0: R = X, no post_norm, no gate (a plain norm of X) */
+    int32_t post_weight, post_bias, pre_weight, pre_bias; /* 0 or 1 */
+    int32_t training;        /* 1: the plan owns the backward pass's workspace */
+    int32_t kept_type;       /* training: 0, the plan's type, MM_FLOAT or MM_INT8 */
+    int32_t reserved;        /* must be 0 */
+} mm_norm_desc;
+
+/* Operands of the forward pass.  Required: residual, block of a plan that has
+ * one, the gate, weights and biases that it has (and no others), out of a plan
+ * with pre_norm.  Others may be NULL: sum (R is not written); of a training
+ * plan, stats and pairs of checkpoint buffers; sum_f32, of one with kept_type
+ * MM_FLOAT. */
+typedef struct mm_norm_forward_args {
+    const void *residual, *block, *gate, *post_weight, *post_bias, *pre_weight, *pre_bias;
+    void *sum, *out;
+    float *stats;
+    float *sum_f32;
+    void *sum_q, *sum_scale, *block_q, *block_scale, *out_q, *out_scale;
+} mm_norm_forward_args;
+
+/* Operands of the backward pass.  Required: stats; sum with pre_norm; block
+ * with post_norm, and with a gate where dgate is wanted; the gate and weights
+ * that the plan has (post_bias where dgate is wanted); dout with pre_norm, dsum
+ * without (else NULL: none); sum_scale and block_scale with checkpoints (sum is
+ * FP32 with kept_type MM_FLOAT).  Each
+ * result may be NULL; what is computed is written, not added. */
+typedef struct mm_norm_backward_args {
+    const float *stats;
+    const void *sum, *sum_scale, *block, *block_scale;
+    const void *gate, *post_weight, *post_bias, *pre_weight;
+    const void *dout, *dsum;
+    void *dresidual, *dblock, *dgate, *dpost_weight, *dpost_bias, *dpre_weight, *dpre_bias;
+} mm_norm_backward_args;
+
+/* Create a norm plan.  MM_ERR_NEG_DIM, MM_ERR_DTYPE, MM_ERR_BAD_OPTION (an
+ * invalid field), MM_ERR_TOO_LARGE (cols, rows of 2^31 - 64 or more, more than
+ * 2^40 elements), MM_ERR_ALLOC.  A training plan owns a
+ * workspace, allocated and bound to a device as described above: its backward
+ * passes must not overlap.  The plan answers the introspection calls (output
+ * shape [rows, cols]). */
+mm_status mm_norm_plan_create(const mm_norm_desc *desc, int dtype, mm_plan_t *out);
+
+/* Enqueue the forward pass on `stream`.  sum may be the residual and out the
+ * block (in place); otherwise no output may overlap an input or another
+ * output.  MM_ERR_NULL_ARG: an operand is missing; MM_ERR_BAD_OPTION: one is
+ * given that the plan does not have. */
+mm_status mm_norm_execute(mm_plan_t plan, const mm_norm_forward_args *args, void *stream);
+
+/* Enqueue the backward pass of a training plan on `stream`.  dresidual may be
+ * dsum and dblock dout (in place); otherwise no output may overlap an input or
+ * another output.  rows == 0 writes zero gradients of weights and biases. */
+mm_status mm_norm_backward(mm_plan_t plan, const mm_norm_backward_args *args, void *stream);
+
 /* Output shape: writes up to MM_MAX_RANK entries to `shape` and the rank to
  * *rank (0 when both inputs are rank one). */
 mm_status mm_plan_output_shape(mm_plan_t plan, int64_t *shape, int *rank);

@@ -23,6 +23,8 @@ ACT_NONE = 0
 ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SIGMOID = 1, 2, 3, 4, 5
 ACTIVATIONS = {"silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "relu": ACT_RELU,
                "sigmoid": ACT_SIGMOID}
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+NORM_MAX_COLS = 16384
 MAX_BATCH_DIMS = 8
 MAX_RANK = MAX_BATCH_DIMS + 2
 
@@ -98,6 +100,28 @@ class LinearDesc(ctypes.Structure):
                 ("z_type", ctypes.c_int32), ("x_type", ctypes.c_int32), ("x_activation", ctypes.c_int32),
                 ("dx_tile", ctypes.c_int32), ("dx_split_k", ctypes.c_int32), ("dw_tile", ctypes.c_int32),
                 ("dw_split_k", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+                ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32), ("post_eps", ctypes.c_float),
+                ("pre_eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("has_block", ctypes.c_int32),
+                ("post_weight", ctypes.c_int32), ("post_bias", ctypes.c_int32), ("pre_weight", ctypes.c_int32),
+                ("pre_bias", ctypes.c_int32), ("training", ctypes.c_int32), ("kept_type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class NormForwardArgs(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("residual", "block", "gate", "post_weight", "post_bias", "pre_weight", "pre_bias", "sum", "out",
+                 "stats", "sum_f32", "sum_q", "sum_scale", "block_q", "block_scale", "out_q", "out_scale")]
+
+
+class NormBackwardArgs(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("stats", "sum", "sum_scale", "block", "block_scale", "gate", "post_weight", "post_bias", "pre_weight",
+                 "dout", "dsum", "dresidual", "dblock", "dgate", "dpost_weight", "dpost_bias", "dpre_weight",
+                 "dpre_bias")]
 
 
 _lib = None
@@ -192,6 +216,12 @@ def lib() -> ctypes.CDLL:
         L.mm_linear_execute.restype = ctypes.c_int
         L.mm_linear_backward.argtypes = [vp] * 11
         L.mm_linear_backward.restype = ctypes.c_int
+        L.mm_norm_plan_create.argtypes = [ctypes.POINTER(NormDesc), ctypes.c_int, ctypes.POINTER(vp)]
+        L.mm_norm_plan_create.restype = ctypes.c_int
+        L.mm_norm_execute.argtypes = [vp, ctypes.POINTER(NormForwardArgs), vp]
+        L.mm_norm_execute.restype = ctypes.c_int
+        L.mm_norm_backward.argtypes = [vp, ctypes.POINTER(NormBackwardArgs), vp]
+        L.mm_norm_backward.restype = ctypes.c_int
         L.mm_status_string.argtypes = [ctypes.c_int]
         L.mm_status_string.restype = ctypes.c_char_p
         L.mm_last_error.argtypes = []
@@ -881,6 +911,100 @@ class LinearPlan(Plan):
                 None if dbias is None else _dense("dbias", dbias, dt, self._b, dev))
         with self._lock:
             _run(dev, stream, self._backward, self._handle, *ptrs)
+
+
+class NormPlan(Plan):
+    """mm_norm_plan_create / mm_norm_execute / mm_norm_backward: the norms on
+    both sides of a block's end, fused with its gate and residual scale,
+
+        sum = X + residual_scale * gate * n1,  n1 = post(block) * post_weight + post_bias (post NORM_NONE: block)
+        out = pre(sum) * pre_weight + pre_bias                                             (pre NORM_NONE: none)
+
+    and their gradients.  block=False: sum is X, out its norm.  gate_rows: row m
+    takes gate row m // gate_rows (0: no gate).  kept_type: the backward pass is
+    given sum and block (0), sum in FP32 as the forward pass kept it in sum_f32
+    (FLOAT), or checkpoints of both (INT8)."""
+
+    def __init__(self, rows: int, cols: int, dtype: int, pre: int = NORM_RMS, post: int = NORM_NONE, block: bool = True,
+                 pre_weight: bool = True, pre_bias: bool = False, post_weight: bool = False, post_bias: bool = False,
+                 gate_rows: int = 0, residual_scale: float = 1.0, pre_eps: float = 1e-6, post_eps: float = 1e-6,
+                 training: bool = False, kept_type: int = 0):
+        import torch
+
+        L = lib()
+        self._handle = ctypes.c_void_p()
+        self.dtype, self.rows, self.cols = int(dtype), int(rows), int(cols)
+        self.training, self.pre, self.post, self.block = bool(training), int(pre), int(post), bool(block)
+        desc = NormDesc(self.rows, self.cols, int(gate_rows), self.post, self.pre, post_eps, pre_eps, residual_scale,
+                        int(self.block), int(post_weight), int(post_bias), int(pre_weight), int(pre_bias),
+                        int(self.training), int(kept_type), 0)
+        _check(L.mm_norm_plan_create(ctypes.byref(desc), self.dtype, ctypes.byref(self._handle)))
+        self._lock = threading.Lock()
+        self._dt, self._f32 = torch_dtype(self.dtype), torch.float32
+        self._kept8 = int(kept_type) == INT8
+        self._sum_dt = self._f32 if int(kept_type) == FLOAT else self._dt
+        self._x = torch.Size((self.rows, self.cols))
+        self._w = torch.Size((self.cols,))
+        self._g = torch.Size((-(-self.rows // gate_rows), self.cols)) if gate_rows else None
+        self._stats = torch.Size((self.rows, 4))
+        self._execute, self._backward = L.mm_norm_execute, L.mm_norm_backward
+
+    def _one(self, name, t, dev, shape):
+        return None if t is None else _dense(name, t, self._dt, shape, dev)
+
+    def _gate(self, name, t, dev):
+        if t is not None and self._g is None:
+            raise ValueError(f"{name}: the plan has no gate")
+        return self._one(name, t, dev, self._g)
+
+    def _pair(self, name, pair, dev):
+        return (None, None) if pair is None else _checkpoint(name, pair[0], pair[1], self._x, dev)
+
+    def execute(self, X, out=None, block=None, sum=None, gate=None, pre_weight=None, pre_bias=None, post_weight=None,
+                post_bias=None, stats=None, sum_f32=None, sum_checkpoint=None, block_checkpoint=None,
+                out_checkpoint=None, stream=None) -> None:
+        """The forward pass into sum (None: not written) and out.  A training
+        plan's stats (FP32 [rows, 4]) and sum_f32 or checkpoints, pairs (q,
+        scale), keep what the backward pass needs.  sum may be X itself, out the block."""
+        dev = _device_of(X)
+        x, w = self._x, self._w
+        args = NormForwardArgs(
+            _dense("X", X, self._dt, x, dev), self._one("block", block, dev, x), self._gate("gate", gate, dev),
+            self._one("post_weight", post_weight, dev, w), self._one("post_bias", post_bias, dev, w),
+            self._one("pre_weight", pre_weight, dev, w), self._one("pre_bias", pre_bias, dev, w),
+            self._one("sum", sum, dev, x), self._one("out", out, dev, x),
+            None if stats is None else _dense("stats", stats, self._f32, self._stats, dev),
+            None if sum_f32 is None else _dense("sum_f32", sum_f32, self._f32, x, dev),
+            *self._pair("sum_checkpoint", sum_checkpoint, dev), *self._pair("block_checkpoint", block_checkpoint, dev),
+            *self._pair("out_checkpoint", out_checkpoint, dev))
+        with self._lock:
+            _run(dev, stream, self._execute, self._handle, args)
+
+    def backward(self, stats, sum=None, block=None, dout=None, dsum=None, gate=None, pre_weight=None, post_weight=None,
+                 post_bias=None, dX=None, dblock=None, dgate=None, dpre_weight=None, dpre_bias=None, dpost_weight=None,
+                 dpost_bias=None, stream=None) -> None:
+        """The backward pass into those results that are given (overwritten).
+        sum and block are tensors, or pairs (q, scale) with kept_type INT8.  dX may
+        be dsum itself, dblock dout."""
+        dev = _device_of(stats)
+        x, w = self._x, self._w
+
+        def kept(name, t, dt):
+            if self._kept8:
+                return self._pair(name, t, dev)
+            return None if t is None else _dense(name, t, dt, x, dev), None
+
+        args = NormBackwardArgs(
+            _dense("stats", stats, self._f32, self._stats, dev), *kept("sum", sum, self._sum_dt),
+            *kept("block", block, self._dt),
+            self._gate("gate", gate, dev), self._one("post_weight", post_weight, dev, w),
+            self._one("post_bias", post_bias, dev, w), self._one("pre_weight", pre_weight, dev, w),
+            self._one("dout", dout, dev, x), self._one("dsum", dsum, dev, x), self._one("dX", dX, dev, x),
+            self._one("dblock", dblock, dev, x), self._gate("dgate", dgate, dev),
+            self._one("dpost_weight", dpost_weight, dev, w), self._one("dpost_bias", dpost_bias, dev, w),
+            self._one("dpre_weight", dpre_weight, dev, w), self._one("dpre_bias", dpre_bias, dev, w))
+        with self._lock:
+            _run(dev, stream, self._backward, self._handle, args)
 
 
 _plan_cache = {}

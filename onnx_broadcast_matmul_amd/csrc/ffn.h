@@ -193,16 +193,13 @@ struct LinearPrep {
 hipError_t launch_linear_prep(int dtype, const LinearPrep &a, hipStream_t s);
 int64_t linear_prep_blocks(const LinearPrep &a, int dtype);
 
-// out[j][n] = sum over p of part[p * stride + j * ldp + n], n < N, j < jobs, in
-// order of p within each of 32 slices and then of the slices; ldp and stride are
-// multiples of four.  NULL out[j]: job left out.
-constexpr int kJoinJobs = 5;
+// out[n] = sum over p < P of part[p * ldp + n], n < N; ldp is a multiple of four.
 struct JoinArgs {
     const float *part;
-    int64_t P, stride, ldp, N;
-    void *out[kJoinJobs];
+    int64_t P, ldp, N;
+    void *out;
 };
-hipError_t launch_join(int dtype, const JoinArgs &a, int jobs, hipStream_t s);
+hipError_t launch_join(int dtype, const JoinArgs &a, hipStream_t s);
 
 // Checkpoints (the format stands in checkpoint.h).
 hipError_t launch_checkpoint_pack(int dtype, const void *X, int64_t rows, int64_t cols, void *q, void *scale, hipStream_t s);

@@ -7,6 +7,7 @@
 #include "checkpoint.h"
 #include "device.h"
 #include "ffn.h"
+#include "join.h"
 #include "pieces.h"
 
 namespace mm {
@@ -143,7 +144,6 @@ __global__ __launch_bounds__(256) void k_linear_prep(LinearPrep a, uint32_t prep
 #pragma unroll
         for (int e = 0; e < VE; ++e) sum[e] = 0.0f;
         if (col < a.ldz) {
-#pragma unroll 2
             for (int64_t row = rb * kPrepRows + r; row < end; row += 8) {
                 S h[VE];
                 const uint4 hv = row_piece<S>((GlobalPtr<S>)((const S *)a.dY + row * a.N + col), left, a.N >= VE);
@@ -248,7 +248,7 @@ template <int DT>
 static hipError_t prep(const LinearPrep &a, hipStream_t s) {
     const int64_t g = linear_prep_blocks(a, DT);
     if (g <= 0) return hipSuccess;
-    if (g > 0x7fffff) return hipErrorInvalidValue;
+    if (g > 0xffffff) return hipErrorInvalidValue;
     const dim3 gr((unsigned)g), bl(256);
     const uint32_t pz = (uint32_t)prep_z_blocks(a, Elem<DT>::kVE);
     if (!a.dZ) hipLaunchKernelGGL((k_linear_prep<DT, 0>), gr, bl, 0, s, a, pz);
@@ -264,44 +264,20 @@ hipError_t launch_linear_prep(int dtype, const LinearPrep &a, hipStream_t s) {
 
 // ---- column sums
 
-// A workgroup joins 32 columns of one job: eight threads of four columns, 32
-// slices of the partial sums, their results added in slice order.
+// A workgroup joins 32 columns (see join.h).
 template <int DT>
 __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
     using E = Elem<DT>;
-    using S = typename E::S;
-    const int t = threadIdx.x & 7, slice = threadIdx.x >> 3;
     const int64_t c0 = (int64_t)blockIdx.x * 32;
-    S *out = (S *)a.out[blockIdx.y];
-    if (!out) return;
-    __shared__ float part[32][33];
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c0 + t * 4 < a.ldp) {
-        const float *p = a.part + blockIdx.y * a.ldp + c0 + t * 4;
-#pragma unroll 4
-        for (int64_t i = slice; i < a.P; i += 32) {
-            const float4 v = *(const float4 *)(p + i * a.stride);
-            sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
-        }
-    }
-    part[slice][t * 4] = sum.x;
-    part[slice][t * 4 + 1] = sum.y;
-    part[slice][t * 4 + 2] = sum.z;
-    part[slice][t * 4 + 3] = sum.w;
-    __syncthreads();
-    if (threadIdx.x < 32 && c0 + threadIdx.x < a.N) {
-        float v = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) v += part[i][threadIdx.x];
-        out[c0 + threadIdx.x] = E::from_f32(v);
-    }
+    const float v = join_columns(a.P, a.ldp - c0, [&](int64_t i) { return a.part + i * a.ldp + c0; });
+    if (threadIdx.x < 32 && c0 + threadIdx.x < a.N) ((typename E::S *)a.out)[c0 + threadIdx.x] = E::from_f32(v);
 }
 
-hipError_t launch_join(int dtype, const JoinArgs &a, int jobs, hipStream_t s) {
+hipError_t launch_join(int dtype, const JoinArgs &a, hipStream_t s) {
     const int64_t g = (a.N + 31) / 32;
-    if (g <= 0 || jobs <= 0) return hipSuccess;
-    if (g > 0x7fffff || jobs > kJoinJobs) return hipErrorInvalidValue;
-    const dim3 gr((unsigned)g, (unsigned)jobs), bl(256);
+    if (g <= 0) return hipSuccess;
+    if (g > 0xffffff) return hipErrorInvalidValue;
+    const dim3 gr((unsigned)g), bl(256);
     if (dtype == MM_FLOAT) hipLaunchKernelGGL(k_join<MM_FLOAT>, gr, bl, 0, s, a);
     else if (dtype == MM_FLOAT16) hipLaunchKernelGGL(k_join<MM_FLOAT16>, gr, bl, 0, s, a);
     else hipLaunchKernelGGL(k_join<MM_BFLOAT16>, gr, bl, 0, s, a);

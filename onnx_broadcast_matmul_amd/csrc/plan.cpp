@@ -1112,6 +1112,12 @@ mm_status mm_plan_get_info(mm_plan_t p, mm_plan_info *info) {
                            (p->has_residual ? 2.0 : 1.0) * (double)p->M * (double)p->N);
         return MM_OK;
     }
+    if (p->is_norm) {  // forward pass: X, B, R and Y once
+        info->flops = 0.0;
+        info->min_bytes = (double)elem_size(p->dtype) * (double)p->out_numel *
+                          (1.0 + (p->norm.has_block ? 2.0 : 0.0) + (p->norm.pre_norm ? 1.0 : 0.0));
+        return MM_OK;
+    }
     int64_t na = 1, nb = 1;
     for (int i = 0; i < p->a_rank; ++i) na *= p->a_shape[i];
     for (int i = 0; i < p->b_rank; ++i) nb *= p->b_shape[i];

@@ -92,11 +92,15 @@ struct mm_plan_s {
     // holds, at d_off, dZ (with an activation: rows of d_pitch elements), then at
     // x_off the values of an X checkpoint (rows of x_pitch elements), at p_off the
     // column sums of dZ (rows of p_pitch floats), at s_off partial sums.
-    bool is_norm = false;
     bool is_linear = false;
     bool has_residual = false;
     int x_type = 0, x_act = 0;
     int64_t x_pitch = 0, x_off = 0, p_pitch = 0, p_off = 0, s_off = 0;
+
+    // Norm (mm_norm_plan_create): M rows of N columns; a training workspace
+    // holds the backward pass's partial sums.
+    bool is_norm = false;
+    mm_norm_desc norm = {};
 
     // Plan-owned constant B (mm_plan_set_constant_b).
     std::mutex cb_mutex;

@@ -330,10 +330,10 @@ mm_status mm_linear_backward(mm_plan_t p, const void *X, const void *x_scale, co
         JoinArgs j = {};
         j.part = prep.part;
         j.P = cdiv(M, kPrepRows);
-        j.stride = j.ldp = p->p_pitch;
+        j.ldp = p->p_pitch;
         j.N = N;
-        j.out[0] = dbias;
-        st = launched(launch_join(p->dtype, j, 1, s));
+        j.out = dbias;
+        st = launched(launch_join(p->dtype, j, s));
     }
     if (st != MM_OK) return st;
     const void *dZ = act ? (const void *)(ws + p->d_off) : dY;
