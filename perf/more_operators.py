@@ -198,11 +198,13 @@ def _plan(case, st, dev, dt):
                                  post_eps=EPS, pre_weight=True, pre_bias=st["b2"] is not None,
                                  post_weight=st["w1"] is not None, post_bias=st["b1"] is not None,
                                  gate_rows=case["gate_rows"], residual_scale=case["alpha"], training=train,
-                                 kept_type=mm.INT8 if small else 0)
+                                 kept_type=(mm.INT8 if small else mm.FLOAT) if train else 0)
         st["sum"], st["out"] = torch.empty_like(st["x"]), torch.empty_like(st["x"])
         if train:
             st["stats"] = torch.empty(m, 4, dtype=torch.float32, device=dev)
+            # A training step keeps R in 32 bits, as the plain form does, or in 8.
             st["kept"] = (packed(m, n), packed(m, n)) if small else (None, None)
+            st["sum32"] = None if small else torch.empty(m, n, dtype=torch.float32, device=dev)
             like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
             st["grads"] = {name: like(st[of]) for name, of in
                            (("dX", "x"), ("dblock", "block"), ("dgate", "gate"), ("dpre_weight", "w2"),
@@ -251,8 +253,8 @@ def _own_norm(st):
         return {"sum": st["sum"], "out": st["out"]}
     ksum, kblock = st["kept"]
     plan.execute(st["x"], st["out"], block=st["block"], sum=st["sum"], pre_bias=st["b2"], post_bias=st["b1"],
-                 stats=st["stats"], sum_checkpoint=ksum, block_checkpoint=kblock, **args)
-    plan.backward(st["stats"], sum=ksum or st["sum"], block=kblock or st["block"], dout=st["dy"], dsum=st["dr"],
+                 stats=st["stats"], sum_f32=st["sum32"], sum_checkpoint=ksum, block_checkpoint=kblock, **args)
+    plan.backward(st["stats"], sum=ksum or st["sum32"], block=kblock or st["block"], dout=st["dy"], dsum=st["dr"],
                   post_bias=st["b1"], **args, **st["grads"])
     return {"sum": st["sum"], "out": st["out"], **st["grads"]}
 
