@@ -33,22 +33,57 @@ __device__ __forceinline__ float ck_scale(uint32_t ex) {
     return __uint_as_float(ex == 255u ? 0x7fc00000u : (ex > 7u ? ex - 6u : 1u) << 23);
 }
 
-// q as a float.  A block without a scale has 1 / s = 0: its NaNs and infinities
-// must not reach the conversion.
-__device__ __forceinline__ float ck_number(float x, float inv) {
-    return inv == 0.0f ? 0.0f : __builtin_amdgcn_fmed3f(rintf(x * inv), -127.0f, 127.0f);
+// q as a whole number n in FP32, or (ck_word) four of them as bytes, the first
+// lowest.  x / s + 1.5 2^23 is rounded to a whole number, ties to even, whose low
+// byte is n's; the limits apply to that sum.  A block without a scale has
+// 1 / s = 0 and its numbers are 0, whatever it holds.
+constexpr float kCkMagic = 12582912.0f;  // 1.5 2^23
+
+__device__ __forceinline__ float ck_sum(float x, float inv) {
+    return __builtin_amdgcn_fmed3f(fmaf(x, inv, kCkMagic), kCkMagic - 127.0f, kCkMagic + 127.0f);
 }
 
-// Four whole numbers of -128 .. 127 as bytes, the first lowest.
-__device__ __forceinline__ uint32_t pack_bytes(float a, float b, float c, float d) {
-    return ((uint32_t)(int)a & 255u) | ((uint32_t)(int)b & 255u) << 8 | ((uint32_t)(int)c & 255u) << 16 |
-           (uint32_t)(int)d << 24;
+__device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d) {
+    const uint32_t ab = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x0c0c0400u);
+    const uint32_t cd = __builtin_amdgcn_perm(__float_as_uint(d), __float_as_uint(c), 0x04000c0cu);
+    return ab | cd;
+}
+
+__device__ __forceinline__ uint32_t ck_word(float a, float b, float c, float d, float inv) {
+    const uint32_t w = low_bytes(ck_sum(a, inv), ck_sum(b, inv), ck_sum(c, inv), ck_sum(d, inv));
+    return inv == 0.0f ? 0u : w;
 }
 
 // The four numbers of a word of bytes, times s.
 __device__ __forceinline__ void unpack_bytes(uint32_t w, float s, float *x) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = (float)(int)(int8_t)(w >> (8 * e)) * s;
+}
+
+// VE bytes (4 or 8) of a row of n at c; past the end zeros.
+template <int VE>
+__device__ __forceinline__ void ck_load(const int8_t *row, int n, int c, uint32_t *w) {
+    if (c + VE <= n) {
+        __builtin_memcpy(w, row + (uint32_t)c, VE);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < VE / 4; ++i) w[i] = 0;
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+        if (c + e < n) w[e / 4] |= (uint32_t)(uint8_t)row[c + e] << (e % 4 * 8);
+}
+
+// Words of numbers to a row of n at c, as far as it goes.
+template <int VE>
+__device__ __forceinline__ void ck_store(int8_t *row, int n, int c, const uint32_t *w) {
+    if (c + VE <= n) {
+        __builtin_memcpy(row + (uint32_t)c, w, VE);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+        if (c + e < n) row[c + e] = (int8_t)(w[e / 4] >> (e % 4 * 8));
 }
 
 }  // namespace mm

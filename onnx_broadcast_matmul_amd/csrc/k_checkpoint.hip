@@ -7,97 +7,96 @@
 
 namespace mm {
 
-// A thread takes 16 bytes of a row, 32 / VE threads a block.
+// The largest magnitude of a piece.  16-bit types order as their bits do.
+template <int DT>
+__device__ __forceinline__ uint32_t piece_top(const uint4 &v) {
+    if constexpr (DT == MM_FLOAT) {
+        return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+    } else {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        auto mag = [](uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7fff7fffu); };
+        const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(mag(v.x), mag(v.y)),
+                                                  __builtin_elementwise_max(mag(v.z), mag(v.w)));
+        return __float_as_uint(Elem<DT>::to_f32(m.x > m.y ? m.x : m.y));
+    }
+}
+
+// A thread takes 16 bytes of a row at a time, 32 / VE threads a block.
 template <int DT>
 __global__ __launch_bounds__(256) void k_checkpoint_pack(const void *X, int64_t rows, int64_t cols, int8_t *q, uint8_t *scale) {
     using E = Elem<DT>;
     using S = typename E::S;
     constexpr int VE = E::kVE, TPB = kCkBlock / VE, U = 4;
+    const int n = (int)cols;
     const int64_t nb = (cols + kCkBlock - 1) / kCkBlock, cpr = nb * TPB, total = rows * cpr;
     const int64_t x0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 * U + threadIdx.x;
     uint4 v[U];
-    int64_t row[U], col[U];
+    int64_t row[U];
+    int col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t x = x0 + u * 256;
+        const int64_t x = x0 + u * 256 < total ? x0 + u * 256 : 0;
         row[u] = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
-        col[u] = (x - row[u] * cpr) * VE;
-        v[u] = x < total ? row_piece<S>((GlobalPtr<S>)((const S *)X + row[u] * cols + col[u]), cols - col[u], cols >= VE)
-                         : make_uint4(0, 0, 0, 0);
+        col[u] = (int)(x - row[u] * cpr) * VE;
+        v[u] = edge_load<S>((GlobalPtr<S>)((const S *)X + row[u] * cols), n, col[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        S e[VE];
-        __builtin_memcpy(e, &v[u], 16);
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < VE; ++i) top = max(top, ck_magnitude(E::to_f32(e[i])));
+        if (x0 + u * 256 >= total) break;  // whole blocks
+        v[u] = edge_piece<S>(v[u], n, col[u]);
+        uint32_t top = piece_top<DT>(v[u]);
 #pragma unroll
         for (int d = 1; d < TPB; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-        if (row[u] >= rows) break;  // whole blocks
         const uint32_t ex = ck_exponent(top);
         const float inv = ck_inverse(ex);
+        S e[VE];
+        __builtin_memcpy(e, &v[u], 16);
         uint32_t w[VE / 4];
 #pragma unroll
         for (int i = 0; i < VE / 4; ++i)
-            w[i] = pack_bytes(ck_number(E::to_f32(e[4 * i]), inv), ck_number(E::to_f32(e[4 * i + 1]), inv),
-                              ck_number(E::to_f32(e[4 * i + 2]), inv), ck_number(E::to_f32(e[4 * i + 3]), inv));
-        int8_t *o = q + row[u] * cols + col[u];
-        const int64_t left = cols - col[u];
-        if (left >= VE) __builtin_memcpy(o, w, VE);
-        else
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                if (i < left) o[i] = (int8_t)(w[i / 4] >> (i % 4 * 8));
+            w[i] = ck_word(E::to_f32(e[4 * i]), E::to_f32(e[4 * i + 1]), E::to_f32(e[4 * i + 2]), E::to_f32(e[4 * i + 3]), inv);
+        ck_store<VE>(q + row[u] * cols, n, col[u], w);
         if (col[u] % kCkBlock == 0) scale[row[u] * nb + col[u] / kCkBlock] = (uint8_t)ex;
     }
 }
 
-// A thread takes eight values.
+// A thread takes 16 bytes of results at a time.
 template <int DT>
 __global__ __launch_bounds__(256) void k_checkpoint_unpack(const int8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
                                                            void *X) {
     using E = Elem<DT>;
     using S = typename E::S;
-    constexpr int U = 4;
-    const int64_t nb = (cols + kCkBlock - 1) / kCkBlock, cpr = (cols + 7) / 8, total = rows * cpr;
+    constexpr int U = 4, VE = E::kVE;
+    const int n = (int)cols;
+    const int64_t nb = (cols + kCkBlock - 1) / kCkBlock, cpr = (cols + VE - 1) / VE, total = rows * cpr;
     const int64_t x0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 * U + threadIdx.x;
-    uint32_t w[U][2];
+    uint32_t w[U][VE / 4];
     float s[U];
+    int64_t row[U];
+    int col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t x = x0 + u * 256;
-        w[u][0] = w[u][1] = 0;
-        s[u] = 0.0f;
-        if (x >= total) continue;
-        const int64_t row = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
-        const int64_t col = (x - row * cpr) * 8, left = cols - col;
-        const int8_t *p = q + row * cols + col;
-        if (left >= 8) __builtin_memcpy(w[u], p, 8);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left) w[u][i / 4] |= (uint32_t)(uint8_t)p[i] << (i % 4 * 8);
-        s[u] = ck_scale(scale[row * nb + col / kCkBlock]);
+        const int64_t x = x0 + u * 256 < total ? x0 + u * 256 : 0;
+        row[u] = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
+        col[u] = (int)(x - row[u] * cpr) * VE;
+        ck_load<VE>(q + row[u] * cols, n, col[u], w[u]);
+        s[u] = ck_scale(scale[row[u] * nb + col[u] / kCkBlock]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t x = x0 + u * 256;
-        if (x >= total) break;
-        const int64_t row = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
-        const int64_t col = (x - row * cpr) * 8, left = cols - col;
-        float f[8];
-        unpack_bytes(w[u][0], s[u], f);
-        unpack_bytes(w[u][1], s[u], f + 4);
-        S o[8];
+        if (x0 + u * 256 >= total) break;
+        float f[VE];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = E::from_f32(f[i]);
-        S *y = (S *)X + row * cols + col;
-        if (left >= 8) __builtin_memcpy(y, o, sizeof(o));
+        for (int i = 0; i < VE / 4; ++i) unpack_bytes(w[u][i], s[u], f + 4 * i);
+        S o[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) o[i] = E::from_f32(f[i]);
+        S *y = (S *)X + row[u] * cols + col[u];
+        if (col[u] + VE <= n) __builtin_memcpy(y, o, 16);
         else
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left) y[i] = o[i];
+            for (int i = 0; i < VE; ++i)
+                if (col[u] + i < n) y[i] = o[i];
     }
 }
 
@@ -130,7 +129,8 @@ hipError_t launch_checkpoint_pack(int dtype, const void *X, int64_t rows, int64_
 template <int DT>
 static hipError_t unpack(const void *q, const void *scale, int64_t rows, int64_t cols, void *X, hipStream_t s) {
     dim3 g;
-    if (!grid_of(rows * ((cols + 7) / 8), &g)) return hipErrorInvalidValue;
+    constexpr int VE = Elem<DT>::kVE;
+    if (!grid_of(rows * ((cols + VE - 1) / VE), &g)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_checkpoint_unpack<DT>, g, dim3(256), 0, s, (const int8_t *)q, (const uint8_t *)scale, rows, cols, X);
     return hipGetLastError();
 }

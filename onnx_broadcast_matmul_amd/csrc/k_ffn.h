@@ -597,9 +597,8 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
                             char *dst = trow + ((cl / OV) ^ (rl & (OCPR - 1))) * 16 + (cl % OV) * OS;
                             const AccT &v = acc[i][jbase + j];
                             if constexpr (std::is_same<O, int8_t>::value) {
-                                // Whole numbers of -127 .. 127.
-                                *(uint32_t *)dst = pack_bytes(value(i, j, cl, v[4 * q]), value(i, j, cl + 1, v[4 * q + 1]),
-                                                              value(i, j, cl + 2, v[4 * q + 2]), value(i, j, cl + 3, v[4 * q + 3]));
+                                // A checkpoint's numbers: `value` is the blocks' 1 / s.
+                                *(uint32_t *)dst = ck_word(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], value(i, j));
                             } else if constexpr (std::is_same<O, int32_t>::value) {
                                 *(uint4 *)dst = make_uint4((uint32_t)v[4 * q], (uint32_t)v[4 * q + 1],
                                                            (uint32_t)v[4 * q + 2], (uint32_t)v[4 * q + 3]);
@@ -728,9 +727,9 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
                             inv[i][j] = ck_inverse(ex);
                             const int64_t row = row_of(i), col = n0 + wc * WNP + j * 32;
                             if (kg == 0 && lane < 32 && row < M && col < N)
-                                ((uint8_t *)a.zs())[row * ((N + 31) / 32) + col / 32] = (uint8_t)ex;
+                                ((uint8_t *)a.zs())[row * ((a.ldy + 31) / 32) + col / 32] = (uint8_t)ex;
                         }
-                    emit((int8_t)0, 0, [&](int i, int j, int, float v) { return ck_number(v, inv[i][j]); }, a.G(), a.ldy,
+                    emit((int8_t)0, 0, [&](int i, int j) { return inv[i][j]; }, a.G(), a.ldy,
                          a.kept_vec());
                 }
             } else if (OD != MM_FLOAT && a.kept32()) {

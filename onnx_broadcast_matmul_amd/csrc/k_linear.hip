@@ -59,7 +59,9 @@ __global__ __launch_bounds__(256) void k_linear_reduce(FfnSlim a) {
         auto *y = (typename std::remove_const<typename std::remove_pointer<decltype(v)>::type>::type *)p + at;
         if (n == 4) __builtin_memcpy(y, v, 4 * sizeof(*v));
         else
-            for (int e = 0; e < n; ++e) y[e] = v[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n) y[e] = v[e];
     };
     if (a.G()) {
         if (a.q8()) {
@@ -70,9 +72,9 @@ __global__ __launch_bounds__(256) void k_linear_reduce(FfnSlim a) {
             for (int d = 1; d < 8; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
             const uint32_t ex = ck_exponent(top);
             const float inv = ck_inverse(ex);
+            const uint32_t w = ck_word(z[0], z[1], z[2], z[3], inv);
             int8_t q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = (int8_t)(int)ck_number(z[e], inv);
+            __builtin_memcpy(q, &w, 4);
             put(a.G(), q);
             if (col % 32 == 0) ((uint8_t *)a.zs())[row * nb + col / 32] = (uint8_t)ex;
         } else if (DT != MM_FLOAT && a.kept32()) {
@@ -108,25 +110,8 @@ hipError_t launch_linear_reduce(int dtype, const FfnArgs &a, hipStream_t s) {
 
 // ---- before the backward products
 
-// VE consecutive values of a checkpoint row (q: its first element, `left`
-// elements before its end) as floats; past the end zeros.
-template <int VE>
-__device__ __forceinline__ void ck_read(const int8_t *q, int64_t left, float s, float *x) {
-    uint32_t w[VE / 4];
-    if (left >= VE) __builtin_memcpy(w, q, VE);
-    else {
-#pragma unroll
-        for (int i = 0; i < VE / 4; ++i) w[i] = 0;
-#pragma unroll
-        for (int e = 0; e < VE; ++e)
-            if (e < left) w[e / 4] |= (uint32_t)(uint8_t)q[e] << (e % 4 * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < VE / 4; ++i) unpack_bytes(w[i], s, x + 4 * i);
-}
-
 // Blocks [0, prep_z) form dZ and its column sums: 32 threads along a row, 16
-// bytes each, eight rows at a time, kPrepRows rows.  The blocks behind them turn
+// bytes each, eight rows side by side, `rows` rows.  The blocks behind them turn
 // the checkpoint of X into rows of the products' type.  Memory bounds both.
 template <int DT, int ZT>
 __global__ __launch_bounds__(256) void k_linear_prep(LinearPrep a, uint32_t prep_z) {
@@ -135,65 +120,85 @@ __global__ __launch_bounds__(256) void k_linear_prep(LinearPrep a, uint32_t prep
     constexpr int VE = E::kVE;
     constexpr bool EXACT = DT == MM_FLOAT;
     if (blockIdx.x < prep_z) {
+        using ZE = Elem<ZT == 0 || ZT == MM_INT8 ? DT : ZT>;
+        using ZS = typename ZE::S;
+        constexpr int ZV = ZE::kVE, ZP = ZT == 0 || ZT == MM_INT8 ? 1 : VE / ZV, U = 2;
         const int t = threadIdx.x & 31, r = threadIdx.x >> 5;
         const uint32_t ncb = (uint32_t)((a.ldz + 32 * VE - 1) / (32 * VE));
-        const int64_t rb = blockIdx.x / ncb, col = ((int64_t)(blockIdx.x % ncb) * 32 + t) * VE;
-        const int64_t left = a.N - col, nb = (a.N + 31) / 32;
-        const int64_t end = (rb + 1) * kPrepRows < a.M ? (rb + 1) * kPrepRows : a.M;
+        const int64_t rb = blockIdx.x / ncb;
+        const int N = (int)a.N, col = ((int)(blockIdx.x % ncb) * 32 + t) * VE, nb = (N + 31) / 32;
+        const int64_t end = (rb + 1) * a.rows < a.M ? (rb + 1) * a.rows : a.M;
         float sum[VE];
 #pragma unroll
         for (int e = 0; e < VE; ++e) sum[e] = 0.0f;
-        if (col < a.ldz) {
-            for (int64_t row = rb * kPrepRows + r; row < end; row += 8) {
-                S h[VE];
-                const uint4 hv = row_piece<S>((GlobalPtr<S>)((const S *)a.dY + row * a.N + col), left, a.N >= VE);
-                __builtin_memcpy(h, &hv, 16);
-                float d[VE];
+        if (col < N) {
+            for (int64_t row0 = rb * a.rows + r; row0 < end; row0 += 8 * U) {
+                uint4 hv[U], zv[U][ZP];
+                uint32_t w[U][VE / 4];
+                float sc[U];
 #pragma unroll
-                for (int e = 0; e < VE; ++e) d[e] = E::to_f32(h[e]);
-                if constexpr (ZT != 0) {
-                    float z[VE];
+                for (int u = 0; u < U; ++u) {
+                    const int64_t row = row0 + 8 * u < end ? row0 + 8 * u : row0;
+                    hv[u] = edge_load<S>((GlobalPtr<S>)((const S *)a.dY + row * N), N, col);
                     if constexpr (ZT == MM_INT8) {
-                        const float sc = left > 0 ? ck_scale(((const uint8_t *)a.zs)[row * nb + col / 32]) : 0.0f;
-                        ck_read<VE>((const int8_t *)a.Z + row * a.N + col, left, sc, z);
-                    } else {
-                        using ZE = Elem<ZT>;
-                        using ZS = typename ZE::S;
-                        constexpr int ZV = ZE::kVE;
+                        ck_load<VE>((const int8_t *)a.Z + row * N, N, col, w[u]);
+                        sc[u] = ck_scale(((const uint8_t *)a.zs)[row * nb + col / kCkBlock]);
+                    } else if constexpr (ZT != 0) {
 #pragma unroll
-                        for (int i = 0; i < VE / ZV; ++i) {
-                            ZS v[ZV];
-                            const uint4 p = row_piece<ZS>((GlobalPtr<ZS>)((const ZS *)a.Z + row * a.N + col + i * ZV),
-                                                          left - i * ZV, a.N >= ZV);
-                            __builtin_memcpy(v, &p, 16);
-#pragma unroll
-                            for (int e = 0; e < ZV; ++e) z[i * ZV + e] = ZE::to_f32(v[e]);
-                        }
+                        for (int i = 0; i < ZP; ++i)
+                            zv[u][i] = edge_load<ZS>((GlobalPtr<ZS>)((const ZS *)a.Z + row * N), N, col + i * ZV);
                     }
-                    auto slope = [&](auto kind) {
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            float f, g;
-                            act_grad<decltype(kind)::value, EXACT>(z[e], f, g);
-                            d[e] *= g;
-                        }
-                    };
-                    switch (a.act) {
-                    case MM_ACT_SILU: slope(std::integral_constant<int, MM_ACT_SILU>()); break;
-                    case MM_ACT_GELU: slope(std::integral_constant<int, MM_ACT_GELU>()); break;
-                    case MM_ACT_GELU_TANH: slope(std::integral_constant<int, MM_ACT_GELU_TANH>()); break;
-                    case MM_ACT_RELU: slope(std::integral_constant<int, MM_ACT_RELU>()); break;
-                    default: slope(std::integral_constant<int, MM_ACT_SIGMOID>()); break;
-                    }
-                    S o[VE];
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) o[e] = E::from_f32(e < left ? d[e] : 0.0f);
-                    uint4 ov;
-                    __builtin_memcpy(&ov, o, 16);
-                    *(uint4 *)((S *)a.dZ + row * a.ldz + col) = ov;
                 }
 #pragma unroll
-                for (int e = 0; e < VE; ++e) sum[e] += d[e];
+                for (int u = 0; u < U; ++u) {
+                    const int64_t row = row0 + 8 * u;
+                    if (row >= end) break;
+                    S h[VE];
+                    hv[u] = edge_piece<S>(hv[u], N, col);
+                    __builtin_memcpy(h, &hv[u], 16);
+                    float d[VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) d[e] = E::to_f32(h[e]);
+                    if constexpr (ZT != 0) {
+                        float z[VE];
+                        if constexpr (ZT == MM_INT8) {
+#pragma unroll
+                            for (int i = 0; i < VE / 4; ++i) unpack_bytes(w[u][i], sc[u], z + 4 * i);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < ZP; ++i) {
+                                ZS v[ZV];
+                                const uint4 p = edge_piece<ZS>(zv[u][i], N, col + i * ZV);
+                                __builtin_memcpy(v, &p, 16);
+#pragma unroll
+                                for (int e = 0; e < ZV; ++e) z[i * ZV + e] = ZE::to_f32(v[e]);
+                            }
+                        }
+                        auto slope = [&](auto kind) {
+#pragma unroll
+                            for (int e = 0; e < VE; ++e) {
+                                float f, g;
+                                act_grad<decltype(kind)::value, EXACT>(z[e], f, g);
+                                d[e] *= g;
+                            }
+                        };
+                        switch (a.act) {
+                        case MM_ACT_SILU: slope(std::integral_constant<int, MM_ACT_SILU>()); break;
+                        case MM_ACT_GELU: slope(std::integral_constant<int, MM_ACT_GELU>()); break;
+                        case MM_ACT_GELU_TANH: slope(std::integral_constant<int, MM_ACT_GELU_TANH>()); break;
+                        case MM_ACT_RELU: slope(std::integral_constant<int, MM_ACT_RELU>()); break;
+                        default: slope(std::integral_constant<int, MM_ACT_SIGMOID>()); break;
+                        }
+                        S o[VE];
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) o[e] = E::from_f32(col + e < N ? d[e] : 0.0f);
+                        uint4 ov;
+                        __builtin_memcpy(&ov, o, 16);
+                        *(uint4 *)((S *)a.dZ + row * a.ldz + col) = ov;
+                    }
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) sum[e] += d[e];
+                }
             }
         }
         if (!a.part) return;
@@ -203,7 +208,7 @@ __global__ __launch_bounds__(256) void k_linear_prep(LinearPrep a, uint32_t prep
         __syncthreads();
         const int64_t c0 = (int64_t)(blockIdx.x % ncb) * 32 * VE;
         for (int x = threadIdx.x; x < 32 * VE; x += 256) {
-            if (c0 + x >= a.N) break;
+            if (c0 + x >= N) break;
             float v = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) v += part[i][x / VE][x % VE];
@@ -211,32 +216,45 @@ __global__ __launch_bounds__(256) void k_linear_prep(LinearPrep a, uint32_t prep
         }
         return;
     }
-    const int64_t cpr = a.ldx / VE, nb = (a.K + 31) / 32, total = a.M * cpr;
+    constexpr int U = 4;
+    const int K = (int)a.K, nb = (K + 31) / 32;
+    const int64_t cpr = a.ldx / VE, total = a.M * cpr;
+    uint32_t w[U][VE / 4];
+    float sc[U];
+    int64_t to[U];
+    int col[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t x = ((int64_t)(blockIdx.x - prep_z) * 4 + i) * 256 + threadIdx.x;
-        if (x >= total) return;
+    for (int u = 0; u < U; ++u) {
+        int64_t x = ((int64_t)(blockIdx.x - prep_z) * U + u) * 256 + threadIdx.x;
+        to[u] = x < total ? x * VE : -1;
+        x = x < total ? x : 0;
         const int64_t row = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
-        const int64_t col = (x - row * cpr) * VE, left = a.K - col;
+        col[u] = (int)(x - row * cpr) * VE;
+        ck_load<VE>((const int8_t *)a.xq + row * K, K, col[u], w[u]);
+        sc[u] = ck_scale(((const uint8_t *)a.xs)[row * nb + col[u] / kCkBlock]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (to[u] < 0) break;
         float v[VE];
-        const float sc = left > 0 ? ck_scale(((const uint8_t *)a.xs)[row * nb + col / 32]) : 0.0f;
-        ck_read<VE>((const int8_t *)a.xq + row * a.K + col, left, sc, v);
+#pragma unroll
+        for (int i = 0; i < VE / 4; ++i) unpack_bytes(w[u][i], sc[u], v + 4 * i);
         S o[VE];
         if (a.x_act != MM_ACT_NONE) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) v[e] = act_run<EXACT>(a.x_act, v[e]);
         }
 #pragma unroll
-        for (int e = 0; e < VE; ++e) o[e] = E::from_f32(e < left ? v[e] : 0.0f);
+        for (int e = 0; e < VE; ++e) o[e] = E::from_f32(col[u] + e < K ? v[e] : 0.0f);
         uint4 ov;
         __builtin_memcpy(&ov, o, 16);
-        *(uint4 *)((S *)a.X + row * a.ldx + col) = ov;
+        *(uint4 *)((S *)a.X + to[u]) = ov;
     }
 }
 
 static int64_t prep_z_blocks(const LinearPrep &a, int ve) {
     if (!a.dZ && !a.part) return 0;
-    return (a.M + kPrepRows - 1) / kPrepRows * ((a.ldz + 32 * ve - 1) / (32 * ve));
+    return (a.M + a.rows - 1) / a.rows * ((a.ldz + 32 * ve - 1) / (32 * ve));
 }
 
 int64_t linear_prep_blocks(const LinearPrep &a, int dtype) {

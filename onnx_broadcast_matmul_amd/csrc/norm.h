@@ -24,7 +24,7 @@ struct NormFwdTrain : NormFwd {
 
 // Rows of the backward pass are dealt to workers, `per` consecutive ones each;
 // a worker keeps its columns' sums over them in registers.  part: [workers][jobs]
-// [ldp] floats, the sums of dpost_weight, dpost_bias, dpre_weight, dpre_bias as far
+// [ldp] floats, the sums of dpost_weight, dpre_weight, dpost_bias, dpre_bias as far
 // as they are wanted; gpart: [workers][2][ldp], of dgate for the worker's first and
 // second group of gate rows (NULL: per is a multiple of gate_rows, and every
 // group is finished by one worker).

@@ -51,4 +51,44 @@ __device__ __forceinline__ uint4 row_piece(GlobalPtr<S> p, int64_t left, bool ba
     return v;
 }
 
+// row_piece in two steps, for rows that are read several pieces at a time: the
+// loads of all of them first, without a test (rows of at least a piece: a
+// piece that would pass the row's end ends there), and what the end needs where
+// they are used.  row_piece waits for its piece before the next one is asked for
+// (8192 x 4096 BF16 norms forward: 74.8 us so, 50 in two steps).
+// The offset is 32 bits of bytes, so that a row whose address is uniform takes
+// one register for it.
+template <typename S>
+__device__ __forceinline__ uint4 edge_load(GlobalPtr<S> row, int n, int c) {
+    constexpr int ES = (int)sizeof(S), VE = 16 / ES;
+    using Bytes = const __attribute__((address_space(1))) char *;
+    if (n >= VE) return whole_piece<S>((GlobalPtr<S>)((Bytes)row + (uint32_t)((c < n - VE ? c : n - VE) * ES)));
+    S tmp[VE];  // the whole row
+#pragma unroll
+    for (int e = 0; e < VE; ++e) tmp[e] = e < n ? row[e] : (S)0;
+    uint4 v;
+    __builtin_memcpy(&v, tmp, 16);
+    return v;
+}
+
+// What edge_load read at c of a row of n: the piece, zeros past the end.
+template <typename S>
+__device__ __forceinline__ uint4 edge_piece(uint4 v, int n, int c) {
+    constexpr int ES = (int)sizeof(S), VE = 16 / ES;
+    if (c + VE <= n || (n < VE && c == 0)) return v;
+    const int miss = c + VE - n;
+    uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+    const int sh = miss * ES * 8;
+    if (miss >= VE) {
+        lo = hi = 0;
+    } else if (sh >= 64) {
+        lo = hi >> (sh - 64);
+        hi = 0;
+    } else {
+        lo = lo >> sh | hi << (64 - sh);
+        hi >>= sh;
+    }
+    return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+}
+
 }  // namespace mm

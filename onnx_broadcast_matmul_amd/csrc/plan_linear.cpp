@@ -164,7 +164,7 @@ mm_status mm_linear_plan_create(const mm_linear_desc *d, int dtype, const mm_pla
         p->x_pitch = x8 ? round_up(K, ve) : K;
         p->p_off = p->x_off + (x8 ? round_up(M * p->x_pitch * es, 256) : 0);
         p->p_pitch = round_up(N, 4);
-        p->s_off = p->p_off + (p->has_bias ? round_up(cdiv(M, kPrepRows) * p->p_pitch * 4, 256) : 0);
+        p->s_off = p->p_off + (p->has_bias ? round_up(cdiv(M, linear_prep_rows(M, N, dtype)) * p->p_pitch * 4, 256) : 0);
         // dW's reduction runs over the rows of X; a 16-bit 32-row tile of its
         // transposed operand has rows too short to stage.
         const unsigned dw_tiles = dtype == MM_FLOAT ? 0xe : 0x17;
@@ -181,6 +181,7 @@ mm_status mm_linear_plan_create(const mm_linear_desc *d, int dtype, const mm_pla
         prep.K = K;
         prep.ldz = round_up(N, ve);
         prep.ldx = round_up(K, ve);
+        prep.rows = linear_prep_rows(M, N, dtype);
         if (st == MM_OK &&
             (!tile_launchable(p->dx, 1, M, K) || !tile_launchable(p->dw, 1, wm, wn) ||
              !launchable((double)linear_prep_blocks(prep, dtype), 256) ||
@@ -325,11 +326,12 @@ mm_status mm_linear_backward(mm_plan_t p, const void *X, const void *x_scale, co
     prep.act = p->act;
     prep.z_type = p->kept;
     prep.x_act = p->x_act;
+    prep.rows = linear_prep_rows(M, N, p->dtype);
     mm_status st = launched(launch_linear_prep(p->dtype, prep, s));
     if (st == MM_OK && want_b) {
         JoinArgs j = {};
         j.part = prep.part;
-        j.P = cdiv(M, kPrepRows);
+        j.P = cdiv(M, prep.rows);
         j.ldp = p->p_pitch;
         j.N = N;
         j.out = dbias;

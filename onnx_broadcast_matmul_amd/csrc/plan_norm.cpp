@@ -227,7 +227,7 @@ mm_status mm_norm_backward(mm_plan_t p, const mm_norm_backward_args *b, void *st
     a.pre = (uint8_t)d.pre_norm;
     a.part = (float *)p->ws;
     a.gpart = b->dgate && shared_groups(p, a.per) ? (float *)((char *)p->ws + p->s_off) : nullptr;
-    void *const sums[4] = {b->dpost_weight, b->dpost_bias, b->dpre_weight, b->dpre_bias};
+    void *const sums[4] = {b->dpost_weight, b->dpre_weight, b->dpost_bias, b->dpre_bias};
     for (int k = 0; k < 4; ++k) {
         a.slot[k] = -1;
         if (!sums[k]) continue;
