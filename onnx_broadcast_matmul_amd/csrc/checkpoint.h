@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "pieces.h"
+
 namespace mm {
 
 constexpr int kCkBlock = 32;
@@ -60,11 +62,18 @@ __device__ __forceinline__ void unpack_bytes(uint32_t w, float s, float *x) {
     for (int e = 0; e < 4; ++e) x[e] = (float)(int)(int8_t)(w >> (8 * e)) * s;
 }
 
-// VE bytes (4 or 8) of a row of n at c; past the end zeros.
+// VE bytes (4 or 8) of a row of n at c; past the end zeros.  Checkpoints are
+// streamed through (see pieces.h).
 template <int VE>
 __device__ __forceinline__ void ck_load(const int8_t *row, int n, int c, uint32_t *w) {
     if (c + VE <= n) {
-        __builtin_memcpy(w, row + (uint32_t)c, VE);
+        if constexpr (VE == 4) {
+            w[0] = __builtin_nontemporal_load((const u32u *)(row + (uint32_t)c));
+        } else {
+            const u32x2u v = __builtin_nontemporal_load((const u32x2u *)(row + (uint32_t)c));
+            w[0] = v.x;
+            w[1] = v.y;
+        }
         return;
     }
 #pragma unroll
@@ -78,7 +87,12 @@ __device__ __forceinline__ void ck_load(const int8_t *row, int n, int c, uint32_
 template <int VE>
 __device__ __forceinline__ void ck_store(int8_t *row, int n, int c, const uint32_t *w) {
     if (c + VE <= n) {
-        __builtin_memcpy(row + (uint32_t)c, w, VE);
+        if constexpr (VE == 4) {
+            __builtin_nontemporal_store(w[0], (u32u *)(row + (uint32_t)c));
+        } else {
+            const u32x2u v = {w[0], w[1]};
+            __builtin_nontemporal_store(v, (u32x2u *)(row + (uint32_t)c));
+        }
         return;
     }
 #pragma unroll

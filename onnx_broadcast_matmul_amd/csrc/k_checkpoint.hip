@@ -21,8 +21,27 @@ __device__ __forceinline__ uint32_t piece_top(const uint4 &v) {
     }
 }
 
+// Where piece x (of cpr a row, VE elements each) lies.  FLAT: rows are whole
+// blocks, so they follow each other without a seam and no row is told from the
+// next (the division costs a third of the arithmetic).
+template <bool FLAT, int VE>
+__device__ __forceinline__ void piece_place(int64_t x, int64_t cpr, int64_t cols, int64_t nb, int64_t &row, int &col, int64_t &at,
+                                            int64_t &block) {
+    if constexpr (FLAT) {
+        at = x * VE;
+        block = x / (kCkBlock / VE);
+        row = 0;
+        col = 0;
+    } else {
+        row = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
+        col = (int)(x - row * cpr) * VE;
+        at = row * cols + col;
+        block = row * nb + col / kCkBlock;
+    }
+}
+
 // A thread takes 16 bytes of a row at a time, 32 / VE threads a block.
-template <int DT>
+template <int DT, bool FLAT>
 __global__ __launch_bounds__(256) void k_checkpoint_pack(const void *X, int64_t rows, int64_t cols, int8_t *q, uint8_t *scale) {
     using E = Elem<DT>;
     using S = typename E::S;
@@ -31,19 +50,20 @@ __global__ __launch_bounds__(256) void k_checkpoint_pack(const void *X, int64_t 
     const int64_t nb = (cols + kCkBlock - 1) / kCkBlock, cpr = nb * TPB, total = rows * cpr;
     const int64_t x0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 * U + threadIdx.x;
     uint4 v[U];
-    int64_t row[U];
+    int64_t at[U], block[U];
     int col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t x = x0 + u * 256 < total ? x0 + u * 256 : 0;
-        row[u] = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
-        col[u] = (int)(x - row[u] * cpr) * VE;
-        v[u] = edge_load<S>((GlobalPtr<S>)((const S *)X + row[u] * cols), n, col[u]);
+        int64_t row;
+        piece_place<FLAT, VE>(x, cpr, cols, nb, row, col[u], at[u], block[u]);
+        if constexpr (FLAT) v[u] = stream_piece<S>((GlobalPtr<S>)X + at[u]);
+        else v[u] = edge_load<S, true>((GlobalPtr<S>)((const S *)X + row * cols), n, col[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (x0 + u * 256 >= total) break;  // whole blocks
-        v[u] = edge_piece<S>(v[u], n, col[u]);
+        if constexpr (!FLAT) v[u] = edge_piece<S>(v[u], n, col[u]);
         uint32_t top = piece_top<DT>(v[u]);
 #pragma unroll
         for (int d = 1; d < TPB; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
@@ -55,13 +75,13 @@ __global__ __launch_bounds__(256) void k_checkpoint_pack(const void *X, int64_t 
 #pragma unroll
         for (int i = 0; i < VE / 4; ++i)
             w[i] = ck_word(E::to_f32(e[4 * i]), E::to_f32(e[4 * i + 1]), E::to_f32(e[4 * i + 2]), E::to_f32(e[4 * i + 3]), inv);
-        ck_store<VE>(q + row[u] * cols, n, col[u], w);
-        if (col[u] % kCkBlock == 0) scale[row[u] * nb + col[u] / kCkBlock] = (uint8_t)ex;
+        ck_store<VE>(q + (at[u] - col[u]), FLAT ? VE : n, col[u], w);
+        if (threadIdx.x % TPB == 0) __builtin_nontemporal_store((uint8_t)ex, scale + block[u]);
     }
 }
 
 // A thread takes 16 bytes of results at a time.
-template <int DT>
+template <int DT, bool FLAT>
 __global__ __launch_bounds__(256) void k_checkpoint_unpack(const int8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
                                                            void *X) {
     using E = Elem<DT>;
@@ -72,15 +92,15 @@ __global__ __launch_bounds__(256) void k_checkpoint_unpack(const int8_t *q, cons
     const int64_t x0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 * U + threadIdx.x;
     uint32_t w[U][VE / 4];
     float s[U];
-    int64_t row[U];
+    int64_t at[U];
     int col[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t x = x0 + u * 256 < total ? x0 + u * 256 : 0;
-        row[u] = x < 0x7fffffff ? (int64_t)((uint32_t)x / (uint32_t)cpr) : x / cpr;
-        col[u] = (int)(x - row[u] * cpr) * VE;
-        ck_load<VE>(q + row[u] * cols, n, col[u], w[u]);
-        s[u] = ck_scale(scale[row[u] * nb + col[u] / kCkBlock]);
+        int64_t row, block;
+        piece_place<FLAT, VE>(x, cpr, cols, nb, row, col[u], at[u], block);
+        ck_load<VE>(q + (at[u] - col[u]), FLAT ? VE : n, col[u], w[u]);
+        s[u] = ck_scale(scale[block]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -91,8 +111,10 @@ __global__ __launch_bounds__(256) void k_checkpoint_unpack(const int8_t *q, cons
         S o[VE];
 #pragma unroll
         for (int i = 0; i < VE; ++i) o[i] = E::from_f32(f[i]);
-        S *y = (S *)X + row[u] * cols + col[u];
-        if (col[u] + VE <= n) __builtin_memcpy(y, o, 16);
+        S *y = (S *)X + at[u];
+        uint4 v;
+        __builtin_memcpy(&v, o, 16);
+        if (FLAT || col[u] + VE <= n) stream_store(y, v);
         else
 #pragma unroll
             for (int i = 0; i < VE; ++i)
@@ -112,7 +134,8 @@ template <int DT>
 static hipError_t pack(const void *X, int64_t rows, int64_t cols, void *q, void *scale, hipStream_t s) {
     dim3 g;
     if (!grid_of(rows * ((cols + kCkBlock - 1) / kCkBlock) * (kCkBlock / Elem<DT>::kVE), &g)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_checkpoint_pack<DT>, g, dim3(256), 0, s, X, rows, cols, (int8_t *)q, (uint8_t *)scale);
+    if (cols % kCkBlock == 0) hipLaunchKernelGGL((k_checkpoint_pack<DT, true>), g, dim3(256), 0, s, X, rows, cols, (int8_t *)q, (uint8_t *)scale);
+    else hipLaunchKernelGGL((k_checkpoint_pack<DT, false>), g, dim3(256), 0, s, X, rows, cols, (int8_t *)q, (uint8_t *)scale);
     return hipGetLastError();
 }
 
@@ -131,7 +154,8 @@ static hipError_t unpack(const void *q, const void *scale, int64_t rows, int64_t
     dim3 g;
     constexpr int VE = Elem<DT>::kVE;
     if (!grid_of(rows * ((cols + VE - 1) / VE), &g)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_checkpoint_unpack<DT>, g, dim3(256), 0, s, (const int8_t *)q, (const uint8_t *)scale, rows, cols, X);
+    if (cols % kCkBlock == 0) hipLaunchKernelGGL((k_checkpoint_unpack<DT, true>), g, dim3(256), 0, s, (const int8_t *)q, (const uint8_t *)scale, rows, cols, X);
+    else hipLaunchKernelGGL((k_checkpoint_unpack<DT, false>), g, dim3(256), 0, s, (const int8_t *)q, (const uint8_t *)scale, rows, cols, X);
     return hipGetLastError();
 }
 

@@ -139,14 +139,14 @@ __global__ __launch_bounds__(256) void k_linear_prep(LinearPrep a, uint32_t prep
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int64_t row = row0 + 8 * u < end ? row0 + 8 * u : row0;
-                    hv[u] = edge_load<S>((GlobalPtr<S>)((const S *)a.dY + row * N), N, col);
+                    hv[u] = edge_load<S, true>((GlobalPtr<S>)((const S *)a.dY + row * N), N, col);
                     if constexpr (ZT == MM_INT8) {
                         ck_load<VE>((const int8_t *)a.Z + row * N, N, col, w[u]);
                         sc[u] = ck_scale(((const uint8_t *)a.zs)[row * nb + col / kCkBlock]);
                     } else if constexpr (ZT != 0) {
 #pragma unroll
                         for (int i = 0; i < ZP; ++i)
-                            zv[u][i] = edge_load<ZS>((GlobalPtr<ZS>)((const ZS *)a.Z + row * N), N, col + i * ZV);
+                            zv[u][i] = edge_load<ZS, true>((GlobalPtr<ZS>)((const ZS *)a.Z + row * N), N, col + i * ZV);
                     }
                 }
 #pragma unroll

@@ -75,12 +75,12 @@ __device__ __forceinline__ void piece_floats(const uint4 &v, float *x) {
 }
 
 // The piece of row p (of N columns) at column c, as loaded and as used (see
-// edge_load); NULL and past the end: zeros.
-template <int DT>
+// edge_load); NULL and past the end: zeros.  ONCE: see stream_piece.
+template <int DT, bool ONCE = false>
 __device__ __forceinline__ uint4 piece_load(const void *p, int64_t row, int N, int c) {
     using S = typename Elem<DT>::S;
     if (!p) return make_uint4(0, 0, 0, 0);
-    return edge_load<S>((GlobalPtr<S>)((const S *)p + row * N), N, c);
+    return edge_load<S, ONCE>((GlobalPtr<S>)((const S *)p + row * N), N, c);
 }
 template <int DT>
 __device__ __forceinline__ void piece_use(const uint4 &v, int N, int c, float *x) {
@@ -101,7 +101,9 @@ __device__ __forceinline__ void piece_store(void *p, int64_t row, int N, int c, 
     }
     if (!p) return;
     S *y = (S *)((char *)((S *)p + row * N) + (uint32_t)(c * (int)sizeof(S)));
-    if (c + VE <= N) __builtin_memcpy(y, o, 16);
+    uint4 v;
+    __builtin_memcpy(&v, o, 16);
+    if (c + VE <= N) stream_store(y, v);
     else
 #pragma unroll
         for (int i = 0; i < VE; ++i)
@@ -161,9 +163,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
     int64_t group = -1;
     auto load = [&](int64_t row, uint4 *x, uint4 *b) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) b[i] = piece_load<DT>(a.B, row, N, col(i));
+        for (int i = 0; i < CH; ++i) b[i] = piece_load<DT, true>(a.B, row, N, col(i));
 #pragma unroll
-        for (int i = 0; i < CH; ++i) x[i] = piece_load<DT>(a.X, row, N, col(i));
+        for (int i = 0; i < CH; ++i) x[i] = piece_load<DT, true>(a.X, row, N, col(i));
     };
     // Rows of a workgroup run together: all of them pass the barriers.
     int64_t first = (int64_t)blockIdx.x * SLOTS;
@@ -388,19 +390,19 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_bwd(NormBwd a
         if (row >= r1) return;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            x.dy[i] = piece_load<DT>(a.dY, row, N, col(i));
+            x.dy[i] = piece_load<DT, true>(a.dY, row, N, col(i));
             if constexpr (KEPT8) {
                 kept_load<VE>(a.R, a.rs, row, N, col(i), x.r[i], x.rs[i]);
             } else {
 #pragma unroll
-                for (int k = 0; k < RP; ++k) x.r[i * RP + k] = piece_load<KEPT>(a.R, row, N, col(i) + k * RV);
+                for (int k = 0; k < RP; ++k) x.r[i * RP + k] = piece_load<KEPT, true>(a.R, row, N, col(i) + k * RV);
             }
         }
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            x.ds[i] = piece_load<DT>(a.dS, row, N, col(i));
+            x.ds[i] = piece_load<DT, true>(a.dS, row, N, col(i));
             if constexpr (KEPT8) kept_load<VE>(a.B, a.bs, row, N, col(i), x.b[i], x.bs[i]);
-            else x.b[i] = piece_load<DT>(a.B, row, N, col(i));
+            else x.b[i] = piece_load<DT, true>(a.B, row, N, col(i));
         }
     };
     // Weights as they lie in memory; absent ones count as 1.

@@ -9,11 +9,27 @@ namespace mm {
 template <typename S>
 using GlobalPtr = const __attribute__((address_space(1))) S *;
 
+// Vectors at any address.
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32u __attribute__((aligned(1)));
+
 // 16 bytes at any address: one load.
 template <typename S>
 __device__ __forceinline__ uint4 whole_piece(GlobalPtr<S> p) {
-    typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
     return __builtin_bit_cast(uint4, *(const __attribute__((address_space(1))) u32x4u *)p);
+}
+
+// The same of a tensor that is read once, and stored to one that is written
+// once: past the caches, which then do not turn over for them (8192 x 11008
+// BF16 to a checkpoint and back 111 -> 87 us, a copy of it 5.5 -> 6.2 TB/s).
+template <typename S>
+__device__ __forceinline__ uint4 stream_piece(GlobalPtr<S> p) {
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4u *)p));
+}
+
+__device__ __forceinline__ void stream_store(void *p, const uint4 &v) {
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4u, v), (u32x4u *)p);
 }
 
 // The piece at p of a row that ends `left` elements after p: those elements
@@ -57,12 +73,16 @@ __device__ __forceinline__ uint4 row_piece(GlobalPtr<S> p, int64_t left, bool ba
 // they are used.  row_piece waits for its piece before the next one is asked for
 // (8192 x 4096 BF16 norms forward: 74.8 us so, 50 in two steps).
 // The offset is 32 bits of bytes, so that a row whose address is uniform takes
-// one register for it.
-template <typename S>
+// one register for it.  ONCE: a tensor that is streamed through (see
+// stream_piece).
+template <typename S, bool ONCE = false>
 __device__ __forceinline__ uint4 edge_load(GlobalPtr<S> row, int n, int c) {
     constexpr int ES = (int)sizeof(S), VE = 16 / ES;
     using Bytes = const __attribute__((address_space(1))) char *;
-    if (n >= VE) return whole_piece<S>((GlobalPtr<S>)((Bytes)row + (uint32_t)((c < n - VE ? c : n - VE) * ES)));
+    if (n >= VE) {
+        const GlobalPtr<S> p = (GlobalPtr<S>)((Bytes)row + (uint32_t)((c < n - VE ? c : n - VE) * ES));
+        return ONCE ? stream_piece<S>(p) : whole_piece<S>(p);
+    }
     S tmp[VE];  // the whole row
 #pragma unroll
     for (int e = 0; e < VE; ++e) tmp[e] = e < n ? row[e] : (S)0;
