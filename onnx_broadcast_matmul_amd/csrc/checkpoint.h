@@ -56,10 +56,14 @@ __device__ __forceinline__ uint32_t ck_word(float a, float b, float c, float d, 
     return inv == 0.0f ? 0u : w;
 }
 
-// The four numbers of a word of bytes, times s.
+// The four numbers of a word of bytes, times s (less m, rounded once).
 __device__ __forceinline__ void unpack_bytes(uint32_t w, float s, float *x) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = (float)(int)(int8_t)(w >> (8 * e)) * s;
+}
+__device__ __forceinline__ void unpack_bytes(uint32_t w, float s, float m, float *x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = fmaf((float)(int)(int8_t)(w >> (8 * e)), s, -m);
 }
 
 // VE bytes (4 or 8) of a row of n at c; past the end zeros.  Checkpoints are

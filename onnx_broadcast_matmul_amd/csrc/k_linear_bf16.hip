@@ -1,4 +1,4 @@
-// k_linear_bf16.hip -- the linear layer's tiled products in BFLOAT16.
+// k_linear_bf16.hip -- the linear layer's tiled products for BFLOAT16 (see k_linear.h).
 #include "k_linear.h"
 
 namespace mm {

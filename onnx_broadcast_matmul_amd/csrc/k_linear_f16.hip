@@ -1,4 +1,4 @@
-// k_linear_f16.hip -- the linear layer's tiled products in FLOAT16.
+// k_linear_f16.hip -- the linear layer's tiled products for FLOAT16 (see k_linear.h).
 #include "k_linear.h"
 
 namespace mm {

@@ -1,4 +1,4 @@
-// k_linear_f32.hip -- the linear layer's tiled products in FLOAT.
+// k_linear_f32.hip -- the linear layer's tiled products for FLOAT (see k_linear.h).
 #include "k_linear.h"
 
 namespace mm {

@@ -49,11 +49,12 @@ struct NormJoin {
 
 // Threads that share a row of N columns in the backward pass, and rows that a
 // workgroup takes at once.
-int norm_bwd_threads(int64_t N);
-inline int norm_bwd_rows(int64_t N) {
-    const int t = norm_bwd_threads(N);
-    return t < 256 ? 256 / t : 1;
+inline int norm_bwd_threads(int64_t N) {
+    return N <= 64 * 8 ? 64 : N <= 128 * 8 ? 128 : N <= 256 * 8 ? 256 : N <= 512 * 8 ? 512 : 1024;
 }
+// A wave that has a row to itself shares a workgroup with three others.
+constexpr int norm_bwd_block(int threads) { return threads == 64 ? 256 : threads; }
+inline int norm_bwd_rows(int64_t N) { return norm_bwd_block(norm_bwd_threads(N)) / norm_bwd_threads(N); }
 
 hipError_t launch_norm_fwd(int dtype, bool train, const NormFwdTrain &a, hipStream_t s);
 // kept: what R and B are given in (dtype; MM_FLOAT: R in FP32; MM_INT8: checkpoints).

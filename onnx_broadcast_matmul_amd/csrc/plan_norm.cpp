@@ -14,8 +14,7 @@ namespace mm {
 // which share a worker: as many as fill the GPU with threads, so that the
 // partial sums stay small against the rows.
 static void deal_rows(const mm_plan_s *p, int32_t *per, int32_t *workers) {
-    const int64_t M = p->M, slots = norm_bwd_rows(p->N), threads = norm_bwd_threads(p->N);
-    const int64_t most = (int64_t)kNumCUs * std::max<int64_t>(1, 1024 / std::max<int64_t>(threads, 256)) * slots;
+    const int64_t M = p->M, most = (int64_t)kNumCUs * 1024 / norm_bwd_threads(p->N);
     int64_t n = std::max<int64_t>(1, cdiv(M, most));
     const int64_t gr = p->norm.gate_rows;
     if (gr > 0 && gr <= n) n = round_up(n, gr);
