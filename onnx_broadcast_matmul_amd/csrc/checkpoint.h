@@ -14,6 +14,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "device.h"
 #include "pieces.h"
 
 namespace mm {
@@ -22,6 +25,33 @@ constexpr int kCkBlock = 32;
 constexpr uint32_t kCkFloor = (127u - 100u) << 23;  // 2^-100
 
 __device__ __forceinline__ uint32_t ck_magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// The largest magnitude of 16 bytes of a row.  16-bit types order as their bits do.
+template <int DT>
+__device__ __forceinline__ uint32_t piece_top(const uint4 &v) {
+    if constexpr (DT == MM_FLOAT) {
+        return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
+    } else {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        auto mag = [](uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7fff7fffu); };
+        const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(mag(v.x), mag(v.y)),
+                                                  __builtin_elementwise_max(mag(v.z), mag(v.w)));
+        return __float_as_uint(Elem<DT>::to_f32(m.x > m.y ? m.x : m.y));
+    }
+}
+
+// The largest of a block, of which 32 / VE neighbouring lanes hold VE elements
+// each: within quads, then (four elements a lane) across the two quads.
+template <int VE>
+__device__ __forceinline__ uint32_t block_top(uint32_t top) {
+    auto other = [](uint32_t x, auto ctrl) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xf, 0xf, true);
+    };
+    top = max(top, other(top, std::integral_constant<int, 0xb1>()));  // quad_perm 1 0 3 2
+    top = max(top, other(top, std::integral_constant<int, 0x4e>()));  // quad_perm 2 3 0 1
+    if constexpr (VE == 4) top = max(top, other(top, std::integral_constant<int, 0x141>()));  // row_half_mirror
+    return top;
+}
 
 // The scale byte of a block whose largest magnitude is `top`.
 __device__ __forceinline__ uint32_t ck_exponent(uint32_t top) { return (top > kCkFloor ? top : kCkFloor) >> 23; }

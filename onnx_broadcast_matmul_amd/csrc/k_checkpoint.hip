@@ -7,20 +7,6 @@
 
 namespace mm {
 
-// The largest magnitude of a piece.  16-bit types order as their bits do.
-template <int DT>
-__device__ __forceinline__ uint32_t piece_top(const uint4 &v) {
-    if constexpr (DT == MM_FLOAT) {
-        return max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
-    } else {
-        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-        auto mag = [](uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7fff7fffu); };
-        const u16x2 m = __builtin_elementwise_max(__builtin_elementwise_max(mag(v.x), mag(v.y)),
-                                                  __builtin_elementwise_max(mag(v.z), mag(v.w)));
-        return __float_as_uint(Elem<DT>::to_f32(m.x > m.y ? m.x : m.y));
-    }
-}
-
 // Where piece x (of cpr a row, VE elements each) lies.  FLAT: rows are whole
 // blocks, so they follow each other without a seam and no row is told from the
 // next (the division costs a third of the arithmetic).
@@ -64,10 +50,7 @@ __global__ __launch_bounds__(256) void k_checkpoint_pack(const void *X, int64_t 
     for (int u = 0; u < U; ++u) {
         if (x0 + u * 256 >= total) break;  // whole blocks
         if constexpr (!FLAT) v[u] = edge_piece<S>(v[u], n, col[u]);
-        uint32_t top = piece_top<DT>(v[u]);
-#pragma unroll
-        for (int d = 1; d < TPB; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-        const uint32_t ex = ck_exponent(top);
+        const uint32_t ex = ck_exponent(block_top<VE>(piece_top<DT>(v[u])));
         const float inv = ck_inverse(ex);
         S e[VE];
         __builtin_memcpy(e, &v[u], 16);

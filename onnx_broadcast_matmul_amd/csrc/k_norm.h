@@ -84,8 +84,7 @@ __device__ __forceinline__ uint4 piece_ones() {
     return make_uint4(one, one, one, one);
 }
 
-// The piece of row p (of N columns) at column c, as loaded and as used (see
-// edge_load); NULL and past the end: zeros.  ONCE: see stream_piece.  !EDGE: rows
+// The piece of row p (of N columns) at column c, as loaded (see edge_load); NULL and past the end: zeros.  ONCE: see stream_piece.  !EDGE: rows
 // are whole pieces and c is inside.
 template <int DT, bool ONCE = false, bool EDGE = true>
 __device__ __forceinline__ uint4 piece_load(const void *p, int64_t row, int N, int c) {
@@ -98,54 +97,54 @@ __device__ __forceinline__ uint4 piece_load(const void *p, int64_t row, int N, i
     if (!p) return make_uint4(0, 0, 0, 0);
     return edge_load<S, ONCE>((GlobalPtr<S>)((const S *)p + row * N), N, c);
 }
+// x rounded to the type.
 template <int DT>
-__device__ __forceinline__ void piece_use(const uint4 &v, int N, int c, float *x) {
-    piece_floats<DT>(edge_piece<typename Elem<DT>::S>(v, N, c), x);
-}
-
-// x rounded to the type, in both forms.
-template <int DT, bool EDGE = true>
-__device__ __forceinline__ void piece_store(void *p, int64_t row, int N, int c, const float *x, float *rounded) {
+__device__ __forceinline__ uint4 piece_pack(const float *x) {
     using E = Elem<DT>;
-    using S = typename E::S;
-    constexpr int VE = E::kVE;
-    S o[VE];
+    typename E::S o[E::kVE];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-        o[i] = E::from_f32(x[i]);
-        if (rounded) rounded[i] = E::to_f32(o[i]);
-    }
-    if (!p) return;
-    S *y = (S *)((char *)((S *)p + row * N) + (uint32_t)(c * (int)sizeof(S)));
+    for (int i = 0; i < E::kVE; ++i) o[i] = E::from_f32(x[i]);
     uint4 v;
     __builtin_memcpy(&v, o, 16);
+    return v;
+}
+
+// A piece to row p at column c, as far as the row goes.
+template <int DT, bool EDGE = true>
+__device__ __forceinline__ void piece_store(void *p, int64_t row, int N, int c, const uint4 &v) {
+    using S = typename Elem<DT>::S;
+    constexpr int VE = Elem<DT>::kVE;
+    S *y = (S *)((char *)((S *)p + row * N) + (uint32_t)(c * (int)sizeof(S)));
     if constexpr (!EDGE) {
         if (c < N) stream_store(y, v);
         return;
     }
-    if (c + VE <= N) stream_store(y, v);
-    else
+    if (c + VE <= N) {
+        stream_store(y, v);
+        return;
+    }
+    S o[VE];
+    __builtin_memcpy(o, &v, 16);
 #pragma unroll
-        for (int i = 0; i < VE; ++i)
-            if (c + i < N) y[i] = o[i];
+    for (int i = 0; i < VE; ++i)
+        if (c + i < N) y[i] = o[i];
 }
 
-// The checkpoint of a piece; 32 / VE neighbouring lanes hold a block.
-template <int DT>
-__device__ __forceinline__ void piece_checkpoint(void *q, void *scale, int64_t row, int N, int c, const float *x) {
+// The checkpoint of a piece (zeros past the end); 32 / VE neighbouring lanes
+// hold a block.
+template <int DT, bool EDGE>
+__device__ __forceinline__ void piece_checkpoint(void *q, void *scale, int64_t row, int N, int c, const uint4 &v) {
     constexpr int VE = Elem<DT>::kVE;
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) top = max(top, c + i < N ? ck_magnitude(x[i]) : 0u);
-#pragma unroll
-    for (int d = 1; d < kCkBlock / VE; d *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    const uint32_t ex = ck_exponent(top);
+    const uint32_t ex = ck_exponent(block_top<VE>(piece_top<DT>(v)));
     const float inv = ck_inverse(ex);
+    float x[VE];
+    piece_floats<DT>(v, x);
     uint32_t w[VE / 4];
 #pragma unroll
     for (int i = 0; i < VE / 4; ++i) w[i] = ck_word(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], inv);
-    ck_store<VE>((int8_t *)q + row * N, N, c, w);
-    if (c < N && c % kCkBlock == 0) ((uint8_t *)scale)[row * ((N + 31) / 32) + c / kCkBlock] = (uint8_t)ex;
+    if (c >= N) return;
+    ck_store<VE>((int8_t *)q + row * N, EDGE ? N : c + VE, c, w);
+    if (c % kCkBlock == 0) ((uint8_t *)scale + row * ((N + 31) / 32))[(uint32_t)(c / kCkBlock)] = (uint8_t)ex;
 }
 
 // Keeps pieces as they lie in memory across a loop, and a thread's number: what
@@ -163,46 +162,65 @@ __device__ __forceinline__ void keep_number(int &t) { asm("" : "+v"(t)); }
 
 constexpr int kFwdCols = 16;  // columns of a thread
 
-// A workgroup takes every gridDim-th row (or four, a wave each) and asks for
-// the next one before it works on the present one; 16-bit weights stay in
-// registers as they lie in memory.  The row is the same for a whole wave and
-// kept in scalar registers, its addresses with it.
-template <int DT, int TPR, bool TRAIN>
+// A workgroup takes every gridDim-th row (or four, a wave each); in 16-bit types
+// it asks for the next one before it works on the present one and keeps the
+// weights in registers as they lie in memory.  The row is the same for a whole
+// wave and kept in scalar registers, its addresses with it.  ALL: layer norms,
+// biases and rows that are no whole number of pieces (see k_norm_bwd).
+template <int DT, int TPR, bool TRAIN, bool ALL>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename std::conditional<TRAIN, NormFwdTrain, NormFwd>::type a) {
     constexpr int VE = Elem<DT>::kVE, CH = kFwdCols / VE, NT = TPR < 256 ? 256 : TPR, SLOTS = NT / TPR;
+    constexpr bool HOLD = VE == 8;
     __shared__ float2 part[2][NT / 64];
     RowSums<NT, TPR> sums{part};
     int t = threadIdx.x % TPR;
     const int N = a.N;
     const int slot = TPR == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
-    const int64_t step = (int64_t)gridDim.x * SLOTS;
-    const bool ragged = N < TPR * kFwdCols;  // some columns of the threads are none of the row's
+    const int step = (int)gridDim.x * SLOTS;
+    const bool edge = N % VE != 0, ragged = N < TPR * kFwdCols;
     const float inv_n = 1.0f / (float)N;
     auto col = [&](int i) { return (i * TPR + t) * VE; };
-    constexpr bool HOLD = VE == 8;  // FP32 weights would take too many registers: read again for each row
-    uint4 xr[CH], br[CH], gr[CH], w1[CH], w2[CH];
-    int64_t group = -1;
-    auto load = [&](int64_t row, uint4 *x, uint4 *b) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) b[i] = piece_load<DT, true>(a.B, row, N, col(i));
-#pragma unroll
-        for (int i = 0; i < CH; ++i) x[i] = piece_load<DT, true>(a.X, row, N, col(i));
-    };
-    // Rows of a workgroup run together: all of them pass the barriers.
-    int64_t first = (int64_t)blockIdx.x * SLOTS;
-    auto row_at = [&](int64_t f) { return f + slot < a.M ? f + slot : (int64_t)a.M - 1; };
-    load(row_at(first), xr, br);
-    if constexpr (HOLD) {
+    auto load = [&](int row, uint4 *x, uint4 *b) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            w1[i] = piece_load<DT>(a.w1, 0, N, col(i));
-            w2[i] = piece_load<DT>(a.w2, 0, N, col(i));
+            if (col(i) >= N) continue;  // absent pieces keep the zeros that they begin with
+            if (a.B) b[i] = piece_load<DT, true, ALL>(a.B, row, N, col(i));
+            x[i] = piece_load<DT, true, ALL>(a.X, row, N, col(i));
+        }
+    };
+    auto settle = [&](uint4 *x) {
+        if (!ALL || !edge) return;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (col(i) < N) x[i] = edge_piece<typename Elem<DT>::S>(x[i], N, col(i));
+    };
+    // A weight's piece, `none` where the plan has no such weight.
+    auto weight_or = [&](const uint4 &none, const void *w, int64_t row, int i) {
+        if (!w) return none;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (col(i) < N) {
+            v = piece_load<DT, false, ALL>(w, row, N, col(i));
+            if constexpr (ALL) v = edge_piece<typename Elem<DT>::S>(v, N, col(i));
+        }
+        return v;
+    };
+    // Rows of a workgroup run together: all of them pass the barriers.
+    int first = (int)blockIdx.x * SLOTS;
+    auto row_at = [&](int f) { return f < a.M - slot ? f + slot : a.M - 1; };
+    uint4 xr[CH] = {}, br[CH] = {}, xn[CH] = {}, bn[CH] = {}, gr[CH], w1[CH], w2[CH];
+    if constexpr (HOLD) {
+        load(row_at(first), xn, bn);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            w1[i] = weight_or(piece_ones<DT>(), a.w1, 0, i);
+            w2[i] = weight_or(piece_ones<DT>(), a.w2, 0, i);
+            gr[i] = piece_ones<DT>();
         }
     }
     // Mean and reciprocal deviation of v.
     auto moments = [&](int kind, float eps, const float (*v)[VE]) {
         float mean = 0.0f, s = 0.0f;
-        if (kind == MM_NORM_LAYER) {
+        if (ALL && kind == MM_NORM_LAYER) {
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
@@ -229,50 +247,70 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             float y[VE];
-            if (kind == MM_NORM_LAYER) {
+            if (ALL && kind == MM_NORM_LAYER) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) v[i][e] -= m.x;
             }
+            if constexpr (HOLD) piece_floats<DT>(held[i], y);
+            else piece_floats<DT>(weight_or(piece_ones<DT>(), w, 0, i), y);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) v[i][e] *= m.y;
-            if (w) {
-                piece_use<DT>(HOLD ? held[i] : piece_load<DT>(w, 0, N, col(i)), N, col(i), y);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) v[i][e] *= y[e];
-            }
-            if (b) {
-                piece_use<DT>(piece_load<DT>(b, 0, N, col(i)), N, col(i), y);
+            for (int e = 0; e < VE; ++e) v[i][e] = v[i][e] * m.y * y[e];
+            if (ALL && b) {
+                piece_floats<DT>(weight_or(make_uint4(0, 0, 0, 0), b, 0, i), y);
 #pragma unroll
                 for (int e = 0; e < VE; ++e) v[i][e] += y[e];
             }
         }
     };
+    // Zeros in a row's absent columns, which a mean or a bias has reached.
+    auto cut = [&](float (*v)[VE]) {
+        if (!ALL || !ragged) return;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (col(i) + e >= N) v[i][e] = 0.0f;
+    };
+    int change = 0;  // the row at which the next group of gate rows begins
     for (; first < a.M; first += step) {
-        const bool live = first + slot < a.M;
-        const int64_t row = row_at(first);
         keep_number(t);
         if constexpr (HOLD) {
             keep_packed(w1);
             keep_packed(w2);
+            keep_packed(gr);
         }
-        if (a.gate) keep_packed(gr);
-        uint4 xn[CH], bn[CH];
-        if (first + step < a.M) load(row_at(first + step), xn, bn);
+        const bool live = first < a.M - slot;
+        const int row = row_at(first);
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                xr[i] = xn[i];
+                br[i] = bn[i];
+            }
+            if (first < a.M - step) load(row_at(first + step), xn, bn);
+        } else {
+            load(row, xr, br);
+        }
+        settle(xr);
         float2 m1 = make_float2(0.0f, 1.0f), m2 = m1;
         float v[CH][VE];
         if (a.B) {
-            const int64_t g = a.gate ? row / a.gate_rows : 0;
-            if (g != group) {
-                group = g;
+            settle(br);
+            const int group = a.gate ? (int)((uint32_t)row / (uint32_t)a.gate_rows) : 0;
+            if constexpr (HOLD) {
+                if (a.gate && row >= change) {
+                    const int64_t next = (int64_t)(group + 1) * a.gate_rows;
+                    change = next < a.M ? (int)next : a.M;
 #pragma unroll
-                for (int i = 0; i < CH; ++i) gr[i] = piece_load<DT>(a.gate, g, N, col(i));
+                    for (int i = 0; i < CH; ++i) gr[i] = weight_or(piece_ones<DT>(), a.gate, group, i);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < CH; ++i) piece_use<DT>(br[i], N, col(i), v[i]);
+            for (int i = 0; i < CH; ++i) piece_floats<DT>(br[i], v[i]);
             if constexpr (TRAIN) {
                 if (a.bq && live) {
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) piece_checkpoint<DT>(a.bq, a.bs, row, N, col(i), v[i]);
+                    for (int i = 0; i < CH; ++i) piece_checkpoint<DT, ALL>(a.bq, a.bs, row, N, col(i), br[i]);
                 }
             }
             if (a.post != MM_NORM_NONE) {
@@ -282,64 +320,50 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 float w[VE], x[VE];
-                piece_use<DT>(xr[i], N, col(i), x);
-                if (a.gate) {
-                    piece_use<DT>(gr[i], N, col(i), w);
+                piece_floats<DT>(xr[i], x);
+                if constexpr (HOLD) piece_floats<DT>(gr[i], w);
+                else piece_floats<DT>(weight_or(piece_ones<DT>(), a.gate, group, i), w);
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) v[i][e] *= w[e];
-                }
-#pragma unroll
-                for (int e = 0; e < VE; ++e) v[i][e] = fmaf(a.alpha, v[i][e], x[e]);
-                if (ragged) {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e)
-                        if (col(i) + e >= N) v[i][e] = 0.0f;
-                }
+                for (int e = 0; e < VE; ++e) v[i][e] = fmaf(a.alpha * w[e], v[i][e], x[e]);
             }
+            cut(v);
         } else {
 #pragma unroll
-            for (int i = 0; i < CH; ++i) piece_use<DT>(xr[i], N, col(i), v[i]);
+            for (int i = 0; i < CH; ++i) piece_floats<DT>(xr[i], v[i]);
         }
         if (live) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
+                const uint4 r = piece_pack<DT>(v[i]);
+                if (a.R) piece_store<DT, ALL>(a.R, row, N, col(i), r);
                 if constexpr (TRAIN) {
-                    float r[VE];
-                    piece_store<DT>(a.R, row, N, col(i), v[i], r);
                     if (a.r32) {
 #pragma unroll
                         for (int k = 0; k < VE / 4; ++k)
-                            piece_store<MM_FLOAT>(a.r32, row, N, col(i) + 4 * k, v[i] + 4 * k, nullptr);
+                            if (VE == 4 || col(i) + 4 * k < N)
+                                piece_store<MM_FLOAT, ALL>(a.r32, row, N, col(i) + 4 * k, piece_pack<MM_FLOAT>(v[i] + 4 * k));
                     }
-                    if (a.rq) piece_checkpoint<DT>(a.rq, a.rs, row, N, col(i), r);
-                } else if (a.R) {
-                    piece_store<DT>(a.R, row, N, col(i), v[i], nullptr);
+                    if (a.rq) piece_checkpoint<DT, ALL>(a.rq, a.rs, row, N, col(i), r);
                 }
             }
         }
         if (a.pre != MM_NORM_NONE) {
             m2 = moments(a.pre, a.eps2, v);
             normalise(v, a.pre, m2, a.w2, w2, a.b2);
+            if (TRAIN) cut(v);
             if (live) {
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
+                    const uint4 y = piece_pack<DT>(v[i]);
+                    piece_store<DT, ALL>(a.Y, row, N, col(i), y);
                     if constexpr (TRAIN) {
-                        float r[VE];
-                        piece_store<DT>(a.Y, row, N, col(i), v[i], r);
-                        if (a.yq) piece_checkpoint<DT>(a.yq, a.ys, row, N, col(i), r);
-                    } else {
-                        piece_store<DT>(a.Y, row, N, col(i), v[i], nullptr);
+                        if (a.yq) piece_checkpoint<DT, ALL>(a.yq, a.ys, row, N, col(i), y);
                     }
                 }
             }
         }
         if constexpr (TRAIN) {
-            if (a.stats && live && t == 0) *(float4 *)(a.stats + row * 4) = make_float4(m1.x, m1.y, m2.x, m2.y);
-        }
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            xr[i] = xn[i];
-            br[i] = bn[i];
+            if (a.stats && live && t == 0) *(float4 *)(a.stats + (int64_t)row * 4) = make_float4(m1.x, m1.y, m2.x, m2.y);
         }
     }
 }
@@ -350,8 +374,11 @@ static hipError_t fwd(bool train, const NormFwdTrain &a, hipStream_t s) {
     // As many workgroups as the GPU holds at once.
     const int64_t n = ((int64_t)a.M + SLOTS - 1) / SLOTS, most = (int64_t)kNumCUs * (1024 / NT);
     const dim3 g((unsigned)(n < most ? n : most)), b(NT);
-    if (train) hipLaunchKernelGGL((k_norm_fwd<DT, TPR, true>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((k_norm_fwd<DT, TPR, false>), g, b, 0, s, (const NormFwd &)a);
+    const bool all = a.post == MM_NORM_LAYER || a.pre == MM_NORM_LAYER || a.b1 || a.b2 || a.N % Elem<DT>::kVE != 0;
+    if (train && all) hipLaunchKernelGGL((k_norm_fwd<DT, TPR, true, true>), g, b, 0, s, a);
+    else if (train) hipLaunchKernelGGL((k_norm_fwd<DT, TPR, true, false>), g, b, 0, s, a);
+    else if (all) hipLaunchKernelGGL((k_norm_fwd<DT, TPR, false, true>), g, b, 0, s, (const NormFwd &)a);
+    else hipLaunchKernelGGL((k_norm_fwd<DT, TPR, false, false>), g, b, 0, s, (const NormFwd &)a);
     return hipGetLastError();
 }
 
@@ -504,7 +531,7 @@ __global__ __launch_bounds__(norm_bwd_block(TPR), 4) void k_norm_bwd(NormBwd a) 
                     if (col(i) + e < N)  // ldp is a multiple of four
                         *(float4 *)(p + col(i) + e) = make_float4(gsum[i][e], gsum[i][e + 1], gsum[i][e + 2], gsum[i][e + 3]);
             } else {
-                piece_store<DT, ALL>(a.dgate, group, N, col(i), gsum[i], nullptr);
+                piece_store<DT, ALL>(a.dgate, group, N, col(i), piece_pack<DT>(gsum[i]));
             }
 #pragma unroll
             for (int e = 0; e < VE; ++e) gsum[i][e] = 0.0f;
@@ -615,7 +642,7 @@ __global__ __launch_bounds__(norm_bwd_block(TPR), 4) void k_norm_bwd(NormBwd a) 
         }
         if (a.dX) {
 #pragma unroll
-            for (int i = 0; i < CH; ++i) piece_store<DT, ALL>(a.dX, row, N, col(i), d[i], nullptr);
+            for (int i = 0; i < CH; ++i) piece_store<DT, ALL>(a.dX, row, N, col(i), piece_pack<DT>(d[i]));
         }
         if (!to_block) continue;
         float s0 = 0.0f, s1 = 0.0f;
@@ -667,7 +694,7 @@ __global__ __launch_bounds__(norm_bwd_block(TPR), 4) void k_norm_bwd(NormBwd a) 
             }
         }
 #pragma unroll
-        for (int i = 0; i < CH; ++i) piece_store<DT, ALL>(a.dB, row, N, col(i), d[i], nullptr);
+        for (int i = 0; i < CH; ++i) piece_store<DT, ALL>(a.dB, row, N, col(i), piece_pack<DT>(d[i]));
     }
     finish_group();
 #pragma unroll
