@@ -90,15 +90,33 @@ __device__ __forceinline__ float act_value(float g) {
     }
 }
 
-// f(z) for an activation known at run time (MM_ACT_NONE: z).
+// f(z) where its derivative is not wanted, for 16-bit results: sigmoid(x) = 1 /
+// (1 + 2^(-x log2 e)) needs no other tail (2^(..) overflows to infinity, whose
+// reciprocal is the 0 that belongs there) and takes half the pair's instructions
+// (8192 x 4096 x 11008 BF16 with tanh gelu: 8 us more than without, so 29).
+template <int ACT, bool EXACT>
+__device__ __forceinline__ float act_only(float z) {
+    constexpr float L = 1.4426950408889634f;  // log2 e
+    if constexpr (EXACT || ACT == MM_ACT_RELU || ACT == MM_ACT_GELU) {
+        return act_value<ACT, EXACT>(z);
+    } else if constexpr (ACT == MM_ACT_GELU_TANH) {
+        const float x = z * fmaf(z * z, -L * kGeluC * kGeluA, -L * kGeluC);
+        return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x));
+    } else {
+        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-L * z));
+        return ACT == MM_ACT_SILU ? z * s : s;
+    }
+}
+
+// The same for an activation known at run time (MM_ACT_NONE: z).
 template <bool EXACT>
 __device__ __forceinline__ float act_run(int act, float z) {
     switch (act) {
-    case MM_ACT_SILU: return act_value<MM_ACT_SILU, EXACT>(z);
-    case MM_ACT_GELU: return act_value<MM_ACT_GELU, EXACT>(z);
-    case MM_ACT_GELU_TANH: return act_value<MM_ACT_GELU_TANH, EXACT>(z);
-    case MM_ACT_RELU: return act_value<MM_ACT_RELU, EXACT>(z);
-    case MM_ACT_SIGMOID: return act_value<MM_ACT_SIGMOID, EXACT>(z);
+    case MM_ACT_SILU: return act_only<MM_ACT_SILU, EXACT>(z);
+    case MM_ACT_GELU: return act_only<MM_ACT_GELU, EXACT>(z);
+    case MM_ACT_GELU_TANH: return act_only<MM_ACT_GELU_TANH, EXACT>(z);
+    case MM_ACT_RELU: return act_only<MM_ACT_RELU, EXACT>(z);
+    case MM_ACT_SIGMOID: return act_only<MM_ACT_SIGMOID, EXACT>(z);
     }
     return z;
 }

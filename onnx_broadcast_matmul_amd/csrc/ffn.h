@@ -35,7 +35,7 @@ struct FfnArgs {
     const void *R;
     void *zs;
     int32_t q8;
-    int32_t r_vec;         // four columns of R are an aligned vector
+    int32_t r_vec;         // rows of R are whole, aligned 16-byte chunks
 };
 
 // The same as the kernels take it: in 88 bytes, because a launch with more
@@ -170,9 +170,9 @@ hipError_t launch_glu_rows(int dtype, bool tb, const FfnArgs &a, hipStream_t s);
 bool rows_quantize(int a_type, int out_dtype, bool tb, int64_t M, int64_t K, int64_t N);
 hipError_t launch_scaled_rows(int out_dtype, bool tb, bool quant, const FfnArgs &a, hipStream_t s);
 // Linear layer: the forward products (also dX's, which has no epilogue), the
-// joining of a split one with the epilogue, the few-row kernel.  dW is a pair of
-// one (launch_glu_dw with batch 1).
+// joining of a split one with the epilogue, the few-row kernel; dW (batch 1).
 hipError_t launch_linear(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
+hipError_t launch_linear_dw(int dtype, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
 hipError_t launch_linear_reduce(int dtype, const FfnArgs &a, hipStream_t s);
 hipError_t launch_linear_rows(int dtype, bool tb, const FfnArgs &a, hipStream_t s);
 

@@ -46,16 +46,21 @@ inline bool pieces_launchable(int64_t M, int64_t pieces) {
 
 inline bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
 
-// Classes of operand types that the time model tells apart.
-enum { kClass16 = 0, kClass8 = 1, kClass32 = 2 };
+// Classes of operand types that the time model tells apart; the linear layer's
+// 16-bit products run another kernel on entry 0 (k_big.h).
+enum { kClass16 = 0, kClass8 = 1, kClass32 = 2, kClassLinear16 = 3 };
 int type_class(int dtype);
 
 double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, int64_t row, double wbytes);
-// The same for the linear layer's one matrix.
+// The same for the linear layer.
 double linear_rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, int64_t row, double wbytes);
 double tiles_us(int cls, const FfnChoice &c, bool nk, bool aligned, int64_t row, double wbytes);
 FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t cols, int64_t kbytes, int terms,
                  unsigned tiles, bool may_split);
+// Whether a product of an entry's tiles runs faster as whole rounds of workgroups
+// over its first columns and another entry (of `tiles`) over the rest: the first
+// column of the rest and its entry, c then is the first's; or 0.
+int64_t balance(int cls, FfnChoice *c, int64_t M, int64_t N, int64_t kbytes, unsigned tiles, int *rest);
 void set_split(FfnChoice *c, int64_t kbytes, int terms, int64_t split);
 mm_status tile_option(const mm_plan_options *opt, int *tile);
 mm_status choose_backward(const char *name, int cls, bool aligned, int64_t batch, int64_t M, int64_t cols,

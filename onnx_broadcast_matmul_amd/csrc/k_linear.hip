@@ -12,7 +12,9 @@
 
 namespace mm {
 
-#define MM_LINEAR_DECLARE(NAME) hipError_t linear_##NAME(bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
+#define MM_LINEAR_DECLARE(NAME)                                                                         \
+    hipError_t linear_##NAME(bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);  \
+    hipError_t linear_dw_##NAME(int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s);
 MM_LINEAR_DECLARE(f32)
 MM_LINEAR_DECLARE(f16)
 MM_LINEAR_DECLARE(bf16)
@@ -20,6 +22,11 @@ MM_LINEAR_DECLARE(bf16)
 hipError_t launch_linear(int dtype, bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {
     return dtype == MM_FLOAT ? linear_f32(tb, tile, split, vec, a, s)
            : dtype == MM_FLOAT16 ? linear_f16(tb, tile, split, vec, a, s) : linear_bf16(tb, tile, split, vec, a, s);
+}
+
+hipError_t launch_linear_dw(int dtype, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {
+    return dtype == MM_FLOAT ? linear_dw_f32(tile, split, vec, a, s)
+           : dtype == MM_FLOAT16 ? linear_dw_f16(tile, split, vec, a, s) : linear_dw_bf16(tile, split, vec, a, s);
 }
 
 // Forward pass over split K: the partitions' sums added in partition order,

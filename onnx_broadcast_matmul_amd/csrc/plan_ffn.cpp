@@ -19,23 +19,26 @@ namespace mm {
 static const int kOcc[kNumFfnTiles] = {1, 2, 2, 1, 1};
 static const double kLaunch = 2.5;                                      // us
 static const double kFixed[kNumFfnTiles] = {7.5, 3.2, 2.5, 1.4, 5.5};  // us
-static const double kStep[2][3][kNumFfnTiles][2] = {                    // us: aligned, not aligned
+static const double kFixedLinear0 = 10.0;                              // us, the linear layer's entry 0
+static const double kStep[2][4][kNumFfnTiles][2] = {                    // us: aligned, not aligned
     {{{0.41, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.240, 0}},
      {{0.41, 0}, {0.17, 0.285}, {0.145, 0.160}, {0.095, 0}, {0.222, 0}},
-     {{1e9, 0}, {0.54, 0.970}, {0.260, 0.490}, {0.148, 0}, {1e9, 0}}},
+     {{1e9, 0}, {0.54, 0.970}, {0.260, 0.490}, {0.148, 0}, {1e9, 0}},
+     {{0.335, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.240, 0}}},
     {{{1e9, 0}, {0.27, 0.345}, {0.200, 0.222}, {0.098, 0}, {0.345, 0}},
      {{1e9, 0}, {0.23, 0.305}, {0.122, 0.182}, {0.080, 0}, {0.310, 0}},
-     {{1e9, 0}, {0.60, 1.050}, {0.355, 0.585}, {0.171, 0}, {1e9, 0}}}};
+     {{1e9, 0}, {0.60, 1.050}, {0.355, 0.585}, {0.171, 0}, {1e9, 0}},
+     {{1e9, 0}, {0.27, 0.345}, {0.200, 0.222}, {0.098, 0}, {0.345, 0}}}};
 
 int type_class(int dtype) { return dtype == MM_FLOAT ? kClass32 : dtype == MM_INT8 ? kClass8 : kClass16; }
 
 static double est_us(int cls, bool aligned, int tile, double wgs, double steps) {
     const double *step = kStep[aligned ? 0 : 1][cls][tile];
     const int occ = kOcc[tile];
-    const double per_cu = ceil(wgs / kNumCUs);
+    const double per_cu = ceil(wgs / kNumCUs), fixed = cls == kClassLinear16 && tile == 0 ? kFixedLinear0 : kFixed[tile];
     const double full = floor(per_cu / occ), rest = per_cu - full * occ;
-    double us = kLaunch + full * (kFixed[tile] + step[occ - 1] * steps);
-    if (rest > 0) us += kFixed[tile] + step[(int)rest - 1] * steps;
+    double us = kLaunch + full * (fixed + step[occ - 1] * steps);
+    if (rest > 0) us += fixed + step[(int)rest - 1] * steps;
     return us;
 }
 
@@ -64,15 +67,34 @@ double rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, int64_t r
     return 3.0 + chain * kib * (odd ? 1.25 : 1.0);
 }
 
+// The linear layer's few-row kernel reads one matrix where the gated block's reads
+// two.  Fitted to M = 1..32, K = 512..11008, N = 512..11008: within 15 % but for
+// FP32 ones that leave a third of the CUs without work.
 double linear_rows_us(int cls, bool nk, int64_t M, int64_t N, int64_t kbytes, int64_t row, double wbytes) {
-    return rows_us(cls, nk, M, N, kbytes, row, wbytes);
+    const bool f32 = cls == kClass32;
+    const int r = M > 16 ? 1 : 0;
+    const double kib = (double)kbytes / 1024.0;
+    if (nk) {
+        static const double kChain[2][2] = {{0.75, 1.15}, {0.8, 1.25}}, kRate[2][2] = {{4.0, 2.8}, {4.1, 2.7}};
+        const bool odd = !f32 && row % 4 != 0;
+        return std::max(3.0 + kChain[f32][r] * kib, wbytes / (kRate[f32][r] * (odd ? 0.5 : 1.0) * 1e6));
+    }
+    // [K, N]: us for each KiB of a column, from the workgroups there are, of 32 or
+    // of half as many columns.
+    const double wgs = (double)cdiv(N, 32), rounds = ceil(wgs / kNumCUs);
+    if (rows_halve(cdiv(N, 32))) {
+        static const double kBase[2][2] = {{0.65, 1.2}, {0.8, 1.35}}, kEach[2][2] = {{0.0035, 0.003}, {0.0025, 0.0013}};
+        return 3.0 + (kBase[f32][r] + kEach[f32][r] * 2.0 * wgs) * kib;
+    }
+    static const double kBase[2][2] = {{1.0, 1.6}, {-0.6, 1.15}}, kEach[2][2] = {{0.8, 0.65}, {2.45, 1.05}};
+    return 3.0 + (kBase[f32][r] + kEach[f32][r] * rounds) * kib;
 }
 
 // The tiles' time over the same few rows: the weights stream at kStream
 // TB/s at best ([K, N] ones at 0.72 of it in the register-staged form, at half
 // with rows off 4-byte alignment), and a second launch follows a split.
 double tiles_us(int cls, const FfnChoice &c, bool nk, bool aligned, int64_t row, double wbytes) {
-    static const double kStream[3] = {4.0, 2.7, 4.0};
+    static const double kStream[4] = {4.0, 2.7, 4.0, 4.0};
     const double part = aligned || nk ? 1.0 : row % 4 == 0 ? 0.72 : 0.5;
     return std::max(c.us + (c.split > 1 ? 3.0 : 0.0), wbytes / (kStream[cls] * part * 1e6));
 }
@@ -106,6 +128,32 @@ FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t cols, 
             }
         }
     }
+    return best;
+}
+
+int64_t balance(int cls, FfnChoice *c, int64_t M, int64_t N, int64_t kbytes, unsigned tiles, int *rest) {
+    const double steps = ceil((double)kbytes / 32.0);
+    int64_t best = 0;
+    FfnChoice main = *c;
+    double top = 0.98 * c->us;  // (a second launch has to bring something)
+    for (int i = 0; i < kNumFfnTiles; ++i) {
+        if (!(tiles >> i & 1)) continue;
+        const FfnTile &t = kFfnTiles[i];
+        const int64_t slots = (int64_t)kNumCUs * kOcc[i], rows = cdiv(M, t.bm), total = rows * cdiv(N, t.bn);
+        if (total > 64 * slots) continue;  // a round less would bring under 2 %
+        const int64_t cols = total / slots * slots / rows;  // columns of tiles in whole rounds
+        if (cols <= 0 || cols * t.bn >= N) continue;
+        const double us = est_us(cls, true, i, (double)(rows * cols), steps);
+        const FfnChoice r = choose(cls, true, 1, M, N - cols * t.bn, kbytes, 1, tiles, false);
+        if (us + r.us >= top) continue;
+        top = us + r.us;
+        best = cols * t.bn;
+        *rest = r.tile;
+        main = *c;
+        main.tile = i;
+        main.us = top;
+    }
+    *c = main;
     return best;
 }
 

@@ -115,7 +115,7 @@ mm_status mm_linear_plan_create(const mm_linear_desc *d, int dtype, const mm_pla
     p->out_numel = M * N;
     p->total_batch = p->batch = 1;
     const int64_t es = elem_size(dtype);
-    const int cls = type_class(dtype);
+    const int cls = dtype == MM_FLOAT ? kClass32 : kClassLinear16;
     if (p->out_numel == 0) {
         p->algo = MM_ALGO_EMPTY;
     } else {
@@ -126,7 +126,7 @@ mm_status mm_linear_plan_create(const mm_linear_desc *d, int dtype, const mm_pla
         FfnChoice c = pick(tiles);
         if (force == MM_ALGO_SKINNY_M ||
             (force == MM_ALGO_AUTO && rows_ok && treq == 0 && sreq == 0 &&
-             linear_rows_us(cls, p->tb != 0, M, N, K * es, p->w_pitch * es, wbytes) <=
+             linear_rows_us(type_class(dtype), p->tb != 0, M, N, K * es, p->w_pitch * es, wbytes) <=
                  tiles_us(cls, c, p->tb != 0, aligned, p->w_pitch * es, wbytes))) {
             p->algo = MM_ALGO_SKINNY_M;
             if (!launchable((double)cdiv(N, 16), 512)) st = fail(MM_ERR_TOO_LARGE, "a launch of more than 2^32 threads");
@@ -142,6 +142,8 @@ mm_status mm_linear_plan_create(const mm_linear_desc *d, int dtype, const mm_pla
                 if (only >= 0) st = fail(MM_ERR_BAD_OPTION, "tile 4 forms no checkpoint of Z without a split");
                 else settle(pick(tiles & ~8u));
             }
+            if (c.split == 1 && treq == 0 && sreq == 0 && force == MM_ALGO_AUTO && aligned)
+                p->tail_col = balance(cls, &c, M, N, K * es, z8 ? any & ~8u : any, &p->tail_tile);
             p->tile = c.tile;
             p->split = c.split;
             p->kstages = c.kstages;
@@ -267,10 +269,26 @@ mm_status mm_linear_execute(mm_plan_t p, const void *X, const void *W, const voi
     a.q8 = p->kept == MM_INT8;
     a.kept32 = p->kept == MM_FLOAT && p->dtype != MM_FLOAT;
     a.kept_vec = aligned16(Z) && (p->N * (a.q8 ? 1 : a.kept32 ? 4 : es)) % 16 == 0;
-    a.r_vec = ((uintptr_t)residual & (uintptr_t)(4 * es - 1)) == 0 && p->N % 4 == 0;
+    a.r_vec = aligned16(residual) && (p->N * es) % 16 == 0;
     if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_linear_rows(p->dtype, p->tb != 0, a, s));
     const bool vec = aligned16(X) && aligned16(W) && (p->K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 &&
                      (p->tb || (p->N * es) % 16 == 0);
+    if (p->algo != MM_ALGO_SPLIT_K && p->tail_col > 0) {
+        // Columns [0, tail_col) in whole rounds of workgroups, the rest on another entry.
+        const int64_t c = p->tail_col;
+        FfnArgs t = a;
+        a.N = c;
+        t.N = p->N - c;
+        t.B[0] = (const char *)W + (p->tb ? c * p->w_pitch : c) * es;
+        t.Y[0] = (char *)Y + c * es;
+        if (Z) t.G = (char *)Z + c * (a.q8 ? 1 : a.kept32 ? 4 : es);
+        if (a.q8 && Z) t.zs = (char *)z_scale + c / MM_CHECKPOINT_BLOCK;
+        if (residual) t.R = (const char *)residual + c * es;
+        if (bias) t.bias = (const char *)bias + c * es;
+        hipError_t e = launch_linear(p->dtype, p->tb != 0, p->tile, false, vec, a, s);
+        if (e == hipSuccess) e = launch_linear(p->dtype, p->tb != 0, p->tail_tile, false, vec, t, s);
+        return launched(e);
+    }
     if (p->algo != MM_ALGO_SPLIT_K) return launched(launch_linear(p->dtype, p->tb != 0, p->tile, false, vec, a, s));
     mm_status st = alloc_workspace(p, false);
     if (st != MM_OK) return st;
@@ -386,7 +404,7 @@ mm_status mm_linear_backward(mm_plan_t p, const void *X, const void *x_scale, co
         a.W = ws + p->s_off;
         a.split = p->dw.split;
         a.kstages = p->dw.kstages;
-        hipError_t e = launch_glu_dw(p->dtype, p->dw.tile, a.split > 1, vec, a, s);
+        hipError_t e = launch_linear_dw(p->dtype, p->dw.tile, a.split > 1, vec, a, s);
         if (e == hipSuccess && a.split > 1) e = launch_sum_reduce(p->dtype, a, s);
         st = launched(e);
         if (st != MM_OK) return st;
