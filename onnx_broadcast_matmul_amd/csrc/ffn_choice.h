@@ -47,7 +47,7 @@ inline bool pieces_launchable(int64_t M, int64_t pieces) {
 inline bool float_type(int t) { return t == MM_FLOAT || t == MM_FLOAT16 || t == MM_BFLOAT16; }
 
 // Classes of operand types that the time model tells apart; the linear layer's
-// 16-bit products run another kernel on entry 0 (k_big.h).
+// 16-bit products run another kernel on entries 0 and 4 (k_big.h).
 enum { kClass16 = 0, kClass8 = 1, kClass32 = 2, kClassLinear16 = 3 };
 int type_class(int dtype);
 

@@ -16,8 +16,13 @@ hipError_t launch_glu_dw(int dtype, int tile, bool split, bool vec, const FfnArg
 #define MM_LINEAR_INSTANCE(DT, NAME)                                                                      \
     hipError_t linear_##NAME(bool tb, int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {   \
         if constexpr (DT != MM_FLOAT) {                                                                   \
-            if (tile == 0 && !split && big_fits(false, tb, vec, a))                                       \
-                return tb ? launch_big<DT, false, true, true>(a, s) : launch_big<DT, false, false, true>(a, s); \
+            if (big_fits(false, tb, tile, split, vec, a)) {                                               \
+                if (tile == 0)                                                                            \
+                    return tb ? launch_big<DT, false, true, true, 256>(a, s)                              \
+                              : launch_big<DT, false, false, true, 256>(a, s);                            \
+                return tb ? launch_big<DT, false, true, true, 128>(a, s)                                  \
+                          : launch_big<DT, false, false, true, 128>(a, s);                                \
+            }                                                                                             \
         }                                                                                                 \
         if (split)                                                                                        \
             return tb ? launch_entry<DT, DT, kLinear, true, false, true>(tile, vec, a, s)                 \
@@ -27,8 +32,9 @@ hipError_t launch_glu_dw(int dtype, int tile, bool split, bool vec, const FfnArg
     }                                                                                                     \
     hipError_t linear_dw_##NAME(int tile, bool split, bool vec, const FfnArgs &a, hipStream_t s) {         \
         if constexpr (DT != MM_FLOAT) {                                                                   \
-            if (tile == 0 && !split && big_fits(true, false, vec, a))                                     \
-                return launch_big<DT, true, false, false>(a, s);                                          \
+            if (big_fits(true, false, tile, split, vec, a))                                               \
+                return tile == 0 ? launch_big<DT, true, false, false, 256>(a, s)                          \
+                                 : launch_big<DT, true, false, false, 128>(a, s);                         \
         }                                                                                                 \
         return launch_glu_dw(DT, tile, split, vec, a, s);                                                 \
     }

@@ -84,6 +84,8 @@ struct mm_plan_s {
     int kept = 0;          // type of G and U
     int64_t w_pitch = 0, d_off = 0, d_pitch = 0, d_bytes = 0;
     mm::FfnChoice dx, dw;  // the backward products
+    int64_t dx_tail_col = 0, dw_tail_col = 0;  // linear layer: as tail_col, tail_tile for them
+    int dx_tail_tile = -1, dw_tail_tile = -1;
     int32_t kstages = 0;   // K stages of a partition (scaled product, forward pass)
 
     // Linear layer (mm_linear_plan_create): M, N, K are rows, out_features,

@@ -19,12 +19,12 @@ namespace mm {
 static const int kOcc[kNumFfnTiles] = {1, 2, 2, 1, 1};
 static const double kLaunch = 2.5;                                      // us
 static const double kFixed[kNumFfnTiles] = {7.5, 3.2, 2.5, 1.4, 5.5};  // us
-static const double kFixedLinear0 = 10.0;                              // us, the linear layer's entry 0
+static const double kFixedLinear[kNumFfnTiles] = {10.0, 3.2, 2.5, 1.4, 7.0};
 static const double kStep[2][4][kNumFfnTiles][2] = {                    // us: aligned, not aligned
     {{{0.41, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.240, 0}},
      {{0.41, 0}, {0.17, 0.285}, {0.145, 0.160}, {0.095, 0}, {0.222, 0}},
      {{1e9, 0}, {0.54, 0.970}, {0.260, 0.490}, {0.148, 0}, {1e9, 0}},
-     {{0.335, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.240, 0}}},
+     {{0.335, 0}, {0.17, 0.285}, {0.147, 0.165}, {0.095, 0}, {0.190, 0}}},
     {{{1e9, 0}, {0.27, 0.345}, {0.200, 0.222}, {0.098, 0}, {0.345, 0}},
      {{1e9, 0}, {0.23, 0.305}, {0.122, 0.182}, {0.080, 0}, {0.310, 0}},
      {{1e9, 0}, {0.60, 1.050}, {0.355, 0.585}, {0.171, 0}, {1e9, 0}},
@@ -35,7 +35,7 @@ int type_class(int dtype) { return dtype == MM_FLOAT ? kClass32 : dtype == MM_IN
 static double est_us(int cls, bool aligned, int tile, double wgs, double steps) {
     const double *step = kStep[aligned ? 0 : 1][cls][tile];
     const int occ = kOcc[tile];
-    const double per_cu = ceil(wgs / kNumCUs), fixed = cls == kClassLinear16 && tile == 0 ? kFixedLinear0 : kFixed[tile];
+    const double per_cu = ceil(wgs / kNumCUs), fixed = (cls == kClassLinear16 && aligned ? kFixedLinear : kFixed)[tile];
     const double full = floor(per_cu / occ), rest = per_cu - full * occ;
     double us = kLaunch + full * (fixed + step[occ - 1] * steps);
     if (rest > 0) us += fixed + step[(int)rest - 1] * steps;
@@ -132,6 +132,7 @@ FfnChoice choose(int cls, bool aligned, int64_t batch, int64_t M, int64_t cols, 
 }
 
 int64_t balance(int cls, FfnChoice *c, int64_t M, int64_t N, int64_t kbytes, unsigned tiles, int *rest) {
+    if (M <= 0 || N <= 0) return 0;
     const double steps = ceil((double)kbytes / 32.0);
     int64_t best = 0;
     FfnChoice main = *c;

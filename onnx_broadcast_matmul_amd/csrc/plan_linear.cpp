@@ -9,6 +9,28 @@
 
 using namespace mm;
 
+namespace mm {
+
+// A product as one launch, or (col > 0) as columns [0, col) in whole rounds of
+// workgroups and the rest on another entry: `run` gets each part's arguments.
+template <class Run>
+static hipError_t in_rounds(const FfnArgs &a, int64_t es, int64_t col, bool tb, Run run) {
+    if (col <= 0) return run(a, false);
+    FfnArgs first = a, rest = a;
+    first.N = col;
+    rest.N = a.N - col;
+    rest.B[0] = (const char *)a.B[0] + (tb ? col * a.ldb : col) * es;
+    rest.Y[0] = (char *)a.Y[0] + col * es;
+    if (a.G) rest.G = (char *)a.G + col * (a.q8 ? 1 : a.kept32 ? 4 : es);
+    if (a.zs) rest.zs = (char *)a.zs + col / MM_CHECKPOINT_BLOCK;
+    if (a.R) rest.R = (const char *)a.R + col * es;
+    if (a.bias) rest.bias = (const char *)a.bias + col * es;
+    const hipError_t e = run(first, false);
+    return e == hipSuccess ? run(rest, true) : e;
+}
+
+}  // namespace mm
+
 extern "C" {
 
 int64_t mm_checkpoint_blocks(int64_t cols) { return cols < 0 ? -1 : cdiv(cols, MM_CHECKPOINT_BLOCK); }
@@ -176,6 +198,10 @@ mm_status mm_linear_plan_create(const mm_linear_desc *d, int dtype, const mm_pla
         st = choose_backward("dX", cls, z_al && w_al, 1, M, K, N * es, 1, any, d->dx_tile, d->dx_split_k, &p->dx);
         if (st == MM_OK)
             st = choose_backward("dW", cls, z_al && x_al, 1, wm, wn, M * es, 1, dw_tiles, d->dw_tile, d->dw_split_k, &p->dw);
+        if (st == MM_OK && p->dx.split == 1 && d->dx_tile == 0 && d->dx_split_k == 0 && z_al && w_al)
+            p->dx_tail_col = balance(cls, &p->dx, M, K, N * es, any, &p->dx_tail_tile);
+        if (st == MM_OK && p->dw.split == 1 && d->dw_tile == 0 && d->dw_split_k == 0 && z_al && x_al)
+            p->dw_tail_col = balance(cls, &p->dw, wm, wn, M * es, dw_tiles, &p->dw_tail_tile);
         LinearPrep prep = {};
         prep.dZ = prep.X = p;  // (not read)
         prep.M = M;
@@ -273,23 +299,10 @@ mm_status mm_linear_execute(mm_plan_t p, const void *X, const void *W, const voi
     if (p->algo == MM_ALGO_SKINNY_M) return launched(launch_linear_rows(p->dtype, p->tb != 0, a, s));
     const bool vec = aligned16(X) && aligned16(W) && (p->K * es) % 16 == 0 && (p->w_pitch * es) % 16 == 0 &&
                      (p->tb || (p->N * es) % 16 == 0);
-    if (p->algo != MM_ALGO_SPLIT_K && p->tail_col > 0) {
-        // Columns [0, tail_col) in whole rounds of workgroups, the rest on another entry.
-        const int64_t c = p->tail_col;
-        FfnArgs t = a;
-        a.N = c;
-        t.N = p->N - c;
-        t.B[0] = (const char *)W + (p->tb ? c * p->w_pitch : c) * es;
-        t.Y[0] = (char *)Y + c * es;
-        if (Z) t.G = (char *)Z + c * (a.q8 ? 1 : a.kept32 ? 4 : es);
-        if (a.q8 && Z) t.zs = (char *)z_scale + c / MM_CHECKPOINT_BLOCK;
-        if (residual) t.R = (const char *)residual + c * es;
-        if (bias) t.bias = (const char *)bias + c * es;
-        hipError_t e = launch_linear(p->dtype, p->tb != 0, p->tile, false, vec, a, s);
-        if (e == hipSuccess) e = launch_linear(p->dtype, p->tb != 0, p->tail_tile, false, vec, t, s);
-        return launched(e);
-    }
-    if (p->algo != MM_ALGO_SPLIT_K) return launched(launch_linear(p->dtype, p->tb != 0, p->tile, false, vec, a, s));
+    if (p->algo != MM_ALGO_SPLIT_K)
+        return launched(in_rounds(a, es, p->tail_col, p->tb != 0, [&](const FfnArgs &part, bool rest) {
+            return launch_linear(p->dtype, p->tb != 0, rest ? p->tail_tile : p->tile, false, vec, part, s);
+        }));
     mm_status st = alloc_workspace(p, false);
     if (st != MM_OK) return st;
     a.W = p->ws;
@@ -379,7 +392,9 @@ mm_status mm_linear_backward(mm_plan_t p, const void *X, const void *x_scale, co
         a.W = ws + p->s_off;
         a.split = p->dx.split;
         a.kstages = p->dx.kstages;
-        hipError_t e = launch_linear(p->dtype, !p->tb, p->dx.tile, a.split > 1, vec, a, s);
+        hipError_t e = in_rounds(a, es, p->dx_tail_col, !p->tb, [&](const FfnArgs &part, bool rest) {
+            return launch_linear(p->dtype, !p->tb, rest ? p->dx_tail_tile : p->dx.tile, a.split > 1, vec, part, s);
+        });
         if (e == hipSuccess && a.split > 1) e = launch_linear_reduce(p->dtype, a, s);
         st = launched(e);
         if (st != MM_OK) return st;
@@ -404,7 +419,9 @@ mm_status mm_linear_backward(mm_plan_t p, const void *X, const void *x_scale, co
         a.W = ws + p->s_off;
         a.split = p->dw.split;
         a.kstages = p->dw.kstages;
-        hipError_t e = launch_linear_dw(p->dtype, p->dw.tile, a.split > 1, vec, a, s);
+        hipError_t e = in_rounds(a, es, p->dw_tail_col, false, [&](const FfnArgs &part, bool rest) {
+            return launch_linear_dw(p->dtype, rest ? p->dw_tail_tile : p->dw.tile, a.split > 1, vec, part, s);
+        });
         if (e == hipSuccess && a.split > 1) e = launch_sum_reduce(p->dtype, a, s);
         st = launched(e);
         if (st != MM_OK) return st;

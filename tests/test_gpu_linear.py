@@ -326,21 +326,23 @@ LARGE = [(256, 64, 256), (1, 8, 8), (257, 72, 264), (300, 128, 520), (513, 136, 
 
 @pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
 @pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("tile", [1, 5])
 @pytest.mark.parametrize("i", range(len(LARGE)), ids=lambda i: "x".join(map(str, LARGE[i])))
-def test_linear_large_tiles(i, dt, nk, dev):
+def test_linear_large_tiles(i, tile, dt, nk, dev):
     """One stage of K and many, whole and in part, each kind of epilogue."""
     for j in range(4):
         p = run_forward(dev, *LARGE[i], TYPES[dt], nk, ACTS[(i + j) % 6], seed=900 + 10 * i + j, bias=j % 2 == 0,
-                        residual=(i + j) % 3 != 0, z=KEEP[(i + j) % 4], tile=1, algo=mm.ALGO_GENERAL)
-        assert p.info()["tile"] == 1
-    run_forward(dev, *LARGE[i], TYPES[dt], nk, "gelu", seed=990 + i, tile=1, algo=mm.ALGO_GENERAL, inplace=True)
+                        residual=(i + j) % 3 != 0, z=KEEP[(i + j) % 4], tile=tile, algo=mm.ALGO_GENERAL)
+        assert p.info()["tile"] == tile
+    run_forward(dev, *LARGE[i], TYPES[dt], nk, "gelu", seed=990 + i, tile=tile, algo=mm.ALGO_GENERAL, inplace=True)
 
 
 @pytest.mark.parametrize("z", KEEP)
-def test_linear_large_tiles_of_odd_columns(z, dev):
+@pytest.mark.parametrize("tile", [1, 5])
+def test_linear_large_tiles_of_odd_columns(tile, z, dev):
     """Rows of X and W are whole 16-byte chunks, those of Y, Z and R are not."""
     for j, (m, k, n) in enumerate(((300, 128, 281), (520, 64, 515), (258, 264, 12), (3, 72, 1))):
-        run_forward(dev, m, k, n, (BF16, F16)[j % 2], True, ACTS[1 + j], seed=930 + j, z=z, tile=1, algo=mm.ALGO_GENERAL)
+        run_forward(dev, m, k, n, (BF16, F16)[j % 2], True, ACTS[1 + j], seed=930 + j, z=z, tile=tile, algo=mm.ALGO_GENERAL)
 
 
 @pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
@@ -465,13 +467,22 @@ def test_linear_backward_every_entry(dt, nk, dev):
 
 @pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
 @pytest.mark.parametrize("dt", ["fp16", "bf16"])
-def test_linear_backward_large_tiles(dt, nk, dev):
+@pytest.mark.parametrize("tile", [1, 5])
+def test_linear_backward_large_tiles(tile, dt, nk, dev):
     for j, (m, k, n) in enumerate(((1, 8, 8), (63, 264, 72), (64, 256, 256), (65, 40, 520), (130, 776, 264),
                                    (1000, 136, 328))):
         p = run_backward(dev, m, k, n, TYPES[dt], nk, ACTS[j], seed=940 + 10 * j, z=KEEP[1 + j % 3], x8=j % 2 == 0,
-                         pitched=j == 3, dx_tile=1, dw_tile=1)
+                         pitched=j == 3, dx_tile=tile, dw_tile=tile)
         d = p.desc()
-        assert (d["dx_tile"], d["dw_tile"]) == (1, 1)
+        assert (d["dx_tile"], d["dw_tile"]) == (tile, tile)
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_linear_backward_whole_rounds_and_a_rest(dt, nk, dev):
+    """Sizes whose forward product runs so: dX's of the first, dW's of the others."""
+    for j, (m, k, n) in enumerate(((4104, 5000, 512), (512, 5000, 4104), (512, 4104, 5000))):
+        run_backward(dev, m, k, n, TYPES[dt], nk, "silu", seed=980 + j, z=mm.INT8, x8=j == 2)
 
 
 def test_linear_backward_without_rows_or_features(dev):
