@@ -241,13 +241,20 @@ def _shape(shape: Sequence[int]):
     return (ctypes.c_int64 * max(1, len(shape)))(*[int(d) for d in shape])
 
 
-def torch_dtype_code(dt) -> int:
-    import torch
+_dtype_codes = {}
 
-    codes = {torch.float32: FLOAT, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16, torch.float64: DOUBLE}
-    if dt not in codes:
-        raise TypeError(f"unsupported tensor dtype {dt}")
-    return codes[dt]
+
+def torch_dtype_code(dt) -> int:
+    code = _dtype_codes.get(dt)
+    if code is None:
+        import torch
+
+        _dtype_codes.update({torch.float32: FLOAT, torch.float16: FLOAT16, torch.bfloat16: BFLOAT16,
+                             torch.float64: DOUBLE})
+        code = _dtype_codes.get(dt)
+        if code is None:
+            raise TypeError(f"unsupported tensor dtype {dt}")
+    return code
 
 
 def torch_dtype(code: int):
@@ -753,14 +760,16 @@ def _checkpoint(name, q, scale, shape, dev):
     """The addresses of a checkpoint of a tensor of `shape` on GPU `dev`."""
     import torch
 
-    qp = _dense(name, q, torch.int8, shape, dev)
-    return qp, _dense(f"{name}'s scale", scale, torch.uint8, shape[:-1] + (checkpoint_blocks(shape[-1]),), dev)
+    *lead, cols = shape
+    return (_dense(name, q, torch.int8, shape, dev),
+            _dense(f"{name}'s scale", scale, torch.uint8, (*lead, -(-cols // CHECKPOINT_BLOCK)), dev))
 
 
 def _rows_cols(shape) -> Tuple[int, int]:
-    if len(shape) < 1:
+    if not shape:
         raise ValueError("a tensor of at least one dimension is needed")
-    return math.prod(shape[:-1]), shape[-1]
+    *lead, cols = shape
+    return math.prod(lead), cols
 
 
 def checkpoint_pack(X, q=None, scale=None, stream=None):
@@ -770,16 +779,17 @@ def checkpoint_pack(X, q=None, scale=None, stream=None):
     (default: the current stream), as if it were current."""
     import torch
 
-    code = torch_dtype_code(X.dtype)
-    rows, cols = _rows_cols(X.shape)
+    dt, shape = X.dtype, X.shape
+    code = torch_dtype_code(dt)
+    rows, cols = _rows_cols(shape)
     dev = _device_of(X)
     if q is None:
-        q = _empty(X.shape, torch.int8, X.device, stream)
+        q = _empty(shape, torch.int8, X.device, stream)
     if scale is None:
-        scale = _empty(X.shape[:-1] + (checkpoint_blocks(cols),), torch.uint8, X.device, stream)
-    xp = _dense("X", X, X.dtype, X.shape, dev)
-    qp, sp = _checkpoint("q", q, scale, X.shape, dev)
-    _run(dev, stream, lib().mm_checkpoint_pack, xp, code, rows, cols, qp, sp)
+        scale = _empty(shape[:-1] + (checkpoint_blocks(cols),), torch.uint8, X.device, stream)
+    xp = _dense("X", X, dt, shape, dev)
+    qp, sp = _checkpoint("q", q, scale, shape, dev)
+    _run(dev, stream, (_lib or lib()).mm_checkpoint_pack, xp, code, rows, cols, qp, sp)
     return q, scale
 
 
@@ -788,15 +798,17 @@ def checkpoint_unpack(q, scale, out, stream=None):
     into a new tensor of ``out`` if that is a torch dtype."""
     import torch
 
-    rows, cols = _rows_cols(q.shape)
+    shape = q.shape
+    rows, cols = _rows_cols(shape)
     dev = _device_of(q)
     if isinstance(out, torch.dtype):
         torch_dtype_code(out)
-        out = _empty(q.shape, out, q.device, stream)
-    code = torch_dtype_code(out.dtype)
-    qp, sp = _checkpoint("q", q, scale, q.shape, dev)
-    op = _dense("out", out, out.dtype, q.shape, dev)
-    _run(dev, stream, lib().mm_checkpoint_unpack, qp, sp, rows, cols, code, op)
+        out = _empty(shape, out, q.device, stream)
+    dt = out.dtype
+    code = torch_dtype_code(dt)
+    qp, sp = _checkpoint("q", q, scale, shape, dev)
+    op = _dense("out", out, dt, shape, dev)
+    _run(dev, stream, (_lib or lib()).mm_checkpoint_unpack, qp, sp, rows, cols, code, op)
     return out
 
 
