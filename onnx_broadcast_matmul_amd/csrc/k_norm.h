@@ -162,7 +162,7 @@ __device__ __forceinline__ void keep_number(int &t) { asm("" : "+v"(t)); }
 
 constexpr int kFwdCols = 16;  // columns of a thread
 
-// A workgroup takes every gridDim-th row (or four, a wave each); in 16-bit types
+// A workgroup takes every gridDim-th row (or four of a wave, two of two); in 16-bit types
 // it asks for the next one before it works on the present one and keeps the
 // weights in registers as they lie in memory.  The row is the same for a whole
 // wave and kept in scalar registers, its addresses with it.  ALL: layer norms,
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
     RowSums<NT, TPR> sums{part};
     int t = threadIdx.x % TPR;
     const int N = a.N;
-    const int slot = TPR == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
+    const int slot = TPR < 256 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
     const int step = (int)gridDim.x * SLOTS;
     const bool edge = N % VE != 0, ragged = N < TPR * kFwdCols;
     const float inv_n = 1.0f / (float)N;
@@ -386,6 +386,7 @@ template <int DT>
 static hipError_t fwd(bool train, const NormFwdTrain &a, hipStream_t s) {
     if (a.N > 1024 * kFwdCols) return hipErrorInvalidValue;
     if (a.N <= 64 * kFwdCols) return fwd<DT, 64>(train, a, s);
+    if (a.N <= 128 * kFwdCols) return fwd<DT, 128>(train, a, s);
     if (a.N <= 256 * kFwdCols) return fwd<DT, 256>(train, a, s);
     if (a.N <= 512 * kFwdCols) return fwd<DT, 512>(train, a, s);
     return fwd<DT, 1024>(train, a, s);
