@@ -26,9 +26,9 @@
 // on, where a product of 8192^3 reaches 1.55 at the clock that random operands
 // leave.  A round of tiles of 256 x 256 takes 10 us and 21 ns for each k, one of 256 x
 // 128 7 us and 12 ns; the 10 us are the first loads' way and the epilogue, during
-// which a CU's one workgroup feeds no matrix core (with a residual 40 us of 530 at
-// 8192 x 4096 x 10240, its 168 MB read in bursts; Z in 16 bits 30, as a checkpoint
-// 45, in FP32 85).
+// which a CU's one workgroup feeds no matrix core (8192 x 4096 x 10240, 475 us: tanh
+// gelu 14 us more, a residual, whose 168 MB are read in bursts, 37, Z in 16 bits 20,
+// as a checkpoint 30, in FP32 50).
 #pragma once
 
 #include <type_traits>
@@ -248,7 +248,9 @@ __global__ __launch_bounds__(256, 1) void k_big(FfnSlim a) {
 #pragma unroll
                 for (int h = 0; h < size / 2; ++h) {
                     U4 v = {w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
-                    __builtin_nontemporal_store(v, (U4 *)dst + h);
+                    // (halves of 32 bytes meet in the cache)
+                    if (size == 4) *((U4 *)dst + h) = v;
+                    else __builtin_nontemporal_store(v, (U4 *)dst + h);
                 }
             }
             return;
@@ -337,38 +339,41 @@ __global__ __launch_bounds__(256, 1) void k_big(FfnSlim a) {
             for (int x = 0; x < GR; ++x) r[x] = rv[x];
             if (a.R() && g + 1 < 2 * STEPS) ask(g + 1);
             each([&](float &z, int e) { z += bias[e]; });
-            if (a.G()) {
+            if (a.G() && a.q8()) {
+                // Columns past the last hold 0, or NaN where the whole row is NaN or
+                // infinite: neither changes a block.
+                uint32_t ex[GR], w[GR][2];
+#pragma unroll
+                for (int x = 0; x < GR; ++x) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = max(top, ck_magnitude(v[x][e]));
+                    ex[x] = ck_exponent(block_top<8>(top));
+                    const float inv = ck_inverse(ex[x]);
+                    w[x][0] = ck_word(v[x][0], v[x][1], v[x][2], v[x][3], inv);
+                    w[x][1] = ck_word(v[x][4], v[x][5], v[x][6], v[x][7], inv);
+                }
 #pragma unroll
                 for (int x = 0; x < GR; ++x) {
                     const int64_t row = row_of(g, x);
+                    if (row >= M || in == 0) continue;
+                    if ((c8 & 3) == 0) ((uint8_t *)a.zs())[row * ((a.ldy + 31) / 32) + col / 32] = (uint8_t)ex[x];
+                    put8(a.G(), 1, row, a.kept_vec(), w[x]);
+                }
+            } else if (a.G()) {
+#pragma unroll
+                for (int x = 0; x < GR; ++x) {
+                    const int64_t row = row_of(g, x);
+                    if (row >= M || in == 0) continue;
                     uint32_t w[8];
-                    if (a.q8()) {
-                        uint32_t top = 0;
+                    if (a.kept32()) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t b = ck_magnitude(v[x][e]);
-                            if (e < in) top = b > top ? b : top;
-                        }
-                        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-                        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-                        const uint32_t ex = ck_exponent(top);
-                        const float inv = ck_inverse(ex);
-                        w[0] = ck_word(v[x][0], v[x][1], v[x][2], v[x][3], inv);
-                        w[1] = ck_word(v[x][4], v[x][5], v[x][6], v[x][7], inv);
-                        if (row < M && in > 0) {
-                            if ((c8 & 3) == 0) ((uint8_t *)a.zs())[row * ((a.ldy + 31) / 32) + col / 32] = (uint8_t)ex;
-                            put8(a.G(), 1, row, a.kept_vec(), w);
-                        }
-                    } else if (row < M && in > 0) {
-                        if (a.kept32()) {
+                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[x][e]);
+                        put8(a.G(), 4, row, a.kept_vec(), w);
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[x][e]);
-                            put8(a.G(), 4, row, a.kept_vec(), w);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = E::pack2(v[x][2 * e], v[x][2 * e + 1]);
-                            put8(a.G(), 2, row, a.kept_vec(), w);
-                        }
+                        for (int e = 0; e < 4; ++e) w[e] = E::pack2(v[x][2 * e], v[x][2 * e + 1]);
+                        put8(a.G(), 2, row, a.kept_vec(), w);
                     }
                 }
             }

@@ -71,7 +71,7 @@ __device__ __forceinline__ uint4 row_piece(GlobalPtr<S> p, int64_t left, bool ba
 // loads of all of them first, without a test (rows of at least a piece: a
 // piece that would pass the row's end ends there), and what the end needs where
 // they are used.  row_piece waits for its piece before the next one is asked for
-// (8192 x 4096 BF16 norms forward: 74.8 us so, 50 in two steps).
+// (8192 x 4096 BF16 norms forward: 75 us so, 61 in two steps).
 // The offset is 32 bits of bytes, so that a row whose address is uniform takes
 // one register for it.  ONCE: a tensor that is streamed through (see
 // stream_piece).
