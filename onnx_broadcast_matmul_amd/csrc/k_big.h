@@ -419,12 +419,12 @@ static hipError_t launch_big(const FfnArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Whether the kernel takes a product (entries 0 and 4, whole K): buffer offsets are 32-bit, and operand
-// rows whole, aligned 16-byte chunks (`vec`).
+// Whether the kernel takes a product (entries 0 and 4, whole K): buffer offsets are
+// 32-bit, and operand rows whole, aligned 16-byte chunks (`vec`).
 inline bool big_fits(bool ta, bool tb, int tile, bool split, bool vec, const FfnArgs &a) {
     if ((tile != 0 && tile != 4) || split) return false;
-    const int64_t span_a = (ta ? 64 : 256) * a.lda * 2, span_b = (tb ? 256 : 64) * a.ldb * 2, span_r = a.R ? 256 * a.ldy * 2 : 0;
-    return vec && span_a < 0x7fff0000LL && span_b < 0x7fff0000LL && span_r < 0x7fff0000LL;
+    const int64_t span_a = (ta ? 64 : 256) * a.lda * 2, span_b = (tb ? 256 : 64) * a.ldb * 2;
+    return vec && span_a < 0x7fff0000LL && span_b < 0x7fff0000LL;
 }
 
 }  // namespace mm

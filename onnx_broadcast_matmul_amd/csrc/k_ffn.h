@@ -696,7 +696,8 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void k_ffn(typename std::condi
         // anything else is done here: lane l of the lower half takes quarters 0
         // and 1 of both halves' columns, lane l + 32 quarters 2 and 3, and two
         // registers' halves are swapped.  (Four columns a lane and when they are
-        // wanted: 8192 x 4096 x 11008 BF16 77 us more than no residual.)
+        // wanted: 77 us more than no residual on 256 x 256 tiles at 8192 x 4096 x
+        // 11008 BF16, so 53.)
         constexpr bool WIDE_R = OD != MM_FLOAT && KG <= 2;
         uint4 rv[WIDE_R ? FM : 1][WIDE_R ? FNP : 1][2];
         const bool wide_r = WIDE_R && a.R() && a.r_vec();
@@ -877,9 +878,9 @@ template <int DT, int OD, int MODE, bool SPLIT, bool TA, bool TB>
 static hipError_t launch_entry(int tile, bool vec, const FfnArgs &a, hipStream_t s) {
     switch (tile) {
     case 0:
-        // FLOAT fills the matrix cores with smaller tiles, and partial sums
-        // of 256 x 256 tiles are never wanted.
-        if constexpr (DT != MM_FLOAT && !SPLIT) return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 256, 256, 2, 4, 1, 64, 4, 4>(vec, a, s);
+        // FLOAT fills the matrix cores with smaller tiles, partial sums of 256 x
+        // 256 tiles are never wanted, and the linear layer has k_big.h's.
+        if constexpr (DT != MM_FLOAT && !SPLIT && MODE != kLinear) return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 256, 256, 2, 4, 1, 64, 4, 4>(vec, a, s);
         break;
     case 1: return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 128, 128, 2, 2, 1, 64, 4, 4>(vec, a, s);
     case 2: return launch_ffn<DT, OD, MODE, SPLIT, TA, TB, 64, 128, 2, 2, 2, 128, 3, 4>(vec, a, s);

@@ -24,6 +24,7 @@ hipError_t launch_glu_dw(int dtype, int tile, bool split, bool vec, const FfnArg
                           : launch_big<DT, false, false, true, 128>(a, s);                                \
             }                                                                                             \
         }                                                                                                 \
+        if (tile == 0) tile = 1; /* rows off alignment, or too far apart */                               \
         if (split)                                                                                        \
             return tb ? launch_entry<DT, DT, kLinear, true, false, true>(tile, vec, a, s)                 \
                       : launch_entry<DT, DT, kLinear, true, false, false>(tile, vec, a, s);               \

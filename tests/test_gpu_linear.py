@@ -354,6 +354,24 @@ def test_linear_whole_rounds_and_a_rest(nk, z, dev):
         assert 0 < p.info()["tail_col"] < n
 
 
+@pytest.mark.parametrize("n,pitch", [(256, 4190000), (8, 1 << 22)])
+def test_linear_rows_far_apart(n, pitch, dev):
+    """A large tile's rows within 2^31 bytes of each other, and farther (other entries then)."""
+    m, k = 300, 72
+    wide = torch.empty(n, pitch, dtype=BF16, device=dev)
+    w = wide[:, :k]
+    w.copy_(rand((n, k), BF16, dev, 1, k ** -0.5))
+    x, dy = rand((m, k), BF16, dev, 2), rand((m, n), BF16, dev, 3)
+    for tile in (1, 5):
+        p = mm.LinearPlan(m, k, n, mm.BFLOAT16, trans_w=True, training=True, w_pitch=pitch, force_algo=mm.ALGO_GENERAL,
+                          tile=tile, dx_tile=tile, dw_tile=tile)
+        y, dx = torch.empty(m, n, dtype=BF16, device=dev), torch.empty(m, k, dtype=BF16, device=dev)
+        p.execute(x, w, y)
+        within(y, *linear64(x, w.t(), None, None, "none", BF16)[0], "Y")
+        p.backward(x, w, dy, dX=dx)
+        within(dx, *backward64(x, torch.zeros_like(x).double(), w.t(), None, dy, "none", BF16)[0], "dX")
+
+
 # ---- linear layer, backward
 
 
