@@ -503,7 +503,9 @@ mm_status mm_checkpoint_unpack(const void *q, const void *scale, int64_t rows, i
  *
  *   Z = X W + bias      Y = f(Z) + residual
  *
- * in one kernel (two where K is split), and its backward pass from dY:
+ * in one kernel (two where K is split, or where the columns behind the last
+ * whole round of workgroups run on another tile entry: mm_plan_info.tail_col),
+ * and its backward pass from dY:
  *
  *   dZ = dY * f'(Z)    dX = dZ W^T    dW = X^T dZ    dbias[n] = sum_m dZ[m][n]
  *
@@ -556,8 +558,8 @@ typedef struct mm_linear_desc {
 mm_status mm_linear_plan_create(const mm_linear_desc *desc, int dtype, const mm_plan_options *opt, mm_plan_t *out);
 
 /* The descriptor of a linear-layer plan, its type and option fields as
- * resolved (a training plan's backward tiling; z_type 0 where nothing is
- * kept). */
+ * resolved (a training plan's backward tiling, of dX and dW without a second
+ * launch's; z_type 0 where nothing is kept). */
 mm_status mm_linear_get_desc(mm_plan_t plan, mm_linear_desc *desc);
 
 /* Enqueue the forward pass on `stream`.  bias and residual are non-NULL exactly

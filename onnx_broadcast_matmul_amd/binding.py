@@ -965,9 +965,11 @@ class NormPlan(Plan):
         return None if t is None else _dense(name, t, self._dt, shape, dev)
 
     def _gate(self, name, t, dev):
-        if t is not None and self._g is None:
+        if t is None:
+            return None
+        if self._g is None:
             raise ValueError(f"{name}: the plan has no gate")
-        return self._one(name, t, dev, self._g)
+        return _dense(name, t, self._dt, self._g, dev)
 
     def _pair(self, name, pair, dev):
         return (None, None) if pair is None else _checkpoint(name, pair[0], pair[1], self._x, dev)
@@ -986,9 +988,13 @@ class NormPlan(Plan):
             self._one("pre_weight", pre_weight, dev, w), self._one("pre_bias", pre_bias, dev, w),
             self._one("sum", sum, dev, x), self._one("out", out, dev, x),
             None if stats is None else _dense("stats", stats, self._f32, self._stats, dev),
-            None if sum_f32 is None else _dense("sum_f32", sum_f32, self._f32, x, dev),
-            *self._pair("sum_checkpoint", sum_checkpoint, dev), *self._pair("block_checkpoint", block_checkpoint, dev),
-            *self._pair("out_checkpoint", out_checkpoint, dev))
+            None if sum_f32 is None else _dense("sum_f32", sum_f32, self._f32, x, dev))
+        if sum_checkpoint is not None:
+            args.sum_q, args.sum_scale = _checkpoint("sum_checkpoint", *sum_checkpoint, x, dev)
+        if block_checkpoint is not None:
+            args.block_q, args.block_scale = _checkpoint("block_checkpoint", *block_checkpoint, x, dev)
+        if out_checkpoint is not None:
+            args.out_q, args.out_scale = _checkpoint("out_checkpoint", *out_checkpoint, x, dev)
         with self._lock:
             _run(dev, stream, self._execute, self._handle, args)
 
