@@ -39,10 +39,10 @@ __device__ __forceinline__ float wave_sum(float x) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
-// Sums of two values (`both`, else of the second) over the TPR threads of a row.  Above a wave they meet in
-// LDS; `turn` alternates between two buffers, so that one barrier serves: a
-// buffer is written again only after the next sum's barrier, which every
-// reader has passed.
+// Sums of two values (`both`, else of the second) over the TPR threads of a row.
+// Above a wave they meet in LDS; `turn` alternates between two buffers, so that
+// one barrier serves: a buffer is written again only after the next sum's barrier,
+// which every reader has passed.
 template <int NT, int TPR>
 struct RowSums {
     static constexpr int W = TPR / 64;
@@ -156,15 +156,23 @@ __device__ __forceinline__ void keep_packed(uint4 (&p)[CH]) {
     for (int i = 0; i < CH; ++i) asm("" : "+v"(p[i].x), "+v"(p[i].y), "+v"(p[i].z), "+v"(p[i].w));
 }
 
+// The same for one piece until `late` is known: FP16 ones otherwise are taken apart
+// before the sums over the row, for which there are no registers (8192 x 4096, RMS
+// norms on both sides: 67 us with what went to scratch, 52 so).
+__device__ __forceinline__ uint4 packed_until(uint4 p, float late) {
+    asm("" : "+v"(p.x), "+v"(p.y), "+v"(p.z), "+v"(p.w) : "v"(late));
+    return p;
+}
+
 __device__ __forceinline__ void keep_number(int &t) { asm("" : "+v"(t)); }
 
 // ---- forward
 
 constexpr int kFwdCols = 16;  // columns of a thread
 
-// A workgroup takes every gridDim-th row (or four of a wave, two of two); in 16-bit types
-// it asks for the next one before it works on the present one and keeps the
-// weights in registers as they lie in memory.  The row is the same for a whole
+// A workgroup takes every gridDim-th row (or four of a wave, two of two); in
+// 16-bit types it asks for the next one before it works on the present one and
+// keeps weights and biases in registers as they lie in memory.  The row is the same for a whole
 // wave and kept in scalar registers, its addresses with it.  ALL: layer norms,
 // biases and rows that are no whole number of pieces (see k_norm_bwd).
 template <int DT, int TPR, bool TRAIN, bool ALL>
@@ -207,14 +215,45 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
     // Rows of a workgroup run together: all of them pass the barriers.
     int first = (int)blockIdx.x * SLOTS;
     auto row_at = [&](int f) { return f < a.M - slot ? f + slot : a.M - 1; };
-    uint4 xr[CH] = {}, br[CH] = {}, xn[CH] = {}, bn[CH] = {}, gr[CH], w1[CH], w2[CH];
+    uint4 xr[CH] = {}, br[CH] = {}, xn[CH] = {}, bn[CH] = {}, gr[CH], w1[CH], w2[CH], b1[CH], b2[CH];
+    int change = 0;  // the row at which the next group of gate rows begins
+    auto gate_group = [&](int row) {
+        const int group = (int)((uint32_t)row / (uint32_t)a.gate_rows);
+        const int64_t next = (int64_t)(group + 1) * a.gate_rows;
+        change = next < a.M ? (int)next : a.M;
+        return group;
+    };
     if constexpr (HOLD) {
+        // Everything that the first row needs is asked for at once.
         load(row_at(first), xn, bn);
+        const int group = a.gate ? gate_group(row_at(first)) : 0;
+        auto ask = [&](const void *w, int row, int i) {
+            return w && col(i) < N ? piece_load<DT, false, ALL>(w, row, N, col(i)) : make_uint4(0, 0, 0, 0);
+        };
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            w1[i] = weight_or(piece_ones<DT>(), a.w1, 0, i);
-            w2[i] = weight_or(piece_ones<DT>(), a.w2, 0, i);
-            gr[i] = piece_ones<DT>();
+            gr[i] = ask(a.gate, group, i);
+            w1[i] = ask(a.w1, 0, i);
+            w2[i] = ask(a.w2, 0, i);
+            if constexpr (ALL) {
+                b1[i] = ask(a.b1, 0, i);
+                b2[i] = ask(a.b2, 0, i);
+            }
+        }
+        if constexpr (ALL) {
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+                    if (col(i) < N)
+                        for (uint4 *v : {&gr[i], &w1[i], &w2[i], &b1[i], &b2[i]})
+                            *v = edge_piece<typename Elem<DT>::S>(*v, N, col(i));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            if (!a.gate) gr[i] = piece_ones<DT>();
+            if (!a.w1) w1[i] = piece_ones<DT>();
+            if (!a.w2) w2[i] = piece_ones<DT>();
         }
     }
     // Mean and reciprocal deviation of v.
@@ -243,7 +282,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
         return make_float2(mean, 1.0f / sqrtf(sums(false, 0.0f, s).y * inv_n + eps));
     };
     // v = (v - mean) r w + b.
-    auto normalise = [&](float (*v)[VE], int kind, const float2 &m, const void *w, const uint4 *held, const void *b) {
+    auto normalise = [&](float (*v)[VE], int kind, const float2 &m, const void *w, const uint4 *held, const void *b,
+                         const uint4 *held_b) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             float y[VE];
@@ -251,12 +291,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
 #pragma unroll
                 for (int e = 0; e < VE; ++e) v[i][e] -= m.x;
             }
-            if constexpr (HOLD) piece_floats<DT>(held[i], y);
+            if constexpr (HOLD) piece_floats<DT>(packed_until(held[i], m.y), y);
             else piece_floats<DT>(weight_or(piece_ones<DT>(), w, 0, i), y);
 #pragma unroll
             for (int e = 0; e < VE; ++e) v[i][e] = v[i][e] * m.y * y[e];
             if (ALL && b) {
-                piece_floats<DT>(weight_or(make_uint4(0, 0, 0, 0), b, 0, i), y);
+                if constexpr (HOLD) piece_floats<DT>(packed_until(held_b[i], m.y), y);
+                else piece_floats<DT>(weight_or(make_uint4(0, 0, 0, 0), b, 0, i), y);
 #pragma unroll
                 for (int e = 0; e < VE; ++e) v[i][e] += y[e];
             }
@@ -271,13 +312,16 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
             for (int e = 0; e < VE; ++e)
                 if (col(i) + e >= N) v[i][e] = 0.0f;
     };
-    int change = 0;  // the row at which the next group of gate rows begins
     for (; first < a.M; first += step) {
         keep_number(t);
         if constexpr (HOLD) {
             keep_packed(w1);
             keep_packed(w2);
             keep_packed(gr);
+            if constexpr (ALL) {
+                keep_packed(b1);
+                keep_packed(b2);
+            }
         }
         const bool live = first < a.M - slot;
         const int row = row_at(first);
@@ -296,14 +340,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
         float v[CH][VE];
         if (a.B) {
             settle(br);
-            const int group = a.gate ? (int)((uint32_t)row / (uint32_t)a.gate_rows) : 0;
+            int group = 0;
             if constexpr (HOLD) {
                 if (a.gate && row >= change) {
-                    const int64_t next = (int64_t)(group + 1) * a.gate_rows;
-                    change = next < a.M ? (int)next : a.M;
+                    group = gate_group(row);
 #pragma unroll
                     for (int i = 0; i < CH; ++i) gr[i] = weight_or(piece_ones<DT>(), a.gate, group, i);
                 }
+            } else if (a.gate) {
+                group = (int)((uint32_t)row / (uint32_t)a.gate_rows);
             }
 #pragma unroll
             for (int i = 0; i < CH; ++i) piece_floats<DT>(br[i], v[i]);
@@ -315,13 +360,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
             }
             if (a.post != MM_NORM_NONE) {
                 m1 = moments(a.post, a.eps1, v);
-                normalise(v, a.post, m1, a.w1, w1, a.b1);
+                normalise(v, a.post, m1, a.w1, w1, a.b1, b1);
             }
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 float w[VE], x[VE];
-                piece_floats<DT>(xr[i], x);
-                if constexpr (HOLD) piece_floats<DT>(gr[i], w);
+                piece_floats<DT>(HOLD ? packed_until(xr[i], m1.y) : xr[i], x);
+                if constexpr (HOLD) piece_floats<DT>(packed_until(gr[i], m1.y), w);
                 else piece_floats<DT>(weight_or(piece_ones<DT>(), a.gate, group, i), w);
 #pragma unroll
                 for (int e = 0; e < VE; ++e) v[i][e] = fmaf(a.alpha * w[e], v[i][e], x[e]);
@@ -349,7 +394,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
         }
         if (a.pre != MM_NORM_NONE) {
             m2 = moments(a.pre, a.eps2, v);
-            normalise(v, a.pre, m2, a.w2, w2, a.b2);
+            normalise(v, a.pre, m2, a.w2, w2, a.b2, b2);
             if (TRAIN) cut(v);
             if (live) {
 #pragma unroll
