@@ -25,12 +25,14 @@
 // layout, so odd sizes run on the same matrix-core loop (512 x 2560 x 5504 gated,
 // BF16: 41 us, with K = 2561 65).
 //
-// What bounds it.  Large products: power.  8192 x 4096 x 11008 in BF16 takes 1.20
-// ms gated (1.23 PFLOP/s), 1.17 for dX, 1.32 for dWg and dWu, and 0.36 in INT8
-// (2.07 POP/s); the matrix cores are busy 67-73 % of the cycles at the clock
+// What bounds it.  Large products: power and issue.  8192 x 4096 x 11008 in BF16
+// takes 1.20 ms gated (1.23 PFLOP/s), 1.17 for dX, 1.32 for dWg and dWu, and 0.36
+// in INT8 (2.07 POP/s); the matrix cores are busy 67-73 % of the cycles at the clock
 // that random operands leave (zeros, which take less power, run at 1.5-1.6
-// PFLOP/s).  A persistent form, which loads the next tile's first stages during
-// the epilogue, gained nothing there and took 10 % more for INT8.  Products
+// PFLOP/s).  The order of instructions has its part in it: four waves in the order
+// of k_big.h reach 1.3 to 1.48 on one matrix.  A persistent form, which loads the
+// next tile's first stages during the epilogue, gained nothing there and took 10 %
+// more for INT8.  Products
 // of about one tile per CU: the 256 x 128 tile's shorter runs of MFMAs (48 % busy:
 // 4096 x 2048 x 5504, dX 0.20 ms) and the ends of a tile, which no other work
 // covers (1000 x 1024 x 4096 gated: 23 us, 15 of them in the K loop).
