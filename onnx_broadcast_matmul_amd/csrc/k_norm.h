@@ -95,7 +95,7 @@ __device__ __forceinline__ uint4 piece_load(const void *p, int64_t row, int N, i
         return ONCE ? stream_piece<S>(at) : whole_piece<S>(at);
     }
     if (!p) return make_uint4(0, 0, 0, 0);
-    return edge_load<S, ONCE>((GlobalPtr<S>)((const S *)p + row * N), N, c);
+    return edge_load<S, ONCE, uint32_t>((GlobalPtr<S>)((const S *)p + row * N), N, c);  // (of at most MM_NORM_MAX_COLS)
 }
 // x rounded to the type.
 template <int DT>

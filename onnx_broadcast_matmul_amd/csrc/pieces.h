@@ -72,15 +72,15 @@ __device__ __forceinline__ uint4 row_piece(GlobalPtr<S> p, int64_t left, bool ba
 // piece that would pass the row's end ends there), and what the end needs where
 // they are used.  row_piece waits for its piece before the next one is asked for
 // (8192 x 4096 BF16 norms forward: 75 us so, 61 in two steps).
-// The offset is 32 bits of bytes, so that a row whose address is uniform takes
-// one register for it.  ONCE: a tensor that is streamed through (see
-// stream_piece).
-template <typename S, bool ONCE = false>
+// ONCE: a tensor that is streamed through (see stream_piece).  Offset: holds the
+// row's bytes.  A row may be longer than 2^32 bytes; where it cannot be, 32 bits are
+// one register for a row whose address is uniform.
+template <typename S, bool ONCE = false, typename Offset = uint64_t>
 __device__ __forceinline__ uint4 edge_load(GlobalPtr<S> row, int n, int c) {
     constexpr int ES = (int)sizeof(S), VE = 16 / ES;
     using Bytes = const __attribute__((address_space(1))) char *;
     if (n >= VE) {
-        const GlobalPtr<S> p = (GlobalPtr<S>)((Bytes)row + (uint32_t)((c < n - VE ? c : n - VE) * ES));
+        const GlobalPtr<S> p = (GlobalPtr<S>)((Bytes)row + (Offset)(uint32_t)(c < n - VE ? c : n - VE) * ES);
         return ONCE ? stream_piece<S>(p) : whole_piece<S>(p);
     }
     S tmp[VE];  // the whole row

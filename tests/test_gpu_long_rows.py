@@ -1,0 +1,78 @@
+"""Rows of the operators around a residual block past 2^32 bytes and near the
+limits of their sizes.
+
+Tensors repeat a pattern of P values, P prime, so that an offset which wraps
+reads other values.  Checkpoints and products by powers of two are exact.
+"""
+import numpy as np
+import pytest
+
+from onnx_broadcast_matmul_amd import binding as mm
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_ffn import BF16, F32, check_guard, guarded, rand  # noqa: E402
+from test_gpu_linear import pack64  # noqa: E402
+
+P = 1_000_003
+FAR = 1 << 30  # FP32 elements in 2^32 bytes
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    mm.lib()
+    return torch.device("cuda:0")
+
+
+@pytest.fixture(autouse=True)
+def empty():
+    yield
+    torch.cuda.empty_cache()
+
+
+def fill(t, seed):
+    """The pattern over a dense tensor: blocks of many magnitudes."""
+    one = rand((P,), F32, t.device, seed) * torch.exp2(torch.arange(P, device=t.device) // 32 % 40 - 20.0)
+    flat, one = t.view(-1), one.to(t.dtype)
+    whole = flat.numel() // P * P
+    flat[:whole].view(-1, P).copy_(one)
+    flat[whole:].copy_(one[:flat.numel() - whole])
+    return t
+
+
+def blocks_to_check(cols):
+    nb, rng = -(-cols // 32), np.random.default_rng(3)
+    near = [0, 1, FAR // 32 - 1, FAR // 32, FAR // 32 + 1, nb - 3, nb - 2, nb - 1]
+    return sorted(b for b in {*near, *rng.integers(0, nb, 20).tolist()} if 0 <= b < nb)
+
+
+def check_checkpoint(x, q, s, back):
+    cols = x.shape[1]
+    for b in blocks_to_check(cols):
+        at = slice(32 * b, min(32 * b + 32, cols))
+        wq, ws, wv = pack64(x[:, at])
+        assert np.array_equal(q[:, at].cpu().numpy(), wq) and np.array_equal(s[:, b:b + 1].cpu().numpy(), ws), b
+        assert np.array_equal(back[:, at].double().cpu().numpy(), wv), b
+
+
+def test_checkpoint_of_an_fp32_row_past_4gib(dev):
+    cols = FAR + 69
+    x = fill(torch.empty(1, cols, device=dev), 1)
+    q, s = mm.checkpoint_pack(x)
+    check_checkpoint(x, q, s, mm.checkpoint_unpack(q, s, F32))
+
+
+def test_linear_backward_of_fp32_rows_past_4gib(dev):
+    """One token, one input feature: dW = x dY where Z > 0."""
+    n = FAR + 69
+    p = mm.LinearPlan(1, 1, n, mm.FLOAT, activation=mm.ACT_RELU, training=True, force_algo=mm.ALGO_GENERAL, tile=2,
+                      dx_tile=2, dw_tile=2)
+    dy, z = fill(torch.empty(1, n, device=dev), 2), fill(torch.empty(1, n, device=dev), 3)
+    dw = torch.empty(1, n, device=dev)
+    p.backward(torch.full((1, 1), 2.0, device=dev), None, dy, Z=z, dW=dw)
+    for i in range(0, n, 1 << 28):
+        at = slice(i, min(i + (1 << 28), n))
+        assert torch.equal(dw[:, at], torch.where(z[:, at] > 0, 2.0 * dy[:, at], 0.0)), i
