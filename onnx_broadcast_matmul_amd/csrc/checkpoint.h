@@ -100,7 +100,7 @@ __device__ __forceinline__ void unpack_bytes(uint32_t w, float s, float m, float
 // streamed through (see pieces.h).
 template <int VE>
 __device__ __forceinline__ void ck_load(const int8_t *row, int n, int c, uint32_t *w) {
-    if (c + VE <= n) {
+    if (c <= n - VE) {
         if constexpr (VE == 4) {
             w[0] = __builtin_nontemporal_load((const u32u *)(row + (uint32_t)c));
         } else {
@@ -120,7 +120,7 @@ __device__ __forceinline__ void ck_load(const int8_t *row, int n, int c, uint32_
 // Words of numbers to a row of n at c, as far as it goes.
 template <int VE>
 __device__ __forceinline__ void ck_store(int8_t *row, int n, int c, const uint32_t *w) {
-    if (c + VE <= n) {
+    if (c <= n - VE) {
         if constexpr (VE == 4) {
             __builtin_nontemporal_store(w[0], (u32u *)(row + (uint32_t)c));
         } else {

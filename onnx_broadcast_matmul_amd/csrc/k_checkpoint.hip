@@ -97,7 +97,7 @@ __global__ __launch_bounds__(256) void k_checkpoint_unpack(const int8_t *q, cons
         S *y = (S *)X + at[u];
         uint4 v;
         __builtin_memcpy(&v, o, 16);
-        if (FLAT || col[u] + VE <= n) stream_store(y, v);
+        if (FLAT || col[u] <= n - VE) stream_store(y, v);
         else
 #pragma unroll
             for (int i = 0; i < VE; ++i)

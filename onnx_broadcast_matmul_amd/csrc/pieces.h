@@ -91,12 +91,13 @@ __device__ __forceinline__ uint4 edge_load(GlobalPtr<S> row, int n, int c) {
     return v;
 }
 
-// What edge_load read at c of a row of n: the piece, zeros past the end.
+// What edge_load read at c of a row of n: the piece, zeros past the end.  (c + VE
+// may pass 2^31 in a row of nearly as many.)
 template <typename S>
 __device__ __forceinline__ uint4 edge_piece(uint4 v, int n, int c) {
     constexpr int ES = (int)sizeof(S), VE = 16 / ES;
-    if (c + VE <= n || (n < VE && c == 0)) return v;
-    const int miss = c + VE - n;
+    if (c <= n - VE || (n < VE && c == 0)) return v;
+    const int miss = VE - (n - c);
     uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
     const int sh = miss * ES * 8;
     if (miss >= VE) {

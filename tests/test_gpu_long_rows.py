@@ -76,3 +76,20 @@ def test_linear_backward_of_fp32_rows_past_4gib(dev):
     for i in range(0, n, 1 << 28):
         at = slice(i, min(i + (1 << 28), n))
         assert torch.equal(dw[:, at], torch.where(z[:, at] > 0, 2.0 * dy[:, at], 0.0)), i
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("cols", [(1 << 31) - 1, (1 << 31) - 7, (1 << 31) - 31])
+def test_checkpoint_of_the_longest_rows(cols, dt, dev):
+    """The last piece ends at the row's last element: nothing behind it is
+    written, and nothing behind it is read into the last block."""
+    x, _ = guarded((1, cols), dt, dev)
+    fill(x, 4)
+    q, qbuf = guarded((1, cols), torch.int8, dev)
+    s = torch.empty(1, mm.checkpoint_blocks(cols), dtype=torch.uint8, device=dev)
+    mm.checkpoint_pack(x, q, s)
+    back, bbuf = guarded((1, cols), dt, dev)
+    mm.checkpoint_unpack(q, s, back)
+    check_checkpoint(x, q, s, back)
+    check_guard(qbuf, q)
+    check_guard(bbuf, back)
