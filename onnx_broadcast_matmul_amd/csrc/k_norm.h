@@ -312,7 +312,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
             for (int e = 0; e < VE; ++e)
                 if (col(i) + e >= N) v[i][e] = 0.0f;
     };
-    for (; first < a.M; first += step) {
+    for (;;) {
         keep_number(t);
         if constexpr (HOLD) {
             keep_packed(w1);
@@ -410,6 +410,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
         if constexpr (TRAIN) {
             if (a.stats && live && t == 0) *(float4 *)(a.stats + (int64_t)row * 4) = make_float4(m1.x, m1.y, m2.x, m2.y);
         }
+        if (first >= a.M - step) break;  // (first + step may pass 2^31)
+        first += step;
     }
 }
 

@@ -93,3 +93,34 @@ def test_checkpoint_of_the_longest_rows(cols, dt, dev):
     check_checkpoint(x, q, s, back)
     check_guard(qbuf, q)
     check_guard(bbuf, back)
+
+
+def test_norm_of_as_many_rows_as_there_may_be(dev):
+    """Rows of one column: the step behind the last ones passes 2^31.  With eps 1
+    and r = 1 / sqrt(x^2 + 1), y = x r and dX = dsum + dout r^3."""
+    m = (1 << 31) - 65
+    p = mm.NormPlan(m, 1, mm.BFLOAT16, block=False, pre_weight=False, pre_eps=1.0, training=True)
+    x, xbuf = guarded((m, 1), BF16, dev)
+    flat = x.view(-1)
+    one = (rand((P,), F32, dev, 5) * 3).to(BF16)
+    whole = m // P * P
+    flat[:whole].view(-1, P).copy_(one)
+    flat[whole:].copy_(one[:m - whole])
+    y, ybuf = guarded((m, 1), BF16, dev)
+    stats = torch.empty(m, 4, device=dev)
+    p.execute(x, y, stats=stats)
+    dx, dbuf = guarded((m, 1), BF16, dev)
+    p.backward(stats, sum=x, dout=y, dsum=x, dX=dx)
+    torch.cuda.synchronize()
+    for buf, t in ((xbuf, x), (ybuf, y), (dbuf, dx)):
+        check_guard(buf, t)
+    size = 1 << 26
+    for i in sorted({*range(0, m, 7 * size), m - size}):
+        at = slice(i, min(i + size, m))
+        v = x[at].double()
+        r = (v * v + 1) ** -0.5
+        # a rounding to BF16, and some FP32 operations on values below 1
+        assert bool(((y[at].double() - v * r).abs() <= 2.0 ** -8 * (v * r).abs() + 2.0 ** -21).all()), i
+        want = v + y[at].double() * r ** 3
+        assert bool(((dx[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * (1 + v.abs())).all()), i
+        assert bool(((stats[at, 3].double() - r[:, 0]).abs() <= 2.0 ** -21 * r[:, 0]).all()), i
