@@ -293,16 +293,18 @@ hipError_t launch_linear_prep(int dtype, const LinearPrep &a, hipStream_t s) {
 template <int DT>
 __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
     using E = Elem<DT>;
-    const int64_t c0 = (int64_t)blockIdx.x * 32;
+    const int64_t c0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 32;
+    if (c0 >= a.N) return;
     const float v = join_columns(a.P, a.ldp - c0, [&](int64_t i) { return a.part + i * a.ldp + c0; });
     if (threadIdx.x < 32 && c0 + threadIdx.x < a.N) ((typename E::S *)a.out)[c0 + threadIdx.x] = E::from_f32(v);
 }
 
 hipError_t launch_join(int dtype, const JoinArgs &a, hipStream_t s) {
-    const int64_t g = (a.N + 31) / 32;
+    // One dimension of a grid holds less than 2^32 threads: 2^29 columns.
+    const int64_t g = (a.N + 31) / 32, gx = g < (1 << 23) ? g : (1 << 23);
     if (g <= 0) return hipSuccess;
-    if (g > 0xffffff) return hipErrorInvalidValue;
-    const dim3 gr((unsigned)g), bl(256);
+    if (g > 0x7ffffff) return hipErrorInvalidValue;
+    const dim3 gr((unsigned)gx, (unsigned)((g + gx - 1) / gx)), bl(256);
     if (dtype == MM_FLOAT) hipLaunchKernelGGL(k_join<MM_FLOAT>, gr, bl, 0, s, a);
     else if (dtype == MM_FLOAT16) hipLaunchKernelGGL(k_join<MM_FLOAT16>, gr, bl, 0, s, a);
     else hipLaunchKernelGGL(k_join<MM_BFLOAT16>, gr, bl, 0, s, a);

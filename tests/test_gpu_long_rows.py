@@ -124,3 +124,15 @@ def test_norm_of_as_many_rows_as_there_may_be(dev):
         want = v + y[at].double() * r ** 3
         assert bool(((dx[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * (1 + v.abs())).all()), i
         assert bool(((stats[at, 3].double() - r[:, 0]).abs() <= 2.0 ** -21 * r[:, 0]).all()), i
+
+
+def test_linear_bias_gradient_of_many_columns(dev):
+    """More columns than one dimension of a grid has threads for: of one row, dbias is dY."""
+    n = (1 << 29) + 71
+    p = mm.LinearPlan(1, 8, n, mm.BFLOAT16, bias=True, training=True, force_algo=mm.ALGO_GENERAL, tile=2)
+    dy = fill(torch.empty(1, n, dtype=BF16, device=dev), 6)
+    db, buf = guarded((n,), BF16, dev)
+    p.backward(None, None, dy, dbias=db)
+    torch.cuda.synchronize()
+    assert torch.equal(db, dy[0])
+    check_guard(buf, db)
