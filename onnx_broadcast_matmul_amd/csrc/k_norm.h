@@ -256,30 +256,42 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_norm_fwd(typename 
             if (!a.w2) w2[i] = piece_ones<DT>();
         }
     }
-    // Mean and reciprocal deviation of v.
+    // Mean and reciprocal deviation of v.  A layer norm's first mean is off by its
+    // sum's roundings, some units in the last place.  The differences to it, small
+    // where a mean is large, are summed too and correct both, so that the mean is
+    // off by its last rounding alone and a constant row is nothing but its mean.
     auto moments = [&](int kind, float eps, const float (*v)[VE]) {
-        float mean = 0.0f, s = 0.0f;
+        float mean = 0.0f, s = 0.0f, var;
         if (ALL && kind == MM_NORM_LAYER) {
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) s += v[i][e];
             mean = sums(false, 0.0f, s).y * inv_n;
+            asm("" : "+v"(mean));  // rounded here, not within the differences' fma
+            float rest = 0.0f;
             s = 0.0f;
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
                     const float d = col(i) + e < N ? v[i][e] - mean : 0.0f;
+                    rest += d;
                     s = fmaf(d, d, s);
                 }
+            const float2 both = sums(true, rest, s);
+            const float more = both.x * inv_n;
+            mean += more;
+            var = fmaf(-more, more, both.y * inv_n);
+            var = var < 0.0f ? 0.0f : var;  // (NaN stays)
         } else {
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) s = fmaf(v[i][e], v[i][e], s);
+            var = sums(false, 0.0f, s).y * inv_n;
         }
-        return make_float2(mean, 1.0f / sqrtf(sums(false, 0.0f, s).y * inv_n + eps));
+        return make_float2(mean, 1.0f / sqrtf(var + eps));
     };
     // v = (v - mean) r w + b.
     auto normalise = [&](float (*v)[VE], int kind, const float2 &m, const void *w, const uint4 *held, const void *b,
