@@ -1,4 +1,5 @@
-"""GPU tests of the norms' statistics: what a large mean does to a layer norm.
+"""GPU tests of the norms' statistics: mean and reciprocal deviation of the
+block and of the sum, and what a large mean does to a layer norm.
 
 Tolerances: a value of a row passes at most 16 additions in its thread, 6 in the
 wave and 15 between waves, so that sums are off by less than 64 2^-24 of the
@@ -12,8 +13,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ffn import BF16, F16, F32, rand  # noqa: E402
-from test_gpu_norm import LAYER, S, mean  # noqa: E402
+from test_gpu_ffn import BF16, F16, F32, TYPES, rand  # noqa: E402
+from test_gpu_norm import KINDS, LAYER, S, SIZES, Case, gate_rows, mean  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -21,6 +22,39 @@ def dev():
     assert torch.cuda.is_available(), "GPU tests need a GPU"
     mm.lib()
     return torch.device("cuda:0")
+
+
+def moments64(v, ev, kind, eps):
+    """Mean and r of v (off by ev) in 64 bits, and how far they may be off."""
+    if not kind:
+        one = torch.ones_like(v[:, :1])
+        return 0 * one, 0 * one, one, 0 * one
+    m = mean(v) if kind == LAYER else 0 * v[:, :1]
+    d = v - m
+    em = mean(ev) + S * m.abs() + 64 * S * mean(d.abs()) if kind == LAYER else 0 * m
+    var = mean(d * d)
+    evar = 2 * mean(d.abs() * ev) + mean(ev * ev) + em * em + 64 * S * var
+    r = (var + eps) ** -0.5
+    return m, em, r, ((var - evar).clamp_min(0) + eps) ** -0.5 - r + 6 * S * r
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=str)
+@pytest.mark.parametrize("i", range(len(SIZES)), ids=lambda i: "x".join(map(str, SIZES[i])))
+def test_norm_statistics(i, dt, dev):
+    """All four of a row, in every form; of a norm that is absent 0 and 1."""
+    m, n = SIZES[i]
+    for j, kind in enumerate(KINDS):
+        c = Case(dev, m, n, TYPES[dt], seed=10 * j, gr=gate_rows(i + j, m), alpha=(1.0, -0.5)[j % 2], shift=(0.0, 5.0)[j % 2], **kind)
+        stats = torch.full((m, 4), -7.0, device=dev)
+        out = torch.empty_like(c.x) if c.pre else None
+        c.plan.execute(c.x, out, block=c.b, gate=c.g, pre_weight=c.w2, pre_bias=c.b2, post_weight=c.w1, post_bias=c.b1,
+                       stats=stats)
+        b = c.x.double() if c.b is None else c.b.double()
+        r, er = c.forward64()["sum"]
+        want = moments64(b, 0 * b, c.post, c.eps) + moments64(r, er, c.pre, c.eps)
+        for k, name in enumerate(("mean of B", "r of B", "mean of R", "r of R")):
+            v, e = want[2 * k], want[2 * k + 1]
+            assert bool(((stats[:, k:k + 1].double() - v).abs() <= e * (1 + 2.0 ** -10)).all()), (name, j)
 
 
 @pytest.mark.parametrize("n", [7, 40, 513, 1000, 2047, 3000, 4099, 8192, 16384])
