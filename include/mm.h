@@ -562,6 +562,17 @@ mm_status mm_linear_plan_create(const mm_linear_desc *desc, int dtype, const mm_
  * launch's; z_type 0 where nothing is kept). */
 mm_status mm_linear_get_desc(mm_plan_t plan, mm_linear_desc *desc);
 
+/* The second launches of a training plan's backward products: > 0 where the
+ * columns [dx_col, in_features) of dX, or [dw_col, row length) of dW as stored,
+ * run behind the others on the tile entry given, else 0 and 0. */
+typedef struct mm_linear_tails {
+    int64_t dx_col, dw_col;
+    int32_t dx_tile, dw_tile;
+} mm_linear_tails;
+
+/* MM_ERR_BAD_OPTION for a plan without training. */
+mm_status mm_linear_get_tails(mm_plan_t plan, mm_linear_tails *tails);
+
 /* Enqueue the forward pass on `stream`.  bias and residual are non-NULL exactly
  * when the plan has them (MM_ERR_NULL_ARG / MM_ERR_BAD_OPTION).  Z, of a training
  * plan with an activation only, receives what the backward pass needs, or is

@@ -102,6 +102,11 @@ class LinearDesc(ctypes.Structure):
                 ("dw_split_k", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class LinearTails(ctypes.Structure):
+    _fields_ = [("dx_col", ctypes.c_int64), ("dw_col", ctypes.c_int64), ("dx_tile", ctypes.c_int32),
+                ("dw_tile", ctypes.c_int32)]
+
+
 class NormDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
                 ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32), ("post_eps", ctypes.c_float),
@@ -212,6 +217,8 @@ def lib() -> ctypes.CDLL:
         L.mm_linear_plan_create.restype = ctypes.c_int
         L.mm_linear_get_desc.argtypes = [vp, ctypes.POINTER(LinearDesc)]
         L.mm_linear_get_desc.restype = ctypes.c_int
+        L.mm_linear_get_tails.argtypes = [vp, ctypes.POINTER(LinearTails)]
+        L.mm_linear_get_tails.restype = ctypes.c_int
         L.mm_linear_execute.argtypes = [vp] * 9
         L.mm_linear_execute.restype = ctypes.c_int
         L.mm_linear_backward.argtypes = [vp] * 11
@@ -860,6 +867,13 @@ class LinearPlan(Plan):
         d = LinearDesc()
         _check(lib().mm_linear_get_desc(self._handle, ctypes.byref(d)))
         return {name: getattr(d, name) for name, _ in d._fields_ if name != "reserved"}
+
+    def tails(self) -> dict:
+        """mm_linear_get_tails: the columns from which a training plan's dX and
+        dW run as second launches, and their tile entries (0: they do not)."""
+        t = LinearTails()
+        _check(lib().mm_linear_get_tails(self._handle, ctypes.byref(t)))
+        return {name: getattr(t, name) for name, _ in t._fields_}
 
     _weight = GluPlan._weight
 

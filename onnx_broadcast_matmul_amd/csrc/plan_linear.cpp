@@ -255,6 +255,14 @@ mm_status mm_linear_get_desc(mm_plan_t p, mm_linear_desc *d) {
     return MM_OK;
 }
 
+mm_status mm_linear_get_tails(mm_plan_t p, mm_linear_tails *t) {
+    clear_error();
+    if (!p || !t) return fail(MM_ERR_NULL_ARG, "plan or tails is NULL");
+    if (!p->is_linear || !p->training) return fail(MM_ERR_BAD_OPTION, "not a linear-layer plan with training");
+    *t = mm_linear_tails{p->dx_tail_col, p->dw_tail_col, p->dx_tail_tile + 1, p->dw_tail_tile + 1};
+    return MM_OK;
+}
+
 mm_status mm_linear_execute(mm_plan_t p, const void *X, const void *W, const void *bias, const void *residual, void *Y,
                             void *Z, void *z_scale, void *stream) {
     clear_error();

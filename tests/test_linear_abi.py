@@ -183,3 +183,30 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         p.execute(x, w, y, bias=b)
     with pytest.raises(ValueError, match="device"):
         linear(**T).backward(x, w, y)
+
+
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+@pytest.mark.parametrize("dtype", [mm.FLOAT16, mm.BFLOAT16])
+def test_linear_backward_second_launches(dtype, nk):
+    """The sizes whose backward pass is compared as whole rounds and a rest run so."""
+    for j, (m, k, n) in enumerate(((4104, 5000, 512), (512, 5000, 4104), (512, 4104, 5000))):
+        p = mm.LinearPlan(m, k, n, dtype, activation=mm.ACT_SILU, trans_w=nk, bias=True, training=True, z_type=mm.INT8,
+                          x_type=mm.INT8 if j == 2 else 0)
+        t = p.tails()
+        width = k if j == 0 or nk else n
+        split, whole = ("dx", "dw") if j == 0 else ("dw", "dx")
+        assert 0 < t[split + "_col"] < width and t[split + "_col"] % 128 == 0 and 1 <= t[split + "_tile"] <= 5, t
+        assert t[whole + "_col"] == t[whole + "_tile"] == 0
+    p = mm.LinearPlan(4104, 5000, 512, dtype, trans_w=nk, training=True, dx_tile=1, dw_tile=1)
+    assert not any(p.tails().values())
+
+
+def test_linear_tails_refusals():
+    L = mm.lib()
+    t = mm.LinearTails()
+    p = mm.LinearPlan(4, 64, 32, mm.FLOAT, training=True)
+    assert L.mm_linear_get_tails(None, ctypes.byref(t)) == mm.ERR_NULL_ARG
+    assert L.mm_linear_get_tails(p._handle, None) == mm.ERR_NULL_ARG
+    assert L.mm_linear_get_tails(p._handle, ctypes.byref(t)) == 0
+    for other in (mm.LinearPlan(4, 64, 32, mm.FLOAT), mm.GluPlan(4, 64, 32, mm.FLOAT, training=True)):
+        assert L.mm_linear_get_tails(other._handle, ctypes.byref(t)) == mm.ERR_BAD_OPTION
