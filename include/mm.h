@@ -494,7 +494,7 @@ mm_status mm_checkpoint_pack(const void *X, int dtype, int64_t rows, int64_t col
 
 /* Enqueue the values of a checkpoint as a dense tensor of type dtype, rounded
  * to nearest even where the type does not hold them (values of a wider
- * tensor's checkpoint). */
+ * tensor's checkpoint).  Scale bytes below 7, which no checkpoint has, are read as 7. */
 mm_status mm_checkpoint_unpack(const void *q, const void *scale, int64_t rows, int64_t cols, int dtype, void *X,
                                void *stream);
 

@@ -3,8 +3,8 @@
 // and dW (both operands as rows of one k).
 //
 // Four waves, one on each SIMD, hold 128 x 128 of the larger tile each: 256
-// accumulator registers, and an LDS read of 32 bytes for every MFMA, where eight
-// waves of 128 x 64 need 48.  One wave alone has to keep its matrix core fed, so
+// accumulator registers, and LDS reads of 256 bytes for every MFMA of 16 x 16 x 32,
+// where eight waves of 128 x 64 need 384 for as many products.  One wave alone has to keep its matrix core fed, so
 // the order of everything is written down: a half stage is 64 MFMAs of 32 k, and the
 // reads of the next half's fragments and the loads of a later stage stand one
 // between every two to four of them.  (In groups between groups of eight MFMAs they

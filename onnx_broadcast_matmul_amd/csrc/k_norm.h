@@ -7,8 +7,8 @@
 // The threads of a row hold it in registers from the first load to the last
 // store, so every tensor is read or written once: memory bounds long runs of
 // rows, the launch a few.  The variance of a layer norm is formed from the
-// differences to the mean (a second sum over the registers), so that a large
-// mean costs no digits.
+// differences to the mean (a second sum over the registers), and the mean
+// corrected by their sum, so that a large mean costs its own rounding alone.
 #pragma once
 
 #include <type_traits>
@@ -477,14 +477,17 @@ __device__ __forceinline__ void kept_load(const void *p, const void *scale, int6
 // sums, in registers; between the two sums over the row only what memory gave and
 // the gradient on its way stay, centred values are formed again.  128 registers
 // keep the GPU full (two workgroups of 512 threads on a CU); in 16-bit types, up
-// to 4096 columns, they also hold the next row, which is asked for before the
-// present one is worked on, and the weights.
+// to 4096 columns and without ALL, they also hold the next row, which is asked for
+// before the present one is worked on, and the weights.  They are too few for both
+// norms with ALL (12 to 280 bytes a lane go to scratch, but for a wave a row from
+// checkpoints and in FP16 and FP32) and for the 16 columns a lane of rows above 8192 (92
+// to 684 in every form).
 //
 // What a plan has is told apart at compile time as far as the loop over a row's
 // columns feels it: its arithmetic bounds the kernel, not memory alone (with
 // every choice made at run time, 70 instructions a column, 94 us for 8192 x 4096
-// from checkpoints).  ALL: layer norms, gradients of biases and rows that are
-// no whole number of pieces; without them absent columns (zeros) stay zero by
+// from checkpoints).  ALL: layer norms, gradients of biases, a post bias where the
+// gate's gradient is wanted, and rows that are no whole number of pieces; without them absent columns (zeros) stay zero by
 // themselves.  Absent weights and gates are ones.
 template <int DT, int KEPT, int TPR, int COLS, bool PRE, bool POST, bool ALL>
 __global__ __launch_bounds__(norm_bwd_block(TPR), 4) void k_norm_bwd(NormBwd a) {

@@ -10,9 +10,9 @@
 
 namespace mm {
 
-// Workers of the backward pass (see norm.h) for `rows` rows at least a few of
-// which share a worker: as many as fill the GPU with threads, so that the
-// partial sums stay small against the rows.
+// Workers of the backward pass (see norm.h): as many as fill the GPU with threads.
+// Their partial sums, up to 24 bytes a column each, are small against the rows (12
+// bytes a column and row in 16-bit types) only where a worker has many of them.
 static void deal_rows(const mm_plan_s *p, int32_t *per, int32_t *workers) {
     const int64_t M = p->M, most = (int64_t)kNumCUs * 1024 / norm_bwd_threads(p->N);
     int64_t n = std::max<int64_t>(1, cdiv(M, most));
