@@ -22,7 +22,7 @@
 // Rows of 64 k, 128 bytes, keep a load's 64 lanes on 8 rows; with rows half as
 // long every load took longer to issue (595 us for 540).
 //
-// What bounds it: the matrix cores, 1.3 to 1.48 PFLOP/s from 8192 x 4096 x 10240
+// What bounds it: the matrix cores, 1.26 to 1.48 PFLOP/s from 8192 x 4096 x 10240
 // on, where a product of 8192^3 reaches 1.55 at the clock that random operands
 // leave.  A round of tiles of 256 x 256 takes 10 us and 21 ns for each k, one of 256 x
 // 128 7 us and 12 ns; the 10 us are the first loads' way and the epilogue, during
