@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_ffn import BF16, F32, check_guard, guarded, rand  # noqa: E402
+from test_gpu_ffn import BF16, F16, F32, check_guard, guarded, rand  # noqa: E402
 from test_gpu_linear import pack64  # noqa: E402
 
 P = 1_000_003
@@ -41,6 +41,13 @@ def fill(t, seed):
     flat[:whole].view(-1, P).copy_(one)
     flat[whole:].copy_(one[:flat.numel() - whole])
     return t
+
+
+def signs(seed, shape, dt, dev):
+    """The pattern of -1, 0 and 1."""
+    n = int(np.prod(shape))
+    one = (rand((P,), F32, dev, seed) * 1.5).round().clamp(-1, 1).to(dt)
+    return one.repeat(-(-n // P))[:n].view(shape)
 
 
 def blocks_to_check(cols):
@@ -136,3 +143,54 @@ def test_linear_bias_gradient_of_many_columns(dev):
     torch.cuda.synchronize()
     assert torch.equal(db, dy[0])
     check_guard(buf, db)
+
+
+@pytest.mark.parametrize("dt,nk", [(BF16, True), (F16, False)], ids=["bf16-nk", "fp16-kn"])
+def test_linear_of_5gb_activations(dt, nk, dev):
+    """Y, the residual, dY and the workspace's dZ past 2^32 bytes, Z's checkpoint
+    past 2^31.  Whole numbers, so that sums are exact and results rounded once."""
+    m, k, n = 65600, 64, 40008
+    whole = lambda seed, *shape: signs(seed, shape, dt, dev)  # noqa: E731
+    x, w, b = whole(1, m, k), whole(2, *((n, k) if nk else (k, n))), whole(3, n)
+    r, dy = whole(4, m, n), whole(5, m, n)
+    p = mm.LinearPlan(m, k, n, mm.torch_dtype_code(dt), activation=mm.ACT_RELU, trans_w=nk, bias=True, residual=True,
+                      training=True, z_type=mm.INT8, x_type=mm.INT8)
+    z, zs = torch.empty(m, n, dtype=torch.int8, device=dev), torch.empty(m, mm.checkpoint_blocks(n), dtype=torch.uint8, device=dev)
+    y = torch.empty_like(r)
+    p.execute(x, w, y, bias=b, residual=r, Z=z, z_scale=zs)
+    xq, xs = mm.checkpoint_pack(x)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    p.backward(xq, w, dy, Z=z, z_scale=zs, x_scale=xs, dX=dx, dW=dw, dbias=db)
+    wf = (w.t() if nk else w).float()
+    sw, sb = torch.zeros(k, n, device=dev), torch.zeros(n, device=dev)
+    for i in range(0, m, 8200):
+        at = slice(i, i + 8200)
+        z32 = x[at].float() @ wf + b.float()
+        assert torch.equal(y[at].float(), z32.clamp_min(0) + r[at].float()), i
+        assert torch.equal(mm.checkpoint_unpack(z[at], zs[at], F32), z32), i
+        dz = dy[at].float() * (z32 > 0)
+        assert torch.equal(dx[at], (dz @ wf.t()).to(dt)), i
+        sw += x[at].float().t() @ dz
+        sb += dz.sum(0)
+    assert torch.equal(dw, (sw.t() if nk else sw).to(dt)) and torch.equal(db, sb.to(dt))
+
+
+@pytest.mark.parametrize("algo", [0, mm.ALGO_GENERAL], ids=["few-rows", "tiles"])
+@pytest.mark.parametrize("nk", [True, False], ids=["nk", "kn"])
+def test_linear_of_5gb_weights(nk, algo, dev):
+    """W and dW past 2^32 bytes, of four rows.  Whole numbers as above."""
+    m, k, n, dt = 4, 33000, 72008, BF16
+    x, w, dy = signs(1, (m, k), dt, dev), signs(2, (n, k) if nk else (k, n), dt, dev), signs(3, (m, n), dt, dev)
+    p = mm.LinearPlan(m, k, n, mm.BFLOAT16, trans_w=nk, training=True, force_algo=algo)
+    assert mm.ALGO_NAMES[p.algo] == ("general" if algo else "skinny_m")
+    y, dx, dw = torch.empty_like(dy), torch.empty_like(x), torch.empty_like(w)
+    p.execute(x, w, y)
+    p.backward(x, w, dy, dX=dx, dW=dw)
+    sums = torch.zeros(m, k, device=dev)
+    for i in range(0, n, 9001):  # output features
+        at = slice(i, i + 9001)
+        part = (w[at].t() if nk else w[:, at]).float()
+        assert torch.equal(y[:, at], (x.float() @ part).to(dt)), i
+        sums += dy[:, at].float() @ part.t()
+        assert torch.equal((dw[at].t() if nk else dw[:, at]).float(), x.float().t() @ dy[:, at].float()), i
+    assert torch.equal(dx, sums.to(dt))
